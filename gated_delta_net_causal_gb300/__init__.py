@@ -106,6 +106,19 @@ def library() -> ctypes.CDLL:
                                        i64, vp]
         L.gdn_decode_layer_workspace_size.restype = ctypes.c_int
         L.gdn_decode_layer_workspace_size.argtypes = [pd, i32, i32, ctypes.POINTER(i64)]
+        L.gdn_decay_step.restype = ctypes.c_int
+        L.gdn_decay_step.argtypes = [pd, i32, vp, i32, vp, i64, vp, i64, vp, i64, vp, i64, ctypes.c_float, vp, vp, vp,
+                                     i64, vp, vp, vp]
+        L.gdn_decay_prefill.restype = ctypes.c_int
+        L.gdn_decay_prefill.argtypes = [pd, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, ctypes.c_float, vp, vp,
+                                        vp, i64, vp, vp, vp, i64, vp]
+        L.gdn_decay_prefill_workspace_size.restype = ctypes.c_int
+        L.gdn_decay_prefill_workspace_size.argtypes = [pd, i32, i64, ctypes.POINTER(i64)]
+        L.gdn_add_rmsnorm.restype = ctypes.c_int
+        L.gdn_add_rmsnorm.argtypes = [i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, ctypes.c_float, vp, i64, vp, i64, vp,
+                                      vp]
+        L.gdn_linear_fp8.restype = ctypes.c_int
+        L.gdn_linear_fp8.argtypes = [i64, i32, i32, vp, i64, vp, vp, vp, vp, i32, vp, i64, vp]
         _lib = L
     return _lib
 
@@ -482,6 +495,165 @@ def gdn_decode_layer(d: GdnDims, x: torch.Tensor, w_in, w_out, conv_w, decay_par
     return y
 
 
+def _here(*tensors):
+    """Every tensor of a call (None allowed) is on the current CUDA device, whose context the library launches in."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise ValueError(f"every tensor must be on the current CUDA device (cuda:{dev}), got {t.device}")
+
+
+def _rows(t: torch.Tensor, name: str, dtype, rows: int, width: int):
+    """Address and row stride of a [rows][width] operand: 2-D, or 3-D with the heads apart, its rows contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    shape, stride = t.shape, t.stride()
+    ok = len(shape) in (2, 3) and shape[0] == rows
+    if ok and len(shape) == 3:
+        ok = shape[1] * shape[2] == width and stride[2] == 1 and (shape[1] == 1 or stride[1] == shape[2])
+    elif ok:
+        ok = shape[1] == width and (width == 1 or stride[1] == 1)
+    if not ok:
+        raise ValueError(f"{name} must hold {rows} rows of {width} contiguous elements, got shape {tuple(shape)}, "
+                         f"strides {tuple(stride)}")
+    return t.data_ptr(), (stride[0] if rows > 1 else width)
+
+
+def _dense(t: Optional[torch.Tensor], name: str, dtype, n: int) -> Optional[int]:
+    """Address of a contiguous operand of n elements."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and hold {n} elements, got shape {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _decay_operands(d: GdnDims, rows, q, k, v, g, core_out, z, norm_w, out, scale):
+    """The operands gdn_decay_step and gdn_decay_prefill share, as their C arguments: those before and after state."""
+    io, f32 = _io(d), torch.float32
+    Hk, Hv, D = d.n_k_heads, d.n_v_heads, d.head_dim
+    gs = 0
+    if g.dim() == 2:
+        gp, gs = _rows(g, "g", f32, rows, Hv)
+    else:
+        gp = _dense(g, "g", f32, Hv)
+    zp, zs = (None, 0) if z is None else _rows(z, "z", io, rows, Hv * D)
+    head = (*_rows(q, "q", io, rows, Hk * D), *_rows(k, "k", io, rows, Hk * D), *_rows(v, "v", io, rows, Hv * D), gp, gs,
+            D ** -0.5 if scale is None else float(scale))
+    tail = (_dense(core_out, "core_out", f32, rows * Hv * D), zp, zs, _dense(norm_w, "norm_w", f32, D),
+            _dense(out, "out", io, rows * Hv * D))
+    return head, tail
+
+
+def gdn_decay_step(d: GdnDims, q, k, v, g, state, core_out=None, z=None, norm_w=None, out=None,
+                   scale: Optional[float] = None, state_slots=None, stream=None):
+    """One token of linear attention with a decay for each head, per row: q, k [B][Hk*D], v, z [B][Hv*D] (rows may be
+    slices of a wider activation; [B][heads][D] too), g fp32 [Hv] or [B][Hv] log decays, state [B or slots][Hv][D][D]
+    fp32 in place. scale None: D ** -0.5."""
+    _here(q, k, v, g, state, core_out, z, norm_w, out, state_slots)
+    rows, slots = q.shape[0], state.shape[0]
+    if state_slots is not None:
+        sp = _dense(state_slots, "state_slots", torch.int32, rows)
+    elif slots != rows:
+        raise ValueError(f"state must hold one state per row ({rows}), got {slots}")
+    else:
+        sp = None
+    head, tail = _decay_operands(d, rows, q, k, v, g, core_out, z, norm_w, out, scale)
+    st = library().gdn_decay_step(
+        ctypes.byref(d), rows, sp, slots, *head,
+        _dense(state, "state", torch.float32, slots * d.n_v_heads * d.head_dim * d.head_dim), *tail, _stream(stream))
+    if st:
+        _check(st, "gdn_decay_step")
+    return core_out, out
+
+
+def gdn_decay_prefill_workspace_size(d: GdnDims, num_seqs: int, total_tokens: int) -> int:
+    n = ctypes.c_int64(0)
+    _check(library().gdn_decay_prefill_workspace_size(ctypes.byref(d), int(num_seqs), int(total_tokens),
+                                                      ctypes.byref(n)), "gdn_decay_prefill_workspace_size")
+    return n.value
+
+
+def gdn_decay_prefill(d: GdnDims, cu_seqlens, q, k, v, g, state, core_out=None, z=None, norm_w=None, out=None,
+                      scale: Optional[float] = None, workspace="auto", stream=None):
+    """The same over packed sequences (cu_seqlens int32 [N+1]), rows of q, k, v, z, g and the outputs being tokens,
+    state [N][Hv][D][D]. workspace: "auto" allocates what the library asks for, None passes none, or a CUDA uint8
+    tensor of at least gdn_decay_prefill_workspace_size bytes."""
+    _here(cu_seqlens, q, k, v, g, state, core_out, z, norm_w, out)
+    rows, n = q.shape[0], cu_seqlens.numel() - 1
+    head, tail = _decay_operands(d, rows, q, k, v, g, core_out, z, norm_w, out, scale)
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError("workspace must be 'auto', None or a CUDA tensor")
+        need = gdn_decay_prefill_workspace_size(d, n, rows)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+        if workspace is not None and isinstance(stream, torch.cuda.Stream):
+            # freed when this call returns: not reused before that stream is done with it
+            workspace.record_stream(stream)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        _here(workspace)
+        ws_ptr, ws_bytes = _ptr(workspace, "workspace", torch.uint8), workspace.numel()
+    st = library().gdn_decay_prefill(
+        ctypes.byref(d), n, _dense(cu_seqlens, "cu_seqlens", torch.int32, n + 1), rows, *head,
+        _dense(state, "state", torch.float32, n * d.n_v_heads * d.head_dim * d.head_dim), *tail, ws_ptr, ws_bytes,
+        _stream(stream))
+    if st:
+        _check(st, "gdn_decay_prefill")
+    return core_out, out
+
+
+def gdn_add_rmsnorm(x: torch.Tensor, norm_w: Optional[torch.Tensor] = None, residual=None, sum_out=None, out=None,
+                    out_q=None, out_scale=None, eps: float = 1e-6, stream=None):
+    """s = x + residual; y = RMSNorm(s) * norm_w (norm_w None: y = s); sum_out = s, out = y in x's dtype, out_q
+    (torch.float8_e4m3fn) with out_scale (fp32, one per row) = y in 8 bits. x, residual, sum_out, out, out_q:
+    [rows][cols], rows may be strided."""
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    io = x.dtype
+    if io not in _TORCH_TO_GDN:
+        raise TypeError(f"x must be float16, bfloat16 or float32, got {io}")
+    _here(x, norm_w, residual, sum_out, out, out_q, out_scale)
+    rows, cols = x.shape
+
+    def opt(t, name, dtype):
+        return (None, 0) if t is None else _rows(t, name, dtype, rows, cols)
+
+    st = library().gdn_add_rmsnorm(
+        rows, cols, _TORCH_TO_GDN[io], *_rows(x, "x", io, rows, cols), *opt(residual, "residual", io),
+        *opt(sum_out, "sum_out", io), _dense(norm_w, "norm_w", torch.float32, cols), eps, *opt(out, "out", io),
+        *opt(out_q, "out_q", torch.float8_e4m3fn), _dense(out_scale, "out_scale", torch.float32, rows), _stream(stream))
+    if st:
+        _check(st, "gdn_add_rmsnorm")
+    return sum_out, out, out_q, out_scale
+
+
+def gdn_linear_fp8(x: torch.Tensor, x_scale, w, w_scale, y: torch.Tensor, bias=None, stream=None) -> torch.Tensor:
+    """y[m][n] = x_scale[m] w_scale[n] sum_k x[m][k] w[n][k] + bias[n]: x [M][K] and w [N][K] torch.float8_e4m3fn
+    (rows of x and y may be strided), scales and bias fp32, y float16, bfloat16 or float32."""
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w must be 2-D")
+    if y.dtype not in _TORCH_TO_GDN:
+        raise TypeError(f"y must be float16, bfloat16 or float32, got {y.dtype}")
+    _here(x, x_scale, w, w_scale, y, bias)
+    M, K = x.shape
+    N = w.shape[0]
+    xp, xs = _rows(x, "x", f8, M, K)
+    yp, ys = _rows(y, "y", y.dtype, M, N)
+    if M == 1:
+        ys = (N + 7) // 8 * 8  # the one row's stride is never used
+    st = library().gdn_linear_fp8(
+        M, N, K, xp, xs, _dense(x_scale, "x_scale", f32, M), _dense(w, "w", f8, N * K),
+        _dense(w_scale, "w_scale", f32, N), _dense(bias, "bias", f32, N), _TORCH_TO_GDN[y.dtype], yp, ys,
+        _stream(stream))
+    if st:
+        _check(st, "gdn_linear_fp8")
+    return y
+
+
 def gdn_selftest_wait_timeout(limit_ns: int, gave_up: torch.Tensor, stream=None):
     """A device-side bounded wait made to give up after limit_ns; gave_up is a
     CUDA int32 tensor of one element, set to 1 by the kernel."""
@@ -504,6 +676,8 @@ __all__ = ["GdnDims", "GdnError", "dims", "library", "status_string", "gdn_conv_
            "gdn_prefill_chunked_static", "GDN_STATIC_SCRATCH_BYTES", "gdn_gated_rmsnorm", "gdn_device_error",
            "gdn_selftest_wait_timeout", "gdn_linear", "gdn_linear_workspace_size", "gdn_decode_layer",
            "gdn_decode_layer_workspace_size", "GdnLayerWeights",
+           "gdn_decay_step", "gdn_decay_prefill", "gdn_decay_prefill_workspace_size", "gdn_add_rmsnorm",
+           "gdn_linear_fp8",
            "gdn_qkv_features", "gdn_version", "gdn_host_pointer", "GDN_MAP_GROUPED", "GDN_MAP_TILED",
            "GDN_DECAY_LOG_RATE", "GDN_DECAY_NEGATIVE_RATE", "GDN_F16", "GDN_BF16", "GDN_F32",
            "GDN_QK_PRENORMALIZED", "GDN_GATES_PRECOMPUTED", "GDN_PREFILL_CUDA_CORES",

@@ -176,7 +176,7 @@ const char* gdn_status_string(int32_t status) {
   }
 }
 
-int32_t gdn_version(void) { return 400; }
+int32_t gdn_version(void) { return 500; }
 
 gdn_status gdn_host_pointer(const void* host, void** device) {
   if (host == nullptr || device == nullptr) return GDN_ERR_INVALID_ARG;
@@ -594,6 +594,247 @@ gdn_status gdn_decode_layer(const gdn_dims* dims, int32_t hidden, int32_t batch,
   return cuda_status(gdn::launch_linear(pout, yc, l.vw, w->w_out, lin, s));
 }
 
+namespace {
+
+// Shared by gdn_decay_step (rows = batch, cu_seqlens NULL) and
+// gdn_decay_prefill (rows = total tokens, states = sequences).
+gdn_status check_decay(const gdn_dims* dims, int64_t rows, int64_t states, const int32_t* index, int64_t index_count,
+                       const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                       int64_t v_stride, const float* g, int64_t g_stride, float scale, float* state, float* core_out,
+                       const void* z, int64_t z_stride, const float* norm_w, void* out, void* workspace,
+                       int64_t ws_bytes, gdn::DecayArgs* p) {
+  const int64_t es = dtype_size(dims->io_dtype);
+  const int64_t Hk = dims->n_k_heads, Hv = dims->n_v_heads, D = dims->head_dim;
+  if (!isfinite(scale)) return GDN_ERR_INVALID_ARG;
+  if (rows > 0) {
+    if (!q || !k || !v || !g || !state) return GDN_ERR_INVALID_ARG;
+    if (core_out == nullptr && out == nullptr) return GDN_ERR_INVALID_ARG;
+    if ((z == nullptr) != (norm_w == nullptr) || (z != nullptr && out == nullptr)) return GDN_ERR_INVALID_ARG;
+    if (g_stride != 0 && g_stride < Hv) return GDN_ERR_INVALID_ARG;
+  }
+  const int64_t zs = z != nullptr ? z_stride : Hv * D;
+  if (q_stride < Hk * D || k_stride < Hk * D || v_stride < Hv * D || zs < Hv * D) return GDN_ERR_INVALID_ARG;
+  int64_t tmp = 0, state_bytes = 0;
+  for (int64_t st : {q_stride, k_stride, v_stride, zs, g_stride})
+    if (!mul_ok(rows, st, &tmp) || !mul_ok(tmp, 4, &tmp)) return GDN_ERR_EXTENT;
+  if (!mul_ok(rows, Hv * D * 4, &tmp) || !mul_ok(states, Hv * D * D * 4, &state_bytes)) return GDN_ERR_EXTENT;
+  for (int64_t st : {q_stride, k_stride, v_stride, zs})
+    if ((st * es) % 16 != 0) return GDN_ERR_ALIGN;
+  const void* ptrs[] = {q, k, v, g, state, core_out, z, norm_w, out, index};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return GDN_ERR_ALIGN;
+  const auto span = [&](const void* ptr, int64_t stride, int64_t width, int64_t size) {
+    return range_of(ptr, ptr != nullptr && rows > 0 ? ((rows - 1) * stride + width) * size : 0);
+  };
+  const Range inputs[] = {span(q, q_stride, Hk * D, es), span(k, k_stride, Hk * D, es), span(v, v_stride, Hv * D, es),
+                          span(z, zs, Hv * D, es),       span(g, g_stride, Hv, 4),      range_of(norm_w, z ? D * 4 : 0),
+                          range_of(index, index ? index_count * 4 : 0)};
+  const Range outputs[] = {range_of(state, state_bytes), span(core_out, Hv * D, Hv * D, 4),
+                           span(out, Hv * D, Hv * D, es), range_of(workspace, ws_bytes)};
+  for (int i = 0; i < 4; ++i) {
+    for (const Range& in : inputs)
+      if (overlap(outputs[i], in)) return GDN_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outputs[i], outputs[j])) return GDN_ERR_ALIAS;
+  }
+  p->q = q;
+  p->q_stride = q_stride;
+  p->k = k;
+  p->k_stride = k_stride;
+  p->v = v;
+  p->v_stride = v_stride;
+  p->g = g;
+  p->g_stride = g_stride;
+  p->state = state;
+  p->core_out = core_out;
+  p->z = z;
+  p->z_stride = zs;
+  p->norm_w = norm_w;
+  p->out = out;
+  p->Hk = (int32_t)Hk;
+  p->Hv = (int32_t)Hv;
+  p->rep = (int32_t)(Hv / Hk);
+  p->map = dims->map;
+  p->scale = scale;
+  p->rms_eps = dims->rms_eps;
+  return GDN_OK;
+}
+
+// Sizes of gdn_decay_prefill and its workspace: the states of the segments,
+// then their decays.
+gdn_status decay_plan(const gdn_dims* dims, int32_t num_seqs, int64_t total_tokens, gdn::DecaySegments* sg,
+                      int64_t* bytes, int64_t* decays_at) {
+  gdn_status st = check_dims(dims);
+  if (st != GDN_OK) return st;
+  if (num_seqs < 0 || total_tokens < 0 || (num_seqs == 0 && total_tokens > 0)) return GDN_ERR_INVALID_ARG;
+  if (num_seqs > kMaxGridY || total_tokens > INT32_MAX - 64) return GDN_ERR_EXTENT;
+  const int64_t Hv = dims->n_v_heads, D = dims->head_dim;
+  *bytes = 0;
+  *decays_at = 0;
+  sg->len = gdn::decay_segment_len(num_seqs, total_tokens, dims->n_v_heads, dims->head_dim, dims->io_dtype);
+  sg->slots = total_tokens / sg->len + num_seqs;
+  sg->states = nullptr;
+  sg->decays = nullptr;
+  int64_t tmp = 0;
+  if (!mul_ok(sg->slots, Hv, &tmp) || tmp > INT32_MAX) return GDN_ERR_EXTENT;
+  if (sg->len < total_tokens) {
+    *decays_at = tmp * D * D * 4;  // tmp <= 2^31, D <= 128: no overflow
+    *bytes = *decays_at + tmp * 4;
+  }
+  return GDN_OK;
+}
+
+}  // namespace
+
+gdn_status gdn_decay_step(const gdn_dims* dims, int32_t batch, const int32_t* state_slots, int32_t num_slots,
+                          const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, const float* g, int64_t g_stride, float scale, float* state,
+                          float* core_out, const void* z, int64_t z_stride, const float* norm_w, void* out,
+                          void* stream) {
+  gdn_status st = check_dims(dims);
+  if (st != GDN_OK) return st;
+  if (batch < 0 || num_slots < 0 || (state_slots == nullptr && num_slots != batch)) return GDN_ERR_INVALID_ARG;
+  if (batch > kMaxGridY) return GDN_ERR_EXTENT;
+  if (batch == 0) return GDN_OK;
+  gdn::DecayArgs p{};
+  st = check_decay(dims, batch, num_slots, state_slots, batch, q, q_stride, k, k_stride, v, v_stride, g, g_stride,
+                   scale, state, core_out, z, z_stride, norm_w, out, nullptr, 0, &p);
+  if (st != GDN_OK) return st;
+  p.slots = state_slots;
+  p.num_slots = num_slots;
+  return cuda_status(
+      gdn::launch_decay_step(p, dims->io_dtype, dims->head_dim, batch, static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_decay_prefill_workspace_size(const gdn_dims* dims, int32_t num_seqs, int64_t total_tokens,
+                                            int64_t* bytes) {
+  if (bytes == nullptr) return GDN_ERR_INVALID_ARG;
+  gdn::DecaySegments sg{};
+  int64_t at = 0;
+  *bytes = 0;
+  return decay_plan(dims, num_seqs, total_tokens, &sg, bytes, &at);
+}
+
+gdn_status gdn_decay_prefill(const gdn_dims* dims, int32_t num_seqs, const int32_t* cu_seqlens, int64_t total_tokens,
+                             const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, const float* g, int64_t g_stride, float scale, float* state,
+                             float* core_out, const void* z, int64_t z_stride, const float* norm_w, void* out,
+                             void* workspace, int64_t workspace_bytes, void* stream) {
+  gdn::DecaySegments sg{};
+  int64_t need = 0, decays_at = 0;
+  gdn_status st = decay_plan(dims, num_seqs, total_tokens, &sg, &need, &decays_at);
+  if (st != GDN_OK) return st;
+  if (total_tokens == 0) return GDN_OK;
+  if (cu_seqlens == nullptr) return GDN_ERR_INVALID_ARG;
+  const bool use_ws = workspace != nullptr && need > 0;
+  if (use_ws && workspace_bytes < need) return GDN_ERR_INVALID_ARG;
+  if (use_ws && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return GDN_ERR_ALIGN;
+  gdn::DecayArgs p{};
+  st = check_decay(dims, total_tokens, num_seqs, cu_seqlens, (int64_t)num_seqs + 1, q, q_stride, k, k_stride, v,
+                   v_stride, g, g_stride, scale, state, core_out, z, z_stride, norm_w, out,
+                   use_ws ? workspace : nullptr, use_ws ? need : 0, &p);
+  if (st != GDN_OK) return st;
+  p.cu_seqlens = cu_seqlens;
+  p.N = num_seqs;
+  p.T = total_tokens;
+  if (use_ws) {
+    sg.states = static_cast<float*>(workspace);
+    sg.decays = reinterpret_cast<float*>(static_cast<char*>(workspace) + decays_at);
+  } else {  // one segment per sequence
+    sg.len = total_tokens + 1;
+    sg.slots = num_seqs;
+  }
+  return cuda_status(gdn::launch_decay_scan(p, sg, dims->io_dtype, dims->head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_add_rmsnorm(int64_t rows, int64_t cols, int32_t io_dtype, const void* x, int64_t x_stride,
+                           const void* residual, int64_t residual_stride, void* sum_out, int64_t sum_stride,
+                           const float* norm_w, float eps, void* out, int64_t out_stride, void* out_q,
+                           int64_t out_q_stride, float* out_scale, void* stream) {
+  const int64_t es = dtype_size(io_dtype);
+  if (es == 0 || rows < 0 || cols < 1) return GDN_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || !isfinite(eps)) return GDN_ERR_INVALID_ARG;
+  if (rows > INT32_MAX || cols > (1 << 30)) return GDN_ERR_EXTENT;
+  if (rows == 0) return GDN_OK;
+  if (x == nullptr || (sum_out == nullptr && out == nullptr && out_q == nullptr)) return GDN_ERR_INVALID_ARG;
+  if ((out_q == nullptr) != (out_scale == nullptr)) return GDN_ERR_INVALID_ARG;
+  if (x_stride < cols || (residual && residual_stride < cols) || (sum_out && sum_stride < cols) ||
+      (out && out_stride < cols) || (out_q && out_q_stride < cols))
+    return GDN_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, residual, sum_out, norm_w, out, out_q, out_scale};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return GDN_ERR_ALIGN;
+  int64_t tmp = 0;
+  const int64_t strides[] = {x_stride, residual ? residual_stride : 0, sum_out ? sum_stride : 0,
+                             out ? out_stride : 0, out_q ? out_q_stride : 0};
+  for (int64_t st : strides)
+    if (!mul_ok(rows, st, &tmp) || !mul_ok(tmp, es, &tmp)) return GDN_ERR_EXTENT;
+  const auto span = [&](const void* ptr, int64_t stride, int64_t size) {
+    return range_of(ptr, ptr != nullptr ? ((rows - 1) * stride + cols) * size : 0);
+  };
+  const Range rx = span(x, x_stride, es), rr = span(residual, residual_stride, es);
+  const Range rw = range_of(norm_w, norm_w ? cols * 4 : 0);
+  const Range outs[] = {span(sum_out, sum_stride, es), span(out, out_stride, es), span(out_q, out_q_stride, 1),
+                        range_of(out_scale, out_scale ? rows * 4 : 0)};
+  for (int i = 0; i < 4; ++i) {
+    const bool same_x = i == 0 && sum_out == x && sum_stride == x_stride;
+    const bool same_r = i == 0 && sum_out == residual && sum_stride == residual_stride;
+    if ((overlap(outs[i], rx) && !same_x) || (overlap(outs[i], rr) && !same_r) || overlap(outs[i], rw))
+      return GDN_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return GDN_ERR_ALIAS;
+  }
+  gdn::AddRmsNormArgs p{};
+  p.rows = rows;
+  p.cols = cols;
+  p.x = x;
+  p.x_stride = x_stride;
+  p.residual = residual;
+  p.residual_stride = residual_stride;
+  p.sum = sum_out;
+  p.sum_stride = sum_stride;
+  p.norm_w = norm_w;
+  p.eps = eps;
+  p.out = out;
+  p.out_stride = out_stride;
+  p.out_q = out_q;
+  p.out_q_stride = out_q_stride;
+  p.out_scale = out_scale;
+  return cuda_status(gdn::launch_add_rmsnorm(p, io_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_linear_fp8(int64_t M, int32_t N, int32_t K, const void* x, int64_t x_stride, const float* x_scale,
+                          const void* w, const float* w_scale, const float* bias, int32_t out_dtype, void* y,
+                          int64_t y_stride, void* stream) {
+  const int64_t es = dtype_size(out_dtype);
+  if (es == 0 || M < 1 || N < 1 || K < 16 || K % 16 != 0) return GDN_ERR_INVALID_ARG;
+  if (M > (1 << 22) || N > (1 << 24) || K > (1 << 24)) return GDN_ERR_EXTENT;
+  if (!x || !x_scale || !w || !w_scale || !y) return GDN_ERR_INVALID_ARG;
+  if (x_stride < K || x_stride % 16 != 0 || y_stride < N || y_stride % 8 != 0) return GDN_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, x_scale, w, w_scale, bias, y};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return GDN_ERR_ALIGN;
+  if (x_stride > (1ll << 39)) return GDN_ERR_EXTENT;  // a tensor map's stride is below 2^40 bytes
+  int64_t tmp = 0;
+  if (!mul_ok(M, x_stride, &tmp) || !mul_ok(M, y_stride, &tmp) || !mul_ok(tmp, es, &tmp)) return GDN_ERR_EXTENT;
+  const Range ry = range_of(y, ((M - 1) * y_stride + N) * es);
+  const Range ins[] = {range_of(x, (M - 1) * x_stride + K), range_of(x_scale, M * 4), range_of(w, (int64_t)N * K),
+                       range_of(w_scale, (int64_t)N * 4), range_of(bias, bias ? (int64_t)N * 4 : 0)};
+  for (const Range& in : ins)
+    if (overlap(ry, in)) return GDN_ERR_ALIAS;
+  if (!gdn::linear_supported()) return GDN_ERR_UNSUPPORTED;
+  gdn::LinearFp8Args p{};
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.x_scale = x_scale;
+  p.w_scale = w_scale;
+  p.bias = bias;
+  p.y = y;
+  p.y_stride = y_stride;
+  return cuda_status(gdn::launch_linear_fp8(p, x, x_stride, w, out_dtype, static_cast<cudaStream_t>(stream)));
+}
+
 gdn_status gdn_selftest_wait_timeout(int64_t limit_ns, int32_t* gave_up, void* stream) {
   if (gave_up == nullptr || limit_ns < 1000 || limit_ns > 10000000000LL) return GDN_ERR_INVALID_ARG;
   return cuda_status(gdn::launch_wait_timeout((uint64_t)limit_ns, gave_up, static_cast<cudaStream_t>(stream)));
@@ -607,7 +848,8 @@ gdn_status gdn_device_error(int32_t* status, int32_t clear) {
                                                gdn::read_error_rmsnorm, gdn::read_error_prefill,
                                                gdn::read_error_prefill_tc,
                                                gdn::read_error_prefill_cp, gdn::read_error_diag,
-                                               gdn::read_error_linear};
+                                               gdn::read_error_linear, gdn::read_error_decay_step,
+                                               gdn::read_error_decay_scan, gdn::read_error_linear_fp8};
   for (auto rd : readers) {
     int32_t v = 0;
     if (rd(&v, clear != 0) != cudaSuccess) return GDN_ERR_CUDA;

@@ -1,0 +1,133 @@
+// Shared device code of linear attention with a decay for each head:
+//   S_t[j][i] = exp(g_t) S_{t-1}[j][i] + v_t[j] k_t[i],  o_t[j] = scale sum_i S_t[j][i] q_t[i]
+// over the library's fp32 states S[h][j][i] (value row j, key column i).
+#pragma once
+
+#include "gdn_common.cuh"
+#include "gdn_internal.h"
+
+namespace gdn {
+
+// exp(g) is 0 in fp32 from about -104 on, so a log decay below this bound
+// acts exactly as the bound does; bounding it keeps sums of log decays finite
+// (g = -inf is a reset of the state). A NaN stays one.
+constexpr float kDecayFloor = -128.f;
+__device__ __forceinline__ float decay_log(float g) { return g < kDecayFloor ? kDecayFloor : g; }
+
+// How the D x D state of a head lies over the threads of a CTA: LPR lanes
+// share a row, each with NV4 groups of four columns (group m of lane sub at
+// column 4 sub + 4 LPR m, so that the lanes of a row read 64 or 128
+// contiguous bytes at a time); a lane has RPL rows, RPW apart.
+template <int D>
+struct DecayGeom {
+  static constexpr int LPR = D == 32 ? 4 : (D == 64 ? 4 : 8);
+  static constexpr int NV4 = D / (4 * LPR);
+  static constexpr int RPW = 32 / LPR;
+  static constexpr int RPL = D == 32 ? 2 : (D == 96 ? 3 : 4);
+  static constexpr int WROWS = RPW * RPL;  // rows a warp owns
+  static constexpr int WARPS = D / WROWS;
+  static constexpr int THREADS = 32 * WARPS;
+  static_assert(WARPS * WROWS == D, "the warps' rows cover the state");
+};
+
+// four consecutive elements as fp32 (16-byte, or 8-byte aligned for 16-bit types)
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+  return *reinterpret_cast<const float4*>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4<__half>(const __half* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+
+// Outputs of one (token, V head): o[D] in shared memory (already scaled);
+// one warp, D/32 consecutive elements a lane. core_out, out and z point at
+// the row; z == nullptr: out is o rounded once.
+template <typename T, int D>
+__device__ __forceinline__ void decay_write_row(const float* o, float* core_out, const T* z,
+                                                const float* norm_w, T* out, float rms_eps, int lane) {
+  constexpr int PER = D / 32;
+  float ov[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) ov[e] = o[lane * PER + e];
+  if (core_out != nullptr) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) core_out[lane * PER + e] = ov[e];
+  }
+  if (out == nullptr) return;
+  if (z != nullptr) {
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) ss += ov[e] * ov[e];
+    ss = group_sum<32>(ss);
+    const float inv = 1.f / sqrtf(ss / (float)D + rms_eps);
+#pragma unroll
+    for (int e = 0; e < PER; ++e)
+      ov[e] = ov[e] * inv * norm_w[lane * PER + e] * silu_f(to_f32(z[lane * PER + e]));
+  }
+#pragma unroll
+  for (int e = 0; e < PER; ++e) out[lane * PER + e] = from_f32<T>(ov[e]);
+}
+
+// ------------------------------------------------------------- segments
+// The packed tokens of a call are cut into segments of at most sg.len tokens,
+// each inside one sequence. Segment i of sequence n has slot
+//   floor(cu[n] / len) + n + i,
+// which is increasing and never reaches the next sequence's first slot
+// (ceil((b - a) / len) <= floor(b / len) - floor(a / len) + 1), so
+// floor(T / len) + N slots hold every segment, the host need not know the
+// lengths, and a slot finds its sequence by a search over cu_seqlens.
+
+__device__ __forceinline__ int64_t seq_bound(const DecayArgs& p, int n) {
+  const int64_t c = p.cu_seqlens[n];
+  return c < 0 ? 0 : (c > p.T ? p.T : c);
+}
+__device__ __forceinline__ int64_t seq_end(const DecayArgs& p, int n, int64_t begin) {
+  const int64_t c = seq_bound(p, n + 1);
+  return c < begin ? begin : c;
+}
+
+struct DecaySegment {
+  int seq;
+  int64_t begin, end;  // tokens
+  bool first, last;    // of the sequence
+};
+
+// The segment of a slot; false where the slot is spare or its sequence is
+// empty. Every lane of a warp calls it: the warp probes 32 sequences at a
+// time, so that up to 32 sequences take one load and up to 1024 two.
+__device__ __forceinline__ bool find_segment(const DecayArgs& p, const DecaySegments& sg, int64_t slot, int lane,
+                                             DecaySegment* out) {
+  int lo = 0, count = p.N;  // the last sequence in [lo, lo + count) whose first slot is <= slot
+  while (count > 1) {
+    const int step = (count + 31) / 32;
+    const int n = lo + lane * step;
+    const bool le = lane * step < count && seq_bound(p, n) / sg.len + n <= slot;
+    const unsigned hits = __ballot_sync(0xffffffffu, le);
+    const int at = hits == 0 ? 0 : 31 - __clz(hits);
+    lo += at * step;
+    count = count - at * step < step ? count - at * step : step;
+  }
+  const int64_t begin = seq_bound(p, lo), end = seq_end(p, lo, begin);
+  const int64_t i = slot - (begin / sg.len + lo);
+  if (i < 0 || i * sg.len >= end - begin) return false;
+  out->seq = lo;
+  out->begin = begin + i * sg.len;
+  out->last = end - out->begin <= sg.len;
+  out->end = out->last ? end : out->begin + sg.len;
+  out->first = i == 0;
+  return true;
+}
+
+}  // namespace gdn

@@ -1,0 +1,242 @@
+// Linear attention with a decay for each head over packed sequences, token
+// by token: the state of one V head stays in the registers of a CTA while it
+// goes through the tokens of a segment. Serves every type and head dim.
+//
+//   S = exp(g_t) S + v_t k_t^T,   o_t = scale S q_t
+//
+// Each lane holds NV4 * 4 columns of RPL rows (64 floats at D = 128), so a
+// token costs a lane 3 paired FMAs per two elements and its q and k columns
+// from shared memory; q, k, v and exp(g) of kTile tokens are staged there in
+// fp32, the next tile's loads in flight in registers meanwhile, and a tile's
+// outputs are normed and written one barrier later, while the next tile runs.
+//
+// The recurrence is a chain over the tokens, so one CTA per V head leaves
+// most SMs idle for few heads and long prompts. With a workspace the tokens
+// are cut into segments: (1) each segment's own contribution from a zero
+// state and its total decay, (2) a scan over the segments of a sequence that
+// leaves the state at the start of each, (3) the segments with their
+// outputs, side by side. That computes the states twice; segments are as
+// long as the SMs allow.
+#include "decay_common.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kTile = 8;  // tokens staged at a time
+
+// whole: outputs and the state after the segment; local: only the segment's
+// own contribution to the state, into the workspace
+enum { kWhole = 0, kLocal = 1 };
+
+template <typename T, int D>
+struct ScanSmem {
+  float q[2][kTile][D], k[2][kTile][D], v[2][kTile][D], o[2][kTile][D];
+  float alpha[2][kTile];
+};
+
+template <typename T, int D, int MODE>
+__global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_scan_kernel(const DecayArgs p, const DecaySegments sg) {
+  using G = DecayGeom<D>;
+  constexpr int LPR = G::LPR, NV4 = G::NV4, RPL = G::RPL, RPW = G::RPW, NT = G::THREADS;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  ScanSmem<T, D>& sm = *reinterpret_cast<ScanSmem<T, D>*>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int sub = lane % LPR, rq = lane / LPR;
+  const int64_t slot = blockIdx.x / (unsigned)p.Hv;  // a segment's V heads side by side: they share q, k in L2
+  const int h = blockIdx.x % (unsigned)p.Hv;
+  const int kh = k_head_of(p.map, h, p.Hk, p.rep);
+  DecaySegment s;
+  if (!find_segment(p, sg, slot, lane, &s)) return;
+  if (MODE == kLocal && s.last) return;
+  float* gS = p.state + ((int64_t)s.seq * p.Hv + h) * (int64_t)(D * D);
+  float* wS = sg.states + (int64_t)blockIdx.x * (int64_t)(D * D);
+  const float* from = s.first && s.last ? gS : wS;
+
+  float4 st[RPL][NV4];
+#pragma unroll
+  for (int u = 0; u < RPL; ++u)
+#pragma unroll
+    for (int m = 0; m < NV4; ++m)
+      st[u][m] = MODE == kLocal ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                : *reinterpret_cast<const float4*>(from + (warp * G::WROWS + u * RPW + rq) * D +
+                                                                   4 * sub + 4 * LPR * m);
+
+  // staging: unit u of a tile is four elements; units of q, k, v in turn
+  constexpr int UNITS = kTile * D / 4, PER = (3 * UNITS + NT - 1) / NT;
+  float4 pre[PER];
+  float pre_g = 0.f;
+  auto fetch = [&](int64_t t0) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int u = tid + i * NT;
+      const int which = u / UNITS, r = u - which * UNITS, tt = r / (D / 4), c = (r - tt * (D / 4)) * 4;
+      if (which < 3 && t0 + tt < s.end && !(MODE == kLocal && which == 0)) {
+        const T* src = which == 0   ? static_cast<const T*>(p.q) + (t0 + tt) * p.q_stride + kh * D + c
+                       : which == 1 ? static_cast<const T*>(p.k) + (t0 + tt) * p.k_stride + kh * D + c
+                                    : static_cast<const T*>(p.v) + (t0 + tt) * p.v_stride + h * D + c;
+        pre[i] = load4(src);
+      }
+    }
+    if (tid < kTile && t0 + tid < s.end) pre_g = decay_log(p.g[(t0 + tid) * p.g_stride + h]);
+  };
+  float total = 0.f;  // thread tt < kTile: its share of the segment's log decay
+  auto stash = [&](int buf, int64_t t0) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int u = tid + i * NT;
+      const int which = u / UNITS, r = u - which * UNITS;
+      if (which < 3) {
+        float* dst = (which == 0 ? &sm.q[buf][0][0] : which == 1 ? &sm.k[buf][0][0] : &sm.v[buf][0][0]) + 4 * r;
+        *reinterpret_cast<float4*>(dst) = pre[i];
+      }
+    }
+    if (tid < kTile && t0 + tid < s.end) {
+      sm.alpha[buf][tid] = expf(pre_g);
+      if (MODE == kLocal) total += pre_g;
+    }
+  };
+  auto write_tile = [&](int buf, int64_t t0) {
+    for (int tt = warp; tt < kTile && t0 + tt < s.end; tt += G::WARPS) {
+      const int64_t t = t0 + tt, orow = (t * p.Hv + h) * D;
+      decay_write_row<T, D>(sm.o[buf][tt], p.core_out == nullptr ? nullptr : p.core_out + orow,
+                            p.z == nullptr ? nullptr : static_cast<const T*>(p.z) + t * p.z_stride + h * D, p.norm_w,
+                            p.out == nullptr ? nullptr : static_cast<T*>(p.out) + orow, p.rms_eps, lane);
+    }
+  };
+
+  fetch(s.begin);
+  stash(0, s.begin);
+  __syncthreads();
+  int buf = 0;
+  for (int64_t t0 = s.begin; t0 < s.end; t0 += kTile, buf ^= 1) {
+    if (t0 + kTile < s.end) fetch(t0 + kTile);
+    const int n = s.end - t0 < kTile ? (int)(s.end - t0) : kTile;
+    for (int tt = 0; tt < n; ++tt) {
+      const float alpha = sm.alpha[buf][tt];
+      float4 kr[NV4];
+#pragma unroll
+      for (int m = 0; m < NV4; ++m) kr[m] = *reinterpret_cast<const float4*>(&sm.k[buf][tt][4 * sub + 4 * LPR * m]);
+#pragma unroll
+      for (int u = 0; u < RPL; ++u)
+        row_update<NV4>(st[u], kr, alpha, sm.v[buf][tt][warp * G::WROWS + u * RPW + rq]);
+      if (MODE == kWhole) {
+        float o[RPL];
+#pragma unroll
+        for (int m = 0; m < NV4; ++m) kr[m] = *reinterpret_cast<const float4*>(&sm.q[buf][tt][4 * sub + 4 * LPR * m]);
+#pragma unroll
+        for (int u = 0; u < RPL; ++u) o[u] = row_dot<NV4>(st[u], kr);
+#pragma unroll
+        for (int d = LPR / 2; d > 0; d >>= 1)
+#pragma unroll
+          for (int u = 0; u < RPL; ++u) o[u] += __shfl_xor_sync(0xffffffffu, o[u], d);
+        if (sub == 0)
+#pragma unroll
+          for (int u = 0; u < RPL; ++u) sm.o[buf][tt][warp * G::WROWS + u * RPW + rq] = o[u] * p.scale;
+      }
+    }
+    if (t0 + kTile < s.end) stash(buf ^ 1, t0 + kTile);
+    __syncthreads();
+    if (MODE == kWhole) write_tile(buf, t0);
+  }
+
+  if (MODE == kLocal || s.last) {
+    float* to = MODE == kLocal ? wS : gS;
+#pragma unroll
+    for (int u = 0; u < RPL; ++u)
+#pragma unroll
+      for (int m = 0; m < NV4; ++m)
+        *reinterpret_cast<float4*>(to + (warp * G::WROWS + u * RPW + rq) * D + 4 * sub + 4 * LPR * m) = st[u][m];
+  }
+  if (MODE == kLocal && warp == 0) {
+    total = group_sum<32>(tid < kTile ? total : 0.f);
+    if (lane == 0) sg.decays[blockIdx.x] = total;
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_scan_td(const DecayArgs& p, const DecaySegments& sg, cudaStream_t stream) {
+  constexpr int smem = (int)sizeof(ScanSmem<T, D>);
+  const unsigned grid = (unsigned)(sg.slots * p.Hv);
+  auto whole = decay_scan_kernel<T, D, kWhole>;
+  auto local = decay_scan_kernel<T, D, kLocal>;
+  cudaError_t e = cudaSuccess;
+  if (sg.states != nullptr) {
+    local<<<grid, DecayGeom<D>::THREADS, smem, stream>>>(p, sg);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_decay_join(p, sg, D, stream);
+    if (e != cudaSuccess) return e;
+  }
+  whole<<<grid, DecayGeom<D>::THREADS, smem, stream>>>(p, sg);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_scan_t(const DecayArgs& p, const DecaySegments& sg, int32_t D, cudaStream_t stream) {
+  switch (D) {
+    case 32: return launch_scan_td<T, 32>(p, sg, stream);
+    case 64: return launch_scan_td<T, 64>(p, sg, stream);
+    case 96: return launch_scan_td<T, 96>(p, sg, stream);
+    case 128: return launch_scan_td<T, 128>(p, sg, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+// (2): per (sequence, V head, four state elements) through the sequence's
+// segments; each segment's contribution is replaced by the state at its
+// start. A sequence of one segment has nothing here (its state is used in
+// place). The last segment's slot is only written.
+__global__ void __launch_bounds__(256) decay_join_kernel(const DecayArgs p, const DecaySegments sg, const int n4) {
+  const int e = blockIdx.x * 256 + threadIdx.x;
+  if (e >= n4) return;
+  const int h = blockIdx.y, seq = blockIdx.z;
+  const int64_t begin = seq_bound(p, seq), end = seq_end(p, seq, begin);
+  const int64_t parts = (end - begin + sg.len - 1) / sg.len;
+  if (parts < 2) return;
+  const int64_t slot0 = begin / sg.len + seq;
+  const float4* gS = reinterpret_cast<const float4*>(p.state) + ((int64_t)seq * p.Hv + h) * n4 + e;
+  float4 s = *gS;
+  for (int64_t i = 0; i < parts; ++i) {
+    const int64_t at = (slot0 + i) * p.Hv + h;
+    float4* w = reinterpret_cast<float4*>(sg.states) + at * n4 + e;
+    float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+    float a = 0.f;
+    if (i + 1 < parts) {
+      add = *w;
+      a = expf(sg.decays[at]);
+    }
+    *w = s;
+    s = make_float4(fmaf(a, s.x, add.x), fmaf(a, s.y, add.y), fmaf(a, s.z, add.z), fmaf(a, s.w, add.w));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_decay_join(const DecayArgs& p, const DecaySegments& sg, int32_t D, cudaStream_t stream) {
+  const int n4 = D * D / 4;
+  decay_join_kernel<<<dim3((unsigned)((n4 + 255) / 256), (unsigned)p.Hv, (unsigned)p.N), 256, 0, stream>>>(p, sg, n4);
+  return cudaGetLastError();
+}
+
+// Sized for the 152 SMs of the one target, so that a workspace asked for on
+// one thread fits the call on another: enough segments for two CTAs on every
+// SM, none where the (sequence, V head) pairs fill them already.
+int64_t decay_segment_len(int32_t N, int64_t T, int32_t Hv, int32_t, int32_t) {
+  constexpr int64_t kCtas = 2 * 152;
+  if ((int64_t)N * Hv >= kCtas) return T + 1;
+  const int64_t len = (T * Hv / kCtas + 63) / 64 * 64;
+  return len < 64 ? 64 : len;
+}
+
+cudaError_t launch_decay_scan(const DecayArgs& p, const DecaySegments& sg, int32_t dtype, int32_t D,
+                              cudaStream_t stream) {
+  switch (dtype) {
+    case GDN_F16: return launch_scan_t<__half>(p, sg, D, stream);
+    case GDN_BF16: return launch_scan_t<__nv_bfloat16>(p, sg, D, stream);
+    case GDN_F32: return launch_scan_t<float>(p, sg, D, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace gdn
+
+GDN_DEFINE_ERROR_READER(decay_scan)

@@ -102,6 +102,67 @@ struct PrefillArgs {
   float l2_eps, rms_eps, scale;
 };
 
+// Linear attention with a decay for each head (decay_step.cu, decay_scan.cu,
+// decay_tc.cu): rows of q, k, v and z are tokens, strides in elements.
+struct DecayArgs {
+  const void* q;
+  int64_t q_stride;
+  const void* k;
+  int64_t k_stride;
+  const void* v;
+  int64_t v_stride;
+  const float* g;    // log decay of (token t, V head h) at g[t * g_stride + h]
+  int64_t g_stride;  // 0: the same for every token
+  float* state;
+  float* core_out;   // [T][Hv][D] or null
+  const void* z;     // null: out is the core output rounded once
+  int64_t z_stride;
+  const float* norm_w;
+  void* out;         // [T][Hv][D] or null
+  const int32_t* slots;  // step: state slot of each row, or null
+  int32_t num_slots;
+  const int32_t* cu_seqlens;  // prefill
+  int32_t N;
+  int64_t T;
+  int32_t Hk, Hv, rep, map;
+  float scale, rms_eps;
+};
+
+// The segments that a prefill is cut into (decay_common.cuh)
+struct DecaySegments {
+  int64_t len;    // tokens a segment holds at most
+  int64_t slots;  // floor(T / len) + N
+  float* states;  // [slots][Hv][D][D] or null: one segment per sequence
+  float* decays;  // [slots][Hv]
+};
+
+struct AddRmsNormArgs {
+  int64_t rows, cols;
+  const void* x;
+  int64_t x_stride;
+  const void* residual;  // or null
+  int64_t residual_stride;
+  void* sum;             // or null
+  int64_t sum_stride;
+  const float* norm_w;   // null: no normalisation
+  float eps;
+  void* out;             // or null
+  int64_t out_stride;
+  void* out_q;           // e4m3, or null
+  int64_t out_q_stride;
+  float* out_scale;
+};
+
+struct LinearFp8Args {
+  int64_t M;
+  int32_t N, K;
+  const float* x_scale;
+  const float* w_scale;
+  const float* bias;  // or null
+  void* y;
+  int64_t y_stride;
+};
+
 // Each launcher dispatches on (io dtype, head_dim) and returns the launch
 // status (cudaSuccess when everything was enqueued).
 cudaError_t launch_decode(const DecodeArgs& p, int32_t dtype, int32_t D, int32_t batch,
@@ -136,6 +197,18 @@ int64_t linear_workspace_bytes(int32_t M, int32_t N, int32_t K);
 bool linear_supported();
 cudaError_t launch_linear(LinearArgs p, const void* x, int64_t x_stride, const void* w, void* workspace,
                           cudaStream_t stream);
+// tokens of a segment (decay_scan.cu)
+int64_t decay_segment_len(int32_t N, int64_t T, int32_t Hv, int32_t D, int32_t dtype);
+cudaError_t launch_decay_step(const DecayArgs& p, int32_t dtype, int32_t D, int32_t batch, cudaStream_t stream);
+cudaError_t launch_decay_scan(const DecayArgs& p, const DecaySegments& sg, int32_t dtype, int32_t D,
+                              cudaStream_t stream);
+cudaError_t launch_decay_join(const DecayArgs& p, const DecaySegments& sg, int32_t D, cudaStream_t stream);
+cudaError_t launch_add_rmsnorm(const AddRmsNormArgs& p, int32_t dtype, cudaStream_t stream);
+cudaError_t launch_linear_fp8(const LinearFp8Args& p, const void* x, int64_t x_stride, const void* w,
+                              int32_t out_dtype, cudaStream_t stream);
+cudaError_t read_error_decay_step(int32_t* status, bool clear);
+cudaError_t read_error_decay_scan(int32_t* status, bool clear);
+cudaError_t read_error_linear_fp8(int32_t* status, bool clear);
 // diag.cu: one warp's bounded wait on an mbarrier nothing arrives on
 cudaError_t launch_wait_timeout(uint64_t limit_ns, int32_t* gave_up, cudaStream_t stream);
 

@@ -1,0 +1,258 @@
+// Linear layer on 8-bit operands, on the 5th-generation tensor cores:
+//   y[m][n] = x_scale[m] w_scale[n] sum_k x[m][k] w[n][k] + bias[n]
+// x and w are e4m3, one scale for each row of x (token) and of w (output
+// feature); products and sums are fp32 in TMEM, the scales and the bias are
+// applied in fp32 and y is rounded once.
+//
+// linear_fp8_band_kernel: a CTA takes 128 rows of x (the MMA's rows; those
+// past M are never stored) and a band of 64 output features, and streams both
+// through a TMA ring of 128-byte K steps. Where the bands leave SMs idle K is
+// split over a cluster whose CTAs add their fp32 tiles in rank order over
+// distributed shared memory, so the result does not depend on which ran
+// first. K past the end of a row reads as zeros.
+#include <cuda.h>
+
+#include "gdn_common.cuh"
+#include "gdn_internal.h"
+#include "tc_common.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kFM = 128;       // rows of x per tile
+constexpr int kFBand = 64;     // output features per CTA
+constexpr int kFK = 128;       // K per stage: one 128-byte swizzle atom
+constexpr uint32_t kFWTile = kFBand * kFK;
+constexpr int kFMaxStages = 12;
+constexpr int kFThreads = 128;
+constexpr int kFMaxSplits = 8;
+
+struct BandPlan {
+  int32_t splits, stages, box_rows;  // box_rows: rows of x per load
+};
+
+template <typename T>
+__device__ __forceinline__ void store8(T* dst, const float* x, int n, bool wide) {
+  if (wide && n >= 8) {
+    alignas(16) T v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = from_f32<T>(x[e]);
+#pragma unroll
+    for (int c = 0; c < (int)sizeof(T) / 2; ++c)
+      reinterpret_cast<uint4*>(dst)[c] = reinterpret_cast<const uint4*>(v)[c];
+  } else {
+    for (int e = 0; e < 8 && e < n; ++e) dst[e] = from_f32<T>(x[e]);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kFThreads, 2)
+    linear_fp8_band_kernel(const LinearFp8Args p, const BandPlan plan, const __grid_constant__ CUtensorMap tm_x,
+                           const __grid_constant__ CUtensorMap tm_w) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ __align__(8) uint64_t full[kFMaxStages], empty[kFMaxStages], done;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n0 = blockIdx.x * kFBand;
+  const int64_t m0 = (int64_t)blockIdx.z * kFM;
+  const int rows = p.M - m0 < kFM ? (int)(p.M - m0) : kFM;
+  const int stages = plan.stages;
+  const uint32_t x_bytes = (uint32_t)plan.box_rows * kFK;
+  const uint32_t x_tile = (x_bytes + 1023) / 1024 * 1024, stage_bytes = x_tile + kFWTile;
+  const int nk = (p.K + kFK - 1) / kFK;
+  const int k_begin = (int)((int64_t)blockIdx.y * nk / plan.splits);
+  const int k_len = (int)((int64_t)(blockIdx.y + 1) * nk / plan.splits) - k_begin;
+
+  if (warp == 0) {
+    tc::tmem_alloc(&s_tmem, kFBand);
+    tc::tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&done, 1);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tb = s_tmem;
+  volatile int* abort_flag = &s_abort;
+  uint32_t n_loads = 0;
+
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < k_len; ++i) {
+      const int s = i % stages;
+      if (i >= stages && !mbar_wait_bounded(&empty[s], ((i / stages) - 1) & 1, abort_flag)) break;
+      mbar_arrive_expect_tx(&full[s], x_bytes + kFWTile);
+      ++n_loads;
+      const int kx = (k_begin + i) * kFK;
+      tc::tma_load_2d(sm + s * stage_bytes, &tm_x, kx, (int)m0, &full[s]);
+      tc::tma_load_2d(sm + s * stage_bytes + x_tile, &tm_w, kx, n0, &full[s]);
+    }
+  } else if (warp == 1) {
+    const uint32_t id = tc::idesc(tc::kE4M3, kFM, kFBand);
+    const uint64_t d0 = tc::sdesc_sw128(smem_u32(sm));
+    for (int i = 0; i < k_len; ++i) {
+      const int s = i % stages;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[s], (i / stages) & 1, abort_flag))) break;
+      tc::fence_after_sync();
+      const uint64_t dx = d0 + (uint64_t)((s * stage_bytes) >> 4);
+      const uint64_t dw = d0 + (uint64_t)((s * stage_bytes + x_tile) >> 4);
+#pragma unroll
+      for (int ks = 0; ks < kFK / 32; ++ks)
+        tc::mma_f8_elect(tb, tc::sdesc_at(dx, kFM, ks), tc::sdesc_at(dw, kFBand, ks), id, i > 0 || ks > 0);
+      tc::mma_commit_elect(&empty[s]);
+    }
+    tc::mma_commit_elect(&done);
+  }
+
+  // epilogue: thread (warp w, lane) holds row 32 w + lane of the accumulator
+  const bool ok = mbar_wait_bounded(&done, 0, abort_flag) && !*abort_flag;
+  tc::fence_after_sync();
+  const int m = 32 * warp + lane;
+  float v[kFBand];
+  if (__all_sync(0xffffffffu, ok)) {
+#pragma unroll
+    for (int c = 0; c < kFBand / 16; ++c)
+      tc::tmem_ld16(tb + ((uint32_t)(32 * warp) << 16) + 16 * c, *reinterpret_cast<float(*)[16]>(v + 16 * c));
+    tc::tmem_wait_ld();
+  } else {
+#pragma unroll
+    for (int e = 0; e < kFBand; ++e) v[e] = 0.f;
+  }
+  auto finish8 = [&](int r, int g8, float* x8) {
+    const int n = n0 + 8 * g8, left = p.N - n;
+    if (left <= 0) return;
+    const float xs = __ldg(p.x_scale + m0 + r);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left)
+        x8[e] = fmaf(x8[e] * xs, __ldg(p.w_scale + n + e), p.bias != nullptr ? __ldg(p.bias + n + e) : 0.f);
+    store8<T>(static_cast<T*>(p.y) + (m0 + r) * p.y_stride + n, x8, left, true);
+  };
+  if (plan.splits == 1) {
+    if (m < rows && !*abort_flag)
+#pragma unroll
+      for (int g8 = 0; g8 < kFBand / 8; ++g8) finish8(m, g8, v + 8 * g8);
+  } else {
+    // each split's fp32 tile in its own shared memory (the ring is idle:
+    // every load it issued was consumed by an MMA that has completed),
+    // 16-byte group c of row r at group c ^ (r % 16); every thread reaches
+    // both cluster barriers, whatever happened before
+    float* part = reinterpret_cast<float*>(sm);
+    if (m < rows) {
+#pragma unroll
+      for (int c = 0; c < kFBand / 4; ++c)
+        *reinterpret_cast<float4*>(part + m * kFBand + 4 * (c ^ (m & 15))) =
+            make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    }
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    const int S = plan.splits, rank = (int)cluster_ctarank();
+    const uint32_t base = smem_u32(part);
+    if (!*abort_flag) {
+      for (int u = rank * kFThreads + tid; u < rows * (kFBand / 8); u += S * kFThreads) {
+        const int r = u >> 3, g8 = u & 7;
+        const uint32_t o0 = (uint32_t)(r * kFBand + 4 * ((2 * g8) ^ (r & 15))) * 4u;
+        const uint32_t o1 = (uint32_t)(r * kFBand + 4 * ((2 * g8 + 1) ^ (r & 15))) * 4u;
+        float x8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int sp = 0; sp < S; ++sp) {
+          const float4 a0 = ld_shared_cluster_f32x4(map_shared_rank(base + o0, (uint32_t)sp));
+          const float4 a1 = ld_shared_cluster_f32x4(map_shared_rank(base + o1, (uint32_t)sp));
+          x8[0] += a0.x, x8[1] += a0.y, x8[2] += a0.z, x8[3] += a0.w;
+          x8[4] += a1.x, x8[5] += a1.y, x8[6] += a1.z, x8[7] += a1.w;
+        }
+        finish8(r, g8, x8);
+      }
+    }
+    cluster_arrive_release();
+    cluster_wait_acquire();
+  }
+
+  // drain: every load this CTA issued has landed before TMEM is released
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0 && lane == 0) {
+    for (uint32_t s = 0; s < (uint32_t)stages && s < n_loads; ++s) {
+      const uint32_t uses = (n_loads - s + stages - 1) / stages;
+      mbar_wait(&full[s], (uses - 1) & 1);
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tb, kFBand);
+  }
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 148;
+  return n;
+}
+
+template <typename T>
+cudaError_t launch_band(const LinearFp8Args& p, const void* x, int64_t x_stride, const void* w, cudaStream_t stream) {
+  BandPlan plan;
+  plan.box_rows = p.M < kFM ? (int32_t)p.M : kFM;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  CUtensorMap mx, mw;
+  if (!tc::make_map_2d(&mx, x, p.M, p.K, x_stride, 1, u8, kFK, (uint32_t)plan.box_rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !tc::make_map_2d(&mw, w, p.N, p.K, p.K, 1, u8, kFK, kFBand, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+    return cudaErrorInvalidValue;
+  const int bands = (p.N + kFBand - 1) / kFBand, nk = (p.K + kFK - 1) / kFK;
+  const int64_t tiles = (p.M + kFM - 1) / kFM;
+  // as many K splits as keep every CTA slot busy in one wave, each of two K steps at least
+  int64_t splits = 2 * sm_count() / (bands * tiles);
+  if (splits > nk / 2) splits = nk / 2;
+  if (splits > kFMaxSplits) splits = kFMaxSplits;
+  plan.splits = splits < 1 ? 1 : (int)splits;
+  const uint32_t x_tile = ((uint32_t)plan.box_rows * kFK + 1023) / 1024 * 1024, stage_bytes = x_tile + kFWTile;
+  const int fit = (int)(96 * 1024 / stage_bytes);
+  plan.stages = fit < kFMaxStages ? fit : kFMaxStages;
+  // the MMA reads kFM rows from a stage's start
+  const uint32_t smem = (uint32_t)plan.stages * stage_bytes + (kFM * kFK - x_tile) + 1024;
+  auto kern = linear_fp8_band_kernel<T>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)bands, (unsigned)plan.splits, (unsigned)tiles);
+  cfg.blockDim = dim3(kFThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = (unsigned)plan.splits;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = plan.splits > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kern, p, plan, mx, mw);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_linear_fp8(const LinearFp8Args& p, const void* x, int64_t x_stride, const void* w,
+                              int32_t out_dtype, cudaStream_t stream) {
+  switch (out_dtype) {
+    case GDN_F16: return launch_band<__half>(p, x, x_stride, w, stream);
+    case GDN_BF16: return launch_band<__nv_bfloat16>(p, x, x_stride, w, stream);
+    case GDN_F32: return launch_band<float>(p, x, x_stride, w, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace gdn
+
+GDN_DEFINE_ERROR_READER(linear_fp8)

@@ -60,6 +60,7 @@ __device__ __forceinline__ uint64_t sdesc_at(uint64_t base, int rows, int s) {
 }
 
 enum : uint32_t { kF16 = 0, kBF16 = 1, kTF32 = 2 };
+constexpr uint32_t kE4M3 = 0;  // operand format of kind::f8f6f4
 
 // Instruction descriptor for kind::f16 / kind::tf32 with fp32 accumulation,
 // both operands K-major: D format (bits 4-5) = F32, A/B formats in bits 7-9 /
@@ -151,6 +152,18 @@ __device__ __forceinline__ void mma_f16_elect(uint32_t d_tmem, uint64_t a, uint6
       "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(id), "r"((uint32_t)accumulate)
+      : "memory");
+}
+// The same with 8-bit floating operands (32 of K in an instruction). The
+// instruction descriptor's operand formats are kE4M3.
+__device__ __forceinline__ void mma_f8_elect(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id,
+                                             bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a), "l"(b), "r"(id), "r"((uint32_t)accumulate)
       : "memory");
 }

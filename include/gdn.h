@@ -93,7 +93,8 @@ const char* gdn_status_string(int32_t status);
 
 /* ABI version: major * 10000 + minor * 100 + patch. 0.3.0 added
  * gdn_decode_multi and gdn_decode_step_slots; 0.4.0 gdn_linear,
- * gdn_decode_layer and gdn_host_pointer. */
+ * gdn_decode_layer and gdn_host_pointer; 0.5.0 gdn_decay_step,
+ * gdn_decay_prefill, gdn_add_rmsnorm and gdn_linear_fp8. */
 int32_t gdn_version(void);
 
 /* Channels of the packed pre-conv activation: C = 2*Hk*D + Hv*D, laid out
@@ -422,6 +423,129 @@ gdn_status gdn_decode_layer(const gdn_dims* dims, int32_t hidden, int32_t batch,
  * workspace for the larger of its two calls, each rounded up to 256 bytes. */
 gdn_status gdn_decode_layer_workspace_size(const gdn_dims* dims, int32_t hidden, int32_t batch,
                                            int64_t* bytes);
+
+/*
+ * Linear attention with a decay for each head, one token for each of `batch`
+ * sequences: the layers that a hybrid model places between gated delta-net
+ * ones, on the same fp32 states and head maps. Per V head h reading K head
+ * kh:
+ *     S = exp(g_h) S + v k^T      o = scale * S q
+ * q and k are used as given (no normalisation); dims->decay and dims->l2_eps
+ * are not used.
+ *
+ * batch        B >= 0, B <= 65535.
+ * state_slots  device int32 [B] or NULL. NULL: row b works on state[b], and
+ *              num_slots must be B. Else row b works on
+ *              state[state_slots[b]] of a pool of num_slots; a negative entry
+ *              marks a padded row (no state touched, its output rows are
+ *              zero), an entry >= num_slots is treated the same and records
+ *              GDN_ERR_EXTENT in the device error word. Two rows naming the
+ *              same slot is a caller error (unspecified result, no fault).
+ * q, k         row b, K head kh, column i at q[b*q_stride + kh*D + i] (io
+ *              dtype); strides in elements, at least the row, a multiple of
+ *              16 bytes. The rows may be slices of one wider activation.
+ * v            row b, V head h at v[b*v_stride + h*D + j].
+ * g            fp32 log decay of (b, h) at g[b*g_stride + h]; g_stride 0 (one
+ *              decay per head for every row) or >= Hv. g = -inf resets the
+ *              state; positive values grow it.
+ * scale        factor of the output, finite (1/sqrt(D) for scaled attention).
+ * state        [num_slots][Hv][D][D] fp32 S[.][h][j][i], in place.
+ * core_out     [B][Hv][D] fp32 o, or NULL.
+ * z, norm_w    z (rows z_stride apart as v) and fp32 [D]: out is the gated
+ *              RMSNorm of o as in gdn_decode_step; both NULL: out is o
+ *              rounded once.
+ * out          [B][Hv][D] io dtype, or NULL. At least one of core_out and out;
+ *              out is required with z.
+ */
+gdn_status gdn_decay_step(const gdn_dims* dims, int32_t batch, const int32_t* state_slots,
+                          int32_t num_slots, const void* q, int64_t q_stride, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, const float* g,
+                          int64_t g_stride, float scale, float* state, float* core_out,
+                          const void* z, int64_t z_stride, const float* norm_w, void* out,
+                          void* stream);
+
+/*
+ * The same recurrence over a packed batch of variable-length sequences, each
+ * continuing from its own state (in place): prompts, or several tokens of a
+ * decode step. Every argument is indexed by the token as in gdn_decay_step,
+ * where that has the row.
+ *
+ * cu_seqlens   device int32 [N+1] as for gdn_conv_update; an empty sequence
+ *              keeps its state. cu[N] may be smaller than total_tokens: the
+ *              rows behind the last sequence (a padded batch) are neither
+ *              read nor written.
+ * total_tokens 0 <= T <= 2^31 - 65; num_seqs 0 <= N <= 65535.
+ * state        [N][Hv][D][D] fp32, in place.
+ * core_out, out  [T][Hv][D].
+ * workspace    device scratch of at least gdn_decay_prefill_workspace_size
+ *              bytes, 256-byte aligned, not overlapping any other argument;
+ *              contents irrelevant. NULL: the call runs without (slower for
+ *              few heads and long sequences). Two calls that may run at the
+ *              same time, replayed graphs among them, need one each.
+ */
+gdn_status gdn_decay_prefill(const gdn_dims* dims, int32_t num_seqs, const int32_t* cu_seqlens,
+                             int64_t total_tokens, const void* q, int64_t q_stride, const void* k,
+                             int64_t k_stride, const void* v, int64_t v_stride, const float* g,
+                             int64_t g_stride, float scale, float* state, float* core_out,
+                             const void* z, int64_t z_stride, const float* norm_w, void* out,
+                             void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace gdn_decay_prefill uses for these sizes (0: none). */
+gdn_status gdn_decay_prefill_workspace_size(const gdn_dims* dims, int32_t num_seqs,
+                                            int64_t total_tokens, int64_t* bytes);
+
+/*
+ * Residual addition, RMSNorm and 8-bit quantisation of rows, in one pass:
+ *     s = x + residual, rounded to io dtype       (residual NULL: s = x)
+ *     y = s * (mean_c s_c^2 + eps)^(-1/2) * norm_w[c]   (norm_w NULL: y = s)
+ *     sum_out = s;  out = y rounded to io dtype;
+ *     out_scale[row] = max(max_c |y_c| / 448, 2^-126)
+ *     out_q = y / out_scale rounded to e4m3 (nearest, ties to even)
+ * so that out_q * out_scale stands for y; with norm_w NULL the call quantises
+ * rows as they are (a weight, one scale per output feature; the input of a
+ * projection). Squares are summed in fp32. A NaN or an infinity in a row
+ * makes NaN codes there.
+ *
+ * rows         0 <= rows <= 2^31 - 1;  cols  1 <= cols <= 2^30.
+ * io_dtype     of x, residual, sum_out and out.
+ * x            [rows][x_stride], residual [rows][residual_stride] or NULL;
+ *              strides in elements, >= cols. 16-byte alignment of the
+ *              pointers is required; where the strides and cols are multiples
+ *              of 16 bytes too the rows are read and written with 16-byte
+ *              accesses, else by elements.
+ * sum_out      [rows][sum_stride] or NULL; may be x or residual itself with
+ *              the same stride (the residual stream updated in place).
+ * norm_w       [cols] fp32, or NULL.
+ * out          [rows][out_stride] io dtype, or NULL.
+ * out_q        [rows][out_q_stride] e4m3 bytes, or NULL; out_scale [rows]
+ *              fp32, needed with out_q. At least one of sum_out, out, out_q.
+ * No output may overlap another output or an input, but for sum_out as above.
+ */
+gdn_status gdn_add_rmsnorm(int64_t rows, int64_t cols, int32_t io_dtype, const void* x,
+                           int64_t x_stride, const void* residual, int64_t residual_stride,
+                           void* sum_out, int64_t sum_stride, const float* norm_w, float eps,
+                           void* out, int64_t out_stride, void* out_q, int64_t out_q_stride,
+                           float* out_scale, void* stream);
+
+/*
+ * Linear layer on 8-bit operands (e4m3, as gdn_add_rmsnorm writes them):
+ *     y[m][n] = x_scale[m] * w_scale[n] * sum_k x[m][k] w[n][k] + bias[n]
+ * with fp32 sums on the tensor cores and one rounding to out_dtype. Unlike
+ * gdn_linear it takes any number of rows (prompts too).
+ *
+ * M            rows, 1 <= M <= 2^22;  N output features, 1 <= N <= 2^24.
+ * K            input features, a positive multiple of 16, <= 2^24.
+ * x            [M][x_stride] e4m3, x_stride >= K, a multiple of 16.
+ * x_scale      [M] fp32;  w_scale [N] fp32;  bias [N] fp32 or NULL.
+ * w            [N][K] e4m3, row-major.
+ * y            [M][y_stride] out_dtype (gdn_dtype), y_stride >= N, a multiple
+ *              of 8; columns at or past N are not written; must not overlap
+ *              any input.
+ */
+gdn_status gdn_linear_fp8(int64_t M, int32_t N, int32_t K, const void* x, int64_t x_stride,
+                          const float* x_scale, const void* w, const float* w_scale,
+                          const float* bias, int32_t out_dtype, void* y, int64_t y_stride,
+                          void* stream);
 
 /*
  * The device address of pinned host memory (cudaHostAlloc, or page-locked
