@@ -495,56 +495,69 @@ def gdn_decode_layer(d: GdnDims, x: torch.Tensor, w_in, w_out, conv_w, decay_par
     return y
 
 
-def _here(*tensors):
-    """Every tensor of a call (None allowed) is on the current CUDA device, whose context the library launches in."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
-            raise ValueError(f"every tensor must be on the current CUDA device (cuda:{dev}), got {t.device}")
+# The calls below are short (a launch takes about 4 us of host time), so their checks read each tensor's properties
+# once and the current stream comes from the binding that torch's own code generators use.
+_current_device = torch._C._cuda_getDevice
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _rows(t: torch.Tensor, name: str, dtype, rows: int, width: int):
-    """Address and row stride of a [rows][width] operand: 2-D, or 3-D with the heads apart, its rows contiguous."""
+def _stream_on(stream, dev: int) -> Optional[int]:
+    return (_current_raw_stream(dev) or None) if stream is None else _stream(stream)
+
+
+def _elsewhere(t, name: str, dtype, dev: int):
+    """Says which of the checks on a tensor's type and place failed."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be on the current CUDA device (cuda:{dev}), got {t.device}")
+
+
+def _rows(t, name: str, dtype, rows: int, width: int, dev: int):
+    """Address and row stride of a [rows][width] operand on the current device: 2-D, or 3-D with the heads apart,
+    its rows contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        _elsewhere(t, name, dtype, dev)
     shape, stride = t.shape, t.stride()
-    ok = len(shape) in (2, 3) and shape[0] == rows
-    if ok and len(shape) == 3:
-        ok = shape[1] * shape[2] == width and stride[2] == 1 and (shape[1] == 1 or stride[1] == shape[2])
-    elif ok:
-        ok = shape[1] == width and (width == 1 or stride[1] == 1)
+    if len(shape) == 2:
+        ok = shape[0] == rows and shape[1] == width and (stride[1] == 1 or width == 1)
+    else:
+        ok = (len(shape) == 3 and shape[0] == rows and shape[1] * shape[2] == width
+              and (stride[2] == 1 or shape[2] == 1) and (shape[1] == 1 or stride[1] == shape[2]))
     if not ok:
         raise ValueError(f"{name} must hold {rows} rows of {width} contiguous elements, got shape {tuple(shape)}, "
                          f"strides {tuple(stride)}")
     return t.data_ptr(), (stride[0] if rows > 1 else width)
 
 
-def _dense(t: Optional[torch.Tensor], name: str, dtype, n: int) -> Optional[int]:
-    """Address of a contiguous operand of n elements."""
-    if t is None:
-        return None
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+def _dense(t, name: str, dtype, n: int, dev: int) -> Optional[int]:
+    """Address of a contiguous operand of n elements on the current device."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        _elsewhere(t, name, dtype, dev)
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous and hold {n} elements, got shape {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _decay_operands(d: GdnDims, rows, q, k, v, g, core_out, z, norm_w, out, scale):
-    """The operands gdn_decay_step and gdn_decay_prefill share, as their C arguments: those before and after state."""
+def _decay_operands(d: GdnDims, rows, q, k, v, g, state, states, core_out, z, norm_w, out, scale, dev):
+    """The operands that gdn_decay_step and gdn_decay_prefill share, as their C arguments from q to out."""
     io, f32 = _io(d), torch.float32
-    Hk, Hv, D = d.n_k_heads, d.n_v_heads, d.head_dim
-    gs = 0
+    hk, hv, dim = d.n_k_heads, d.n_v_heads, d.head_dim
+    qk, vw = hk * dim, hv * dim
+    qp, qs = _rows(q, "q", io, rows, qk, dev)
+    kp, ks = _rows(k, "k", io, rows, qk, dev)
+    vp, vs = _rows(v, "v", io, rows, vw, dev)
     if g.dim() == 2:
-        gp, gs = _rows(g, "g", f32, rows, Hv)
+        gp, gs = _rows(g, "g", f32, rows, hv, dev)
     else:
-        gp = _dense(g, "g", f32, Hv)
-    zp, zs = (None, 0) if z is None else _rows(z, "z", io, rows, Hv * D)
-    head = (*_rows(q, "q", io, rows, Hk * D), *_rows(k, "k", io, rows, Hk * D), *_rows(v, "v", io, rows, Hv * D), gp, gs,
-            D ** -0.5 if scale is None else float(scale))
-    tail = (_dense(core_out, "core_out", f32, rows * Hv * D), zp, zs, _dense(norm_w, "norm_w", f32, D),
-            _dense(out, "out", io, rows * Hv * D))
-    return head, tail
+        gp, gs = _dense(g, "g", f32, hv, dev), 0
+    zp, zs = (None, 0) if z is None else _rows(z, "z", io, rows, vw, dev)
+    return (qp, qs, kp, ks, vp, vs, gp, gs, dim ** -0.5 if scale is None else scale,
+            _dense(state, "state", f32, states * vw * dim, dev),
+            None if core_out is None else _dense(core_out, "core_out", f32, rows * vw, dev), zp, zs,
+            None if norm_w is None else _dense(norm_w, "norm_w", f32, dim, dev),
+            None if out is None else _dense(out, "out", io, rows * vw, dev))
 
 
 def gdn_decay_step(d: GdnDims, q, k, v, g, state, core_out=None, z=None, norm_w=None, out=None,
@@ -552,18 +565,17 @@ def gdn_decay_step(d: GdnDims, q, k, v, g, state, core_out=None, z=None, norm_w=
     """One token of linear attention with a decay for each head, per row: q, k [B][Hk*D], v, z [B][Hv*D] (rows may be
     slices of a wider activation; [B][heads][D] too), g fp32 [Hv] or [B][Hv] log decays, state [B or slots][Hv][D][D]
     fp32 in place. scale None: D ** -0.5."""
-    _here(q, k, v, g, state, core_out, z, norm_w, out, state_slots)
+    dev = _current_device()
     rows, slots = q.shape[0], state.shape[0]
+    sp = None
     if state_slots is not None:
-        sp = _dense(state_slots, "state_slots", torch.int32, rows)
+        sp = _dense(state_slots, "state_slots", torch.int32, rows, dev)
     elif slots != rows:
         raise ValueError(f"state must hold one state per row ({rows}), got {slots}")
-    else:
-        sp = None
-    head, tail = _decay_operands(d, rows, q, k, v, g, core_out, z, norm_w, out, scale)
     st = library().gdn_decay_step(
-        ctypes.byref(d), rows, sp, slots, *head,
-        _dense(state, "state", torch.float32, slots * d.n_v_heads * d.head_dim * d.head_dim), *tail, _stream(stream))
+        ctypes.byref(d), rows, sp, slots,
+        *_decay_operands(d, rows, q, k, v, g, state, slots, core_out, z, norm_w, out, scale, dev),
+        _stream_on(stream, dev))
     if st:
         _check(st, "gdn_decay_step")
     return core_out, out
@@ -571,8 +583,9 @@ def gdn_decay_step(d: GdnDims, q, k, v, g, state, core_out=None, z=None, norm_w=
 
 def gdn_decay_prefill_workspace_size(d: GdnDims, num_seqs: int, total_tokens: int) -> int:
     n = ctypes.c_int64(0)
-    _check(library().gdn_decay_prefill_workspace_size(ctypes.byref(d), int(num_seqs), int(total_tokens),
-                                                      ctypes.byref(n)), "gdn_decay_prefill_workspace_size")
+    st = library().gdn_decay_prefill_workspace_size(ctypes.byref(d), num_seqs, total_tokens, ctypes.byref(n))
+    if st:
+        _check(st, "gdn_decay_prefill_workspace_size")
     return n.value
 
 
@@ -581,9 +594,10 @@ def gdn_decay_prefill(d: GdnDims, cu_seqlens, q, k, v, g, state, core_out=None, 
     """The same over packed sequences (cu_seqlens int32 [N+1]), rows of q, k, v, z, g and the outputs being tokens,
     state [N][Hv][D][D]. workspace: "auto" allocates what the library asks for, None passes none, or a CUDA uint8
     tensor of at least gdn_decay_prefill_workspace_size bytes."""
-    _here(cu_seqlens, q, k, v, g, state, core_out, z, norm_w, out)
+    dev = _current_device()
     rows, n = q.shape[0], cu_seqlens.numel() - 1
-    head, tail = _decay_operands(d, rows, q, k, v, g, core_out, z, norm_w, out, scale)
+    cp = _dense(cu_seqlens, "cu_seqlens", torch.int32, n + 1, dev)
+    operands = _decay_operands(d, rows, q, k, v, g, state, n, core_out, z, norm_w, out, scale, dev)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto', None or a CUDA tensor")
@@ -594,12 +608,9 @@ def gdn_decay_prefill(d: GdnDims, cu_seqlens, q, k, v, g, state, core_out=None, 
             workspace.record_stream(stream)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
-        _here(workspace)
-        ws_ptr, ws_bytes = _ptr(workspace, "workspace", torch.uint8), workspace.numel()
-    st = library().gdn_decay_prefill(
-        ctypes.byref(d), n, _dense(cu_seqlens, "cu_seqlens", torch.int32, n + 1), rows, *head,
-        _dense(state, "state", torch.float32, n * d.n_v_heads * d.head_dim * d.head_dim), *tail, ws_ptr, ws_bytes,
-        _stream(stream))
+        ws_bytes = workspace.numel()
+        ws_ptr = _dense(workspace, "workspace", torch.uint8, ws_bytes, dev)
+    st = library().gdn_decay_prefill(ctypes.byref(d), n, cp, rows, *operands, ws_ptr, ws_bytes, _stream_on(stream, dev))
     if st:
         _check(st, "gdn_decay_prefill")
     return core_out, out
@@ -610,21 +621,28 @@ def gdn_add_rmsnorm(x: torch.Tensor, norm_w: Optional[torch.Tensor] = None, resi
     """s = x + residual; y = RMSNorm(s) * norm_w (norm_w None: y = s); sum_out = s, out = y in x's dtype, out_q
     (torch.float8_e4m3fn) with out_scale (fp32, one per row) = y in 8 bits. x, residual, sum_out, out, out_q:
     [rows][cols], rows may be strided."""
-    if x.dim() != 2:
-        raise ValueError("x must be 2-D")
-    io = x.dtype
-    if io not in _TORCH_TO_GDN:
-        raise TypeError(f"x must be float16, bfloat16 or float32, got {io}")
-    _here(x, norm_w, residual, sum_out, out, out_q, out_scale)
-    rows, cols = x.shape
-
-    def opt(t, name, dtype):
-        return (None, 0) if t is None else _rows(t, name, dtype, rows, cols)
-
-    st = library().gdn_add_rmsnorm(
-        rows, cols, _TORCH_TO_GDN[io], *_rows(x, "x", io, rows, cols), *opt(residual, "residual", io),
-        *opt(sum_out, "sum_out", io), _dense(norm_w, "norm_w", torch.float32, cols), eps, *opt(out, "out", io),
-        *opt(out_q, "out_q", torch.float8_e4m3fn), _dense(out_scale, "out_scale", torch.float32, rows), _stream(stream))
+    io, shape = x.dtype, x.shape
+    if len(shape) != 2 or io not in _TORCH_TO_GDN:
+        raise TypeError(f"x must be 2-D float16, bfloat16 or float32, got {io} {tuple(shape)}")
+    dev = _current_device()
+    rows, cols = shape
+    xp, xs = _rows(x, "x", io, rows, cols, dev)
+    rp = sp = wp = op = qp = tp = None
+    rs = ss = os_ = qs = 0
+    if residual is not None:
+        rp, rs = _rows(residual, "residual", io, rows, cols, dev)
+    if sum_out is not None:
+        sp, ss = _rows(sum_out, "sum_out", io, rows, cols, dev)
+    if norm_w is not None:
+        wp = _dense(norm_w, "norm_w", torch.float32, cols, dev)
+    if out is not None:
+        op, os_ = _rows(out, "out", io, rows, cols, dev)
+    if out_q is not None:
+        qp, qs = _rows(out_q, "out_q", torch.float8_e4m3fn, rows, cols, dev)
+    if out_scale is not None:
+        tp = _dense(out_scale, "out_scale", torch.float32, rows, dev)
+    st = library().gdn_add_rmsnorm(rows, cols, _TORCH_TO_GDN[io], xp, xs, rp, rs, sp, ss, wp, eps, op, os_, qp, qs, tp,
+                                   _stream_on(stream, dev))
     if st:
         _check(st, "gdn_add_rmsnorm")
     return sum_out, out, out_q, out_scale
@@ -633,22 +651,22 @@ def gdn_add_rmsnorm(x: torch.Tensor, norm_w: Optional[torch.Tensor] = None, resi
 def gdn_linear_fp8(x: torch.Tensor, x_scale, w, w_scale, y: torch.Tensor, bias=None, stream=None) -> torch.Tensor:
     """y[m][n] = x_scale[m] w_scale[n] sum_k x[m][k] w[n][k] + bias[n]: x [M][K] and w [N][K] torch.float8_e4m3fn
     (rows of x and y may be strided), scales and bias fp32, y float16, bfloat16 or float32."""
-    f8, f32 = torch.float8_e4m3fn, torch.float32
+    f8, f32, io = torch.float8_e4m3fn, torch.float32, y.dtype
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w must be 2-D")
-    if y.dtype not in _TORCH_TO_GDN:
-        raise TypeError(f"y must be float16, bfloat16 or float32, got {y.dtype}")
-    _here(x, x_scale, w, w_scale, y, bias)
+    if io not in _TORCH_TO_GDN:
+        raise TypeError(f"y must be float16, bfloat16 or float32, got {io}")
+    dev = _current_device()
     M, K = x.shape
     N = w.shape[0]
-    xp, xs = _rows(x, "x", f8, M, K)
-    yp, ys = _rows(y, "y", y.dtype, M, N)
+    xp, xs = _rows(x, "x", f8, M, K, dev)
+    yp, ys = _rows(y, "y", io, M, N, dev)
     if M == 1:
         ys = (N + 7) // 8 * 8  # the one row's stride is never used
     st = library().gdn_linear_fp8(
-        M, N, K, xp, xs, _dense(x_scale, "x_scale", f32, M), _dense(w, "w", f8, N * K),
-        _dense(w_scale, "w_scale", f32, N), _dense(bias, "bias", f32, N), _TORCH_TO_GDN[y.dtype], yp, ys,
-        _stream(stream))
+        M, N, K, xp, xs, _dense(x_scale, "x_scale", f32, M, dev), _dense(w, "w", f8, N * K, dev),
+        _dense(w_scale, "w_scale", f32, N, dev), None if bias is None else _dense(bias, "bias", f32, N, dev),
+        _TORCH_TO_GDN[io], yp, ys, _stream_on(stream, dev))
     if st:
         _check(st, "gdn_linear_fp8")
     return y

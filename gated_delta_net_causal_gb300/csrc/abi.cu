@@ -744,6 +744,8 @@ gdn_status gdn_decay_prefill(const gdn_dims* dims, int32_t num_seqs, const int32
     sg.len = total_tokens + 1;
     sg.slots = num_seqs;
   }
+  if (gdn::decay_tc_supported(p, dims->io_dtype, dims->head_dim))
+    return cuda_status(gdn::launch_decay_tc(p, sg, static_cast<cudaStream_t>(stream)));
   return cuda_status(gdn::launch_decay_scan(p, sg, dims->io_dtype, dims->head_dim, static_cast<cudaStream_t>(stream)));
 }
 
@@ -849,7 +851,8 @@ gdn_status gdn_device_error(int32_t* status, int32_t clear) {
                                                gdn::read_error_prefill_tc,
                                                gdn::read_error_prefill_cp, gdn::read_error_diag,
                                                gdn::read_error_linear, gdn::read_error_decay_step,
-                                               gdn::read_error_decay_scan, gdn::read_error_linear_fp8};
+                                               gdn::read_error_decay_scan, gdn::read_error_decay_tc,
+                                               gdn::read_error_linear_fp8};
   for (auto rd : readers) {
     int32_t v = 0;
     if (rd(&v, clear != 0) != cudaSuccess) return GDN_ERR_CUDA;

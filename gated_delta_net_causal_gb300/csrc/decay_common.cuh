@@ -14,6 +14,33 @@ namespace gdn {
 constexpr float kDecayFloor = -128.f;
 __device__ __forceinline__ float decay_log(float g) { return g < kDecayFloor ? kDecayFloor : g; }
 
+// s <- exp(g) s + d v on a lane's groups. Near 1 the factor's own rounding
+// would add up over a long memory (1000 tokens of it at g = -0.001 are 3e-5),
+// so from one half up s + expm1(g) s is taken instead, whose error is a
+// rounding of the result alone. keep is 1 and factor expm1(g) there, else 0
+// and exp(g): one branch for the whole CTA, the same two FMAs an element.
+struct Decay {
+  float keep, factor;
+};
+__device__ __forceinline__ Decay decay_factor(float g) {
+  return g > -0.69f ? Decay{1.f, expm1f(g)} : Decay{0.f, expf(g)};
+}
+template <int NV4>
+__device__ __forceinline__ void decay_update(float4 (&s)[NV4], const float4 (&v)[NV4], Decay a, float d) {
+  if (a.keep == 0.f) {
+    row_update<NV4>(s, v, a.factor, d);
+    return;
+  }
+  const float2 al = make_float2(a.factor, a.factor), dd = make_float2(d, d);
+#pragma unroll
+  for (int m = 0; m < NV4; ++m) {
+    const float2 s0 = make_float2(s[m].x, s[m].y), s1 = make_float2(s[m].z, s[m].w);
+    const float2 lo = fma2(dd, make_float2(v[m].x, v[m].y), fma2(al, s0, s0));
+    const float2 hi = fma2(dd, make_float2(v[m].z, v[m].w), fma2(al, s1, s1));
+    s[m] = make_float4(lo.x, lo.y, hi.x, hi.y);
+  }
+}
+
 // How the D x D state of a head lies over the threads of a CTA: LPR lanes
 // share a row, each with NV4 groups of four columns (group m of lane sub at
 // column 4 sub + 4 LPR m, so that the lanes of a row read 64 or 128
@@ -100,8 +127,9 @@ __device__ __forceinline__ int64_t seq_end(const DecayArgs& p, int n, int64_t be
 
 struct DecaySegment {
   int seq;
+  int index, parts;    // which of the sequence's segments, and how many it has
+  int64_t slot;        // of its first segment
   int64_t begin, end;  // tokens
-  bool first, last;    // of the sequence
 };
 
 // The segment of a slot; false where the slot is spare or its sequence is
@@ -120,14 +148,46 @@ __device__ __forceinline__ bool find_segment(const DecayArgs& p, const DecaySegm
     count = count - at * step < step ? count - at * step : step;
   }
   const int64_t begin = seq_bound(p, lo), end = seq_end(p, lo, begin);
-  const int64_t i = slot - (begin / sg.len + lo);
+  out->slot = begin / sg.len + lo;
+  const int64_t i = slot - out->slot;
   if (i < 0 || i * sg.len >= end - begin) return false;
   out->seq = lo;
+  out->index = (int)i;
+  out->parts = (int)((end - begin + sg.len - 1) / sg.len);
   out->begin = begin + i * sg.len;
-  out->last = end - out->begin <= sg.len;
-  out->end = out->last ? end : out->begin + sg.len;
-  out->first = i == 0;
+  out->end = end - out->begin <= sg.len ? end : out->begin + sg.len;
   return true;
 }
+
+// The first pass over a sequence of several segments leaves in slot m of the
+// workspace what segment m adds to the state (segment 0: the state after it)
+// and in decays[m] what it multiplies the state by. The last segment is not
+// in that pass; its slot keeps a copy of the state before the call, which
+// the call overwrites. These read and write four elements at `at` of V head
+// h's state.
+struct DecaySlots {
+  const float* base;  // slot of segment 0, V head h
+  int64_t step;       // floats between slots
+  const float* decay;
+  int32_t dstep;
+  __device__ __forceinline__ DecaySlots(const DecayArgs& p, const DecaySegments& sg, const DecaySegment& s, int h,
+                                        int dd) {
+    base = sg.states + (s.slot * p.Hv + h) * dd;
+    step = (int64_t)p.Hv * dd;
+    decay = sg.decays + s.slot * p.Hv + h;
+    dstep = p.Hv;
+  }
+  // the state at the start of segment i
+  __device__ __forceinline__ float4 start(int i, int parts, int at) const {
+    if (i == 0) return *reinterpret_cast<const float4*>(base + (parts - 1) * step + at);
+    float4 s = *reinterpret_cast<const float4*>(base + at);
+    for (int m = 1; m < i; ++m) {
+      const float a = decay[m * dstep];
+      const float4 add = *reinterpret_cast<const float4*>(base + m * step + at);
+      s = make_float4(fmaf(a, s.x, add.x), fmaf(a, s.y, add.y), fmaf(a, s.z, add.z), fmaf(a, s.w, add.w));
+    }
+    return s;
+  }
+};
 
 }  // namespace gdn

@@ -12,11 +12,10 @@
 //
 // The recurrence is a chain over the tokens, so one CTA per V head leaves
 // most SMs idle for few heads and long prompts. With a workspace the tokens
-// are cut into segments: (1) each segment's own contribution from a zero
-// state and its total decay, (2) a scan over the segments of a sequence that
-// leaves the state at the start of each, (3) the segments with their
-// outputs, side by side. That computes the states twice; segments are as
-// long as the SMs allow.
+// are cut into segments that run side by side: a first pass computes what
+// each segment adds to the state and multiplies it by, a second one the
+// outputs, each segment starting from what those before it add up to. That
+// goes through the states twice; segments are as long as the SMs allow.
 #include "decay_common.cuh"
 
 namespace gdn {
@@ -24,14 +23,13 @@ namespace {
 
 constexpr int kTile = 8;  // tokens staged at a time
 
-// whole: outputs and the state after the segment; local: only the segment's
-// own contribution to the state, into the workspace
+// whole: outputs, and the state after the sequence; local: the first pass
 enum { kWhole = 0, kLocal = 1 };
 
 template <typename T, int D>
 struct ScanSmem {
   float q[2][kTile][D], k[2][kTile][D], v[2][kTile][D], o[2][kTile][D];
-  float alpha[2][kTile];
+  Decay decay[2][kTile];
 };
 
 template <typename T, int D, int MODE>
@@ -47,19 +45,26 @@ __global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_scan_kernel(const
   const int kh = k_head_of(p.map, h, p.Hk, p.rep);
   DecaySegment s;
   if (!find_segment(p, sg, slot, lane, &s)) return;
-  if (MODE == kLocal && s.last) return;
+  if (MODE == kLocal && s.index + 1 == s.parts) return;
   float* gS = p.state + ((int64_t)s.seq * p.Hv + h) * (int64_t)(D * D);
-  float* wS = sg.states + (int64_t)blockIdx.x * (int64_t)(D * D);
-  const float* from = s.first && s.last ? gS : wS;
-
   float4 st[RPL][NV4];
+  const DecaySlots ws(p, sg, s, h, D * D);
+  const int at0 = (warp * G::WROWS + rq) * D + 4 * sub;
 #pragma unroll
   for (int u = 0; u < RPL; ++u)
 #pragma unroll
-    for (int m = 0; m < NV4; ++m)
-      st[u][m] = MODE == kLocal ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                : *reinterpret_cast<const float4*>(from + (warp * G::WROWS + u * RPW + rq) * D +
-                                                                   4 * sub + 4 * LPR * m);
+    for (int m = 0; m < NV4; ++m) {
+      const int at = at0 + u * RPW * D + 4 * LPR * m;
+      if (MODE == kLocal) {
+        st[u][m] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s.index == 0) {
+          st[u][m] = *reinterpret_cast<const float4*>(gS + at);
+          *reinterpret_cast<float4*>(sg.states + ((s.slot + s.parts - 1) * p.Hv + h) * (int64_t)(D * D) + at) = st[u][m];
+        }
+      } else {
+        st[u][m] = s.parts == 1 ? *reinterpret_cast<const float4*>(gS + at) : ws.start(s.index, s.parts, at);
+      }
+    }
 
   // staging: unit u of a tile is four elements; units of q, k, v in turn
   constexpr int UNITS = kTile * D / 4, PER = (3 * UNITS + NT - 1) / NT;
@@ -91,7 +96,7 @@ __global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_scan_kernel(const
       }
     }
     if (tid < kTile && t0 + tid < s.end) {
-      sm.alpha[buf][tid] = expf(pre_g);
+      sm.decay[buf][tid] = decay_factor(pre_g);
       if (MODE == kLocal) total += pre_g;
     }
   };
@@ -112,13 +117,13 @@ __global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_scan_kernel(const
     if (t0 + kTile < s.end) fetch(t0 + kTile);
     const int n = s.end - t0 < kTile ? (int)(s.end - t0) : kTile;
     for (int tt = 0; tt < n; ++tt) {
-      const float alpha = sm.alpha[buf][tt];
+      const Decay decay = sm.decay[buf][tt];
       float4 kr[NV4];
 #pragma unroll
       for (int m = 0; m < NV4; ++m) kr[m] = *reinterpret_cast<const float4*>(&sm.k[buf][tt][4 * sub + 4 * LPR * m]);
 #pragma unroll
       for (int u = 0; u < RPL; ++u)
-        row_update<NV4>(st[u], kr, alpha, sm.v[buf][tt][warp * G::WROWS + u * RPW + rq]);
+        decay_update<NV4>(st[u], kr, decay, sm.v[buf][tt][warp * G::WROWS + u * RPW + rq]);
       if (MODE == kWhole) {
         float o[RPL];
 #pragma unroll
@@ -139,17 +144,17 @@ __global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_scan_kernel(const
     if (MODE == kWhole) write_tile(buf, t0);
   }
 
-  if (MODE == kLocal || s.last) {
-    float* to = MODE == kLocal ? wS : gS;
+  if (MODE == kLocal || s.index + 1 == s.parts) {
+    float* to = MODE == kLocal ? sg.states + (int64_t)blockIdx.x * (D * D) : gS;
 #pragma unroll
     for (int u = 0; u < RPL; ++u)
 #pragma unroll
       for (int m = 0; m < NV4; ++m)
-        *reinterpret_cast<float4*>(to + (warp * G::WROWS + u * RPW + rq) * D + 4 * sub + 4 * LPR * m) = st[u][m];
+        *reinterpret_cast<float4*>(to + at0 + u * RPW * D + 4 * LPR * m) = st[u][m];
   }
   if (MODE == kLocal && warp == 0) {
     total = group_sum<32>(tid < kTile ? total : 0.f);
-    if (lane == 0) sg.decays[blockIdx.x] = total;
+    if (lane == 0) sg.decays[blockIdx.x] = expf(total);
   }
 }
 
@@ -159,11 +164,9 @@ cudaError_t launch_scan_td(const DecayArgs& p, const DecaySegments& sg, cudaStre
   const unsigned grid = (unsigned)(sg.slots * p.Hv);
   auto whole = decay_scan_kernel<T, D, kWhole>;
   auto local = decay_scan_kernel<T, D, kLocal>;
-  cudaError_t e = cudaSuccess;
   if (sg.states != nullptr) {
     local<<<grid, DecayGeom<D>::THREADS, smem, stream>>>(p, sg);
-    e = cudaGetLastError();
-    if (e == cudaSuccess) e = launch_decay_join(p, sg, D, stream);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   whole<<<grid, DecayGeom<D>::THREADS, smem, stream>>>(p, sg);
@@ -181,41 +184,7 @@ cudaError_t launch_scan_t(const DecayArgs& p, const DecaySegments& sg, int32_t D
   }
 }
 
-// (2): per (sequence, V head, four state elements) through the sequence's
-// segments; each segment's contribution is replaced by the state at its
-// start. A sequence of one segment has nothing here (its state is used in
-// place). The last segment's slot is only written.
-__global__ void __launch_bounds__(256) decay_join_kernel(const DecayArgs p, const DecaySegments sg, const int n4) {
-  const int e = blockIdx.x * 256 + threadIdx.x;
-  if (e >= n4) return;
-  const int h = blockIdx.y, seq = blockIdx.z;
-  const int64_t begin = seq_bound(p, seq), end = seq_end(p, seq, begin);
-  const int64_t parts = (end - begin + sg.len - 1) / sg.len;
-  if (parts < 2) return;
-  const int64_t slot0 = begin / sg.len + seq;
-  const float4* gS = reinterpret_cast<const float4*>(p.state) + ((int64_t)seq * p.Hv + h) * n4 + e;
-  float4 s = *gS;
-  for (int64_t i = 0; i < parts; ++i) {
-    const int64_t at = (slot0 + i) * p.Hv + h;
-    float4* w = reinterpret_cast<float4*>(sg.states) + at * n4 + e;
-    float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
-    float a = 0.f;
-    if (i + 1 < parts) {
-      add = *w;
-      a = expf(sg.decays[at]);
-    }
-    *w = s;
-    s = make_float4(fmaf(a, s.x, add.x), fmaf(a, s.y, add.y), fmaf(a, s.z, add.z), fmaf(a, s.w, add.w));
-  }
-}
-
 }  // namespace
-
-cudaError_t launch_decay_join(const DecayArgs& p, const DecaySegments& sg, int32_t D, cudaStream_t stream) {
-  const int n4 = D * D / 4;
-  decay_join_kernel<<<dim3((unsigned)((n4 + 255) / 256), (unsigned)p.Hv, (unsigned)p.N), 256, 0, stream>>>(p, sg, n4);
-  return cudaGetLastError();
-}
 
 // Sized for the 152 SMs of the one target, so that a workspace asked for on
 // one thread fits the call on another: enough segments for two CTAs on every

@@ -54,11 +54,11 @@ __global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_step_kernel(const
   float vr[RPL];
 #pragma unroll
   for (int u = 0; u < RPL; ++u) vr[u] = to_f32(v[warp * G::WROWS + u * RPW + rq]);
-  const float alpha = expf(decay_log(p.g[(int64_t)b * p.g_stride + h]));
+  const Decay decay = decay_factor(decay_log(p.g[(int64_t)b * p.g_stride + h]));
   float o[RPL];
 #pragma unroll
   for (int u = 0; u < RPL; ++u) {
-    row_update<NV4>(s[u], kr, alpha, vr[u]);
+    decay_update<NV4>(s[u], kr, decay, vr[u]);
     o[u] = row_dot<NV4>(s[u], qr);
     float* row = S + (warp * G::WROWS + u * RPW + rq) * D;
 #pragma unroll

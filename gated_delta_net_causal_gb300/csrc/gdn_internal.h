@@ -133,7 +133,7 @@ struct DecaySegments {
   int64_t len;    // tokens a segment holds at most
   int64_t slots;  // floor(T / len) + N
   float* states;  // [slots][Hv][D][D] or null: one segment per sequence
-  float* decays;  // [slots][Hv]
+  float* decays;  // [slots][Hv] factors of the state over a segment
 };
 
 struct AddRmsNormArgs {
@@ -202,7 +202,10 @@ int64_t decay_segment_len(int32_t N, int64_t T, int32_t Hv, int32_t D, int32_t d
 cudaError_t launch_decay_step(const DecayArgs& p, int32_t dtype, int32_t D, int32_t batch, cudaStream_t stream);
 cudaError_t launch_decay_scan(const DecayArgs& p, const DecaySegments& sg, int32_t dtype, int32_t D,
                               cudaStream_t stream);
-cudaError_t launch_decay_join(const DecayArgs& p, const DecaySegments& sg, int32_t D, cudaStream_t stream);
+// decay_tc.cu: the tensor-core prefill (head_dim 128, bf16)
+bool decay_tc_supported(const DecayArgs& p, int32_t dtype, int32_t D);
+cudaError_t launch_decay_tc(const DecayArgs& p, const DecaySegments& sg, cudaStream_t stream);
+cudaError_t read_error_decay_tc(int32_t* status, bool clear);
 cudaError_t launch_add_rmsnorm(const AddRmsNormArgs& p, int32_t dtype, cudaStream_t stream);
 cudaError_t launch_linear_fp8(const LinearFp8Args& p, const void* x, int64_t x_stride, const void* w,
                               int32_t out_dtype, cudaStream_t stream);

@@ -249,7 +249,24 @@ def test_prefill_nan_stays_behind_its_token():
     gdn.gdn_decay_prefill(c.d, cu, c.q, c.k, c.v, c.g, c.state, core_out=c.core, out=c.out)
     c.check(0, 100, S0[0], c.state[0], "before", SPLIT)
     c.check(190, 250, S0[2], c.state[2], "after", SPLIT)
+    o, _, do, mag, _, _ = c.reference(100, 140, S0[1])  # its own tokens before, most of them in the same chunk
+    ref.check(f64(c.core[100:140]), o, do * 1.02 + SPLIT * mag, "own tokens before")
     assert torch.isnan(c.core[140]).all() and torch.isnan(c.state[1]).all()
+
+
+def test_prefill_infinite_value_spoils_its_value_row_alone():
+    """An infinity in one element of v makes that value row non-finite from its token on, and nothing else."""
+    T = 140
+    c = Case(22, 1, 2, 128, "bf16", T, 1, gated=False)
+    c.v[75, 128 + 9] = float("inf")  # V head 1, value row 9
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    gdn.gdn_decay_prefill(c.d, cu, c.q, c.k, c.v, c.g, c.state, core_out=c.core, out=c.out)
+    spoilt = torch.zeros((T, 2, 128), dtype=torch.bool)
+    spoilt[75:, 1, 9] = True
+    assert torch.equal(~torch.isfinite(c.core).cpu(), spoilt)
+    rows = torch.zeros((2, 128, 128), dtype=torch.bool)
+    rows[1, 9] = True
+    assert torch.equal(~torch.isfinite(c.state[0]).cpu(), rows)
 
 
 def test_prefill_nothing_to_do():
