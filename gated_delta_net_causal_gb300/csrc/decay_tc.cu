@@ -10,15 +10,21 @@
 // so no chunk waits on anything but the state before it. The products, with
 // value rows j or tokens t on the 128 or 64 MMA rows:
 //   scores  [t][s] = Q K^T               both tiles as TMA loads them
-//   O1      [j][t] = S Q^T               S from TMEM as bf16 hi + lo
-//   O2      [j][t] = V^T P^T             V read transposed, P as bf16 hi + lo
+//   O1      [j][t] = S Q^T               S from TMEM, rounded to bf16
+//   O2      [j][t] = V^T P^T             V read transposed, P rounded to bf16
 //   dS      [j][i] = V^T K'              K' = e^(G_n - G_s) k as bf16 hi + mid + lo
-// q, k and v are exact in bf16. Two parts leave 2^-17 of a factor, below what
-// the 16-bit output keeps but visible in a state that is stored in fp32, so
-// what is added to the state has three (2^-25).
+// q, k and v are exact in bf16. What is added to the state has three bf16
+// parts (2^-25 of a factor), as the state is kept in fp32. S and P only reach
+// the outputs: one part each where out alone is asked for, whose own rounding
+// is as large (together 1.4 times it), two (2^-17) where core_out is.
 //
-// A CTA takes 96 KB of shared memory and 256 TMEM columns, so two share an SM
+// An MMA of these sizes holds the tensor pipe for about 73 cycles whatever
+// its M and N, so what counts is their number: 32 a chunk (44 with core_out).
+// A CTA takes 104 KB of shared memory and 256 TMEM columns, so two share an SM
 // and one's loads, exponentials and stores run under the other's products.
+// The outputs leave TMEM as 8 x 8 blocks, are normed and gated in registers
+// (z comes by TMA as they go, transposed in shared memory) and whole chunks
+// are stored by TMA while dS is computed.
 // Exponents are differences of sums of up to 64 log decays, which a decay of
 // -100 a token makes large where the difference is small; the sums are held
 // as two floats each.
@@ -40,19 +46,20 @@ namespace {
 constexpr int kTc = 64;  // tokens per chunk
 constexpr int kTd = 128;
 constexpr int kTThreads = 256;
+constexpr int kGateWarp = 1, kStoreWarp = 2, kDeltaWarp = 6;
 enum { kTWhole = 0, kTLocal = 1 };
 
-// shared memory, from a 1024-byte boundary
-constexpr uint32_t kOffQ = 0;        // [2 boxes of 64 columns][64 t][128 B] SW128
-constexpr uint32_t kOffP = 16384;    // P hi, lo: [64 t][64 s] SW128 each
-constexpr uint32_t kOffK = 32768;    // K, then K' hi in place
-constexpr uint32_t kOffMid = 49152;  // K' mid
-constexpr uint32_t kOffLo = 65536;   // K' lo
-constexpr uint32_t kOffV = 81920;
-constexpr uint32_t kTSmem = 98304;
+// shared memory, from a 1024-byte boundary; tiles of 64 tokens x 128 columns
+// are two boxes of 64 columns, 128-byte swizzled rows
+constexpr uint32_t kOffQ = 0;
+constexpr uint32_t kOffK = 16384;    // K, then K' hi in place
+constexpr uint32_t kOffMid = 32768;  // K' mid
+constexpr uint32_t kOffLo = 49152;   // K' lo
+constexpr uint32_t kOffV = 65536;
+constexpr uint32_t kOffO = 81920;    // z, then the outputs in its place
+constexpr uint32_t kOffP = 98304;    // P [64 t][64 s] SW128, with core_out its low part behind it
 constexpr uint32_t kTile16 = 16384;
-// outputs [64 t][128 j] fp32 for the row pass, over Q and P once both are used
-constexpr uint32_t kOffO = 0;
+constexpr uint32_t tc_smem(bool core) { return kOffP + (core ? 16384 : 8192); }
 
 // TMEM columns
 constexpr uint32_t kColS = 0;    // S hi (64 packed columns), S lo (64)
@@ -89,24 +96,43 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Four 8 x 8 blocks of 16-bit elements between shared memory and registers,
+// transposed: lane l gives the address of row l % 8 of block l / 8, and its
+// register m holds elements (2 (l % 4), l / 4) and (2 (l % 4) + 1, l / 4) of
+// block m as (shared row, shared column).
+__device__ __forceinline__ void ldmatrix_t4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void stmatrix_t4(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// two floats to packed bf16 (a in the low half), and what the rounding left
-__device__ __forceinline__ uint32_t split2(float& a, float& b) {
+// two floats to packed bf16 (x in the low half)
+__device__ __forceinline__ uint32_t pack2(float2 a) {
   uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  a -= __uint_as_float(r << 16);
-  b -= __uint_as_float(r & 0xffff0000u);
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(a.y), "f"(a.x));
   return r;
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+__device__ __forceinline__ float2 unpack2(uint32_t r) {
+  return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+}
+// the same, leaving in a what the rounding dropped
+__device__ __forceinline__ uint32_t split2(float2& a) {
+  const uint32_t r = pack2(a);
+  a = fma2(unpack2(r), make_float2(-1.f, -1.f), a);
   return r;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float b) { return fma2(a, make_float2(b, b), make_float2(-0.f, -0.f)); }
 
 // a + b as two floats
 struct Two {
@@ -128,22 +154,28 @@ __device__ __forceinline__ Two to_log2(float g) {
   return Two{h, fmaf(g, kLog2e, -h) + g * kLog2eLo};
 }
 
+// of one chunk, from its log decays
+struct Gates {
+  Two G[kTc];     // sums of log2 decays
+  float E[kTc];   // scale e^(G_t)
+  float dk[kTc];  // e^(G_n - G_s), 0 past the chunk's tokens
+  Decay whole;    // e^(G_n)
+};
 struct TcShared {
-  Two G[kTc];       // sums of log2 decays
-  float E[kTc];     // scale e^(G_t)
-  float dk[kTc];    // e^(G_n - G_s), 0 past the chunk's tokens
-  Decay whole;      // e^(G_n)
-  int bad[kTd];     // first token of the chunk with a non-finite v in this value row, or kTc
-  int any_bad;
+  Gates gates[2];   // by chunk parity
+  float red[4][kTc];  // squares of the outputs by TMEM lane quadrant
+  int bad[2][kTd];  // by chunk parity: first token with a non-finite v in this value row, or kTc
+  int any_bad[2];
   int abort;
   uint32_t tmem;
-  uint64_t load, scores, outs, delta;  // mbarriers
+  uint64_t load_q, load_kv, load_z, scores, outs, delta;  // mbarriers
 };
 
-template <int MODE>
+template <int MODE, bool CORE, bool GATED>
 __global__ void __launch_bounds__(kTThreads, 2)
     decay_tc_kernel(const DecayArgs p, const DecaySegments sg, const __grid_constant__ CUtensorMap tm_q,
-                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_o) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ TcShared sh;
@@ -162,19 +194,21 @@ __global__ void __launch_bounds__(kTThreads, 2)
     tc::tmem_relinquish();
   }
   if (tid == 0) {
-    mbar_init(&sh.load, 1);
+    mbar_init(&sh.load_q, 1);
+    mbar_init(&sh.load_kv, 1);
+    mbar_init(&sh.load_z, 1);
     mbar_init(&sh.scores, 1);
-    mbar_init(&sh.outs, 1);
+    mbar_init(&sh.outs, 2);  // O1 and O2
     mbar_init(&sh.delta, 1);
     sh.abort = 0;
-    sh.any_bad = 0;
+    sh.any_bad[0] = sh.any_bad[1] = 0;
     fence_mbar_init();
   }
-  if (tid < kTd) sh.bad[tid] = kTc;
+  if (tid < 2 * kTd) (&sh.bad[0][0])[tid] = kTc;
   volatile int* abort_flag = &sh.abort;
 
   // the state: columns 64 hh .. 64 hh + 63 of row j
-  float S[64];
+  float2 S[32];
   float* gS = p.state + ((int64_t)s.seq * p.Hv + h) * (int64_t)(kTd * kTd);
   const int at0 = j * kTd + 64 * hh;
   {
@@ -191,7 +225,8 @@ __global__ void __launch_bounds__(kTThreads, 2)
       } else {
         x = s.parts == 1 ? *reinterpret_cast<const float4*>(gS + at0 + 4 * c) : ws.start(s.index, s.parts, at0 + 4 * c);
       }
-      S[4 * c] = x.x, S[4 * c + 1] = x.y, S[4 * c + 2] = x.z, S[4 * c + 3] = x.w;
+      S[2 * c] = make_float2(x.x, x.y);
+      S[2 * c + 1] = make_float2(x.z, x.w);
     }
   }
   tc::fence_before_sync();
@@ -199,92 +234,124 @@ __global__ void __launch_bounds__(kTThreads, 2)
   tc::fence_after_sync();
   const uint32_t tb = sh.tmem, tq = tb + ((uint32_t)(32 * qd) << 16);
 
-  // S as the A operand of O1: packed pairs, hi then lo
-  auto put_state = [&]() {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint32_t hi[16], lo[16];
+  // columns 64 hh + 32 c .. + 31 of S as the A operand of O1: packed pairs,
+  // and with core_out what their rounding left
+  auto put_state = [&](int c) {
+    uint32_t hi[16];
+    if (CORE) {
+      uint32_t lo[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        float a = S[32 * c + 2 * e], b = S[32 * c + 2 * e + 1];
-        hi[e] = split2(a, b);
-        lo[e] = pack2(a, b);
+        float2 a = S[16 * c + e];
+        hi[e] = split2(a);
+        lo[e] = pack2(a);
       }
-      tc::tmem_st16u(tq + kColS + 32 * hh + 16 * c, hi);
       tc::tmem_st16u(tq + kColS + 64 + 32 * hh + 16 * c, lo);
-    }
-    tc::tmem_wait_st();
-  };
-  auto issue_loads = [&](int64_t t0) {
-    mbar_arrive_expect_tx(&sh.load, (MODE == kTWhole ? 3 : 2) * kTile16);
+    } else {
 #pragma unroll
+      for (int e = 0; e < 16; ++e) hi[e] = pack2(S[16 * c + e]);
+    }
+    tc::tmem_st16u(tq + kColS + 32 * hh + 16 * c, hi);
+  };
+  uint32_t q_loads = 0, kv_loads = 0, z_loads = 0;  // thread 0's, z the store warp's lane 0's
+  auto load_q = [&](int64_t t0) {
+    ++q_loads;
+    mbar_arrive_expect_tx(&sh.load_q, kTile16);
+    for (int b = 0; b < 2; ++b) tc::tma_load_2d(sm + kOffQ + 8192 * b, &tm_q, kh * kTd + 64 * b, (int)t0, &sh.load_q);
+  };
+  auto load_kv = [&](int64_t t0) {
+    ++kv_loads;
+    mbar_arrive_expect_tx(&sh.load_kv, 2 * kTile16);
     for (int b = 0; b < 2; ++b) {
-      if (MODE == kTWhole) tc::tma_load_2d(sm + kOffQ + 8192 * b, &tm_q, kh * kTd + 64 * b, (int)t0, &sh.load);
-      tc::tma_load_2d(sm + kOffK + 8192 * b, &tm_k, kh * kTd + 64 * b, (int)t0, &sh.load);
-      tc::tma_load_2d(sm + kOffV + 8192 * b, &tm_v, h * kTd + 64 * b, (int)t0, &sh.load);
+      tc::tma_load_2d(sm + kOffK + 8192 * b, &tm_k, kh * kTd + 64 * b, (int)t0, &sh.load_kv);
+      tc::tma_load_2d(sm + kOffV + 8192 * b, &tm_v, h * kTd + 64 * b, (int)t0, &sh.load_kv);
     }
   };
-  // log decays of tokens 2 lane and 2 lane + 1 of a chunk (warp 1)
+  auto load_z = [&](int64_t t0) {
+    ++z_loads;
+    mbar_arrive_expect_tx(&sh.load_z, kTile16);
+    for (int b = 0; b < 2; ++b) tc::tma_load_2d(sm + kOffO + 8192 * b, &tm_z, h * kTd + 64 * b, (int)t0, &sh.load_z);
+  };
+  // log decays of tokens 2 lane and 2 lane + 1 of a chunk, and its gates (warp 1)
   float g0 = 0.f, g1 = 0.f;
+  Two total{0.f, 0.f}, gn{0.f, 0.f};  // log2, of the segment and the chunk
   auto fetch_g = [&](int64_t t0) {
     const int64_t t = t0 + 2 * lane;
     g0 = t < s.end ? decay_log(p.g[t * p.g_stride + h]) : 0.f;
     g1 = t + 1 < s.end ? decay_log(p.g[(t + 1) * p.g_stride + h]) : 0.f;
   };
+  auto put_gates = [&](Gates& to, int n) {
+    // inclusive sums over the chunk, as two floats; tokens past the chunk's
+    // have log decay 0, so lane 31 ends with G_n
+    const Two first = to_log2(g0);
+    Two incl = add2(first, to_log2(g1));
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const Two o{__shfl_up_sync(0xffffffffu, incl.hi, d), __shfl_up_sync(0xffffffffu, incl.lo, d)};
+      if (lane >= d) incl = add2(incl, o);
+    }
+    const Two prev{__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+    const Two a = lane > 0 ? add2(prev, first) : first, b = incl;
+    gn = Two{__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)};
+    if (MODE == kTWhole) {
+      to.G[2 * lane] = a;
+      to.G[2 * lane + 1] = b;
+      to.E[2 * lane] = p.scale * exp2_fast(a.hi + a.lo);
+      to.E[2 * lane + 1] = p.scale * exp2_fast(b.hi + b.lo);
+    }
+    to.dk[2 * lane] = 2 * lane < n ? exp2_fast((gn.hi - a.hi) + (gn.lo - a.lo)) : 0.f;
+    to.dk[2 * lane + 1] = 2 * lane + 1 < n ? exp2_fast((gn.hi - b.hi) + (gn.lo - b.lo)) : 0.f;
+    if (lane == 0) to.whole = decay_factor((gn.hi + gn.lo) * kLn2);
+  };
+  const auto tokens = [&](int64_t t0) { return s.end - t0 < kTc ? (int)(s.end - t0) : kTc; };
 
-  if (MODE == kTWhole) put_state();
-  if (tid == 0) issue_loads(s.begin);
-  if (warp == 1) fetch_g(s.begin);
-  Two total{0.f, 0.f};  // of the segment, log2
-  uint32_t loads = 1;
-  const uint32_t aQ = smem_u32(sm + kOffQ), aP = smem_u32(sm + kOffP);
-  const uint64_t dQ = tc::sdesc_sw128(aQ), dK = tc::sdesc_sw128(smem_u32(sm + kOffK)), dP = tc::sdesc_sw128(aP);
+  if (tid == 0) {
+    load_kv(s.begin);
+    if (MODE == kTWhole) load_q(s.begin);
+  }
+  if (GATED && warp == kStoreWarp && lane == 0) load_z(s.begin);
+  if (warp == 1) {
+    fetch_g(s.begin);
+    put_gates(sh.gates[0], tokens(s.begin));
+    total = gn;
+    fetch_g(s.begin + kTc);
+  }
+  if (MODE == kTWhole) {
+    put_state(0);
+    put_state(1);
+    tc::tmem_wait_st();
+  }
+  const uint64_t dQ = tc::sdesc_sw128(smem_u32(sm + kOffQ)), dK = tc::sdesc_sw128(smem_u32(sm + kOffK));
+  const uint64_t dP = tc::sdesc_sw128(smem_u32(sm + kOffP));
   const uint64_t dV = sdesc_mn128(smem_u32(sm + kOffV)), dKp = sdesc_mn128(smem_u32(sm + kOffK));
   bool failed = false;
   uint32_t phase = 0;
-  // #1: the state operand is in TMEM and the buffers are free
+  // #1: the state operand is in TMEM, the gates in shared memory
   tc::fence_before_sync();
   __syncthreads();
 
   for (int64_t t0 = s.begin; t0 < s.end; t0 += kTc, phase ^= 1) {
-    const int n = s.end - t0 < kTc ? (int)(s.end - t0) : kTc;
-    if (!mbar_wait_bounded(&sh.load, phase, abort_flag)) failed = true;
-    if (MODE == kTWhole && warp == 0) {
-      tc::fence_after_sync();
-      const uint32_t id_s = tc::idesc(tc::kBF16, 64, 64), id_o = tc::idesc(tc::kBF16, 128, 64);
+    const int n = tokens(t0);
+    const bool more = t0 + kTc < s.end;
+    const Gates& gt = sh.gates[phase];
+    if (!mbar_wait_bounded(&sh.load_kv, phase, abort_flag)) failed = true;
+    if (MODE == kTWhole) {
+      if (!mbar_wait_bounded(&sh.load_q, phase, abort_flag)) failed = true;
+      if (warp == 0) {
+        tc::fence_after_sync();
+        const uint32_t id = tc::idesc(tc::kBF16, 64, 64);
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        tc::mma_f16_elect(tb + kColX, tc::sdesc_at(dQ, 64, k), tc::sdesc_at(dK, 64, k), id_s, k > 0);
-      tc::mma_commit_elect(&sh.scores);
+        for (int k = 0; k < 8; ++k)
+          tc::mma_f16_elect(tb + kColX, tc::sdesc_at(dQ, 64, k), tc::sdesc_at(dK, 64, k), id, k > 0);
+        tc::mma_commit_elect(&sh.scores);
+      } else if (warp == 2) {
+        tc::fence_after_sync();
+        const uint32_t id = tc::idesc(tc::kBF16, 128, 64);
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        tc::mma_f16_ts_elect(tb + kColO1, tb + kColS + 8 * k, tc::sdesc_at(dQ, 64, k & 7), id_o, k > 0);
-    }
-    if (warp == 1) {
-      // inclusive sums over the chunk, as two floats
-      const Two first = to_log2(g0);
-      Two incl = add2(first, to_log2(g1));
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const Two o{__shfl_up_sync(0xffffffffu, incl.hi, d), __shfl_up_sync(0xffffffffu, incl.lo, d)};
-        if (lane >= d) incl = add2(incl, o);
+        for (int k = 0; k < (CORE ? 16 : 8); ++k)
+          tc::mma_f16_ts_elect(tb + kColO1, tb + kColS + 8 * k, tc::sdesc_at(dQ, 64, k & 7), id, k > 0);
+        tc::mma_commit_elect(&sh.outs);
       }
-      const Two prev{__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
-      const Two a = lane > 0 ? add2(prev, first) : first, b = incl;
-      // tokens past the chunk's have log decay 0, so lane 31 holds G_n
-      const Two gn{__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)};
-      if (MODE == kTWhole) {
-        sh.G[2 * lane] = a;
-        sh.G[2 * lane + 1] = b;
-        sh.E[2 * lane] = p.scale * exp2_fast(a.hi + a.lo);
-        sh.E[2 * lane + 1] = p.scale * exp2_fast(b.hi + b.lo);
-      } else {
-        total = add2(total, gn);
-      }
-      sh.dk[2 * lane] = 2 * lane < n ? exp2_fast((gn.hi - a.hi) + (gn.lo - a.lo)) : 0.f;
-      sh.dk[2 * lane + 1] = 2 * lane + 1 < n ? exp2_fast((gn.hi - b.hi) + (gn.lo - b.lo)) : 0.f;
-      if (lane == 0) sh.whole = decay_factor((gn.hi + gn.lo) * kLn2);
-      if (t0 + kTc < s.end) fetch_g(t0 + kTc);
     }
     // v: rows past the chunk's tokens are another sequence's (or stale): 0
     // there; non-finite elements are noted and replaced by 0
@@ -293,28 +360,25 @@ __global__ void __launch_bounds__(kTThreads, 2)
       for (int i = 0; i < 4; ++i) {
         const int u = tid + i * kTThreads, row = u >> 4, c16 = u & 15;
         uint4* at = reinterpret_cast<uint4*>(sm + kOffV + (c16 >> 3) * 8192 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4));
+        uint4 x = *at;
+        uint32_t* w = &x.x;
+        uint32_t hit = 0;  // an exponent of all ones carries into the sign's place
+#pragma unroll
+        for (int e = 0; e < 4; ++e) hit |= (w[e] & 0x7f807f80u) + 0x00800080u;
         if (row >= n) {
           *at = make_uint4(0, 0, 0, 0);
-        } else if (MODE == kTWhole) {
-          uint4 x = *at;
-          uint32_t* w = &x.x;
-          uint32_t hit = 0;
+        } else if (MODE == kTWhole && (hit & 0x80008000u) != 0) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) hit |= __vcmpeq2(w[e] & 0x7f807f80u, 0x7f807f80u);
-          if (hit != 0) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (((w[e >> 1] >> (16 * (e & 1))) & 0x7f80u) == 0x7f80u) {
-                atomicMin(&sh.bad[8 * c16 + e], row);
-                w[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
-              }
-            *at = x;
-            sh.any_bad = 1;
-          }
+          for (int e = 0; e < 8; ++e)
+            if (((w[e >> 1] >> (16 * (e & 1))) & 0x7f80u) == 0x7f80u) {
+              atomicMin(&sh.bad[phase][8 * c16 + e], row);
+              w[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+            }
+          *at = x;
+          sh.any_bad[phase] = 1;
         }
       }
     }
-    __syncthreads();  // #2: the sums are in shared memory
 
     if (MODE == kTWhole) {
       if (!mbar_wait_bounded(&sh.scores, phase, abort_flag)) failed = true;
@@ -322,36 +386,45 @@ __global__ void __launch_bounds__(kTThreads, 2)
       float x[16];
       tmem_ld_16x32(tq + kColX + 32 * hh, x);
       tc::tmem_wait_ld();
-      const int ta = 16 * qd + (lane >> 2), tb2 = ta + 8, s0 = 32 * hh + 2 * (lane & 3);
-      const Two ga = sh.G[ta], gb = sh.G[tb2];
+      const int ta = 16 * qd + (lane >> 2), s0 = 32 * hh + 2 * (lane & 3);  // rows ta and ta + 8
+      const Two ga = gt.G[ta], gb = gt.G[ta + 8];
+      unsigned char* pp = sm + kOffP + ta * 128 + 4 * (lane & 3);  // the rows are eight apart: the same swizzle
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int sc = s0 + 8 * c;
-        const Two u0 = sh.G[sc], u1 = sh.G[sc + 1];
-        float y[4];
-        y[0] = sc <= ta ? x[4 * c] * p.scale * exp2_fast((ga.hi - u0.hi) + (ga.lo - u0.lo)) : 0.f;
-        y[1] = sc + 1 <= ta ? x[4 * c + 1] * p.scale * exp2_fast((ga.hi - u1.hi) + (ga.lo - u1.lo)) : 0.f;
-        y[2] = sc <= tb2 ? x[4 * c + 2] * p.scale * exp2_fast((gb.hi - u0.hi) + (gb.lo - u0.lo)) : 0.f;
-        y[3] = sc + 1 <= tb2 ? x[4 * c + 3] * p.scale * exp2_fast((gb.hi - u1.hi) + (gb.lo - u1.lo)) : 0.f;
-        // rows ta and tb2 are eight apart: the same swizzle
-        const uint32_t off = ta * 128 + (((4 * hh + c) ^ (ta & 7)) << 4) + 4 * (lane & 3);
-        *reinterpret_cast<uint32_t*>(sm + kOffP + off) = split2(y[0], y[1]);
-        *reinterpret_cast<uint32_t*>(sm + kOffP + 8192 + off) = pack2(y[0], y[1]);
-        *reinterpret_cast<uint32_t*>(sm + kOffP + off + 1024) = split2(y[2], y[3]);
-        *reinterpret_cast<uint32_t*>(sm + kOffP + 8192 + off + 1024) = pack2(y[2], y[3]);
+        const Two u0 = gt.G[sc], u1 = gt.G[sc + 1];
+        float2 y = make_float2(x[4 * c] * exp2_fast((ga.hi - u0.hi) + (ga.lo - u0.lo)),
+                               x[4 * c + 1] * exp2_fast((ga.hi - u1.hi) + (ga.lo - u1.lo)));
+        float2 z = make_float2(x[4 * c + 2] * exp2_fast((gb.hi - u0.hi) + (gb.lo - u0.lo)),
+                               x[4 * c + 3] * exp2_fast((gb.hi - u1.hi) + (gb.lo - u1.lo)));
+        y = mul2(y, p.scale);
+        z = mul2(z, p.scale);
+        if (sc > ta) y.x = 0.f;
+        if (sc + 1 > ta) y.y = 0.f;
+        if (sc > ta + 8) z.x = 0.f;
+        if (sc + 1 > ta + 8) z.y = 0.f;
+        unsigned char* at = pp + (((4 * hh + c) ^ (ta & 7)) << 4);
+        *reinterpret_cast<uint32_t*>(at) = CORE ? split2(y) : pack2(y);
+        *reinterpret_cast<uint32_t*>(at + 1024) = CORE ? split2(z) : pack2(z);
+        if (CORE) {
+          *reinterpret_cast<uint32_t*>(at + 8192) = pack2(y);
+          *reinterpret_cast<uint32_t*>(at + 8192 + 1024) = pack2(z);
+        }
       }
       fence_proxy_async_smem();
       tc::fence_before_sync();
-      __syncthreads();  // #3: P and v are in shared memory, the scores are read
-      if (warp == 0) {
+      __syncthreads();  // #2: P and v are in shared memory, the scores are read
+      if (warp == 4) {
         tc::fence_after_sync();
         const uint32_t id = tc::idesc(tc::kBF16, 128, 64) | kTransA;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          tc::mma_f16_elect(tb + kColX, dV + ((k & 3) * 2048 >> 4),
-                            dP + (((k >> 2) * 8192 + (k & 3) * 32) >> 4), id, k > 0);
+        for (int k = 0; k < (CORE ? 8 : 4); ++k)
+          tc::mma_f16_elect(tb + kColX, dV + ((k & 3) * 2048 >> 4), dP + (((k >> 2) * 8192 + (k & 3) * 32) >> 4), id,
+                            k > 0);
         tc::mma_commit_elect(&sh.outs);
       }
+    } else if (n < kTc) {
+      fence_proxy_async_smem();
     }
 
     // K' = e^(G_n - G_s) k in three parts, the first in place of K
@@ -359,46 +432,126 @@ __global__ void __launch_bounds__(kTThreads, 2)
     for (int i = 0; i < 4; ++i) {
       const int u = tid + i * kTThreads, row = u >> 4, c16 = u & 15;
       const uint32_t off = (c16 >> 3) * 8192 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4);
-      const uint4 x = *reinterpret_cast<const uint4*>(sm + kOffK + off);
+      uint4 x = *reinterpret_cast<const uint4*>(sm + kOffK + off);
+      if (row >= n) x = make_uint4(0, 0, 0, 0);  // another sequence's: may be a NaN
       const uint32_t* w = &x.x;
-      const float d = sh.dk[row];
+      const float d = gt.dk[row];
       uint4 part[3];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float a = __uint_as_float(w[e] << 16) * d, b = __uint_as_float(w[e] & 0xffff0000u) * d;
-        if (row >= n) a = b = 0.f;  // not a product: the row may hold a NaN
-        (&part[0].x)[e] = split2(a, b);
-        (&part[1].x)[e] = split2(a, b);
-        (&part[2].x)[e] = pack2(a, b);
+        float2 a = mul2(unpack2(w[e]), d);
+        (&part[0].x)[e] = split2(a);
+        (&part[1].x)[e] = split2(a);
+        (&part[2].x)[e] = pack2(a);
       }
       *reinterpret_cast<uint4*>(sm + kOffK + off) = part[0];
       *reinterpret_cast<uint4*>(sm + kOffMid + off) = part[1];
       *reinterpret_cast<uint4*>(sm + kOffLo + off) = part[2];
     }
     fence_proxy_async_smem();
-
+    if (MODE == kTWhole) {  // for the next chunk, which writes them after #1
+      if (tid < kTd) sh.bad[phase ^ 1][tid] = kTc;
+      if (tid == 0) sh.any_bad[phase ^ 1] = 0;
+    }
     if (MODE == kTWhole) {
       if (!mbar_wait_bounded(&sh.outs, phase, abort_flag)) failed = true;
       tc::fence_after_sync();
-      const int bad = sh.any_bad ? sh.bad[j] : kTc;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float a[16], b[16];
-        tc::tmem_ld16(tq + kColO1 + 32 * hh + 16 * c, a);
-        tc::tmem_ld16(tq + kColX + 32 * hh + 16 * c, b);
+      if (tid == 0 && more) load_q(t0 + kTc);
+      if (GATED && !mbar_wait_bounded(&sh.load_z, phase, abort_flag)) failed = true;
+      // a lane holds value rows jj + 8 b + 16 a (a, b of 0, 1) and tokens
+      // tt + 8 c, tt + 8 c + 1 (c of 0..3)
+      const int jj = 32 * qd + (lane >> 2), tt = 32 * hh + 2 * (lane & 3);
+      auto read_half = [&](int a, float (&o)[16]) {
+        float x[16];
+        tmem_ld_16x32(tq + ((uint32_t)(16 * a) << 16) + kColO1 + 32 * hh, o);
+        tmem_ld_16x32(tq + ((uint32_t)(16 * a) << 16) + kColX + 32 * hh, x);
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int t = 32 * hh + 16 * c + e;
-          float o = fmaf(a[e], sh.E[t], b[e]);
-          if (t >= bad) o = __int_as_float(0x7fc00000);
-          *reinterpret_cast<float*>(sm + kOffO + (t * kTd + j) * 4) = o;
+        for (int c = 0; c < 4; ++c) {
+          const float2 e = *reinterpret_cast<const float2*>(&gt.E[tt + 8 * c]);
+          o[4 * c] = fmaf(o[4 * c], e.x, x[4 * c]);
+          o[4 * c + 1] = fmaf(o[4 * c + 1], e.y, x[4 * c + 1]);
+          o[4 * c + 2] = fmaf(o[4 * c + 2], e.x, x[4 * c + 2]);
+          o[4 * c + 3] = fmaf(o[4 * c + 3], e.y, x[4 * c + 3]);
+        }
+        if (sh.any_bad[phase])
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (tt + 8 * (i >> 2) + (i & 1) >= sh.bad[phase][jj + 16 * a + 8 * ((i >> 1) & 1)])
+              o[i] = __int_as_float(0x7fc00000);
+      };
+      float inv[8];
+      if (GATED) {
+        float sq[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sq[i] = 0.f;
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          float o[16];
+          read_half(a, o);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sq[2 * (i >> 2) + (i & 1)] = fmaf(o[i], o[i], sq[2 * (i >> 2) + (i & 1)]);
+        }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sq[i] += __shfl_xor_sync(0xffffffffu, sq[i], d);
+        if (lane < 4)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<float2*>(&sh.red[qd][tt + 8 * c]) = make_float2(sq[2 * c], sq[2 * c + 1]);
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + hh) : "memory");
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float2 r = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float2 x = *reinterpret_cast<const float2*>(&sh.red[w][tt + 8 * c]);
+            r.x += x.x, r.y += x.y;
+          }
+          inv[2 * c] = 1.f / sqrtf(r.x * (1.f / kTd) + p.rms_eps);
+          inv[2 * c + 1] = 1.f / sqrtf(r.y * (1.f / kTd) + p.rms_eps);
         }
       }
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        float o[16];
+        read_half(a, o);
+        if (CORE)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int t = tt + 8 * (i >> 2) + (i & 1);
+            if (t < n) p.core_out[((t0 + t) * p.Hv + h) * kTd + jj + 16 * a + 8 * ((i >> 1) & 1)] = o[i];
+          }
+        // blocks (rows jj block 0 and 1 of this half) x (token blocks 2 d, 2 d + 1)
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const int t = 32 * hh + 16 * d + 8 * (lane >> 4) + (lane & 7), c8 = 4 * qd + 2 * a + ((lane >> 3) & 1);
+          const uint32_t at = smem_u32(sm + kOffO) + (c8 >> 3) * 8192 + t * 128 + (((c8 & 7) ^ (t & 7)) << 4);
+          float* x = o + 8 * d;
+          uint32_t r[4];
+          if (GATED) {
+            ldmatrix_t4(at, r);
+            const float w0 = __ldg(p.norm_w + jj + 16 * a), w1 = __ldg(p.norm_w + jj + 16 * a + 8);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const float2 z = unpack2(r[m]);
+              const float w = m & 1 ? w1 : w0;
+              const int c = 2 * d + (m >> 1);
+              x[2 * m] *= inv[2 * c] * w * silu_fast(z.x);
+              x[2 * m + 1] *= inv[2 * c + 1] * w * silu_fast(z.y);
+            }
+          }
+#pragma unroll
+          for (int m = 0; m < 4; ++m) r[m] = pack2(make_float2(x[2 * m], x[2 * m + 1]));
+          stmatrix_t4(at, r);
+        }
+      }
+      fence_proxy_async_smem();
     }
     tc::fence_before_sync();
-    __syncthreads();  // #4: K' is in shared memory, the outputs are staged and their TMEM columns read
-    if (warp == 0) {
+    __syncthreads();  // #3: K' is in shared memory, the outputs are staged and their TMEM columns read
+    if (warp == kDeltaWarp) {
       tc::fence_after_sync();
       const uint32_t id = tc::idesc(tc::kBF16, 128, 128) | kTransA | kTransB;
 #pragma unroll
@@ -406,63 +559,63 @@ __global__ void __launch_bounds__(kTThreads, 2)
         tc::mma_f16_elect(tb + kColX, dV + ((k & 3) * 2048 >> 4), dKp + (((k >> 2) * kTile16 + (k & 3) * 2048) >> 4), id,
                           k > 0);
       tc::mma_commit_elect(&sh.delta);
-    }
-    if (MODE == kTWhole) {
-      // rows of the outputs: eight tokens a warp, four value rows a lane
-      const __nv_bfloat16* z = static_cast<const __nv_bfloat16*>(p.z);
-      float4 w4 = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (z != nullptr) w4 = *reinterpret_cast<const float4*>(p.norm_w + 4 * lane);
-#pragma unroll 4
-      for (int r = 0; r < 8; ++r) {
-        const int t = 8 * warp + r;
-        if (t >= n) break;
-        const int64_t orow = ((t0 + t) * p.Hv + h) * kTd + 4 * lane;
-        float4 o = *reinterpret_cast<const float4*>(sm + kOffO + (t * kTd + 4 * lane) * 4);
-        if (p.core_out != nullptr) *reinterpret_cast<float4*>(p.core_out + orow) = o;
-        if (z != nullptr) {
-          const float4 zz = load4(z + (t0 + t) * p.z_stride + h * kTd + 4 * lane);
-          const float ss = group_sum<32>(o.x * o.x + o.y * o.y + (o.z * o.z + o.w * o.w));
-          const float inv = 1.f / sqrtf(ss * (1.f / kTd) + p.rms_eps);
-          o = make_float4(o.x * inv * w4.x * silu_fast(zz.x), o.y * inv * w4.y * silu_fast(zz.y),
-                          o.z * inv * w4.z * silu_fast(zz.z), o.w * inv * w4.w * silu_fast(zz.w));
+    } else if (warp == kGateWarp) {
+      if (more) {
+        // one decay for all tokens: full chunks share their gates, in both buffers after the second
+        if (p.g_stride != 0 || t0 == s.begin || tokens(t0 + kTc) < kTc)
+          put_gates(sh.gates[phase ^ 1], tokens(t0 + kTc));
+        total = add2(total, gn);
+        fetch_g(t0 + 2 * kTc);
+      }
+    } else if (MODE == kTWhole && (!CORE || p.out != nullptr)) {
+      if (n == kTc) {
+        if (warp == kStoreWarp && lane == 0) {
+          for (int b = 0; b < 2; ++b) tc::tma_store_2d(&tm_o, h * kTd + 64 * b, (int)t0, sm + kOffO + 8192 * b);
+          bulk_commit();
+          bulk_wait_read_all();
         }
-        if (p.out != nullptr)
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow) =
-              make_uint2(pack2(o.x, o.y), pack2(o.z, o.w));
+      } else if (warp != 7) {
+        // a last, shorter chunk: its rows alone, by the warps 0, 2, 3, 4 and 5
+        const int first = warp == 0 ? 0 : warp - 1;
+        for (int u = first * 32 + lane; u < 16 * n; u += 5 * 32) {
+          const int t = u >> 4, c8 = u & 15;
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + ((t0 + t) * p.Hv + h) * kTd + 8 * c8) =
+              *reinterpret_cast<const uint4*>(sm + kOffO + (c8 >> 3) * 8192 + t * 128 + (((c8 & 7) ^ (t & 7)) << 4));
+        }
       }
     }
+    if (GATED && more && warp == kStoreWarp && lane == 0) load_z(t0 + kTc);
     if (!mbar_wait_bounded(&sh.delta, phase, abort_flag)) failed = true;
     tc::fence_after_sync();
+    if (tid == 0 && more) load_kv(t0 + kTc);
     {
-      const Decay a = sh.whole;
-      const bool spoilt = MODE == kTWhole && sh.any_bad && sh.bad[j] < kTc;
+      const Decay a = gt.whole;
+      const float2 f = make_float2(a.factor, a.factor), keep = make_float2(a.keep, a.keep);
+      const bool spoilt = MODE == kTWhole && sh.any_bad[phase] && sh.bad[phase][j] < kTc;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float d[16];
-        tc::tmem_ld16(tq + kColX + 64 * hh + 16 * c, d);
+      for (int c = 0; c < 2; ++c) {
+        float d[32];
+        tc::tmem_ld16(tq + kColX + 64 * hh + 32 * c, *reinterpret_cast<float(*)[16]>(d));
+        tc::tmem_ld16(tq + kColX + 64 * hh + 32 * c + 16, *reinterpret_cast<float(*)[16]>(d + 16));
         tc::tmem_wait_ld();
+        if (a.keep != 0.f) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          S[16 * c + e] = fmaf(a.factor, S[16 * c + e], a.keep != 0.f ? S[16 * c + e] + d[e] : d[e]);
-          if (spoilt) S[16 * c + e] = __int_as_float(0x7fc00000);
+          for (int e = 0; e < 16; ++e)
+            S[16 * c + e] = fma2(f, S[16 * c + e], fma2(keep, S[16 * c + e], make_float2(d[2 * e], d[2 * e + 1])));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) S[16 * c + e] = fma2(f, S[16 * c + e], make_float2(d[2 * e], d[2 * e + 1]));
         }
+        if (spoilt)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) S[16 * c + e] = make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
+        if (MODE == kTWhole && more) put_state(c);
       }
-      if (MODE == kTWhole) put_state();
+      if (MODE == kTWhole && more) tc::tmem_wait_st();
     }
-    fence_proxy_async_smem();
     tc::fence_before_sync();
     // #1 of the next chunk: everything of this one is read
     if (__syncthreads_or(failed)) break;
-    if (MODE == kTWhole && sh.any_bad) {
-      __syncthreads();
-      if (tid < kTd) sh.bad[tid] = kTc;
-      if (tid == 0) sh.any_bad = 0;
-      __syncthreads();
-    }
-    if (t0 + kTc < s.end && tid == 0) {
-      issue_loads(t0 + kTc);
-      ++loads;
-    }
   }
 
   if (!failed && !*abort_flag) {
@@ -471,12 +624,20 @@ __global__ void __launch_bounds__(kTThreads, 2)
 #pragma unroll
       for (int c = 0; c < 16; ++c)
         *reinterpret_cast<float4*>(to + at0 + 4 * c) =
-            make_float4(S[4 * c], S[4 * c + 1], S[4 * c + 2], S[4 * c + 3]);
+            make_float4(S[2 * c].x, S[2 * c].y, S[2 * c + 1].x, S[2 * c + 1].y);
     }
     if (MODE == kTLocal && warp == 1 && lane == 0) sg.decays[blockIdx.x] = exp2f(total.hi + total.lo);
   }
-  // no load may still be in flight when the CTA ends
-  if (tid == 0) mbar_wait(&sh.load, (loads - 1) & 1);
+  // no load may still be in flight when the CTA ends: after a wait that gave
+  // up the next chunk's may be
+  if (tid == 0) {
+    mbar_wait(&sh.load_kv, (kv_loads - 1) & 1);
+    if (MODE == kTWhole) mbar_wait(&sh.load_q, (q_loads - 1) & 1);
+  }
+  if (MODE == kTWhole && warp == kStoreWarp && lane == 0) {
+    if (GATED) mbar_wait(&sh.load_z, (z_loads - 1) & 1);
+    bulk_wait_all();
+  }
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 0) {
@@ -493,25 +654,34 @@ bool decay_tc_supported(const DecayArgs&, int32_t dtype, int32_t D) {
 
 cudaError_t launch_decay_tc(const DecayArgs& p, const DecaySegments& sg, cudaStream_t stream) {
   const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mz{}, mo{};
+  bool mz_ok, mo_ok;
   if (!tc::make_map_2d(&mq, p.q, p.T, (int64_t)p.Hk * kTd, p.q_stride, 2, bf, 64, kTc, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tc::make_map_2d(&mk, p.k, p.T, (int64_t)p.Hk * kTd, p.k_stride, 2, bf, 64, kTc, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tc::make_map_2d(&mv, p.v, p.T, (int64_t)p.Hv * kTd, p.v_stride, 2, bf, 64, kTc, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
+  // z and out: the maps of those that are not there are never used
+  mz_ok = p.z == nullptr || tc::make_map_2d(&mz, p.z, p.T, (int64_t)p.Hv * kTd, p.z_stride, 2, bf, 64, kTc,
+                                            CU_TENSOR_MAP_SWIZZLE_128B);
+  mo_ok = p.out == nullptr || tc::make_map_2d(&mo, p.out, p.T, (int64_t)p.Hv * kTd, (int64_t)p.Hv * kTd, 2, bf, 64, kTc,
+                                              CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!mz_ok || !mo_ok) return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)(sg.slots * p.Hv);
-  constexpr int smem = (int)kTSmem + 1024;
-  auto whole = decay_tc_kernel<kTWhole>;
-  auto local = decay_tc_kernel<kTLocal>;
-  cudaError_t e = cudaFuncSetAttribute(whole, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(local, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  const auto run = [&](auto* kernel, bool core) {
+    const int smem = (int)tc_smem(core) + 1024;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kTThreads, smem, stream>>>(p, sg, mq, mk, mv, mz, mo);
+    return cudaGetLastError();
+  };
   if (sg.states != nullptr) {
-    local<<<grid, kTThreads, smem, stream>>>(p, sg, mq, mk, mv);
-    e = cudaGetLastError();
+    const cudaError_t e = run(decay_tc_kernel<kTLocal, false, false>, false);
     if (e != cudaSuccess) return e;
   }
-  whole<<<grid, kTThreads, smem, stream>>>(p, sg, mq, mk, mv);
-  return cudaGetLastError();
+  if (p.core_out != nullptr)
+    return p.z != nullptr ? run(decay_tc_kernel<kTWhole, true, true>, true) : run(decay_tc_kernel<kTWhole, true, false>, true);
+  return p.z != nullptr ? run(decay_tc_kernel<kTWhole, false, true>, false)
+                        : run(decay_tc_kernel<kTWhole, false, false>, false);
 }
 
 }  // namespace gdn
