@@ -736,12 +736,12 @@ gdn_status gdn_decay_prefill(const gdn_dims* dims, int32_t num_seqs, const int32
   if (st != GDN_OK) return st;
   p.cu_seqlens = cu_seqlens;
   p.N = num_seqs;
-  p.T = total_tokens;
+  p.T = (int32_t)total_tokens;
   if (use_ws) {
     sg.states = static_cast<float*>(workspace);
     sg.decays = reinterpret_cast<float*>(static_cast<char*>(workspace) + decays_at);
   } else {  // one segment per sequence
-    sg.len = total_tokens + 1;
+    sg.len = (int32_t)total_tokens + 1;
     sg.slots = num_seqs;
   }
   if (gdn::decay_tc_supported(p, dims->io_dtype, dims->head_dim))

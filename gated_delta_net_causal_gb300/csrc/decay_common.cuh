@@ -116,26 +116,26 @@ __device__ __forceinline__ void decay_write_row(const float* o, float* core_out,
 // floor(T / len) + N slots hold every segment, the host need not know the
 // lengths, and a slot finds its sequence by a search over cu_seqlens.
 
-__device__ __forceinline__ int64_t seq_bound(const DecayArgs& p, int n) {
-  const int64_t c = p.cu_seqlens[n];
+__device__ __forceinline__ int seq_bound(const DecayArgs& p, int n) {
+  const int c = p.cu_seqlens[n];
   return c < 0 ? 0 : (c > p.T ? p.T : c);
 }
-__device__ __forceinline__ int64_t seq_end(const DecayArgs& p, int n, int64_t begin) {
-  const int64_t c = seq_bound(p, n + 1);
+__device__ __forceinline__ int seq_end(const DecayArgs& p, int n, int begin) {
+  const int c = seq_bound(p, n + 1);
   return c < begin ? begin : c;
 }
 
 struct DecaySegment {
   int seq;
   int index, parts;    // which of the sequence's segments, and how many it has
-  int64_t slot;        // of its first segment
-  int64_t begin, end;  // tokens
+  int slot;            // of its first segment
+  int begin, end;      // tokens
 };
 
 // The segment of a slot; false where the slot is spare or its sequence is
 // empty. Every lane of a warp calls it: the warp probes 32 sequences at a
 // time, so that up to 32 sequences take one load and up to 1024 two.
-__device__ __forceinline__ bool find_segment(const DecayArgs& p, const DecaySegments& sg, int64_t slot, int lane,
+__device__ __forceinline__ bool find_segment(const DecayArgs& p, const DecaySegments& sg, int slot, int lane,
                                              DecaySegment* out) {
   int lo = 0, count = p.N;  // the last sequence in [lo, lo + count) whose first slot is <= slot
   while (count > 1) {
@@ -147,13 +147,13 @@ __device__ __forceinline__ bool find_segment(const DecayArgs& p, const DecaySegm
     lo += at * step;
     count = count - at * step < step ? count - at * step : step;
   }
-  const int64_t begin = seq_bound(p, lo), end = seq_end(p, lo, begin);
+  const int begin = seq_bound(p, lo), end = seq_end(p, lo, begin);
   out->slot = begin / sg.len + lo;
-  const int64_t i = slot - out->slot;
-  if (i < 0 || i * sg.len >= end - begin) return false;
+  const int i = slot - out->slot;
+  if (i < 0 || i >= (end - begin + sg.len - 1) / sg.len) return false;
   out->seq = lo;
-  out->index = (int)i;
-  out->parts = (int)((end - begin + sg.len - 1) / sg.len);
+  out->index = i;
+  out->parts = (end - begin + sg.len - 1) / sg.len;
   out->begin = begin + i * sg.len;
   out->end = end - out->begin <= sg.len ? end : out->begin + sg.len;
   return true;
@@ -172,9 +172,9 @@ struct DecaySlots {
   int32_t dstep;
   __device__ __forceinline__ DecaySlots(const DecayArgs& p, const DecaySegments& sg, const DecaySegment& s, int h,
                                         int dd) {
-    base = sg.states + (s.slot * p.Hv + h) * dd;
+    base = sg.states + ((int64_t)s.slot * p.Hv + h) * dd;
     step = (int64_t)p.Hv * dd;
-    decay = sg.decays + s.slot * p.Hv + h;
+    decay = sg.decays + ((int64_t)s.slot * p.Hv + h);
     dstep = p.Hv;
   }
   // the state at the start of segment i

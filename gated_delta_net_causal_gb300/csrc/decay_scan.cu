@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_scan_kernel(const
   ScanSmem<T, D>& sm = *reinterpret_cast<ScanSmem<T, D>*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sub = lane % LPR, rq = lane / LPR;
-  const int64_t slot = blockIdx.x / (unsigned)p.Hv;  // a segment's V heads side by side: they share q, k in L2
+  const int slot = blockIdx.x / (unsigned)p.Hv;  // a segment's V heads side by side: they share q, k in L2
   const int h = blockIdx.x % (unsigned)p.Hv;
   const int kh = k_head_of(p.map, h, p.Hk, p.rep);
   DecaySegment s;
@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_scan_kernel(const
         st[u][m] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (s.index == 0) {
           st[u][m] = *reinterpret_cast<const float4*>(gS + at);
-          *reinterpret_cast<float4*>(sg.states + ((s.slot + s.parts - 1) * p.Hv + h) * (int64_t)(D * D) + at) = st[u][m];
+          *reinterpret_cast<float4*>(sg.states + ((int64_t)(s.slot + s.parts - 1) * p.Hv + h) * (D * D) + at) = st[u][m];
         }
       } else {
         st[u][m] = s.parts == 1 ? *reinterpret_cast<const float4*>(gS + at) : ws.start(s.index, s.parts, at);
@@ -70,22 +70,22 @@ __global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_scan_kernel(const
   constexpr int UNITS = kTile * D / 4, PER = (3 * UNITS + NT - 1) / NT;
   float4 pre[PER];
   float pre_g = 0.f;
-  auto fetch = [&](int64_t t0) {
+  auto fetch = [&](int t0) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int u = tid + i * NT;
       const int which = u / UNITS, r = u - which * UNITS, tt = r / (D / 4), c = (r - tt * (D / 4)) * 4;
       if (which < 3 && t0 + tt < s.end && !(MODE == kLocal && which == 0)) {
-        const T* src = which == 0   ? static_cast<const T*>(p.q) + (t0 + tt) * p.q_stride + kh * D + c
-                       : which == 1 ? static_cast<const T*>(p.k) + (t0 + tt) * p.k_stride + kh * D + c
-                                    : static_cast<const T*>(p.v) + (t0 + tt) * p.v_stride + h * D + c;
+        const T* src = which == 0   ? static_cast<const T*>(p.q) + (int64_t)(t0 + tt) * p.q_stride + kh * D + c
+                       : which == 1 ? static_cast<const T*>(p.k) + (int64_t)(t0 + tt) * p.k_stride + kh * D + c
+                                    : static_cast<const T*>(p.v) + (int64_t)(t0 + tt) * p.v_stride + h * D + c;
         pre[i] = load4(src);
       }
     }
-    if (tid < kTile && t0 + tid < s.end) pre_g = decay_log(p.g[(t0 + tid) * p.g_stride + h]);
+    if (tid < kTile && t0 + tid < s.end) pre_g = decay_log(p.g[(int64_t)(t0 + tid) * p.g_stride + h]);
   };
   float total = 0.f;  // thread tt < kTile: its share of the segment's log decay
-  auto stash = [&](int buf, int64_t t0) {
+  auto stash = [&](int buf, int t0) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int u = tid + i * NT;
@@ -100,9 +100,9 @@ __global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_scan_kernel(const
       if (MODE == kLocal) total += pre_g;
     }
   };
-  auto write_tile = [&](int buf, int64_t t0) {
+  auto write_tile = [&](int buf, int t0) {
     for (int tt = warp; tt < kTile && t0 + tt < s.end; tt += G::WARPS) {
-      const int64_t t = t0 + tt, orow = (t * p.Hv + h) * D;
+      const int64_t t = (int64_t)t0 + tt, orow = (t * p.Hv + h) * D;
       decay_write_row<T, D>(sm.o[buf][tt], p.core_out == nullptr ? nullptr : p.core_out + orow,
                             p.z == nullptr ? nullptr : static_cast<const T*>(p.z) + t * p.z_stride + h * D, p.norm_w,
                             p.out == nullptr ? nullptr : static_cast<T*>(p.out) + orow, p.rms_eps, lane);
@@ -113,9 +113,9 @@ __global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_scan_kernel(const
   stash(0, s.begin);
   __syncthreads();
   int buf = 0;
-  for (int64_t t0 = s.begin; t0 < s.end; t0 += kTile, buf ^= 1) {
+  for (int t0 = s.begin; t0 < s.end; t0 += kTile, buf ^= 1) {
     if (t0 + kTile < s.end) fetch(t0 + kTile);
-    const int n = s.end - t0 < kTile ? (int)(s.end - t0) : kTile;
+    const int n = s.end - t0 < kTile ? s.end - t0 : kTile;
     for (int tt = 0; tt < n; ++tt) {
       const Decay decay = sm.decay[buf][tt];
       float4 kr[NV4];
@@ -189,11 +189,11 @@ cudaError_t launch_scan_t(const DecayArgs& p, const DecaySegments& sg, int32_t D
 // Sized for the 152 SMs of the one target, so that a workspace asked for on
 // one thread fits the call on another: enough segments for two CTAs on every
 // SM, none where the (sequence, V head) pairs fill them already.
-int64_t decay_segment_len(int32_t N, int64_t T, int32_t Hv, int32_t, int32_t) {
+int32_t decay_segment_len(int32_t N, int64_t T, int32_t Hv, int32_t, int32_t) {
   constexpr int64_t kCtas = 2 * 152;
-  if ((int64_t)N * Hv >= kCtas) return T + 1;
-  const int64_t len = (T * Hv / kCtas + 63) / 64 * 64;
-  return len < 64 ? 64 : len;
+  if ((int64_t)N * Hv >= kCtas) return (int32_t)T + 1;
+  const int64_t len = (T * Hv / kCtas + 63) / 64 * 64;  // below T + 64
+  return len < 64 ? 64 : (int32_t)len;
 }
 
 cudaError_t launch_decay_scan(const DecayArgs& p, const DecaySegments& sg, int32_t dtype, int32_t D,

@@ -154,15 +154,11 @@ __device__ __forceinline__ Two to_log2(float g) {
   return Two{h, fmaf(g, kLog2e, -h) + g * kLog2eLo};
 }
 
-// of one chunk, from its log decays
-struct Gates {
-  Two G[kTc];     // sums of log2 decays
-  float E[kTc];   // scale e^(G_t)
-  float dk[kTc];  // e^(G_n - G_s), 0 past the chunk's tokens
-  Decay whole;    // e^(G_n)
-};
+
 struct TcShared {
-  Gates gates[2];   // by chunk parity
+  Two G[2][kTc];    // sums of a chunk's log2 decays, by chunk parity
+  float E[kTc];     // scale e^(G_t)
+  float dk[kTc];    // e^(G_n - G_s), 0 past the chunk's tokens
   float red[4][kTc];  // squares of the outputs by TMEM lane quadrant
   int bad[2][kTd];  // by chunk parity: first token with a non-finite v in this value row, or kTc
   int any_bad[2];
@@ -182,7 +178,7 @@ __global__ void __launch_bounds__(kTThreads, 2)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int qd = warp & 3, hh = warp >> 2;  // TMEM lane quadrant, column half
   const int j = 32 * qd + lane;             // this thread's value row
-  const int64_t slot = blockIdx.x / (unsigned)p.Hv;  // a segment's V heads side by side: they share q, k in L2
+  const int slot = blockIdx.x / (unsigned)p.Hv;  // a segment's V heads side by side: they share q, k in L2
   const int h = blockIdx.x % (unsigned)p.Hv;
   const int kh = k_head_of(p.map, h, p.Hk, p.rep);
   DecaySegment s;
@@ -213,7 +209,7 @@ __global__ void __launch_bounds__(kTThreads, 2)
   const int at0 = j * kTd + 64 * hh;
   {
     const DecaySlots ws(p, sg, s, h, kTd * kTd);
-    float* keep = sg.states + ((s.slot + s.parts - 1) * p.Hv + h) * (int64_t)(kTd * kTd);
+    float* keep = sg.states + ((int64_t)(s.slot + s.parts - 1) * p.Hv + h) * (kTd * kTd);
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -254,56 +250,49 @@ __global__ void __launch_bounds__(kTThreads, 2)
     tc::tmem_st16u(tq + kColS + 32 * hh + 16 * c, hi);
   };
   uint32_t q_loads = 0, kv_loads = 0, z_loads = 0;  // thread 0's, z the store warp's lane 0's
-  auto load_q = [&](int64_t t0) {
+  auto load_q = [&](int t0) {
     ++q_loads;
     mbar_arrive_expect_tx(&sh.load_q, kTile16);
-    for (int b = 0; b < 2; ++b) tc::tma_load_2d(sm + kOffQ + 8192 * b, &tm_q, kh * kTd + 64 * b, (int)t0, &sh.load_q);
+    for (int b = 0; b < 2; ++b) tc::tma_load_2d(sm + kOffQ + 8192 * b, &tm_q, kh * kTd + 64 * b, t0, &sh.load_q);
   };
-  auto load_kv = [&](int64_t t0) {
+  auto load_kv = [&](int t0) {
     ++kv_loads;
     mbar_arrive_expect_tx(&sh.load_kv, 2 * kTile16);
     for (int b = 0; b < 2; ++b) {
-      tc::tma_load_2d(sm + kOffK + 8192 * b, &tm_k, kh * kTd + 64 * b, (int)t0, &sh.load_kv);
-      tc::tma_load_2d(sm + kOffV + 8192 * b, &tm_v, h * kTd + 64 * b, (int)t0, &sh.load_kv);
+      tc::tma_load_2d(sm + kOffK + 8192 * b, &tm_k, kh * kTd + 64 * b, t0, &sh.load_kv);
+      tc::tma_load_2d(sm + kOffV + 8192 * b, &tm_v, h * kTd + 64 * b, t0, &sh.load_kv);
     }
   };
-  auto load_z = [&](int64_t t0) {
+  auto load_z = [&](int t0) {
     ++z_loads;
     mbar_arrive_expect_tx(&sh.load_z, kTile16);
-    for (int b = 0; b < 2; ++b) tc::tma_load_2d(sm + kOffO + 8192 * b, &tm_z, h * kTd + 64 * b, (int)t0, &sh.load_z);
+    for (int b = 0; b < 2; ++b) tc::tma_load_2d(sm + kOffO + 8192 * b, &tm_z, h * kTd + 64 * b, t0, &sh.load_z);
   };
   // log decays of tokens 2 lane and 2 lane + 1 of a chunk, and its gates (warp 1)
   float g0 = 0.f, g1 = 0.f;
   Two total{0.f, 0.f}, gn{0.f, 0.f};  // log2, of the segment and the chunk
-  auto fetch_g = [&](int64_t t0) {
-    const int64_t t = t0 + 2 * lane;
-    g0 = t < s.end ? decay_log(p.g[t * p.g_stride + h]) : 0.f;
-    g1 = t + 1 < s.end ? decay_log(p.g[(t + 1) * p.g_stride + h]) : 0.f;
+  auto fetch_g = [&](int t0) {
+    const int t = t0 + 2 * lane;
+    const float* g = p.g + t * p.g_stride + h;
+    g0 = t < s.end ? g[0] : 0.f;
+    g1 = t + 1 < s.end ? g[p.g_stride] : 0.f;
   };
-  auto put_gates = [&](Gates& to, int n) {
+  auto put_sums = [&](Two* to) {
     // inclusive sums over the chunk, as two floats; tokens past the chunk's
     // have log decay 0, so lane 31 ends with G_n
-    const Two first = to_log2(g0);
-    Two incl = add2(first, to_log2(g1));
+    const Two first = to_log2(decay_log(g0));
+    Two incl = add2(first, to_log2(decay_log(g1)));
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const Two o{__shfl_up_sync(0xffffffffu, incl.hi, d), __shfl_up_sync(0xffffffffu, incl.lo, d)};
       if (lane >= d) incl = add2(incl, o);
     }
     const Two prev{__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
-    const Two a = lane > 0 ? add2(prev, first) : first, b = incl;
-    gn = Two{__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)};
-    if (MODE == kTWhole) {
-      to.G[2 * lane] = a;
-      to.G[2 * lane + 1] = b;
-      to.E[2 * lane] = p.scale * exp2_fast(a.hi + a.lo);
-      to.E[2 * lane + 1] = p.scale * exp2_fast(b.hi + b.lo);
-    }
-    to.dk[2 * lane] = 2 * lane < n ? exp2_fast((gn.hi - a.hi) + (gn.lo - a.lo)) : 0.f;
-    to.dk[2 * lane + 1] = 2 * lane + 1 < n ? exp2_fast((gn.hi - b.hi) + (gn.lo - b.lo)) : 0.f;
-    if (lane == 0) to.whole = decay_factor((gn.hi + gn.lo) * kLn2);
+    to[2 * lane] = lane > 0 ? add2(prev, first) : first;
+    to[2 * lane + 1] = incl;
+    if (MODE == kTLocal) gn = Two{__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)};
   };
-  const auto tokens = [&](int64_t t0) { return s.end - t0 < kTc ? (int)(s.end - t0) : kTc; };
+  const auto tokens = [&](int t0) { return s.end - t0 < kTc ? s.end - t0 : kTc; };
 
   if (tid == 0) {
     load_kv(s.begin);
@@ -312,7 +301,7 @@ __global__ void __launch_bounds__(kTThreads, 2)
   if (GATED && warp == kStoreWarp && lane == 0) load_z(s.begin);
   if (warp == 1) {
     fetch_g(s.begin);
-    put_gates(sh.gates[0], tokens(s.begin));
+    put_sums(sh.G[0]);
     total = gn;
     fetch_g(s.begin + kTc);
   }
@@ -330,27 +319,47 @@ __global__ void __launch_bounds__(kTThreads, 2)
   tc::fence_before_sync();
   __syncthreads();
 
-  for (int64_t t0 = s.begin; t0 < s.end; t0 += kTc, phase ^= 1) {
+  for (int t0 = s.begin; t0 < s.end; t0 += kTc, phase ^= 1) {
     const int n = tokens(t0);
     const bool more = t0 + kTc < s.end;
-    const Gates& gt = sh.gates[phase];
+    const Two* G = sh.G[phase];
+    // the buffers are single: the next chunk's tiles come into L2 meanwhile, so
+    // that its loads, issued late in this chunk, are short
+    if (warp == 7 && lane == 0 && more) {
+      for (int b = 0; b < 2; ++b) {
+        tc::tma_prefetch_2d(&tm_k, kh * kTd + 64 * b, t0 + kTc);
+        tc::tma_prefetch_2d(&tm_v, h * kTd + 64 * b, t0 + kTc);
+        if (MODE == kTWhole) tc::tma_prefetch_2d(&tm_q, kh * kTd + 64 * b, t0 + kTc);
+        if (GATED) tc::tma_prefetch_2d(&tm_z, h * kTd + 64 * b, t0 + kTc);
+      }
+    }
     if (!mbar_wait_bounded(&sh.load_kv, phase, abort_flag)) failed = true;
     if (MODE == kTWhole) {
       if (!mbar_wait_bounded(&sh.load_q, phase, abort_flag)) failed = true;
       if (warp == 0) {
         tc::fence_after_sync();
         const uint32_t id = tc::idesc(tc::kBF16, 64, 64);
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < 8; ++k)
           tc::mma_f16_elect(tb + kColX, tc::sdesc_at(dQ, 64, k), tc::sdesc_at(dK, 64, k), id, k > 0);
         tc::mma_commit_elect(&sh.scores);
       } else if (warp == 2) {
         tc::fence_after_sync();
         const uint32_t id = tc::idesc(tc::kBF16, 128, 64);
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < (CORE ? 16 : 8); ++k)
           tc::mma_f16_ts_elect(tb + kColO1, tb + kColS + 8 * k, tc::sdesc_at(dQ, 64, k & 7), id, k > 0);
         tc::mma_commit_elect(&sh.outs);
+      }
+    }
+    if (warp == kGateWarp) {
+      const Two gl = G[kTc - 1];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = lane + 32 * i;
+        const Two a = G[t];
+        if (MODE == kTWhole) sh.E[t] = p.scale * exp2_fast(a.hi + a.lo);
+        sh.dk[t] = t < n ? exp2_fast((gl.hi - a.hi) + (gl.lo - a.lo)) : 0.f;
       }
     }
     // v: rows past the chunk's tokens are another sequence's (or stale): 0
@@ -387,12 +396,12 @@ __global__ void __launch_bounds__(kTThreads, 2)
       tmem_ld_16x32(tq + kColX + 32 * hh, x);
       tc::tmem_wait_ld();
       const int ta = 16 * qd + (lane >> 2), s0 = 32 * hh + 2 * (lane & 3);  // rows ta and ta + 8
-      const Two ga = gt.G[ta], gb = gt.G[ta + 8];
+      const Two ga = G[ta], gb = G[ta + 8];
       unsigned char* pp = sm + kOffP + ta * 128 + 4 * (lane & 3);  // the rows are eight apart: the same swizzle
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int sc = s0 + 8 * c;
-        const Two u0 = gt.G[sc], u1 = gt.G[sc + 1];
+        const Two u0 = G[sc], u1 = G[sc + 1];
         float2 y = make_float2(x[4 * c] * exp2_fast((ga.hi - u0.hi) + (ga.lo - u0.lo)),
                                x[4 * c + 1] * exp2_fast((ga.hi - u1.hi) + (ga.lo - u1.lo)));
         float2 z = make_float2(x[4 * c + 2] * exp2_fast((gb.hi - u0.hi) + (gb.lo - u0.lo)),
@@ -417,14 +426,15 @@ __global__ void __launch_bounds__(kTThreads, 2)
       if (warp == 4) {
         tc::fence_after_sync();
         const uint32_t id = tc::idesc(tc::kBF16, 128, 64) | kTransA;
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < (CORE ? 8 : 4); ++k)
           tc::mma_f16_elect(tb + kColX, dV + ((k & 3) * 2048 >> 4), dP + (((k >> 2) * 8192 + (k & 3) * 32) >> 4), id,
                             k > 0);
         tc::mma_commit_elect(&sh.outs);
       }
-    } else if (n < kTc) {
-      fence_proxy_async_smem();
+    } else {
+      if (n < kTc) fence_proxy_async_smem();
+      __syncthreads();  // dk is in shared memory
     }
 
     // K' = e^(G_n - G_s) k in three parts, the first in place of K
@@ -435,7 +445,7 @@ __global__ void __launch_bounds__(kTThreads, 2)
       uint4 x = *reinterpret_cast<const uint4*>(sm + kOffK + off);
       if (row >= n) x = make_uint4(0, 0, 0, 0);  // another sequence's: may be a NaN
       const uint32_t* w = &x.x;
-      const float d = gt.dk[row];
+      const float d = sh.dk[row];
       uint4 part[3];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -468,7 +478,7 @@ __global__ void __launch_bounds__(kTThreads, 2)
         tc::tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const float2 e = *reinterpret_cast<const float2*>(&gt.E[tt + 8 * c]);
+          const float2 e = *reinterpret_cast<const float2*>(&sh.E[tt + 8 * c]);
           o[4 * c] = fmaf(o[4 * c], e.x, x[4 * c]);
           o[4 * c + 1] = fmaf(o[4 * c + 1], e.y, x[4 * c + 1]);
           o[4 * c + 2] = fmaf(o[4 * c + 2], e.x, x[4 * c + 2]);
@@ -509,8 +519,8 @@ __global__ void __launch_bounds__(kTThreads, 2)
             const float2 x = *reinterpret_cast<const float2*>(&sh.red[w][tt + 8 * c]);
             r.x += x.x, r.y += x.y;
           }
-          inv[2 * c] = 1.f / sqrtf(r.x * (1.f / kTd) + p.rms_eps);
-          inv[2 * c + 1] = 1.f / sqrtf(r.y * (1.f / kTd) + p.rms_eps);
+          inv[2 * c] = rsqrtf(r.x * (1.f / kTd) + p.rms_eps);
+          inv[2 * c + 1] = rsqrtf(r.y * (1.f / kTd) + p.rms_eps);
         }
       }
 #pragma unroll
@@ -521,7 +531,7 @@ __global__ void __launch_bounds__(kTThreads, 2)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int t = tt + 8 * (i >> 2) + (i & 1);
-            if (t < n) p.core_out[((t0 + t) * p.Hv + h) * kTd + jj + 16 * a + 8 * ((i >> 1) & 1)] = o[i];
+            if (t < n) p.core_out[((int64_t)(t0 + t) * p.Hv + h) * kTd + jj + 16 * a + 8 * ((i >> 1) & 1)] = o[i];
           }
         // blocks (rows jj block 0 and 1 of this half) x (token blocks 2 d, 2 d + 1)
 #pragma unroll
@@ -554,23 +564,22 @@ __global__ void __launch_bounds__(kTThreads, 2)
     if (warp == kDeltaWarp) {
       tc::fence_after_sync();
       const uint32_t id = tc::idesc(tc::kBF16, 128, 128) | kTransA | kTransB;
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < 12; ++k)
         tc::mma_f16_elect(tb + kColX, dV + ((k & 3) * 2048 >> 4), dKp + (((k >> 2) * kTile16 + (k & 3) * 2048) >> 4), id,
                           k > 0);
       tc::mma_commit_elect(&sh.delta);
     } else if (warp == kGateWarp) {
       if (more) {
-        // one decay for all tokens: full chunks share their gates, in both buffers after the second
-        if (p.g_stride != 0 || t0 == s.begin || tokens(t0 + kTc) < kTc)
-          put_gates(sh.gates[phase ^ 1], tokens(t0 + kTc));
-        total = add2(total, gn);
+        // one decay for all tokens: full chunks share their sums, in both buffers after the second
+        if (p.g_stride != 0 || t0 == s.begin || tokens(t0 + kTc) < kTc) put_sums(sh.G[phase ^ 1]);
+        if (MODE == kTLocal) total = add2(total, gn);
         fetch_g(t0 + 2 * kTc);
       }
     } else if (MODE == kTWhole && (!CORE || p.out != nullptr)) {
       if (n == kTc) {
         if (warp == kStoreWarp && lane == 0) {
-          for (int b = 0; b < 2; ++b) tc::tma_store_2d(&tm_o, h * kTd + 64 * b, (int)t0, sm + kOffO + 8192 * b);
+          for (int b = 0; b < 2; ++b) tc::tma_store_2d(&tm_o, h * kTd + 64 * b, t0, sm + kOffO + 8192 * b);
           bulk_commit();
           bulk_wait_read_all();
         }
@@ -579,17 +588,17 @@ __global__ void __launch_bounds__(kTThreads, 2)
         const int first = warp == 0 ? 0 : warp - 1;
         for (int u = first * 32 + lane; u < 16 * n; u += 5 * 32) {
           const int t = u >> 4, c8 = u & 15;
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + ((t0 + t) * p.Hv + h) * kTd + 8 * c8) =
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + ((int64_t)(t0 + t) * p.Hv + h) * kTd + 8 * c8) =
               *reinterpret_cast<const uint4*>(sm + kOffO + (c8 >> 3) * 8192 + t * 128 + (((c8 & 7) ^ (t & 7)) << 4));
         }
       }
     }
     if (GATED && more && warp == kStoreWarp && lane == 0) load_z(t0 + kTc);
+    const Decay a = decay_factor((G[kTc - 1].hi + G[kTc - 1].lo) * kLn2);
     if (!mbar_wait_bounded(&sh.delta, phase, abort_flag)) failed = true;
     tc::fence_after_sync();
     if (tid == 0 && more) load_kv(t0 + kTc);
     {
-      const Decay a = gt.whole;
       const float2 f = make_float2(a.factor, a.factor), keep = make_float2(a.keep, a.keep);
       const bool spoilt = MODE == kTWhole && sh.any_bad[phase] && sh.bad[phase][j] < kTc;
 #pragma unroll

@@ -122,15 +122,14 @@ struct DecayArgs {
   const int32_t* slots;  // step: state slot of each row, or null
   int32_t num_slots;
   const int32_t* cu_seqlens;  // prefill
-  int32_t N;
-  int64_t T;
+  int32_t N, T;               // T <= 2^31 - 65
   int32_t Hk, Hv, rep, map;
   float scale, rms_eps;
 };
 
 // The segments that a prefill is cut into (decay_common.cuh)
 struct DecaySegments {
-  int64_t len;    // tokens a segment holds at most
+  int32_t len;    // tokens a segment holds at most, a multiple of 64 where there are several
   int64_t slots;  // floor(T / len) + N
   float* states;  // [slots][Hv][D][D] or null: one segment per sequence
   float* decays;  // [slots][Hv] factors of the state over a segment
@@ -198,7 +197,7 @@ bool linear_supported();
 cudaError_t launch_linear(LinearArgs p, const void* x, int64_t x_stride, const void* w, void* workspace,
                           cudaStream_t stream);
 // tokens of a segment (decay_scan.cu)
-int64_t decay_segment_len(int32_t N, int64_t T, int32_t Hv, int32_t D, int32_t dtype);
+int32_t decay_segment_len(int32_t N, int64_t T, int32_t Hv, int32_t D, int32_t dtype);
 cudaError_t launch_decay_step(const DecayArgs& p, int32_t dtype, int32_t D, int32_t batch, cudaStream_t stream);
 cudaError_t launch_decay_scan(const DecayArgs& p, const DecaySegments& sg, int32_t dtype, int32_t D,
                               cudaStream_t stream);
