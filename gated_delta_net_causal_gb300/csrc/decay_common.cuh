@@ -107,6 +107,18 @@ __device__ __forceinline__ void decay_write_row(const float* o, float* core_out,
   for (int e = 0; e < PER; ++e) out[lane * PER + e] = from_f32<T>(ov[e]);
 }
 
+// eight consecutive floats as one 32-byte access
+__device__ __forceinline__ void load8(const float* p, float4& a, float4& b) {
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w), "=f"(b.x), "=f"(b.y), "=f"(b.z), "=f"(b.w)
+               : "l"(p));
+}
+__device__ __forceinline__ void store8(float* p, float4 a, float4 b) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(a.x), "f"(a.y), "f"(a.z),
+               "f"(a.w), "f"(b.x), "f"(b.y), "f"(b.z), "f"(b.w)
+               : "memory");
+}
+
 // ------------------------------------------------------------- segments
 // The packed tokens of a call are cut into segments of at most sg.len tokens,
 // each inside one sequence. Segment i of sequence n has slot
@@ -176,6 +188,24 @@ struct DecaySlots {
     step = (int64_t)p.Hv * dd;
     decay = sg.decays + ((int64_t)s.slot * p.Hv + h);
     dstep = p.Hv;
+  }
+  // n times eight elements from `at`, for a thread that holds part of a row:
+  // whole 32-byte sectors, the loads of a segment in flight together
+  template <int N>
+  __device__ __forceinline__ void start8(int i, int parts, int at, float4 (&s)[2 * N]) const {
+    const float* first = base + (i == 0 ? (parts - 1) * step : 0) + at;
+#pragma unroll
+    for (int c = 0; c < N; ++c) load8(first + 8 * c, s[2 * c], s[2 * c + 1]);
+    for (int m = 1; m < i; ++m) {
+      const float a = decay[m * dstep];
+      float4 x[2 * N];
+#pragma unroll
+      for (int c = 0; c < N; ++c) load8(base + m * step + at + 8 * c, x[2 * c], x[2 * c + 1]);
+#pragma unroll
+      for (int c = 0; c < 2 * N; ++c)
+        s[c] = make_float4(fmaf(a, s[c].x, x[c].x), fmaf(a, s[c].y, x[c].y), fmaf(a, s[c].z, x[c].z),
+                           fmaf(a, s[c].w, x[c].w));
+    }
   }
   // the state at the start of segment i
   __device__ __forceinline__ float4 start(int i, int parts, int at) const {

@@ -187,13 +187,20 @@ cudaError_t launch_scan_t(const DecayArgs& p, const DecaySegments& sg, int32_t D
 }  // namespace
 
 // Sized for the 152 SMs of the one target, so that a workspace asked for on
-// one thread fits the call on another: enough segments for two CTAs on every
-// SM, none where the (sequence, V head) pairs fill them already.
+// one thread fits the call on another: as many segments as give every SM two
+// CTAs and no CTA a second turn ((T / len + N) Hv <= 304), none where the
+// (sequence, V head) pairs come near that by themselves. With few heads that
+// would be many short ones, and the last of them reads the states that all
+// others add: a chunk of 64 tokens costs about as much as seven such states,
+// so n chunks in segments of m cost m + n / (7 m), least at m = sqrt(n / 7).
 int32_t decay_segment_len(int32_t N, int64_t T, int32_t Hv, int32_t, int32_t) {
   constexpr int64_t kCtas = 2 * 152;
-  if ((int64_t)N * Hv >= kCtas) return (int32_t)T + 1;
-  const int64_t len = (T * Hv / kCtas + 63) / 64 * 64;  // below T + 64
-  return len < 64 ? 64 : (int32_t)len;
+  const int64_t more = kCtas / Hv - N;  // segments beyond one for each sequence
+  if (more < 1 || T <= 64) return (int32_t)T + 1;
+  int64_t len = ((T + more - 1) / more + 63) / 64 * 64;  // below T + 64
+  const int64_t n = (T + 63) / 64;
+  while (7 * (len / 64) * (len / 64) < n) len += 64;
+  return (int32_t)len;
 }
 
 cudaError_t launch_decay_scan(const DecayArgs& p, const DecaySegments& sg, int32_t dtype, int32_t D,

@@ -59,6 +59,9 @@ constexpr uint32_t kOffV = 65536;
 constexpr uint32_t kOffO = 81920;    // z, then the outputs in its place
 constexpr uint32_t kOffP = 98304;    // P [64 t][64 s] SW128, with core_out its low part behind it
 constexpr uint32_t kTile16 = 16384;
+// the first pass has no q, P or outputs: their place is a second stage of K and V
+__device__ __forceinline__ uint32_t k_at(int stage) { return stage ? kOffO : kOffK; }
+__device__ __forceinline__ uint32_t v_at(int stage) { return stage ? kOffQ : kOffV; }
 constexpr uint32_t tc_smem(bool core) { return kOffP + (core ? 16384 : 8192); }
 
 // TMEM columns
@@ -164,7 +167,7 @@ struct TcShared {
   int any_bad[2];
   int abort;
   uint32_t tmem;
-  uint64_t load_q, load_kv, load_z, scores, outs, delta;  // mbarriers
+  uint64_t load_q, load_kv[2], load_z, scores, outs, delta;  // mbarriers
 };
 
 template <int MODE, bool CORE, bool GATED>
@@ -191,7 +194,8 @@ __global__ void __launch_bounds__(kTThreads, 2)
   }
   if (tid == 0) {
     mbar_init(&sh.load_q, 1);
-    mbar_init(&sh.load_kv, 1);
+    mbar_init(&sh.load_kv[0], 1);
+    mbar_init(&sh.load_kv[1], 1);
     mbar_init(&sh.load_z, 1);
     mbar_init(&sh.scores, 1);
     mbar_init(&sh.outs, 2);  // O1 and O2
@@ -211,18 +215,28 @@ __global__ void __launch_bounds__(kTThreads, 2)
     const DecaySlots ws(p, sg, s, h, kTd * kTd);
     float* keep = sg.states + ((int64_t)(s.slot + s.parts - 1) * p.Hv + h) * (kTd * kTd);
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < 2; ++c) {
+      float4 x[8];
       if (MODE == kTLocal) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (s.index == 0) {
-          x = *reinterpret_cast<const float4*>(gS + at0 + 4 * c);
-          *reinterpret_cast<float4*>(keep + at0 + 4 * c) = x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) load8(gS + at0 + 32 * c + 8 * e, x[2 * e], x[2 * e + 1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) store8(keep + at0 + 32 * c + 8 * e, x[2 * e], x[2 * e + 1]);
         }
+      } else if (s.parts == 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) load8(gS + at0 + 32 * c + 8 * e, x[2 * e], x[2 * e + 1]);
       } else {
-        x = s.parts == 1 ? *reinterpret_cast<const float4*>(gS + at0 + 4 * c) : ws.start(s.index, s.parts, at0 + 4 * c);
+        ws.start8<4>(s.index, s.parts, at0 + 32 * c, x);
       }
-      S[2 * c] = make_float2(x.x, x.y);
-      S[2 * c + 1] = make_float2(x.z, x.w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        S[16 * c + 2 * e] = make_float2(x[e].x, x[e].y);
+        S[16 * c + 2 * e + 1] = make_float2(x[e].z, x[e].w);
+      }
     }
   }
   tc::fence_before_sync();
@@ -255,12 +269,12 @@ __global__ void __launch_bounds__(kTThreads, 2)
     mbar_arrive_expect_tx(&sh.load_q, kTile16);
     for (int b = 0; b < 2; ++b) tc::tma_load_2d(sm + kOffQ + 8192 * b, &tm_q, kh * kTd + 64 * b, t0, &sh.load_q);
   };
-  auto load_kv = [&](int t0) {
+  auto load_kv = [&](int t0, int stage) {
     ++kv_loads;
-    mbar_arrive_expect_tx(&sh.load_kv, 2 * kTile16);
+    mbar_arrive_expect_tx(&sh.load_kv[stage], 2 * kTile16);
     for (int b = 0; b < 2; ++b) {
-      tc::tma_load_2d(sm + kOffK + 8192 * b, &tm_k, kh * kTd + 64 * b, t0, &sh.load_kv);
-      tc::tma_load_2d(sm + kOffV + 8192 * b, &tm_v, h * kTd + 64 * b, t0, &sh.load_kv);
+      tc::tma_load_2d(sm + k_at(stage) + 8192 * b, &tm_k, kh * kTd + 64 * b, t0, &sh.load_kv[stage]);
+      tc::tma_load_2d(sm + v_at(stage) + 8192 * b, &tm_v, h * kTd + 64 * b, t0, &sh.load_kv[stage]);
     }
   };
   auto load_z = [&](int t0) {
@@ -295,7 +309,8 @@ __global__ void __launch_bounds__(kTThreads, 2)
   const auto tokens = [&](int t0) { return s.end - t0 < kTc ? s.end - t0 : kTc; };
 
   if (tid == 0) {
-    load_kv(s.begin);
+    load_kv(s.begin, 0);
+    if (MODE == kTLocal && s.begin + kTc < s.end) load_kv(s.begin + kTc, 1);
     if (MODE == kTWhole) load_q(s.begin);
   }
   if (GATED && warp == kStoreWarp && lane == 0) load_z(s.begin);
@@ -312,28 +327,31 @@ __global__ void __launch_bounds__(kTThreads, 2)
   }
   const uint64_t dQ = tc::sdesc_sw128(smem_u32(sm + kOffQ)), dK = tc::sdesc_sw128(smem_u32(sm + kOffK));
   const uint64_t dP = tc::sdesc_sw128(smem_u32(sm + kOffP));
-  const uint64_t dV = sdesc_mn128(smem_u32(sm + kOffV)), dKp = sdesc_mn128(smem_u32(sm + kOffK));
+  const uint64_t dMid = sdesc_mn128(smem_u32(sm + kOffMid));
   bool failed = false;
-  uint32_t phase = 0;
+  uint32_t phase = 0, round = 0;  // parities of the chunk and, in the first pass, of its stage
   // #1: the state operand is in TMEM, the gates in shared memory
   tc::fence_before_sync();
   __syncthreads();
 
-  for (int t0 = s.begin; t0 < s.end; t0 += kTc, phase ^= 1) {
+  for (int t0 = s.begin; t0 < s.end; t0 += kTc, phase ^= 1, round ^= phase ^ 1) {
     const int n = tokens(t0);
     const bool more = t0 + kTc < s.end;
     const Two* G = sh.G[phase];
+    const int stage = MODE == kTLocal ? (int)phase : 0;
+    unsigned char *kt = sm + k_at(stage), *vt = sm + v_at(stage);
+    const uint64_t dV = sdesc_mn128(smem_u32(vt));
     // the buffers are single: the next chunk's tiles come into L2 meanwhile, so
     // that its loads, issued late in this chunk, are short
-    if (warp == 7 && lane == 0 && more) {
+    if (MODE == kTWhole && warp == 7 && lane == 0 && more) {
       for (int b = 0; b < 2; ++b) {
         tc::tma_prefetch_2d(&tm_k, kh * kTd + 64 * b, t0 + kTc);
         tc::tma_prefetch_2d(&tm_v, h * kTd + 64 * b, t0 + kTc);
-        if (MODE == kTWhole) tc::tma_prefetch_2d(&tm_q, kh * kTd + 64 * b, t0 + kTc);
+        tc::tma_prefetch_2d(&tm_q, kh * kTd + 64 * b, t0 + kTc);
         if (GATED) tc::tma_prefetch_2d(&tm_z, h * kTd + 64 * b, t0 + kTc);
       }
     }
-    if (!mbar_wait_bounded(&sh.load_kv, phase, abort_flag)) failed = true;
+    if (!mbar_wait_bounded(&sh.load_kv[stage], MODE == kTLocal ? round : phase, abort_flag)) failed = true;
     if (MODE == kTWhole) {
       if (!mbar_wait_bounded(&sh.load_q, phase, abort_flag)) failed = true;
       if (warp == 0) {
@@ -368,7 +386,7 @@ __global__ void __launch_bounds__(kTThreads, 2)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int u = tid + i * kTThreads, row = u >> 4, c16 = u & 15;
-        uint4* at = reinterpret_cast<uint4*>(sm + kOffV + (c16 >> 3) * 8192 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4));
+        uint4* at = reinterpret_cast<uint4*>(vt + (c16 >> 3) * 8192 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4));
         uint4 x = *at;
         uint32_t* w = &x.x;
         uint32_t hit = 0;  // an exponent of all ones carries into the sign's place
@@ -442,7 +460,7 @@ __global__ void __launch_bounds__(kTThreads, 2)
     for (int i = 0; i < 4; ++i) {
       const int u = tid + i * kTThreads, row = u >> 4, c16 = u & 15;
       const uint32_t off = (c16 >> 3) * 8192 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4);
-      uint4 x = *reinterpret_cast<const uint4*>(sm + kOffK + off);
+      uint4 x = *reinterpret_cast<const uint4*>(kt + off);
       if (row >= n) x = make_uint4(0, 0, 0, 0);  // another sequence's: may be a NaN
       const uint32_t* w = &x.x;
       const float d = sh.dk[row];
@@ -454,7 +472,7 @@ __global__ void __launch_bounds__(kTThreads, 2)
         (&part[1].x)[e] = split2(a);
         (&part[2].x)[e] = pack2(a);
       }
-      *reinterpret_cast<uint4*>(sm + kOffK + off) = part[0];
+      *reinterpret_cast<uint4*>(kt + off) = part[0];
       *reinterpret_cast<uint4*>(sm + kOffMid + off) = part[1];
       *reinterpret_cast<uint4*>(sm + kOffLo + off) = part[2];
     }
@@ -564,10 +582,11 @@ __global__ void __launch_bounds__(kTThreads, 2)
     if (warp == kDeltaWarp) {
       tc::fence_after_sync();
       const uint32_t id = tc::idesc(tc::kBF16, 128, 128) | kTransA | kTransB;
+      const uint64_t dK0 = sdesc_mn128(smem_u32(kt));
 #pragma unroll 1
       for (int k = 0; k < 12; ++k)
-        tc::mma_f16_elect(tb + kColX, dV + ((k & 3) * 2048 >> 4), dKp + (((k >> 2) * kTile16 + (k & 3) * 2048) >> 4), id,
-                          k > 0);
+        tc::mma_f16_elect(tb + kColX, dV + ((k & 3) * 2048 >> 4),
+                          (k < 4 ? dK0 : dMid + (k < 8 ? 0 : kTile16 >> 4)) + ((k & 3) * 2048 >> 4), id, k > 0);
       tc::mma_commit_elect(&sh.delta);
     } else if (warp == kGateWarp) {
       if (more) {
@@ -597,7 +616,7 @@ __global__ void __launch_bounds__(kTThreads, 2)
     const Decay a = decay_factor((G[kTc - 1].hi + G[kTc - 1].lo) * kLn2);
     if (!mbar_wait_bounded(&sh.delta, phase, abort_flag)) failed = true;
     tc::fence_after_sync();
-    if (tid == 0 && more) load_kv(t0 + kTc);
+    if (tid == 0 && (MODE == kTLocal ? t0 + 2 * kTc < s.end : more)) load_kv(t0 + (MODE == kTLocal ? 2 : 1) * kTc, stage);
     {
       const float2 f = make_float2(a.factor, a.factor), keep = make_float2(a.keep, a.keep);
       const bool spoilt = MODE == kTWhole && sh.any_bad[phase] && sh.bad[phase][j] < kTc;
@@ -631,16 +650,21 @@ __global__ void __launch_bounds__(kTThreads, 2)
     if (MODE == kTLocal || s.index + 1 == s.parts) {
       float* to = MODE == kTLocal ? sg.states + (int64_t)blockIdx.x * (kTd * kTd) : gS;
 #pragma unroll
-      for (int c = 0; c < 16; ++c)
-        *reinterpret_cast<float4*>(to + at0 + 4 * c) =
-            make_float4(S[2 * c].x, S[2 * c].y, S[2 * c + 1].x, S[2 * c + 1].y);
+      for (int c = 0; c < 8; ++c)
+        store8(to + at0 + 8 * c, make_float4(S[4 * c].x, S[4 * c].y, S[4 * c + 1].x, S[4 * c + 1].y),
+               make_float4(S[4 * c + 2].x, S[4 * c + 2].y, S[4 * c + 3].x, S[4 * c + 3].y));
     }
     if (MODE == kTLocal && warp == 1 && lane == 0) sg.decays[blockIdx.x] = exp2f(total.hi + total.lo);
   }
   // no load may still be in flight when the CTA ends: after a wait that gave
   // up the next chunk's may be
   if (tid == 0) {
-    mbar_wait(&sh.load_kv, (kv_loads - 1) & 1);
+    if (MODE == kTLocal) {  // load i goes to stage i % 2
+      mbar_wait(&sh.load_kv[0], ((kv_loads + 1) / 2 - 1) & 1);
+      if (kv_loads > 1) mbar_wait(&sh.load_kv[1], (kv_loads / 2 - 1) & 1);
+    } else {
+      mbar_wait(&sh.load_kv[0], (kv_loads - 1) & 1);
+    }
     if (MODE == kTWhole) mbar_wait(&sh.load_q, (q_loads - 1) & 1);
   }
   if (MODE == kTWhole && warp == kStoreWarp && lane == 0) {
@@ -657,8 +681,9 @@ __global__ void __launch_bounds__(kTThreads, 2)
 
 }  // namespace
 
-bool decay_tc_supported(const DecayArgs&, int32_t dtype, int32_t D) {
-  return dtype == GDN_BF16 && D == kTd && tc::encode_fn() != nullptr;
+bool decay_tc_supported(const DecayArgs& p, int32_t dtype, int32_t D) {
+  // states are read and written in 32-byte accesses
+  return dtype == GDN_BF16 && D == kTd && reinterpret_cast<uintptr_t>(p.state) % 32 == 0 && tc::encode_fn() != nullptr;
 }
 
 cudaError_t launch_decay_tc(const DecayArgs& p, const DecaySegments& sg, cudaStream_t stream) {
