@@ -10,7 +10,17 @@
 // split over a cluster whose CTAs add their fp32 tiles in rank order over
 // distributed shared memory, so the result does not depend on which ran
 // first. K past the end of a row reads as zeros.
+//
+// linear_fp8_tile_kernel: 128 x 256 tiles for prompts. An MMA of N = 256
+// keeps the tensor pipe as long as its 8192 multiply-adds a cycle need (one
+// of N = 64 holds it more than twice as long as its work), so these tiles
+// reach the pipe's rate and read 12 KB of shared memory in 124 cycles.
+// Persistent: one CTA per SM, warp 0 loads, warp 1 issues the MMAs, four
+// warps scale and store the previous tile out of the other half of TMEM,
+// through swizzled shared memory and TMA, which also clips the edges.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
@@ -192,6 +202,167 @@ __global__ void __launch_bounds__(kFThreads, 2)
   }
 }
 
+constexpr int kTN = 256;        // output features of a tile
+constexpr int kTStages = 4;
+constexpr uint32_t kTX = kFM * kFK, kTW = kTN * kFK, kTStage = kTX + kTW;
+constexpr int kTThreads = 192;  // loads, MMAs, four epilogue warps
+constexpr uint32_t kTOut = 4096;  // one staged block: 32 rows of 128 bytes
+constexpr uint32_t kTileSmem = kTStages * kTStage + 4 * kTOut;
+
+template <typename T>
+__global__ void __launch_bounds__(kTThreads, 1)
+    linear_fp8_tile_kernel(const LinearFp8Args p, const __grid_constant__ CUtensorMap tm_x,
+                           const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_y) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ __align__(8) uint64_t full[kTStages], empty[kTStages], acc_full[2], acc_empty[2];
+  __shared__ __align__(16) float s_scale[2][kTN], s_bias[2][kTN];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nk = (p.K + kFK - 1) / kFK;
+  const int m_tiles = (int)((p.M + kFM - 1) / kFM), n_tiles = (p.N + kTN - 1) / kTN;
+  const int tiles = m_tiles * n_tiles;
+
+  if (warp == 0) {
+    tc::tmem_alloc(&s_tmem, 2 * kTN);
+    tc::tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int s = 0; s < kTStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_empty[a], 4);
+    }
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tb = s_tmem;
+  volatile int* abort_flag = &s_abort;
+  uint32_t loads = 0;
+
+  // the row tiles of a column tile run side by side: its rows of w are read
+  // once from memory, x stays in L2
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int m0 = (tile % m_tiles) * kFM, n0 = (tile / m_tiles) * kTN;
+        for (int k = 0; k < nk; ++k, ++loads) {
+          const int s = loads % kTStages;
+          if (loads >= kTStages && !mbar_wait_bounded(&empty[s], (loads / kTStages - 1) & 1, abort_flag)) goto loaded;
+          mbar_arrive_expect_tx(&full[s], kTStage);
+          tc::tma_load_2d(sm + s * kTStage, &tm_x, k * kFK, m0, &full[s]);
+          tc::tma_load_2d(sm + s * kTStage + kTX, &tm_w, k * kFK, n0, &full[s]);
+        }
+      }
+    }
+  loaded:
+    __syncwarp();
+  } else if (warp == 1) {
+    const uint32_t id = tc::idesc(tc::kE4M3, kFM, kTN);
+    const uint64_t d0 = tc::sdesc_sw128(smem_u32(sm));
+    uint32_t i = 0;
+    int n = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++n) {
+      const int a = n & 1;
+      if (n >= 2) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_empty[a], (n / 2 - 1) & 1, abort_flag));
+      if (!ok) break;
+      for (int k = 0; k < nk; ++k, ++i) {
+        const int s = i % kTStages;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[s], (i / kTStages) & 1, abort_flag));
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint64_t dx = d0 + (uint64_t)((s * kTStage) >> 4), dw = dx + (uint64_t)(kTX >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kFK / 32; ++ks)
+          tc::mma_f8_elect(tb + a * kTN, tc::sdesc_at(dx, kFM, ks), tc::sdesc_at(dw, kTN, ks), id, k > 0 || ks > 0);
+        tc::mma_commit_elect(&empty[s]);
+      }
+      tc::mma_commit_elect(&acc_full[a]);
+    }
+  } else {
+    const int qd = warp & 3;  // TMEM lane quadrant
+    constexpr int kCols = 128 / (int)sizeof(T);  // columns of a staged block
+    unsigned char* at = sm + kTStages * kTStage + (warp - 2) * kTOut;
+    int n = 0;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++n) {
+      const int a = n & 1;
+      const int64_t m0 = (int64_t)(tile % m_tiles) * kFM;
+      const int n0 = (tile / m_tiles) * kTN;
+      // this tile's scales and bias; the buffers are two tiles apart in use
+      for (int c = tid - 64; c < kTN; c += 128) {
+        const bool in = n0 + c < p.N;
+        s_scale[a][c] = in ? __ldg(p.w_scale + n0 + c) : 0.f;
+        s_bias[a][c] = in && p.bias != nullptr ? __ldg(p.bias + n0 + c) : 0.f;
+      }
+      const int64_t m = m0 + 32 * qd + lane;
+      const float xs = m < p.M ? __ldg(p.x_scale + m) : 0.f;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      // after a wait that gave up the warps still meet at the barrier above
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[a], (n / 2) & 1, abort_flag))) continue;
+      tc::fence_after_sync();
+      const uint32_t tq = tb + ((uint32_t)(32 * qd) << 16) + a * kTN;
+      for (int c0 = 0; c0 < kTN; c0 += kCols) {
+        float v[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16) tc::tmem_ld16(tq + c0 + c, *reinterpret_cast<float(*)[16]>(v + c));
+        tc::tmem_wait_ld();
+        if (c0 + kCols == kTN) {  // the accumulator is read
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[a]);
+        }
+        if (n0 + c0 >= p.N || m0 + 32 * qd >= p.M) continue;
+#pragma unroll
+        for (int c = 0; c < kCols; c += 4) {
+          const float4 ws = *reinterpret_cast<const float4*>(&s_scale[a][c0 + c]);
+          const float4 b = *reinterpret_cast<const float4*>(&s_bias[a][c0 + c]);
+          v[c] = fmaf(v[c] * xs, ws.x, b.x);
+          v[c + 1] = fmaf(v[c + 1] * xs, ws.y, b.y);
+          v[c + 2] = fmaf(v[c + 2] * xs, ws.z, b.z);
+          v[c + 3] = fmaf(v[c + 3] * xs, ws.w, b.w);
+        }
+        if (lane == 0) bulk_wait_read_all();  // the last block's store has read the buffer
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          alignas(16) T x[16 / sizeof(T)];
+#pragma unroll
+          for (int i = 0; i < 16 / (int)sizeof(T); ++i) x[i] = from_f32<T>(v[c * (16 / sizeof(T)) + i]);
+          *reinterpret_cast<uint4*>(at + lane * 128 + ((c ^ (lane & 7)) << 4)) = *reinterpret_cast<const uint4*>(x);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tc::tma_store_2d(&tm_y, n0 + c0, (int)m0 + 32 * qd, at);
+          bulk_commit();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+
+  // no load or MMA may be in flight when the CTA ends
+  tc::fence_before_sync();
+  __syncthreads();
+  if (tid == 0) {
+    for (uint32_t s = 0; s < (uint32_t)kTStages && s < loads; ++s)
+      mbar_wait(&full[s], ((loads - s + kTStages - 1) / kTStages - 1) & 1);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tb, 2 * kTN);
+  }
+}
+
 int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -241,14 +412,46 @@ cudaError_t launch_band(const LinearFp8Args& p, const void* x, int64_t x_stride,
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <typename T>
+cudaError_t launch_tile(const LinearFp8Args& p, const void* x, int64_t x_stride, const void* w, cudaStream_t stream) {
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const CUtensorMapDataType yt = sizeof(T) == 4                            ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                 : std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap mx, mw, my;
+  if (!tc::make_map_2d(&mx, x, p.M, p.K, x_stride, 1, u8, kFK, kFM, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+      !tc::make_map_2d(&mw, w, p.N, p.K, p.K, 1, u8, kFK, kTN, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+      !tc::make_map_2d(&my, p.y, p.M, p.N, p.y_stride, sizeof(T), yt, 128 / sizeof(T), 32, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  auto kern = linear_fp8_tile_kernel<T>;
+  constexpr int smem = (int)kTileSmem + 1024;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (p.M + kFM - 1) / kFM * ((p.N + kTN - 1) / kTN);
+  const int sms = sm_count();
+  kern<<<(unsigned)(tiles < sms ? tiles : sms), kTThreads, smem, stream>>>(p, mx, mw, my);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_t(const LinearFp8Args& p, const void* x, int64_t x_stride, const void* w, cudaStream_t stream) {
+  // tiles from where they keep half the SMs busy; below, and for one row tile
+  // (a stream of w), bands and K splits give more CTAs
+  const int64_t tiles = (p.M + kFM - 1) / kFM * ((p.N + kTN - 1) / kTN);
+  if (p.M > kFM && 2 * tiles >= sm_count() && tiles <= INT32_MAX / 2) return launch_tile<T>(p, x, x_stride, w, stream);
+  return launch_band<T>(p, x, x_stride, w, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_linear_fp8(const LinearFp8Args& p, const void* x, int64_t x_stride, const void* w,
                               int32_t out_dtype, cudaStream_t stream) {
   switch (out_dtype) {
-    case GDN_F16: return launch_band<__half>(p, x, x_stride, w, stream);
-    case GDN_BF16: return launch_band<__nv_bfloat16>(p, x, x_stride, w, stream);
-    case GDN_F32: return launch_band<float>(p, x, x_stride, w, stream);
+    case GDN_F16: return launch_t<__half>(p, x, x_stride, w, stream);
+    case GDN_BF16: return launch_t<__nv_bfloat16>(p, x, x_stride, w, stream);
+    case GDN_F32: return launch_t<float>(p, x, x_stride, w, stream);
     default: return cudaErrorInvalidValue;
   }
 }
