@@ -11,13 +11,16 @@
 // distributed shared memory, so the result does not depend on which ran
 // first. K past the end of a row reads as zeros.
 //
-// linear_fp8_tile_kernel: 128 x 256 tiles for prompts. An MMA of N = 256
-// keeps the tensor pipe as long as its 8192 multiply-adds a cycle need (one
-// of N = 64 holds it more than twice as long as its work), so these tiles
-// reach the pipe's rate and read 12 KB of shared memory in 124 cycles.
-// Persistent: one CTA per SM, warp 0 loads, warp 1 issues the MMAs, four
-// warps scale and store the previous tile out of the other half of TMEM,
-// through swizzled shared memory and TMA, which also clips the edges.
+// linear_fp8_tile_kernel: 256 x 256 tiles for prompts, each on a pair of CTAs
+// (cta_group::2). An MMA of N = 256 holds the tensor pipe as long as its work
+// takes (one of N = 64 more than twice as long), about 124 cycles a K step of
+// 32. What it reads then counts: a CTA alone with 128 x 256 tiles writes and
+// reads 24 KB of shared memory in that time, more than the 128 bytes a cycle
+// there are (measured 81 us at 4096 x 12352 x 2048); the pair keeps half of w
+// in either CTA, 16 KB. Persistent: warp 0 loads, warp 1 of the first CTA
+// issues the MMAs, four warps of each scale and store the previous tile's 128
+// rows out of the other half of TMEM, through swizzled shared memory and TMA,
+// which also clips the edges.
 #include <cuda.h>
 
 #include <type_traits>
@@ -203,8 +206,9 @@ __global__ void __launch_bounds__(kFThreads, 2)
 }
 
 constexpr int kTN = 256;        // output features of a tile
-constexpr int kTStages = 4;
-constexpr uint32_t kTX = kFM * kFK, kTW = kTN * kFK, kTStage = kTX + kTW;
+constexpr int kTM = 256;        // rows of a tile, half in either CTA
+constexpr int kTStages = 6;
+constexpr uint32_t kTX = kFM * kFK, kTW = kTN / 2 * kFK, kTStage = kTX + kTW;  // of one CTA
 constexpr int kTThreads = 192;  // loads, MMAs, four epilogue warps
 constexpr uint32_t kTOut = 4096;  // one staged block: 32 rows of 128 bytes
 constexpr uint32_t kTileSmem = kTStages * kTStage + 4 * kTOut;
@@ -221,13 +225,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nk = (p.K + kFK - 1) / kFK;
-  const int m_tiles = (int)((p.M + kFM - 1) / kFM), n_tiles = (p.N + kTN - 1) / kTN;
+  const int m_tiles = (int)((p.M + kTM - 1) / kTM), n_tiles = (p.N + kTN - 1) / kTN;
   const int tiles = m_tiles * n_tiles;
+  const int rank = (int)cluster_ctarank(), pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
-  if (warp == 0) {
-    tc::tmem_alloc(&s_tmem, 2 * kTN);
-    tc::tmem_relinquish();
-  }
+  if (warp == 0) tc::tmem_alloc_pair(&s_tmem, 2 * kTN);
   if (tid == 0) {
     for (int s = 0; s < kTStages; ++s) {
       mbar_init(&full[s], 1);
@@ -235,13 +237,16 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&acc_full[a], 1);
-      mbar_init(&acc_empty[a], 4);
+      mbar_init(&acc_empty[a], 8);  // the epilogue warps of both CTAs
     }
     s_abort = 0;
     fence_mbar_init();
   }
   tc::fence_before_sync();
   __syncthreads();
+  // both CTAs' barriers and TMEM are there before either is used by the other
+  cluster_arrive_release();
+  cluster_wait_acquire();
   tc::fence_after_sync();
   const uint32_t tb = s_tmem;
   volatile int* abort_flag = &s_abort;
@@ -251,26 +256,28 @@ __global__ void __launch_bounds__(kTThreads, 1)
   // once from memory, x stays in L2
   if (warp == 0) {
     if (lane == 0) {
-      for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int m0 = (tile % m_tiles) * kFM, n0 = (tile / m_tiles) * kTN;
+      for (int tile = pair; tile < tiles; tile += pairs) {
+        const int m0 = (tile % m_tiles) * kTM + rank * kFM, n0 = (tile / m_tiles) * kTN + rank * (kTN / 2);
         for (int k = 0; k < nk; ++k, ++loads) {
           const int s = loads % kTStages;
           if (loads >= kTStages && !mbar_wait_bounded(&empty[s], (loads / kTStages - 1) & 1, abort_flag)) goto loaded;
-          mbar_arrive_expect_tx(&full[s], kTStage);
-          tc::tma_load_2d(sm + s * kTStage, &tm_x, k * kFK, m0, &full[s]);
-          tc::tma_load_2d(sm + s * kTStage + kTX, &tm_w, k * kFK, n0, &full[s]);
+          // both CTAs' loads complete on the first one's barrier
+          const uint32_t bar = map_shared_rank(smem_u32(&full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kTStage);
+          tc::tma_load_2d_pair(sm + s * kTStage, &tm_x, k * kFK, m0, bar);
+          tc::tma_load_2d_pair(sm + s * kTStage + kTX, &tm_w, k * kFK, n0, bar);
         }
       }
     }
   loaded:
     __syncwarp();
-  } else if (warp == 1) {
-    const uint32_t id = tc::idesc(tc::kE4M3, kFM, kTN);
+  } else if (warp == 1 && rank == 0) {
+    const uint32_t id = tc::idesc(tc::kE4M3, kTM, kTN);
     const uint64_t d0 = tc::sdesc_sw128(smem_u32(sm));
     uint32_t i = 0;
     int n = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++n) {
+    for (int tile = pair; ok && tile < tiles; tile += pairs, ++n) {
       const int a = n & 1;
       if (n >= 2) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_empty[a], (n / 2 - 1) & 1, abort_flag));
       if (!ok) break;
@@ -282,19 +289,19 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const uint64_t dx = d0 + (uint64_t)((s * kTStage) >> 4), dw = dx + (uint64_t)(kTX >> 4);
 #pragma unroll
         for (int ks = 0; ks < kFK / 32; ++ks)
-          tc::mma_f8_elect(tb + a * kTN, tc::sdesc_at(dx, kFM, ks), tc::sdesc_at(dw, kTN, ks), id, k > 0 || ks > 0);
-        tc::mma_commit_elect(&empty[s]);
+          tc::mma_f8_pair_elect(tb + a * kTN, tc::sdesc_at(dx, kFM, ks), tc::sdesc_at(dw, kTN / 2, ks), id, k > 0 || ks > 0);
+        tc::mma_commit_pair_elect(&empty[s]);
       }
-      tc::mma_commit_elect(&acc_full[a]);
+      tc::mma_commit_pair_elect(&acc_full[a]);
     }
-  } else {
+  } else if (warp >= 2) {
     const int qd = warp & 3;  // TMEM lane quadrant
     constexpr int kCols = 128 / (int)sizeof(T);  // columns of a staged block
     unsigned char* at = sm + kTStages * kTStage + (warp - 2) * kTOut;
     int n = 0;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++n) {
+    for (int tile = pair; tile < tiles; tile += pairs, ++n) {
       const int a = n & 1;
-      const int64_t m0 = (int64_t)(tile % m_tiles) * kFM;
+      const int64_t m0 = (int64_t)(tile % m_tiles) * kTM + rank * kFM;
       const int n0 = (tile / m_tiles) * kTN;
       // this tile's scales and bias; the buffers are two tiles apart in use
       for (int c = tid - 64; c < kTN; c += 128) {
@@ -317,7 +324,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (c0 + kCols == kTN) {  // the accumulator is read
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[a]);
+          if (lane == 0) mbar_arrive_cluster(map_shared_rank(smem_u32(&acc_empty[a]), 0));
         }
         if (n0 + c0 >= p.N || m0 + 32 * qd >= p.M) continue;
 #pragma unroll
@@ -349,17 +356,23 @@ __global__ void __launch_bounds__(kTThreads, 1)
     if (lane == 0) bulk_wait_all();
   }
 
-  // no load or MMA may be in flight when the CTA ends
+  // no load or MMA may be in flight, and nothing of the other CTA under way to
+  // this one, when the CTA ends: the last loads into each stage, then the pair
   tc::fence_before_sync();
   __syncthreads();
   if (tid == 0) {
-    for (uint32_t s = 0; s < (uint32_t)kTStages && s < loads; ++s)
-      mbar_wait(&full[s], ((loads - s + kTStages - 1) / kTStages - 1) & 1);
+    for (uint32_t s = 0; s < (uint32_t)kTStages && s < loads; ++s) {
+      const uint32_t last = ((loads - s + kTStages - 1) / kTStages - 1) & 1;
+      if (rank == 0) mbar_wait(&full[s], last);
+      mbar_wait_bounded(&empty[s], last, abort_flag);
+    }
   }
   __syncthreads();
+  cluster_arrive_release();
+  cluster_wait_acquire();
   if (warp == 0) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tb, 2 * kTN);
+    tc::tmem_dealloc_pair(tb, 2 * kTN);
   }
 }
 
@@ -421,7 +434,7 @@ cudaError_t launch_tile(const LinearFp8Args& p, const void* x, int64_t x_stride,
   CUtensorMap mx, mw, my;
   if (!tc::make_map_2d(&mx, x, p.M, p.K, x_stride, 1, u8, kFK, kFM, CU_TENSOR_MAP_SWIZZLE_128B,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
-      !tc::make_map_2d(&mw, w, p.N, p.K, p.K, 1, u8, kFK, kTN, CU_TENSOR_MAP_SWIZZLE_128B,
+      !tc::make_map_2d(&mw, w, p.N, p.K, p.K, 1, u8, kFK, kTN / 2, CU_TENSOR_MAP_SWIZZLE_128B,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
       !tc::make_map_2d(&my, p.y, p.M, p.N, p.y_stride, sizeof(T), yt, 128 / sizeof(T), 32, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
@@ -429,18 +442,29 @@ cudaError_t launch_tile(const LinearFp8Args& p, const void* x, int64_t x_stride,
   constexpr int smem = (int)kTileSmem + 1024;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (p.M + kFM - 1) / kFM * ((p.N + kTN - 1) / kTN);
-  const int sms = sm_count();
-  kern<<<(unsigned)(tiles < sms ? tiles : sms), kTThreads, smem, stream>>>(p, mx, mw, my);
-  return cudaGetLastError();
+  const int64_t tiles = (p.M + kTM - 1) / kTM * ((p.N + kTN - 1) / kTN);
+  const int pairs = sm_count() / 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs));
+  cfg.blockDim = dim3(kTThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t r = cudaLaunchKernelEx(&cfg, kern, p, mx, mw, my);
+  return r != cudaSuccess ? r : cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_t(const LinearFp8Args& p, const void* x, int64_t x_stride, const void* w, cudaStream_t stream) {
   // tiles from where they keep half the SMs busy; below, and for one row tile
   // (a stream of w), bands and K splits give more CTAs
-  const int64_t tiles = (p.M + kFM - 1) / kFM * ((p.N + kTN - 1) / kTN);
-  if (p.M > kFM && 2 * tiles >= sm_count() && tiles <= INT32_MAX / 2) return launch_tile<T>(p, x, x_stride, w, stream);
+  const int64_t tiles = (p.M + kTM - 1) / kTM * ((p.N + kTN - 1) / kTN);
+  if (p.M > kFM && 4 * tiles >= sm_count() && tiles <= INT32_MAX / 2) return launch_tile<T>(p, x, x_stride, w, stream);
   return launch_band<T>(p, x, x_stride, w, stream);
 }
 
