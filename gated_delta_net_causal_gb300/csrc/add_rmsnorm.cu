@@ -52,42 +52,56 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) add_rmsnorm_kernel(const 
   const int nvec = (int)(p.cols / VEC);
 
   float ss = 0.f, top = 0.f;
-  // t = s w of vector i; the first time its squares and maximum too, and s is
-  // stored (the second time it is read back: sum may be the residual itself)
-  auto take = [&](int i, float (&t)[VEC], bool again) {
-    const P a = *reinterpret_cast<const P*>((again && sum != nullptr ? sum : x) + (int64_t)i * VEC);
-    float s[VEC];
-    if (r != nullptr && !(again && sum != nullptr)) {
-      const P b = *reinterpret_cast<const P*>(r + (int64_t)i * VEC);
-      P c;
+  // s = x (+ residual) of vector i, stored; read back the second time (sum may
+  // be the residual itself)
+  auto load = [&](int i, P& a, P& b, bool again) {
+    const bool stored = again && sum != nullptr;
+    a = *reinterpret_cast<const P*>((stored ? sum : x) + (int64_t)i * VEC);
+    if (r != nullptr && !stored) b = *reinterpret_cast<const P*>(r + (int64_t)i * VEC);
+  };
+  // t = s w, and the first time its squares and maximum
+  auto take = [&](int i, const P& a, const P& b, float (&t)[VEC], bool again) {
+    P c = a;
+    if (r != nullptr && !(again && sum != nullptr))
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        c.v[e] = from_f32<T>(to_f32(a.v[e]) + to_f32(b.v[e]));
-        s[e] = to_f32(c.v[e]);
-      }
-      if (sum != nullptr && !again) *reinterpret_cast<P*>(sum + (int64_t)i * VEC) = c;
+      for (int e = 0; e < VEC; ++e) c.v[e] = from_f32<T>(to_f32(a.v[e]) + to_f32(b.v[e]));
+    if (sum != nullptr && !again) *reinterpret_cast<P*>(sum + (int64_t)i * VEC) = c;
+    alignas(16) float w[VEC];
+    if (p.norm_w == nullptr) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) w[e] = 1.f;
+    } else if constexpr (VEC % 4 == 0) {
+#pragma unroll
+      for (int e = 0; e < VEC; e += 4)
+        *reinterpret_cast<float4*>(w + e) = __ldg(reinterpret_cast<const float4*>(p.norm_w + (int64_t)i * VEC + e));
     } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) s[e] = to_f32(a.v[e]);
-      if (sum != nullptr && !again) *reinterpret_cast<P*>(sum + (int64_t)i * VEC) = a;
+      w[0] = __ldg(p.norm_w + i);
     }
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      if (!again) ss = fmaf(s[e], s[e], ss);
-      t[e] = p.norm_w == nullptr ? s[e] : s[e] * __ldg(p.norm_w + (int64_t)i * VEC + e);
+      const float s = to_f32(c.v[e]);
+      if (!again) ss = fmaf(s, s, ss);
+      t[e] = s * w[e];
       if (!again) top = fmaxf(top, fabsf(t[e]));
     }
   };
+  // all of the row's loads before the first store, which they might not pass
   float t[NV][VEC];
+  {
+    P a[NV], b[NV];
 #pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    const int i = tid + n * NT;
-    if (i < nvec) take(i, t[n], false);
+    for (int n = 0; n < NV; ++n)
+      if (tid + n * NT < nvec) load(tid + n * NT, a[n], b[n], false);
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+      if (tid + n * NT < nvec) take(tid + n * NT, a[n], b[n], t[n], false);
   }
   if (REST)
     for (int i = tid + NV * NT; i < nvec; i += NT) {
+      P a, b;
       float u[VEC];
-      take(i, u, false);
+      load(i, a, b, false);
+      take(i, a, b, u, false);
     }
 
   ss = group_sum<32>(ss);
@@ -141,8 +155,10 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) add_rmsnorm_kernel(const 
   }
   if (REST)
     for (int i = tid + NV * NT; i < nvec; i += NT) {
+      P a, b;
       float u[VEC];
-      take(i, u, true);
+      load(i, a, b, true);
+      take(i, a, b, u, true);
       give(i, u);
     }
 }

@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(kFThreads, 2)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ __align__(8) uint64_t full[kFMaxStages], empty[kFMaxStages], done;
+  __shared__ __align__(16) float s_scale[kFBand], s_bias[kFBand];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
 
@@ -124,12 +125,22 @@ __global__ void __launch_bounds__(kFThreads, 2)
       tc::mma_commit_elect(&empty[s]);
     }
     tc::mma_commit_elect(&done);
+  } else if (warp >= 2) {
+    // the band's scales and bias while the weights stream in
+    static_assert(kFBand == 64, "one column for each thread of warps 2 and 3");
+    const int c = tid - 64;
+    const bool in = n0 + c < p.N;
+    s_scale[c] = in ? __ldg(p.w_scale + n0 + c) : 0.f;
+    s_bias[c] = in && p.bias != nullptr ? __ldg(p.bias + n0 + c) : 0.f;
   }
 
   // epilogue: thread (warp w, lane) holds row 32 w + lane of the accumulator
-  const bool ok = mbar_wait_bounded(&done, 0, abort_flag) && !*abort_flag;
-  tc::fence_after_sync();
   const int m = 32 * warp + lane;
+  const float my_scale = m < rows ? __ldg(p.x_scale + m0 + m) : 0.f;
+  __syncwarp();
+  const bool ok = mbar_wait_bounded(&done, 0, abort_flag) && !*abort_flag;
+  __syncthreads();  // s_scale, s_bias
+  tc::fence_after_sync();
   float v[kFBand];
   if (__all_sync(0xffffffffu, ok)) {
 #pragma unroll
@@ -140,20 +151,17 @@ __global__ void __launch_bounds__(kFThreads, 2)
 #pragma unroll
     for (int e = 0; e < kFBand; ++e) v[e] = 0.f;
   }
-  auto finish8 = [&](int r, int g8, float* x8) {
+  auto finish8 = [&](int r, int g8, float* x8, float xs) {
     const int n = n0 + 8 * g8, left = p.N - n;
     if (left <= 0) return;
-    const float xs = __ldg(p.x_scale + m0 + r);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < left)
-        x8[e] = fmaf(x8[e] * xs, __ldg(p.w_scale + n + e), p.bias != nullptr ? __ldg(p.bias + n + e) : 0.f);
+    for (int e = 0; e < 8; ++e) x8[e] = fmaf(x8[e] * xs, s_scale[8 * g8 + e], s_bias[8 * g8 + e]);
     store8<T>(static_cast<T*>(p.y) + (m0 + r) * p.y_stride + n, x8, left, true);
   };
   if (plan.splits == 1) {
     if (m < rows && !*abort_flag)
 #pragma unroll
-      for (int g8 = 0; g8 < kFBand / 8; ++g8) finish8(m, g8, v + 8 * g8);
+      for (int g8 = 0; g8 < kFBand / 8; ++g8) finish8(m, g8, v + 8 * g8, my_scale);
   } else {
     // each split's fp32 tile in its own shared memory (the ring is idle:
     // every load it issued was consumed by an MMA that has completed),
@@ -175,6 +183,7 @@ __global__ void __launch_bounds__(kFThreads, 2)
         const int r = u >> 3, g8 = u & 7;
         const uint32_t o0 = (uint32_t)(r * kFBand + 4 * ((2 * g8) ^ (r & 15))) * 4u;
         const uint32_t o1 = (uint32_t)(r * kFBand + 4 * ((2 * g8 + 1) ^ (r & 15))) * 4u;
+        const float xs = __ldg(p.x_scale + m0 + r);
         float x8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         for (int sp = 0; sp < S; ++sp) {
           const float4 a0 = ld_shared_cluster_f32x4(map_shared_rank(base + o0, (uint32_t)sp));
@@ -182,7 +191,7 @@ __global__ void __launch_bounds__(kFThreads, 2)
           x8[0] += a0.x, x8[1] += a0.y, x8[2] += a0.z, x8[3] += a0.w;
           x8[4] += a1.x, x8[5] += a1.y, x8[6] += a1.z, x8[7] += a1.w;
         }
-        finish8(r, g8, x8);
+        finish8(r, g8, x8, xs);
       }
     }
     cluster_arrive_release();
