@@ -6,7 +6,7 @@
 // in fp32. With t = s w, max|y| is max|t| times the inverse root, so both
 // reductions of a row go through one barrier and its values stay in
 // registers between: x and r are read once, each output is written once.
-#include <cuda_fp8.h>
+#include <type_traits>
 
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
@@ -32,13 +32,154 @@ struct alignas(16) Pack<T, 8> {
   T v[8];
 };
 
-__device__ __forceinline__ uint8_t e4m3(float x) {
-  return (uint8_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+// x, y to two e4m3 codes (x in the low byte), nearest with ties to even
+__device__ __forceinline__ uint32_t e4m3x2(float x, float y) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y), "f"(x));
+  return r;
 }
 
-// One CTA of NT threads per row (NT = 32: one warp per row, eight rows per
-// CTA). Thread t holds the NV vectors t, t + NT, ... of its row; rows longer
-// than NT * NV * VEC go through their tail twice (REST).
+// what the values of a row become once its reductions are there
+struct RowScale {
+  float inv, inv_q, scale;
+};
+__device__ __forceinline__ RowScale row_scale(const AddRmsNormArgs& p, float ss, float top) {
+  RowScale r;
+  r.inv = p.norm_w == nullptr ? 1.f : 1.f / sqrtf(ss / (float)p.cols + p.eps);
+  r.scale = fmaxf(top * r.inv / kE4m3Max, kScaleFloor);
+  r.inv_q = r.inv / r.scale;
+  return r;
+}
+// Elements 2 k and 2 k + 1 of a vector in fp32 (the second is 0 where VEC is 1)
+template <int VEC>
+__device__ __forceinline__ float2 pair(const Pack<float, VEC>& a, int k) {
+  return make_float2(a.v[2 * k], VEC > 1 ? a.v[VEC > 1 ? 2 * k + 1 : 0] : 0.f);
+}
+template <int VEC>
+__device__ __forceinline__ float2 pair(const Pack<__half, VEC>& a, int k) {
+  if constexpr (VEC == 1) return make_float2(__half2float(a.v[0]), 0.f);
+  else return __half22float2(reinterpret_cast<const __half2*>(a.v)[k]);
+}
+template <int VEC>
+__device__ __forceinline__ float2 pair(const Pack<__nv_bfloat16, VEC>& a, int k) {
+  if constexpr (VEC == 1) return make_float2(__bfloat162float(a.v[0]), 0.f);
+  const uint32_t u = reinterpret_cast<const uint32_t*>(a.v)[VEC == 1 ? 0 : k];
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+// a + b rounded to T, two elements an instruction where T has 16 bits
+template <int VEC>
+__device__ __forceinline__ Pack<float, VEC> add(const Pack<float, VEC>& a, const Pack<float, VEC>& b) {
+  Pack<float, VEC> c;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) c.v[e] = a.v[e] + b.v[e];
+  return c;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> add(const Pack<T, VEC>& a, const Pack<T, VEC>& b) {
+  Pack<T, VEC> c;
+  if constexpr (VEC == 1) {
+    c.v[0] = __hadd(a.v[0], b.v[0]);
+  } else {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+#pragma unroll
+    for (int k = 0; k < VEC / 2; ++k)
+      reinterpret_cast<T2*>(c.v)[k] = __hadd2(reinterpret_cast<const T2*>(a.v)[k], reinterpret_cast<const T2*>(b.v)[k]);
+  }
+  return c;
+}
+// weights of vector i (1 without)
+template <int VEC>
+struct Weights {
+  float2 v[(VEC + 1) / 2];
+};
+template <int VEC>
+__device__ __forceinline__ Weights<VEC> weights(const AddRmsNormArgs& p, int i) {
+  Weights<VEC> w;
+#pragma unroll
+  for (int k = 0; k < (VEC + 1) / 2; ++k) w.v[k] = make_float2(1.f, 1.f);
+  if (p.norm_w == nullptr) return w;
+  if constexpr (VEC == 1) {
+    w.v[0].x = __ldg(p.norm_w + i);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 4) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(p.norm_w + (int64_t)i * VEC + e));
+      w.v[e / 2] = make_float2(x.x, x.y);
+      w.v[e / 2 + 1] = make_float2(x.z, x.w);
+    }
+  }
+  return w;
+}
+__device__ __forceinline__ float2 times(float2 a, float2 b) { return fma2(a, b, make_float2(-0.f, -0.f)); }
+// squares of s, and the maximum of |s w|
+template <typename T, int VEC>
+__device__ __forceinline__ void weigh(const Pack<T, VEC>& s, const Weights<VEC>& w, float2& ss, float& top) {
+#pragma unroll
+  for (int k = 0; k < (VEC + 1) / 2; ++k) {
+    const float2 x = pair<VEC>(s, k);
+    const float2 t = times(x, w.v[k]);
+    ss = fma2(x, x, ss);
+    top = fmaxf(top, fmaxf(fabsf(t.x), fabsf(t.y)));
+  }
+}
+// vector i of the outputs of a row, from s
+template <typename T, int VEC>
+__device__ __forceinline__ void give(const AddRmsNormArgs& p, int64_t row, int i, const Pack<T, VEC>& s,
+                                     const Weights<VEC>& w, const RowScale& r) {
+  constexpr int N2 = (VEC + 1) / 2;
+  float2 t[N2];
+#pragma unroll
+  for (int k = 0; k < N2; ++k) t[k] = times(pair<VEC>(s, k), w.v[k]);
+  if (p.out != nullptr) {
+    Pack<T, VEC> c;
+#pragma unroll
+    for (int k = 0; k < N2; ++k) {
+      const float2 y = times(t[k], make_float2(r.inv, r.inv));
+      c.v[2 * k] = from_f32<T>(y.x);
+      if (VEC > 1) c.v[VEC > 1 ? 2 * k + 1 : 0] = from_f32<T>(y.y);
+    }
+    reinterpret_cast<Pack<T, VEC>*>(static_cast<T*>(p.out) + row * p.out_stride)[i] = c;
+  }
+  if (p.out_q != nullptr) {
+    uint32_t q[N2];
+#pragma unroll
+    for (int k = 0; k < N2; ++k) {
+      const float2 y = times(t[k], make_float2(r.inv_q, r.inv_q));
+      q[k] = e4m3x2(y.x, y.y);
+    }
+    uint8_t* oq = static_cast<uint8_t*>(p.out_q) + row * p.out_q_stride + (int64_t)i * VEC;
+    if constexpr (VEC == 8) *reinterpret_cast<uint2*>(oq) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+    else if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(oq) = q[0] | q[1] << 16;
+    else *oq = (uint8_t)q[0];
+  }
+}
+// sum of ss and maximum of top over the NT threads of a row; buf: its own for
+// two rows in turn, so that one barrier a row is enough
+template <int NT>
+__device__ __forceinline__ void reduce_row(float2 ss2, float& ss, float& top, float (&buf)[2][32], int tid) {
+  ss = group_sum<32>(ss2.x + ss2.y);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  if (NT > 32) {
+    if ((tid & 31) == 0) {
+      buf[0][tid >> 5] = ss;
+      buf[1][tid >> 5] = top;
+    }
+    __syncthreads();
+    ss = 0.f;
+    top = 0.f;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+      ss += buf[0][w];
+      top = fmaxf(top, buf[1][w]);
+    }
+  }
+}
+
+// One row for NT threads (NT = 32: a warp, eight rows per CTA), for few rows
+// and for rows that do not allow 16-byte accesses: thread t holds the NV
+// vectors t, t + NT, ... in registers, all its loads issued before the first
+// store. Rows longer than NT * NV * VEC go through their tail twice (REST).
 template <typename T, int VEC, int NT, int NV, bool REST>
 __global__ void __launch_bounds__(NT == 32 ? 256 : NT) add_rmsnorm_kernel(const AddRmsNormArgs p) {
   constexpr int ROWS = NT == 32 ? 8 : 1;
@@ -46,133 +187,184 @@ __global__ void __launch_bounds__(NT == 32 ? 256 : NT) add_rmsnorm_kernel(const 
   const int64_t row = (int64_t)blockIdx.x * ROWS + (NT == 32 ? (threadIdx.x >> 5) : 0);
   if (row >= p.rows) return;
   using P = Pack<T, VEC>;
-  const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
-  const T* r = p.residual == nullptr ? nullptr : static_cast<const T*>(p.residual) + row * p.residual_stride;
-  T* sum = p.sum == nullptr ? nullptr : static_cast<T*>(p.sum) + row * p.sum_stride;
+  __shared__ float red[2][32];
+  const P* x = reinterpret_cast<const P*>(static_cast<const T*>(p.x) + row * p.x_stride);
+  const P* r = p.residual == nullptr
+                   ? nullptr
+                   : reinterpret_cast<const P*>(static_cast<const T*>(p.residual) + row * p.residual_stride);
+  P* sum = p.sum == nullptr ? nullptr : reinterpret_cast<P*>(static_cast<T*>(p.sum) + row * p.sum_stride);
   const int nvec = (int)(p.cols / VEC);
-
-  float ss = 0.f, top = 0.f;
-  // s = x (+ residual) of vector i, stored; read back the second time (sum may
-  // be the residual itself)
-  auto load = [&](int i, P& a, P& b, bool again) {
-    const bool stored = again && sum != nullptr;
-    a = *reinterpret_cast<const P*>((stored ? sum : x) + (int64_t)i * VEC);
-    if (r != nullptr && !stored) b = *reinterpret_cast<const P*>(r + (int64_t)i * VEC);
-  };
-  // t = s w, and the first time its squares and maximum
-  auto take = [&](int i, const P& a, const P& b, float (&t)[VEC], bool again) {
-    P c = a;
-    if (r != nullptr && !(again && sum != nullptr))
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) c.v[e] = from_f32<T>(to_f32(a.v[e]) + to_f32(b.v[e]));
-    if (sum != nullptr && !again) *reinterpret_cast<P*>(sum + (int64_t)i * VEC) = c;
-    alignas(16) float w[VEC];
-    if (p.norm_w == nullptr) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) w[e] = 1.f;
-    } else if constexpr (VEC % 4 == 0) {
-#pragma unroll
-      for (int e = 0; e < VEC; e += 4)
-        *reinterpret_cast<float4*>(w + e) = __ldg(reinterpret_cast<const float4*>(p.norm_w + (int64_t)i * VEC + e));
-    } else {
-      w[0] = __ldg(p.norm_w + i);
-    }
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const float s = to_f32(c.v[e]);
-      if (!again) ss = fmaf(s, s, ss);
-      t[e] = s * w[e];
-      if (!again) top = fmaxf(top, fabsf(t[e]));
-    }
-  };
-  // all of the row's loads before the first store, which they might not pass
-  float t[NV][VEC];
+  float2 ss2 = make_float2(0.f, 0.f);
+  float ss, top = 0.f;
+  P a[NV];
   {
-    P a[NV], b[NV];
+    P b[NV];
 #pragma unroll
     for (int n = 0; n < NV; ++n)
-      if (tid + n * NT < nvec) load(tid + n * NT, a[n], b[n], false);
+      if (tid + n * NT < nvec) {
+        a[n] = x[tid + n * NT];
+        if (r != nullptr) b[n] = r[tid + n * NT];
+      }
 #pragma unroll
-    for (int n = 0; n < NV; ++n)
-      if (tid + n * NT < nvec) take(tid + n * NT, a[n], b[n], t[n], false);
-  }
-  if (REST)
-    for (int i = tid + NV * NT; i < nvec; i += NT) {
-      P a, b;
-      float u[VEC];
-      load(i, a, b, false);
-      take(i, a, b, u, false);
-    }
-
-  ss = group_sum<32>(ss);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  if (NT > 32) {
-    __shared__ float red[2][32];
-    if ((tid & 31) == 0) {
-      red[0][tid >> 5] = ss;
-      red[1][tid >> 5] = top;
-    }
-    __syncthreads();
-    ss = 0.f;
-    top = 0.f;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-      ss += red[0][w];
-      top = fmaxf(top, red[1][w]);
-    }
-  }
-  const float inv = p.norm_w == nullptr ? 1.f : 1.f / sqrtf(ss / (float)p.cols + p.eps);
-  const float scale = fmaxf(top * inv / kE4m3Max, kScaleFloor);
-  const float inv_q = inv / scale;
-  T* out = p.out == nullptr ? nullptr : static_cast<T*>(p.out) + row * p.out_stride;
-  uint8_t* oq = p.out_q == nullptr ? nullptr : static_cast<uint8_t*>(p.out_q) + row * p.out_q_stride;
-  if (oq != nullptr && tid == 0) p.out_scale[row] = scale;
-  auto give = [&](int i, const float (&u)[VEC]) {
-    if (out != nullptr) {
-      P c;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) c.v[e] = from_f32<T>(u[e] * inv);
-      *reinterpret_cast<P*>(out + (int64_t)i * VEC) = c;
-    }
-    if (oq != nullptr) {
-      uint8_t b[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) b[e] = e4m3(u[e] * inv_q);
-      if constexpr (VEC == 8) {
-        *reinterpret_cast<uint2*>(oq + (int64_t)i * VEC) = *reinterpret_cast<const uint2*>(b);
-      } else if constexpr (VEC == 4) {
-        *reinterpret_cast<uint32_t*>(oq + (int64_t)i * VEC) = *reinterpret_cast<const uint32_t*>(b);
-      } else {
-        oq[i] = b[0];
+    for (int n = 0; n < NV; ++n) {
+      const int i = tid + n * NT;
+      if (i < nvec) {
+        if (r != nullptr) a[n] = add(a[n], b[n]);
+        if (sum != nullptr) sum[i] = a[n];
+        weigh<T, VEC>(a[n], weights<VEC>(p, i), ss2, top);
       }
     }
-  };
-#pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    const int i = tid + n * NT;
-    if (i < nvec) give(i, t[n]);
   }
   if (REST)
     for (int i = tid + NV * NT; i < nvec; i += NT) {
-      P a, b;
-      float u[VEC];
-      load(i, a, b, true);
-      take(i, a, b, u, true);
-      give(i, u);
+      P s = x[i];
+      if (r != nullptr) s = add(s, r[i]);
+      if (sum != nullptr) sum[i] = s;
+      weigh<T, VEC>(s, weights<VEC>(p, i), ss2, top);
     }
+  reduce_row<NT>(ss2, ss, top, red, tid);
+  const RowScale sc = row_scale(p, ss, top);
+  if (p.out_q != nullptr && tid == 0) p.out_scale[row] = sc.scale;
+#pragma unroll
+  for (int n = 0; n < NV; ++n)
+    if (tid + n * NT < nvec) give<T, VEC>(p, row, tid + n * NT, a[n], weights<VEC>(p, tid + n * NT), sc);
+  if (REST)
+    for (int i = tid + NV * NT; i < nvec; i += NT) {
+      // the sum as stored: it may be where x or the residual was
+      P s = sum != nullptr ? sum[i] : x[i];
+      if (r != nullptr && sum == nullptr) s = add(s, r[i]);
+      give<T, VEC>(p, row, i, s, weights<VEC>(p, i), sc);
+    }
+}
+
+// Many rows: as many CTAs as the SMs hold, each with a ring of rows of x and
+// the residual that bulk copies fill ahead, so that the memory is read while
+// rows are reduced and stored. A thread keeps its columns' weights for all of
+// its rows, and its part of a row between the two passes. The barrier of a
+// row's reduction is also the one after which its place is filled again.
+constexpr int kRingSlots = 8;
+
+template <typename T, int NT, int NV>
+__global__ void __launch_bounds__(NT) add_rmsnorm_ring_kernel(const AddRmsNormArgs p, const int slots) {
+  constexpr int VEC = 16 / sizeof(T);
+  using P = Pack<T, VEC>;
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ __align__(8) uint64_t full[kRingSlots];
+  __shared__ float red[2][2][32];
+  __shared__ int s_abort;
+  const int tid = threadIdx.x;
+  const uint32_t bytes = (uint32_t)p.cols * sizeof(T), slot_bytes = p.residual == nullptr ? bytes : 2 * bytes;
+  const int nvec = (int)(p.cols / VEC);
+  if (tid == 0) {
+    for (int s = 0; s < slots; ++s) mbar_init(&full[s], 1);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  volatile int* abort_flag = &s_abort;
+  const auto fill = [&](int s, int64_t row) {
+    mbar_arrive_expect_tx(&full[s], slot_bytes);
+    bulk_load(ring + (size_t)s * slot_bytes, static_cast<const T*>(p.x) + row * p.x_stride, bytes, &full[s]);
+    if (p.residual != nullptr)
+      bulk_load(ring + (size_t)s * slot_bytes + bytes, static_cast<const T*>(p.residual) + row * p.residual_stride, bytes,
+                &full[s]);
+  };
+  if (tid == 0)
+    for (int s = 0; s < slots && blockIdx.x + (int64_t)s * gridDim.x < p.rows; ++s)
+      fill(s, blockIdx.x + (int64_t)s * gridDim.x);
+  Weights<VEC> w[NV];
+#pragma unroll
+  for (int n = 0; n < NV; ++n)
+    if (tid + n * NT < nvec) w[n] = weights<VEC>(p, tid + n * NT);
+  int slot = 0, parity = 0;
+  uint32_t phase = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
+    const bool ok = mbar_wait_bounded(&full[slot], phase, abort_flag);
+    const P* x = reinterpret_cast<const P*>(ring + (size_t)slot * slot_bytes);
+    P* sum = p.sum == nullptr ? nullptr : reinterpret_cast<P*>(static_cast<T*>(p.sum) + row * p.sum_stride);
+    float2 ss2 = make_float2(0.f, 0.f);
+    float ss, top = 0.f;
+    P a[NV];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int i = tid + n * NT;
+      if (i < nvec && ok) {
+        a[n] = x[i];
+        if (p.residual != nullptr) a[n] = add(a[n], x[nvec + i]);
+        if (sum != nullptr) sum[i] = a[n];
+        weigh<T, VEC>(a[n], w[n], ss2, top);
+      }
+    }
+    reduce_row<NT>(ss2, ss, top, red[parity], tid);
+    // every thread has read the row
+    if (tid == 0 && !*abort_flag) {
+      const int64_t next = row + (int64_t)slots * gridDim.x;
+      if (next < p.rows) fill(slot, next);
+    }
+    if (ok) {
+      const RowScale sc = row_scale(p, ss, top);
+      if (p.out_q != nullptr && tid == 0) p.out_scale[row] = sc.scale;
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+        if (tid + n * NT < nvec) give<T, VEC>(p, row, tid + n * NT, a[n], w[n], sc);
+    }
+    if (++slot == slots) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+}
+
+int norm_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 148;
+  return n;
+}
+
+template <typename T, int NT, int NV>
+cudaError_t launch_ring(const AddRmsNormArgs& p, int ctas_per_sm, int slots, int64_t slot_bytes, cudaStream_t stream) {
+  auto kern = add_rmsnorm_ring_kernel<T, NT, NV>;
+  const int smem = (int)(slots * slot_bytes);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)(ctas_per_sm * norm_sms()), NT, smem, stream>>>(p, slots);
+  return cudaGetLastError();
+}
+
+template <typename T, int VEC, int NT, int NV, bool REST>
+cudaError_t launch_norm_k(const AddRmsNormArgs& p, cudaStream_t stream) {
+  constexpr int ROWS = NT == 32 ? 8 : 1;
+  add_rmsnorm_kernel<T, VEC, NT, NV, REST>
+      <<<(unsigned)((p.rows + ROWS - 1) / ROWS), NT == 32 ? 256 : NT, 0, stream>>>(p);
+  return cudaGetLastError();
 }
 
 template <typename T, int VEC>
 cudaError_t launch_norm_v(const AddRmsNormArgs& p, cudaStream_t stream) {
   const int64_t nvec = p.cols / VEC;
-  const unsigned rows = (unsigned)p.rows, rows8 = (unsigned)((p.rows + 7) / 8);
-  if (nvec <= 64) add_rmsnorm_kernel<T, VEC, 32, 2, false><<<rows8, 256, 0, stream>>>(p);
-  else if (nvec <= 256) add_rmsnorm_kernel<T, VEC, 128, 2, false><<<rows, 128, 0, stream>>>(p);
-  else if (nvec <= 1024) add_rmsnorm_kernel<T, VEC, 256, 4, false><<<rows, 256, 0, stream>>>(p);
-  else if (nvec <= 2048) add_rmsnorm_kernel<T, VEC, 512, 4, false><<<rows, 512, 0, stream>>>(p);
-  else add_rmsnorm_kernel<T, VEC, 512, 4, true><<<rows, 512, 0, stream>>>(p);
-  return cudaGetLastError();
+  if constexpr (VEC > 1) {
+    // the ring where every CTA has rows enough to run ahead, and two of them fit
+    const int64_t slot_bytes = p.cols * (int64_t)sizeof(T) * (p.residual == nullptr ? 1 : 2);
+    const int per_sm = slot_bytes <= 36 * 1024 ? 3 : 2;
+    int64_t slots = (per_sm == 3 ? 72 : 110) * 1024 / slot_bytes;
+    if (slots > kRingSlots) slots = kRingSlots;
+    if (nvec > 64 && nvec <= 2048 && slots >= 2 && p.rows >= 4ll * per_sm * norm_sms()) {
+      const int n = (int)slots;
+      if (nvec <= 128) return launch_ring<T, 128, 1>(p, per_sm, n, slot_bytes, stream);
+      if (nvec <= 256) return launch_ring<T, 256, 1>(p, per_sm, n, slot_bytes, stream);
+      if (nvec <= 512) return launch_ring<T, 256, 2>(p, per_sm, n, slot_bytes, stream);
+      if (nvec <= 1024) return launch_ring<T, 256, 4>(p, per_sm, n, slot_bytes, stream);
+      return launch_ring<T, 512, 4>(p, per_sm, n, slot_bytes, stream);
+    }
+  }
+  if (nvec <= 64) return launch_norm_k<T, VEC, 32, 2, false>(p, stream);
+  if (nvec <= 256) return launch_norm_k<T, VEC, 128, 2, false>(p, stream);
+  if (nvec <= 512) return launch_norm_k<T, VEC, 256, 2, false>(p, stream);
+  if (nvec <= 1024) return launch_norm_k<T, VEC, 256, 4, false>(p, stream);
+  if (nvec <= 2048) return launch_norm_k<T, VEC, 512, 4, false>(p, stream);
+  return launch_norm_k<T, VEC, 512, 4, true>(p, stream);
 }
 
 template <typename T>
@@ -201,3 +393,5 @@ cudaError_t launch_add_rmsnorm(const AddRmsNormArgs& p, int32_t dtype, cudaStrea
 }
 
 }  // namespace gdn
+
+GDN_DEFINE_ERROR_READER(add_rmsnorm)

@@ -208,6 +208,7 @@ cudaError_t read_error_decay_tc(int32_t* status, bool clear);
 cudaError_t launch_add_rmsnorm(const AddRmsNormArgs& p, int32_t dtype, cudaStream_t stream);
 cudaError_t launch_linear_fp8(const LinearFp8Args& p, const void* x, int64_t x_stride, const void* w,
                               int32_t out_dtype, cudaStream_t stream);
+cudaError_t read_error_add_rmsnorm(int32_t* status, bool clear);
 cudaError_t read_error_decay_step(int32_t* status, bool clear);
 cudaError_t read_error_decay_scan(int32_t* status, bool clear);
 cudaError_t read_error_linear_fp8(int32_t* status, bool clear);

@@ -71,6 +71,38 @@ def test_every_output(dtype, rows, cols, stride):
             assert torch.equal(kw["out_q"].view(torch.uint8), q.contiguous().view(torch.uint8))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,cols,stride", [(2000, 520, 520), (1999, 2048, 2064), (1850, 8192, 8192),
+                                              (1300, 16384, 16384), (3000, 513, 513)])
+@pytest.mark.parametrize("residual", [True, False])
+def test_many_rows(dtype, rows, cols, stride, residual):
+    """Rows enough for every CTA to go through several of them, in place and not; a part of them checked one by one,
+    all of them against the same rows given a few at a time."""
+    gen = torch.Generator().manual_seed(cols)
+    x = rows_of(gen, rows, cols, stride, dtype)
+    r = rows_of(gen, rows, cols, stride, dtype, 3.0) if residual else None
+    w = (1 + 0.3 * torch.randn(cols, generator=gen)).cuda()
+    y, q = torch.empty_like(x), torch.empty(x.shape, dtype=torch.float8_e4m3fn, device="cuda")
+    sc = torch.empty(rows, device="cuda")
+    s = torch.empty_like(x) if residual else None
+    gdn.gdn_add_rmsnorm(x, w, residual=r, sum_out=s, out=y, out_q=q, out_scale=sc)
+    some = torch.tensor([0, 1, 2, 700, rows // 2, rows - 2, rows - 1], device="cuda")
+    verify(x[some], r[some] if residual else None, w, 1e-6, dtype, s[some] if residual else None, y[some],
+           q.view(torch.uint8)[some].view(torch.float8_e4m3fn), sc[some])
+    for a in range(0, rows, 304):  # (304 rows of any width end on 16 bytes)
+        b = min(a + 304, rows)
+        y1 = torch.empty_like(y[a:b])
+        gdn.gdn_add_rmsnorm(x[a:b], w, residual=r[a:b] if residual else None, out=y1)
+        # another order of the same fp32 sums: each is within verify's bound, half a step and (cols / 32 + 40) u of
+        # the value, so the two are within twice that (of the larger, which 1.01 covers)
+        bound = 2.02 * (HALF_STEP[dtype] + (cols / 32 + 40) * U) * y1.float().abs() + 2 * TINY[dtype]
+        assert ((y1.float() - y[a:b].float()).abs() <= bound).all()
+    if residual:
+        gdn.gdn_add_rmsnorm(x, w, residual=r, sum_out=r, out=y)
+        assert torch.equal(r, s)
+    assert gdn.gdn_device_error() == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("cols", [100, 2048, 20000])
 def test_without_residual_or_weight(dtype, cols):
