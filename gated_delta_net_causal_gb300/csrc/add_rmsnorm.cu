@@ -364,6 +364,7 @@ cudaError_t launch_norm_v(const AddRmsNormArgs& p, cudaStream_t stream) {
   if (nvec <= 512) return launch_norm_k<T, VEC, 256, 2, false>(p, stream);
   if (nvec <= 1024) return launch_norm_k<T, VEC, 256, 4, false>(p, stream);
   if (nvec <= 2048) return launch_norm_k<T, VEC, 512, 4, false>(p, stream);
+  if (VEC == 1 && nvec <= 4096) return launch_norm_k<T, VEC, 512, VEC == 1 ? 8 : 4, false>(p, stream);
   return launch_norm_k<T, VEC, 512, 4, true>(p, stream);
 }
 

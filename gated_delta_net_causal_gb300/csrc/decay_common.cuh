@@ -17,8 +17,8 @@ __device__ __forceinline__ float decay_log(float g) { return g < kDecayFloor ? k
 // s <- exp(g) s + d v on a lane's groups. Near 1 the factor's own rounding
 // would add up over a long memory (1000 tokens of it at g = -0.001 are 3e-5),
 // so from one half up s + expm1(g) s is taken instead, whose error is a
-// rounding of the result alone. keep is 1 and factor expm1(g) there, else 0
-// and exp(g): one branch for the whole CTA, the same two FMAs an element.
+// rounding of the result alone: keep is 1 and factor expm1(g) there, else 0
+// and exp(g), two FMAs an element either way.
 struct Decay {
   float keep, factor;
 };
@@ -26,12 +26,8 @@ __device__ __forceinline__ Decay decay_factor(float g) {
   return g > -0.69f ? Decay{1.f, expm1f(g)} : Decay{0.f, expf(g)};
 }
 template <int NV4>
-__device__ __forceinline__ void decay_update(float4 (&s)[NV4], const float4 (&v)[NV4], Decay a, float d) {
-  if (a.keep == 0.f) {
-    row_update<NV4>(s, v, a.factor, d);
-    return;
-  }
-  const float2 al = make_float2(a.factor, a.factor), dd = make_float2(d, d);
+__device__ __forceinline__ void decay_update_near(float4 (&s)[NV4], const float4 (&v)[NV4], float factor, float d) {
+  const float2 al = make_float2(factor, factor), dd = make_float2(d, d);
 #pragma unroll
   for (int m = 0; m < NV4; ++m) {
     const float2 s0 = make_float2(s[m].x, s[m].y), s1 = make_float2(s[m].z, s[m].w);
@@ -40,17 +36,23 @@ __device__ __forceinline__ void decay_update(float4 (&s)[NV4], const float4 (&v)
     s[m] = make_float4(lo.x, lo.y, hi.x, hi.y);
   }
 }
+template <int NV4>
+__device__ __forceinline__ void decay_update(float4 (&s)[NV4], const float4 (&v)[NV4], Decay a, float d) {
+  if (a.keep == 0.f) row_update<NV4>(s, v, a.factor, d);
+  else decay_update_near<NV4>(s, v, a.factor, d);
+}
 
 // How the D x D state of a head lies over the threads of a CTA: LPR lanes
 // share a row, each with NV4 groups of four columns (group m of lane sub at
 // column 4 sub + 4 LPR m, so that the lanes of a row read 64 or 128
-// contiguous bytes at a time); a lane has RPL rows, RPW apart.
-template <int D>
+// contiguous bytes at a time); a lane has RPL rows, RPW apart: fewer (FEW)
+// where few CTAs run and a token's latency counts, not what it issues.
+template <int D, bool FEW = false>
 struct DecayGeom {
   static constexpr int LPR = D == 32 ? 4 : (D == 64 ? 4 : 8);
   static constexpr int NV4 = D / (4 * LPR);
   static constexpr int RPW = 32 / LPR;
-  static constexpr int RPL = D == 32 ? 2 : (D == 96 ? 3 : 4);
+  static constexpr int RPL = FEW ? (D == 128 || D == 96 ? 2 : 1) : (D == 32 ? 2 : (D == 96 ? 3 : 4));
   static constexpr int WROWS = RPW * RPL;  // rows a warp owns
   static constexpr int WARPS = D / WROWS;
   static constexpr int THREADS = 32 * WARPS;
@@ -207,16 +209,23 @@ struct DecaySlots {
                            fmaf(a, s[c].w, x[c].w));
     }
   }
-  // the state at the start of segment i
-  __device__ __forceinline__ float4 start(int i, int parts, int at) const {
-    if (i == 0) return *reinterpret_cast<const float4*>(base + (parts - 1) * step + at);
-    float4 s = *reinterpret_cast<const float4*>(base + at);
+  // four elements at each of N places at + c * stride of the state at the start
+  // of segment i, the loads of a segment in flight together
+  template <int N>
+  __device__ __forceinline__ void start4(int i, int parts, int at, int stride, float4 (&s)[N]) const {
+    const float* first = base + (i == 0 ? (parts - 1) * step : 0) + at;
+#pragma unroll
+    for (int c = 0; c < N; ++c) s[c] = *reinterpret_cast<const float4*>(first + c * stride);
     for (int m = 1; m < i; ++m) {
       const float a = decay[m * dstep];
-      const float4 add = *reinterpret_cast<const float4*>(base + m * step + at);
-      s = make_float4(fmaf(a, s.x, add.x), fmaf(a, s.y, add.y), fmaf(a, s.z, add.z), fmaf(a, s.w, add.w));
+      float4 x[N];
+#pragma unroll
+      for (int c = 0; c < N; ++c) x[c] = *reinterpret_cast<const float4*>(base + m * step + at + c * stride);
+#pragma unroll
+      for (int c = 0; c < N; ++c)
+        s[c] = make_float4(fmaf(a, s[c].x, x[c].x), fmaf(a, s[c].y, x[c].y), fmaf(a, s[c].z, x[c].z),
+                           fmaf(a, s[c].w, x[c].w));
     }
-    return s;
   }
 };
 

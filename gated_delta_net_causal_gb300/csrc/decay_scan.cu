@@ -16,6 +16,8 @@
 // each segment adds to the state and multiplies it by, a second one the
 // outputs, each segment starting from what those before it add up to. That
 // goes through the states twice; segments are as long as the SMs allow.
+#include <type_traits>
+
 #include "decay_common.cuh"
 
 namespace gdn {
@@ -30,11 +32,13 @@ template <typename T, int D>
 struct ScanSmem {
   float q[2][kTile][D], k[2][kTile][D], v[2][kTile][D], o[2][kTile][D];
   Decay decay[2][kTile];
+  int near[2];  // every token of the tile decays by less than half
 };
 
-template <typename T, int D, int MODE>
-__global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_scan_kernel(const DecayArgs p, const DecaySegments sg) {
-  using G = DecayGeom<D>;
+template <typename T, int D, int MODE, bool FEW>
+__global__ void __launch_bounds__(DecayGeom<D, FEW>::THREADS, FEW ? 1 : 512 / DecayGeom<D>::THREADS)
+    decay_scan_kernel(const DecayArgs p, const DecaySegments sg) {
+  using G = DecayGeom<D, FEW>;
   constexpr int LPR = G::LPR, NV4 = G::NV4, RPL = G::RPL, RPW = G::RPW, NT = G::THREADS;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   ScanSmem<T, D>& sm = *reinterpret_cast<ScanSmem<T, D>*>(smem_raw);
@@ -50,21 +54,29 @@ __global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_scan_kernel(const
   float4 st[RPL][NV4];
   const DecaySlots ws(p, sg, s, h, D * D);
   const int at0 = (warp * G::WROWS + rq) * D + 4 * sub;
+  if (MODE == kLocal) {
+    float* keep = sg.states + ((int64_t)(s.slot + s.parts - 1) * p.Hv + h) * (D * D);
 #pragma unroll
-  for (int u = 0; u < RPL; ++u)
+    for (int u = 0; u < RPL; ++u)
 #pragma unroll
-    for (int m = 0; m < NV4; ++m) {
-      const int at = at0 + u * RPW * D + 4 * LPR * m;
-      if (MODE == kLocal) {
+      for (int m = 0; m < NV4; ++m) {
+        const int at = at0 + u * RPW * D + 4 * LPR * m;
         st[u][m] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (s.index == 0) {
           st[u][m] = *reinterpret_cast<const float4*>(gS + at);
-          *reinterpret_cast<float4*>(sg.states + ((int64_t)(s.slot + s.parts - 1) * p.Hv + h) * (D * D) + at) = st[u][m];
+          *reinterpret_cast<float4*>(keep + at) = st[u][m];
         }
-      } else {
-        st[u][m] = s.parts == 1 ? *reinterpret_cast<const float4*>(gS + at) : ws.start(s.index, s.parts, at);
       }
-    }
+  } else if (s.parts == 1) {
+#pragma unroll
+    for (int u = 0; u < RPL; ++u)
+#pragma unroll
+      for (int m = 0; m < NV4; ++m)
+        st[u][m] = *reinterpret_cast<const float4*>(gS + at0 + u * RPW * D + 4 * LPR * m);
+  } else {
+#pragma unroll
+    for (int u = 0; u < RPL; ++u) ws.start4<NV4>(s.index, s.parts, at0 + u * RPW * D, 4 * LPR, st[u]);
+  }
 
   // staging: unit u of a tile is four elements; units of q, k, v in turn
   constexpr int UNITS = kTile * D / 4, PER = (3 * UNITS + NT - 1) / NT;
@@ -82,7 +94,7 @@ __global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_scan_kernel(const
         pre[i] = load4(src);
       }
     }
-    if (tid < kTile && t0 + tid < s.end) pre_g = decay_log(p.g[(int64_t)(t0 + tid) * p.g_stride + h]);
+    if (tid < kTile && t0 + tid < s.end) pre_g = p.g[(int64_t)(t0 + tid) * p.g_stride + h];
   };
   float total = 0.f;  // thread tt < kTile: its share of the segment's log decay
   auto stash = [&](int buf, int t0) {
@@ -95,9 +107,16 @@ __global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_scan_kernel(const
         *reinterpret_cast<float4*>(dst) = pre[i];
       }
     }
-    if (tid < kTile && t0 + tid < s.end) {
-      sm.decay[buf][tid] = decay_factor(pre_g);
-      if (MODE == kLocal) total += pre_g;
+    if (warp == 0) {
+      Decay d{0.f, 0.f};
+      if (tid < kTile && t0 + tid < s.end) {
+        const float g = decay_log(pre_g);
+        d = decay_factor(g);
+        sm.decay[buf][tid] = d;
+        if (MODE == kLocal) total += g;
+      }
+      const bool near = __all_sync(0xffffffffu, tid >= kTile || d.keep != 0.f);
+      if (tid == 0) sm.near[buf] = near;
     }
   };
   auto write_tile = [&](int buf, int t0) {
@@ -116,14 +135,17 @@ __global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_scan_kernel(const
   for (int t0 = s.begin; t0 < s.end; t0 += kTile, buf ^= 1) {
     if (t0 + kTile < s.end) fetch(t0 + kTile);
     const int n = s.end - t0 < kTile ? s.end - t0 : kTile;
-    for (int tt = 0; tt < n; ++tt) {
+    const auto token = [&](int tt, auto near) {
       const Decay decay = sm.decay[buf][tt];
       float4 kr[NV4];
 #pragma unroll
       for (int m = 0; m < NV4; ++m) kr[m] = *reinterpret_cast<const float4*>(&sm.k[buf][tt][4 * sub + 4 * LPR * m]);
 #pragma unroll
-      for (int u = 0; u < RPL; ++u)
-        decay_update<NV4>(st[u], kr, decay, sm.v[buf][tt][warp * G::WROWS + u * RPW + rq]);
+      for (int u = 0; u < RPL; ++u) {
+        const float v = sm.v[buf][tt][warp * G::WROWS + u * RPW + rq];
+        if constexpr (decltype(near)::value) decay_update_near<NV4>(st[u], kr, decay.factor, v);
+        else decay_update<NV4>(st[u], kr, decay, v);
+      }
       if (MODE == kWhole) {
         float o[RPL];
 #pragma unroll
@@ -138,6 +160,14 @@ __global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_scan_kernel(const
 #pragma unroll
           for (int u = 0; u < RPL; ++u) sm.o[buf][tt][warp * G::WROWS + u * RPW + rq] = o[u] * p.scale;
       }
+    };
+    // a whole tile of slow decays unrolled, so that one token's loads and sums
+    // run under the next one's updates
+    if (sm.near[buf]) {
+#pragma unroll
+      for (int tt = 0; tt < kTile; ++tt) token(tt, std::true_type());
+    } else {
+      for (int tt = 0; tt < n; ++tt) token(tt, std::false_type());
     }
     if (t0 + kTile < s.end) stash(buf ^ 1, t0 + kTile);
     __syncthreads();
@@ -158,19 +188,22 @@ __global__ void __launch_bounds__(DecayGeom<D>::THREADS) decay_scan_kernel(const
   }
 }
 
-template <typename T, int D>
-cudaError_t launch_scan_td(const DecayArgs& p, const DecaySegments& sg, cudaStream_t stream) {
-  constexpr int smem = (int)sizeof(ScanSmem<T, D>);
+template <typename T, int D, bool FEW>
+cudaError_t launch_scan_k(const DecayArgs& p, const DecaySegments& sg, cudaStream_t stream) {
+  constexpr int smem = (int)sizeof(ScanSmem<T, D>), threads = DecayGeom<D, FEW>::THREADS;
   const unsigned grid = (unsigned)(sg.slots * p.Hv);
-  auto whole = decay_scan_kernel<T, D, kWhole>;
-  auto local = decay_scan_kernel<T, D, kLocal>;
   if (sg.states != nullptr) {
-    local<<<grid, DecayGeom<D>::THREADS, smem, stream>>>(p, sg);
+    decay_scan_kernel<T, D, kLocal, FEW><<<grid, threads, smem, stream>>>(p, sg);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  whole<<<grid, DecayGeom<D>::THREADS, smem, stream>>>(p, sg);
+  decay_scan_kernel<T, D, kWhole, FEW><<<grid, threads, smem, stream>>>(p, sg);
   return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_scan_td(const DecayArgs& p, const DecaySegments& sg, cudaStream_t stream) {
+  return sg.slots * p.Hv <= 152 ? launch_scan_k<T, D, true>(p, sg, stream) : launch_scan_k<T, D, false>(p, sg, stream);
 }
 
 template <typename T>
@@ -191,15 +224,19 @@ cudaError_t launch_scan_t(const DecayArgs& p, const DecaySegments& sg, int32_t D
 // CTAs and no CTA a second turn ((T / len + N) Hv <= 304), none where the
 // (sequence, V head) pairs come near that by themselves. With few heads that
 // would be many short ones, and the last of them reads the states that all
-// others add: a chunk of 64 tokens costs about as much as seven such states,
-// so n chunks in segments of m cost m + n / (7 m), least at m = sqrt(n / 7).
-int32_t decay_segment_len(int32_t N, int64_t T, int32_t Hv, int32_t, int32_t) {
+// others add: on the tensor cores a chunk of 64 tokens costs about as much as
+// seven such states, so n chunks in segments of m cost m + n / (7 m), least
+// at m = sqrt(n / 7); token by token a state costs about as much as two
+// tokens (whatever D: both go with the state's size), so n tokens in segments
+// of m cost 2 m + 2 n / m, least at m = sqrt(n).
+int32_t decay_segment_len(int32_t N, int64_t T, int32_t Hv, bool chunks) {
   constexpr int64_t kCtas = 2 * 152;
   const int64_t more = kCtas / Hv - N;  // segments beyond one for each sequence
-  if (more < 1 || T <= 64) return (int32_t)T + 1;
-  int64_t len = ((T + more - 1) / more + 63) / 64 * 64;  // below T + 64
-  const int64_t n = (T + 63) / 64;
-  while (7 * (len / 64) * (len / 64) < n) len += 64;
+  const int64_t unit = chunks ? 64 : kTile;
+  if (more < 1 || T <= (chunks ? 64 : 32)) return (int32_t)T + 1;
+  int64_t len = ((T + more - 1) / more + unit - 1) / unit * unit;  // below T + unit
+  const int64_t n = (T + unit - 1) / unit, per = chunks ? 7 : 8;   // 8 tokens a unit: m^2 >= T
+  while (per * (len / unit) * (len / unit) < n) len += unit;
   return (int32_t)len;
 }
 

@@ -681,9 +681,11 @@ __global__ void __launch_bounds__(kTThreads, 2)
 
 }  // namespace
 
-bool decay_tc_supported(const DecayArgs& p, int32_t dtype, int32_t D) {
+bool decay_tc_fits(int32_t dtype, int32_t D) { return dtype == GDN_BF16 && D == kTd; }
+
+bool decay_tc_supported(const DecayArgs& p) {
   // states are read and written in 32-byte accesses
-  return dtype == GDN_BF16 && D == kTd && reinterpret_cast<uintptr_t>(p.state) % 32 == 0 && tc::encode_fn() != nullptr;
+  return reinterpret_cast<uintptr_t>(p.state) % 32 == 0 && tc::encode_fn() != nullptr;
 }
 
 cudaError_t launch_decay_tc(const DecayArgs& p, const DecaySegments& sg, cudaStream_t stream) {
