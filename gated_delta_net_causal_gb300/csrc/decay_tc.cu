@@ -14,7 +14,7 @@
 //   O2      [j][t] = V^T P^T             V read transposed, P rounded to bf16
 //   dS      [j][i] = V^T K'              K' = e^(G_n - G_s) k as bf16 hi + mid + lo
 // q, k and v are exact in bf16. What is added to the state has three bf16
-// parts (2^-25 of a factor), as the state is kept in fp32. S and P only reach
+// parts (2^-24 of a factor), as the state is kept in fp32. S and P only reach
 // the outputs: one part each where out alone is asked for, whose own rounding
 // is as large (together 1.4 times it), two (2^-17) where core_out is.
 //
@@ -135,6 +135,13 @@ __device__ __forceinline__ uint32_t split2(float2& a) {
   a = fma2(unpack2(r), make_float2(-1.f, -1.f), a);
   return r;
 }
+// the same with the hi part cut off instead of rounded: no conversion, and
+// what is left is exact too
+__device__ __forceinline__ uint32_t cut2(float2& a) {
+  const uint32_t x = __float_as_uint(a.x), y = __float_as_uint(a.y);
+  a = fma2(make_float2(__uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u)), make_float2(-1.f, -1.f), a);
+  return __byte_perm(x, y, 0x7632);
+}
 __device__ __forceinline__ float2 mul2(float2 a, float b) { return fma2(a, make_float2(b, b), make_float2(-0.f, -0.f)); }
 
 // a + b as two floats
@@ -162,6 +169,7 @@ struct TcShared {
   Two G[2][kTc];    // sums of a chunk's log2 decays, by chunk parity
   float E[kTc];     // scale e^(G_t)
   float dk[kTc];    // e^(G_n - G_s), 0 past the chunk's tokens
+  float w[kTd];       // the norm's weights
   float red[4][kTc];  // squares of the outputs by TMEM lane quadrant
   int bad[2][kTd];  // by chunk parity: first token with a non-finite v in this value row, or kTc
   int any_bad[2];
@@ -205,6 +213,7 @@ __global__ void __launch_bounds__(kTThreads, 2)
     fence_mbar_init();
   }
   if (tid < 2 * kTd) (&sh.bad[0][0])[tid] = kTc;
+  if (GATED && tid < kTd) sh.w[tid] = p.norm_w[tid];
   volatile int* abort_flag = &sh.abort;
 
   // the state: columns 64 hh .. 64 hh + 63 of row j
@@ -468,9 +477,9 @@ __global__ void __launch_bounds__(kTThreads, 2)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float2 a = mul2(unpack2(w[e]), d);
-        (&part[0].x)[e] = split2(a);
-        (&part[1].x)[e] = split2(a);
-        (&part[2].x)[e] = pack2(a);
+        (&part[0].x)[e] = cut2(a);
+        (&part[1].x)[e] = cut2(a);
+        (&part[2].x)[e] = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x7632);
       }
       *reinterpret_cast<uint4*>(kt + off) = part[0];
       *reinterpret_cast<uint4*>(sm + kOffMid + off) = part[1];
@@ -489,45 +498,50 @@ __global__ void __launch_bounds__(kTThreads, 2)
       // a lane holds value rows jj + 8 b + 16 a (a, b of 0, 1) and tokens
       // tt + 8 c, tt + 8 c + 1 (c of 0..3)
       const int jj = 32 * qd + (lane >> 2), tt = 32 * hh + 2 * (lane & 3);
-      auto read_half = [&](int a, float (&o)[16]) {
-        float x[16];
-        tmem_ld_16x32(tq + ((uint32_t)(16 * a) << 16) + kColO1 + 32 * hh, o);
-        tmem_ld_16x32(tq + ((uint32_t)(16 * a) << 16) + kColX + 32 * hh, x);
+      // o[2 c + b]: tokens tt + 8 c and the next, value row jj + 8 b + 16 a
+      auto read_half = [&](int a, float2 (&o)[8]) {
+        float x[16], y[16];
+        tmem_ld_16x32(tq + ((uint32_t)(16 * a) << 16) + kColO1 + 32 * hh, x);
+        tmem_ld_16x32(tq + ((uint32_t)(16 * a) << 16) + kColX + 32 * hh, y);
         tc::tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float2 e = *reinterpret_cast<const float2*>(&sh.E[tt + 8 * c]);
-          o[4 * c] = fmaf(o[4 * c], e.x, x[4 * c]);
-          o[4 * c + 1] = fmaf(o[4 * c + 1], e.y, x[4 * c + 1]);
-          o[4 * c + 2] = fmaf(o[4 * c + 2], e.x, x[4 * c + 2]);
-          o[4 * c + 3] = fmaf(o[4 * c + 3], e.y, x[4 * c + 3]);
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            o[2 * c + b] = fma2(make_float2(x[4 * c + 2 * b], x[4 * c + 2 * b + 1]), e,
+                                make_float2(y[4 * c + 2 * b], y[4 * c + 2 * b + 1]));
         }
         if (sh.any_bad[phase])
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (tt + 8 * (i >> 2) + (i & 1) >= sh.bad[phase][jj + 16 * a + 8 * ((i >> 1) & 1)])
-              o[i] = __int_as_float(0x7fc00000);
+          for (int i = 0; i < 8; ++i) {
+            const int bad = sh.bad[phase][jj + 16 * a + 8 * (i & 1)], t = tt + 8 * (i >> 1);
+            if (t >= bad) o[i].x = __int_as_float(0x7fc00000);
+            if (t + 1 >= bad) o[i].y = __int_as_float(0x7fc00000);
+          }
       };
-      float inv[8];
+      float2 inv[4];
       if (GATED) {
-        float sq[8];
+        float2 sq[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sq[i] = 0.f;
+        for (int c = 0; c < 4; ++c) sq[c] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
-          float o[16];
+          float2 o[8];
           read_half(a, o);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) sq[2 * (i >> 2) + (i & 1)] = fmaf(o[i], o[i], sq[2 * (i >> 2) + (i & 1)]);
+          for (int i = 0; i < 8; ++i) sq[i >> 1] = fma2(o[i], o[i], sq[i >> 1]);
         }
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sq[i] += __shfl_xor_sync(0xffffffffu, sq[i], d);
+          for (int c = 0; c < 4; ++c) {
+            sq[c].x += __shfl_xor_sync(0xffffffffu, sq[c].x, d);
+            sq[c].y += __shfl_xor_sync(0xffffffffu, sq[c].y, d);
+          }
         if (lane < 4)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<float2*>(&sh.red[qd][tt + 8 * c]) = make_float2(sq[2 * c], sq[2 * c + 1]);
+          for (int c = 0; c < 4; ++c) *reinterpret_cast<float2*>(&sh.red[qd][tt + 8 * c]) = sq[c];
         asm volatile("bar.sync %0, 128;" ::"r"(1 + hh) : "memory");
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -537,41 +551,42 @@ __global__ void __launch_bounds__(kTThreads, 2)
             const float2 x = *reinterpret_cast<const float2*>(&sh.red[w][tt + 8 * c]);
             r.x += x.x, r.y += x.y;
           }
-          inv[2 * c] = rsqrtf(r.x * (1.f / kTd) + p.rms_eps);
-          inv[2 * c + 1] = rsqrtf(r.y * (1.f / kTd) + p.rms_eps);
+          inv[c] = make_float2(rsqrtf(r.x * (1.f / kTd) + p.rms_eps), rsqrtf(r.y * (1.f / kTd) + p.rms_eps));
         }
       }
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
-        float o[16];
+        float2 o[8];
         read_half(a, o);
         if (CORE)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int t = tt + 8 * (i >> 2) + (i & 1);
-            if (t < n) p.core_out[((int64_t)(t0 + t) * p.Hv + h) * kTd + jj + 16 * a + 8 * ((i >> 1) & 1)] = o[i];
+          for (int i = 0; i < 8; ++i) {
+            const int t = tt + 8 * (i >> 1);
+            float* at = p.core_out + ((int64_t)(t0 + t) * p.Hv + h) * kTd + jj + 16 * a + 8 * (i & 1);
+            if (t < n) at[0] = o[i].x;
+            if (t + 1 < n) at[p.Hv * kTd] = o[i].y;
           }
         // blocks (rows jj block 0 and 1 of this half) x (token blocks 2 d, 2 d + 1)
 #pragma unroll
         for (int d = 0; d < 2; ++d) {
           const int t = 32 * hh + 16 * d + 8 * (lane >> 4) + (lane & 7), c8 = 4 * qd + 2 * a + ((lane >> 3) & 1);
           const uint32_t at = smem_u32(sm + kOffO) + (c8 >> 3) * 8192 + t * 128 + (((c8 & 7) ^ (t & 7)) << 4);
-          float* x = o + 8 * d;
           uint32_t r[4];
           if (GATED) {
             ldmatrix_t4(at, r);
-            const float w0 = __ldg(p.norm_w + jj + 16 * a), w1 = __ldg(p.norm_w + jj + 16 * a + 8);
+            const float w0 = sh.w[jj + 16 * a], w1 = sh.w[jj + 16 * a + 8];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
               const float2 z = unpack2(r[m]);
-              const float w = m & 1 ? w1 : w0;
-              const int c = 2 * d + (m >> 1);
-              x[2 * m] *= inv[2 * c] * w * silu_fast(z.x);
-              x[2 * m + 1] *= inv[2 * c + 1] * w * silu_fast(z.y);
+              const float2 e = mul2(z, -kLog2e);
+              const float2 den = make_float2(1.f + exp2_fast(e.x), 1.f + exp2_fast(e.y));
+              const float2 silu = make_float2(__fdividef(z.x, den.x), __fdividef(z.y, den.y));
+              const float2 g = fma2(silu, mul2(inv[2 * d + (m >> 1)], m & 1 ? w1 : w0), make_float2(-0.f, -0.f));
+              o[4 * d + m] = fma2(o[4 * d + m], g, make_float2(-0.f, -0.f));
             }
           }
 #pragma unroll
-          for (int m = 0; m < 4; ++m) r[m] = pack2(make_float2(x[2 * m], x[2 * m + 1]));
+          for (int m = 0; m < 4; ++m) r[m] = pack2(o[4 * d + m]);
           stmatrix_t4(at, r);
         }
       }
