@@ -1,0 +1,643 @@
+// The chunk-wise form of decay_tc.cu as a pipeline, for sequences of several
+// chunks: one CTA per SM, whose warps hand each other tiles through mbarriers
+// instead of meeting at barriers.
+//
+// Sixteen warps compute, one issues the MMAs, one loads, one sums the log
+// decays and one stores the outputs and loads z into their places. Per chunk c the compute warps go
+//   P(c)   from the scores, which were issued a chunk ahead
+//   K'(c)  in three bf16 parts
+//   the outputs, from O1(c) and O2(c)
+//   S      from dS(c), and its bf16 copy for O1(c + 1)
+// while the tensor cores run O2(c), dS(c), the scores of c + 1 and O1(c + 1),
+// each as soon as its operands are there: O2 runs under K', dS under the
+// outputs, the scores and O1 under everything. q, k, v, z and the outputs have
+// two stages, and TMEM holds every accumulator side by side.
+//
+// The first pass over a sequence of several segments (kTLocal) is K' and dS
+// alone, with two stages of K' and of the accumulator too.
+//
+// A wait that gives up raises the CTA's abort flag; every role then runs
+// through its remaining waits at once and the kernel ends.
+#include "decay_tc.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kPCompute = 16;  // compute warps: TMEM lane quadrant warp % 4, column quarter warp / 4
+constexpr int kPMma = 16, kPLoad = 17, kPGates = 18, kPStore = 19;
+constexpr int kPThreads = 32 * 20;
+enum { kPWhole = 0, kPLocal = 1 };
+
+// shared memory, from a 1024-byte boundary; tiles of 64 tokens x 128 columns
+// are two boxes of 64 columns, 128-byte swizzled rows
+constexpr uint32_t kPTile = 16384;
+constexpr uint32_t kPQ = 0;            // [2]
+constexpr uint32_t kPK = 2 * kPTile;   // [2] K, then K' hi in place
+constexpr uint32_t kPV = 4 * kPTile;   // [2]
+constexpr uint32_t kPMid = 6 * kPTile;  // K' mid, K' lo
+constexpr uint32_t kPP = 8 * kPTile;   // P and its low part; first pass: the second K' mid and lo
+constexpr uint32_t kPO = 9 * kPTile;   // [2] z, then the outputs in its place
+constexpr uint32_t kPSmem = 11 * kPTile;
+__device__ __forceinline__ uint32_t mid_at(int stage) { return stage ? kPO : kPMid; }
+
+// TMEM columns
+constexpr uint32_t kPColS = 0;     // S hi (64 packed columns), S lo (64)
+constexpr uint32_t kPColSc = 128;  // scores
+constexpr uint32_t kPColO2 = 192;
+constexpr uint32_t kPColO1 = 256;
+constexpr uint32_t kPColKv = 320;  // dS; first pass: at 0 and 128
+constexpr uint32_t kPCols = 512;
+
+// 16 lanes x 16 columns, as tmem_ld_16x32
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+struct PipeShared {
+  Two G[4][kTc];     // by chunk % 4: sums of log2 decays
+  float E[4][kTc];   // scale e^(G_t)
+  float dk[4][kTc];  // e^(G_n - G_s), 0 past the chunk's tokens
+  Decay whole[4];    // e^(G_n)
+  int bad[4][kTd];   // first token with a non-finite v in this value row, or kTc
+  int any_bad[4];
+  float red[4][kTc];  // squares of the outputs by TMEM lane quadrant
+  float w[kTd];       // the norm's weights
+  int abort;
+  uint32_t tmem;
+  // by chunk % 2, but gates by chunk % 4
+  uint64_t full[2], empty[2], z[2], gates[4], p[2], k[2], o[2];
+  uint64_t s, scores, outs, delta[2];
+};
+
+template <int MODE, bool CORE, bool GATED>
+__global__ void __launch_bounds__(kPThreads, 1)
+    decay_pipe_kernel(const DecayArgs p, const DecaySegments sg, const __grid_constant__ CUtensorMap tm_q,
+                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_o) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ PipeShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int slot = blockIdx.x / (unsigned)p.Hv;  // a segment's V heads side by side: they share q, k in L2
+  const int h = blockIdx.x % (unsigned)p.Hv;
+  const int kh = k_head_of(p.map, h, p.Hk, p.rep);
+  DecaySegment s;
+  if (!find_segment(p, sg, slot, lane, &s)) return;
+  if (MODE == kPLocal && s.index + 1 == s.parts) return;
+  const int chunks = (s.end - s.begin + kTc - 1) / kTc;
+
+  if (warp == kPMma) {
+    tc::tmem_alloc(&sh.tmem, kPCols);
+    tc::tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.z[i], 1);
+      mbar_init(&sh.p[i], kPCompute);
+      mbar_init(&sh.k[i], kPCompute);
+      mbar_init(&sh.o[i], kPCompute);
+      mbar_init(&sh.delta[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh.gates[i], 1);
+      sh.any_bad[i] = 0;
+    }
+    mbar_init(&sh.s, kPCompute);
+    mbar_init(&sh.scores, 1);
+    mbar_init(&sh.outs, 1);
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (tid < 4 * kTd) (&sh.bad[0][0])[tid] = kTc;
+  if (GATED && tid < kTd) sh.w[tid] = p.norm_w[tid];
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tb = sh.tmem;
+  volatile int* abort_flag = &sh.abort;
+  const auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, abort_flag); };
+  const auto tokens = [&](int c) { return s.end - s.begin - c * kTc < kTc ? s.end - s.begin - c * kTc : kTc; };
+
+  if (warp == kPMma) {
+    // ---------------------------------------------------------------- MMAs
+    const uint32_t id_s = tc::idesc(tc::kBF16, 64, 64), id_o1 = tc::idesc(tc::kBF16, 128, 64);
+    const uint32_t id_o2 = id_o1 | kTransA, id_d = tc::idesc(tc::kBF16, 128, 128) | kTransA | kTransB;
+    const uint64_t dP = tc::sdesc_sw128(smem_u32(sm + kPP));
+    const auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
+    const auto issue_scores = [&](int st) {
+      const uint64_t dQ = tc::sdesc_sw128(smem_u32(sm + kPQ + st * kPTile));
+      const uint64_t dK = tc::sdesc_sw128(smem_u32(sm + kPK + st * kPTile));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        tc::mma_f16_elect(tb + kPColSc, tc::sdesc_at(dQ, 64, i), tc::sdesc_at(dK, 64, i), id_s, i > 0);
+      tc::mma_commit_elect(&sh.scores);
+    };
+    const auto issue_o1 = [&](int st) {
+      const uint64_t dQ = tc::sdesc_sw128(smem_u32(sm + kPQ + st * kPTile));
+#pragma unroll
+      for (int i = 0; i < (CORE ? 16 : 8); ++i)
+        tc::mma_f16_ts_elect(tb + kPColO1, tb + kPColS + 8 * i, tc::sdesc_at(dQ, 64, i & 7), id_o1, i > 0);
+    };
+    bool ok = true;
+    if (MODE == kPWhole) {
+      ok = all(wait(&sh.full[0], 0));
+      if (ok) issue_scores(0);
+      ok = ok && all(wait(&sh.s, 0));
+      tc::fence_after_sync();
+      if (ok) issue_o1(0);
+    }
+    for (int c = 0; ok && c < chunks; ++c) {
+      const int st = c & 1;
+      const uint32_t round = (c >> 1) & 1;
+      const uint64_t dV = sdesc_mn128(smem_u32(sm + kPV + st * kPTile));
+      if (MODE == kPWhole) {
+        ok = all(wait(&sh.p[st], round));
+        if (!ok) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int i = 0; i < (CORE ? 8 : 4); ++i)
+          tc::mma_f16_elect(tb + kPColO2, dV + ((i & 3) * 2048 >> 4), dP + (((i >> 2) * 8192 + (i & 3) * 32) >> 4), id_o2,
+                            i > 0);
+        tc::mma_commit_elect(&sh.outs);
+      }
+      ok = all(wait(&sh.k[st], round));
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint64_t dK0 = sdesc_mn128(smem_u32(sm + kPK + st * kPTile));
+      const uint64_t dK1 = sdesc_mn128(smem_u32(sm + (MODE == kPLocal ? mid_at(st) : kPMid)));
+      const uint32_t acc = tb + (MODE == kPLocal ? 128u * st : kPColKv);
+#pragma unroll
+      for (int i = 0; i < 12; ++i)
+        tc::mma_f16_elect(acc, dV + ((i & 3) * 2048 >> 4),
+                          (i < 4 ? dK0 : dK1 + (i < 8 ? 0 : kPTile >> 4)) + ((i & 3) * 2048 >> 4), id_d, i > 0);
+      tc::mma_commit_elect(&sh.delta[MODE == kPLocal ? st : 0]);
+      tc::mma_commit_elect(&sh.empty[st]);
+      if (MODE == kPWhole && c + 1 < chunks) {
+        ok = all(wait(&sh.full[st ^ 1], ((c + 1) >> 1) & 1));
+        if (!ok) break;
+        issue_scores(st ^ 1);
+        ok = all(wait(&sh.s, (c + 1) & 1));
+        if (!ok) break;
+        tc::fence_after_sync();
+        issue_o1(st ^ 1);
+      }
+    }
+  } else if (warp == kPLoad) {
+    // --------------------------------------------------------------- loads
+    if (lane == 0) {
+      const auto load = [&](int c) {
+        const int st = c & 1, t0 = s.begin + c * kTc;
+        mbar_arrive_expect_tx(&sh.full[st], (MODE == kPWhole ? 3 : 2) * kPTile);
+        for (int b = 0; b < 2; ++b) {
+          if (MODE == kPWhole)
+            tc::tma_load_2d(sm + kPQ + st * kPTile + 8192 * b, &tm_q, kh * kTd + 64 * b, t0, &sh.full[st]);
+          tc::tma_load_2d(sm + kPK + st * kPTile + 8192 * b, &tm_k, kh * kTd + 64 * b, t0, &sh.full[st]);
+          tc::tma_load_2d(sm + kPV + st * kPTile + 8192 * b, &tm_v, h * kTd + 64 * b, t0, &sh.full[st]);
+        }
+      };
+      load(0);
+      int n = 1;
+      for (; n < chunks; ++n) {
+        if (n >= 2 && !wait(&sh.empty[n & 1], ((n >> 1) - 1) & 1)) break;
+        load(n);
+      }
+      // none may be in flight when the CTA ends: load i went to stage i % 2
+      mbar_wait(&sh.full[0], ((n + 1) / 2 - 1) & 1);
+      if (n > 1) mbar_wait(&sh.full[1], (n / 2 - 1) & 1);
+    }
+  } else if (warp == kPGates) {
+    // ------------------------------------------------- sums of log decays
+    // A buffer is written again four chunks later; o(c) seen means that every
+    // warp has left chunk c - 1 (in the first pass: that the state has taken
+    // chunk c). The compute warps cannot reach o(c + 2) before gates(c + 2),
+    // given after o(c) was seen, so none is missed.
+    float g0 = 0.f, g1 = 0.f;  // log decays of tokens 2 lane and 2 lane + 1 of a chunk
+    const auto fetch_g = [&](int c) {
+      const int t = s.begin + c * kTc + 2 * lane;
+      const float* g = p.g + t * p.g_stride + h;
+      g0 = t < s.end ? g[0] : 0.f;
+      g1 = t + 1 < s.end ? g[p.g_stride] : 0.f;
+    };
+    Two total{0.f, 0.f};  // of the segment, log2
+    fetch_g(0);
+    for (int c = 0; c < chunks; ++c) {
+      if (MODE == kPWhole && c >= 2) __all_sync(0xffffffffu, wait(&sh.o[c & 1], ((c - 2) >> 1) & 1));
+      if (MODE == kPLocal && c >= 3) __all_sync(0xffffffffu, wait(&sh.o[(c - 3) & 1], ((c - 3) >> 1) & 1));
+      // inclusive sums over the chunk, as two floats; tokens past the chunk's
+      // have log decay 0, so lane 31 ends with G_n
+      const int at = c & 3, n = tokens(c);
+      const Two first = to_log2(decay_log(g0));
+      Two incl = add2(first, to_log2(decay_log(g1)));
+      fetch_g(c + 1);
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const Two o{__shfl_up_sync(0xffffffffu, incl.hi, d), __shfl_up_sync(0xffffffffu, incl.lo, d)};
+        if (lane >= d) incl = add2(incl, o);
+      }
+      const Two prev{__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+      const Two a = lane > 0 ? add2(prev, first) : first, b = incl;
+      const Two gn{__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)};
+      if (MODE == kPWhole) {
+        sh.G[at][2 * lane] = a;
+        sh.G[at][2 * lane + 1] = b;
+        sh.E[at][2 * lane] = p.scale * exp2_fast(a.hi + a.lo);
+        sh.E[at][2 * lane + 1] = p.scale * exp2_fast(b.hi + b.lo);
+        for (int i = lane; i < kTd; i += 32) sh.bad[at][i] = kTc;
+        if (lane == 0) sh.any_bad[at] = 0;
+      } else {
+        total = add2(total, gn);
+      }
+      sh.dk[at][2 * lane] = 2 * lane < n ? exp2_fast((gn.hi - a.hi) + (gn.lo - a.lo)) : 0.f;
+      sh.dk[at][2 * lane + 1] = 2 * lane + 1 < n ? exp2_fast((gn.hi - b.hi) + (gn.lo - b.lo)) : 0.f;
+      if (lane == 0) sh.whole[at] = decay_factor((gn.hi + gn.lo) * kLn2);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.gates[at]);
+    }
+    if (MODE == kPLocal && lane == 0 && !*abort_flag) sg.decays[blockIdx.x] = exp2f(total.hi + total.lo);
+  } else if (warp == kPStore) {
+    // ------------------------------------------------------ z in, outputs out
+    // (as for the gates: z(c + 2), or its place, is given after o(c) was seen)
+    if (MODE == kPWhole) {
+      uint32_t n_z = 0;
+      const auto give_z = [&](int c) {
+        const int st = c & 1;
+        if (GATED) {
+          ++n_z;
+          mbar_arrive_expect_tx(&sh.z[st], kPTile);
+          for (int b = 0; b < 2; ++b)
+            tc::tma_load_2d(sm + kPO + st * kPTile + 8192 * b, &tm_z, h * kTd + 64 * b, s.begin + c * kTc, &sh.z[st]);
+        } else {
+          mbar_arrive(&sh.z[st]);
+        }
+      };
+      if (lane == 0) {
+        give_z(0);
+        if (chunks > 1) give_z(1);
+      }
+      for (int c = 0; c < chunks; ++c) {
+        const int st = c & 1;
+        const bool ok = __all_sync(0xffffffffu, wait(&sh.o[st], (c >> 1) & 1));
+        const int n = tokens(c), t0 = s.begin + c * kTc;
+        const unsigned char* tile = sm + kPO + st * kPTile;
+        if (ok && (!CORE || p.out != nullptr)) {
+          if (n == kTc) {
+            if (lane == 0) {
+              for (int b = 0; b < 2; ++b) tc::tma_store_2d(&tm_o, h * kTd + 64 * b, t0, tile + 8192 * b);
+              bulk_commit();
+              bulk_wait_read_all();
+            }
+          } else {  // a last, shorter chunk: its rows alone
+            for (int u = lane; u < 16 * n; u += 32) {
+              const int t = u >> 4, c8 = u & 15;
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + ((int64_t)(t0 + t) * p.Hv + h) * kTd + 8 * c8) =
+                  *reinterpret_cast<const uint4*>(tile + (c8 >> 3) * 8192 + t * 128 + (((c8 & 7) ^ (t & 7)) << 4));
+            }
+          }
+        }
+        if (lane == 0 && c + 2 < chunks) give_z(c + 2);
+      }
+      if (lane == 0) {
+        if (GATED) {
+          mbar_wait(&sh.z[0], ((n_z + 1) / 2 - 1) & 1);
+          if (n_z > 1) mbar_wait(&sh.z[1], (n_z / 2 - 1) & 1);
+        }
+        bulk_wait_all();
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- compute
+    const int qd = warp & 3, hh = warp >> 2;
+    const int j = 32 * qd + lane;  // this thread's value row; columns 32 hh .. 32 hh + 31 of the state
+    const uint32_t tq = tb + ((uint32_t)(32 * qd) << 16);
+    float2 S[16];
+    float* gS = p.state + ((int64_t)s.seq * p.Hv + h) * (int64_t)(kTd * kTd);
+    const int at0 = j * kTd + 32 * hh;
+    {
+      float4 x[8];
+      if (MODE == kPLocal) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s.index == 0) {
+          float* keep = sg.states + ((int64_t)(s.slot + s.parts - 1) * p.Hv + h) * (kTd * kTd);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) load8(gS + at0 + 8 * e, x[2 * e], x[2 * e + 1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) store8(keep + at0 + 8 * e, x[2 * e], x[2 * e + 1]);
+        }
+      } else if (s.parts == 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) load8(gS + at0 + 8 * e, x[2 * e], x[2 * e + 1]);
+      } else {
+        DecaySlots(p, sg, s, h, kTd * kTd).start8<4>(s.index, s.parts, at0, x);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        S[2 * e] = make_float2(x[e].x, x[e].y);
+        S[2 * e + 1] = make_float2(x[e].z, x[e].w);
+      }
+    }
+    bool failed = false;
+    // all of the warp's tile is in place for the tensor cores or for TMA
+    const auto hand = [&](uint64_t* bar) {
+      fence_proxy_async_smem();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    // S as the A operand of O1: packed pairs, and with core_out what their rounding left
+    const auto put_state = [&]() {
+      uint32_t hi[16];
+      if (CORE) {
+        uint32_t lo[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float2 a = S[e];
+          hi[e] = split2(a);
+          lo[e] = pack2(a);
+        }
+        tc::tmem_st16u(tq + kPColS + 64 + 16 * hh, lo);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) hi[e] = pack2(S[e]);
+      }
+      tc::tmem_st16u(tq + kPColS + 16 * hh, hi);
+      tc::tmem_wait_st();
+      hand(&sh.s);
+    };
+    // S <- e^(G_n) S + dS of chunk c
+    const auto take_delta = [&](int c) {
+      const Decay a = sh.whole[c & 3];
+      const uint32_t parity = MODE == kPLocal ? (c >> 1) & 1 : c & 1;
+      if (!wait(&sh.delta[MODE == kPLocal ? c & 1 : 0], parity)) failed = true;
+      tc::fence_after_sync();
+      float d[32];
+      const uint32_t col = tq + (MODE == kPLocal ? 128u * (c & 1) : kPColKv) + 32 * hh;
+      tc::tmem_ld16(col, *reinterpret_cast<float(*)[16]>(d));
+      tc::tmem_ld16(col + 16, *reinterpret_cast<float(*)[16]>(d + 16));
+      tc::tmem_wait_ld();
+      const float2 f = make_float2(a.factor, a.factor), keep = make_float2(a.keep, a.keep);
+      if (a.keep != 0.f) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) S[e] = fma2(f, S[e], fma2(keep, S[e], make_float2(d[2 * e], d[2 * e + 1])));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) S[e] = fma2(f, S[e], make_float2(d[2 * e], d[2 * e + 1]));
+      }
+      if (MODE == kPWhole && sh.any_bad[c & 3] && sh.bad[c & 3][j] < kTc)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) S[e] = make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
+    };
+    if (MODE == kPWhole) put_state();
+
+    for (int c = 0; c < chunks; ++c) {
+      const int n = tokens(c), st = c & 1, at = c & 3;
+      const uint32_t round = (c >> 1) & 1;
+      const Two* G = sh.G[at];
+      if (!wait(&sh.gates[at], (c >> 2) & 1)) failed = true;
+      if (!wait(&sh.full[st], round)) failed = true;
+      unsigned char* kt = sm + kPK + st * kPTile;
+      if (MODE == kPWhole) {
+        // v: rows past the chunk's tokens are another sequence's (or stale): 0
+        // there; non-finite elements are noted and replaced by 0
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int u = tid + i * 32 * kPCompute, row = u >> 4, c16 = u & 15;
+          uint4* v = reinterpret_cast<uint4*>(sm + kPV + st * kPTile + (c16 >> 3) * 8192 + row * 128 +
+                                              (((c16 & 7) ^ (row & 7)) << 4));
+          uint4 x = *v;
+          uint32_t* w = &x.x;
+          uint32_t hit = 0;  // an exponent of all ones carries into the sign's place
+#pragma unroll
+          for (int e = 0; e < 4; ++e) hit |= (w[e] & 0x7f807f80u) + 0x00800080u;
+          if (row >= n) {
+            *v = make_uint4(0, 0, 0, 0);
+          } else if ((hit & 0x80008000u) != 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (((w[e >> 1] >> (16 * (e & 1))) & 0x7f80u) == 0x7f80u) {
+                atomicMin(&sh.bad[at][8 * c16 + e], row);
+                w[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+              }
+            *v = x;
+            sh.any_bad[at] = 1;
+          }
+        }
+        // P: a lane has rows ta and ta + 8, columns s0 + 8 c and the next
+        const int ta = 16 * qd + (lane >> 2), s0 = 16 * hh + 2 * (lane & 3);
+        if (!wait(&sh.scores, c & 1)) failed = true;
+        tc::fence_after_sync();
+        float x[8];
+        tmem_ld_16x16(tq + kPColSc + 16 * hh, x);
+        tc::tmem_wait_ld();
+        const Two ga = G[ta], gb = G[ta + 8];
+        unsigned char* pp = sm + kPP + ta * 128 + 4 * (lane & 3);  // the rows are eight apart: the same swizzle
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int sc = s0 + 8 * i;
+          const Two u0 = G[sc], u1 = G[sc + 1];
+          float2 y = make_float2(x[4 * i] * exp2_fast((ga.hi - u0.hi) + (ga.lo - u0.lo)),
+                                 x[4 * i + 1] * exp2_fast((ga.hi - u1.hi) + (ga.lo - u1.lo)));
+          float2 z = make_float2(x[4 * i + 2] * exp2_fast((gb.hi - u0.hi) + (gb.lo - u0.lo)),
+                                 x[4 * i + 3] * exp2_fast((gb.hi - u1.hi) + (gb.lo - u1.lo)));
+          y = mul2(y, p.scale);
+          z = mul2(z, p.scale);
+          if (sc > ta) y.x = 0.f;
+          if (sc + 1 > ta) y.y = 0.f;
+          if (sc > ta + 8) z.x = 0.f;
+          if (sc + 1 > ta + 8) z.y = 0.f;
+          unsigned char* to = pp + (((2 * hh + i) ^ (ta & 7)) << 4);
+          *reinterpret_cast<uint32_t*>(to) = CORE ? split2(y) : pack2(y);
+          *reinterpret_cast<uint32_t*>(to + 1024) = CORE ? split2(z) : pack2(z);
+          if (CORE) {
+            *reinterpret_cast<uint32_t*>(to + 8192) = pack2(y);
+            *reinterpret_cast<uint32_t*>(to + 8192 + 1024) = pack2(z);
+          }
+        }
+        hand(&sh.p[st]);
+      }
+
+      // K' = e^(G_n - G_s) k in three parts, the first in place of K
+      {
+        unsigned char* mid = sm + (MODE == kPLocal ? mid_at(st) : kPMid);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int u = tid + i * 32 * kPCompute, row = u >> 4, c16 = u & 15;
+          const uint32_t off = (c16 >> 3) * 8192 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4);
+          uint4 x = *reinterpret_cast<const uint4*>(kt + off);
+          if (row >= n) x = make_uint4(0, 0, 0, 0);  // another sequence's: may be a NaN
+          const uint32_t* w = &x.x;
+          const float d = sh.dk[at][row];
+          uint4 part[3];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float2 a = mul2(unpack2(w[e]), d);
+            (&part[0].x)[e] = cut2(a);
+            (&part[1].x)[e] = cut2(a);
+            (&part[2].x)[e] = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x7632);
+          }
+          *reinterpret_cast<uint4*>(kt + off) = part[0];
+          *reinterpret_cast<uint4*>(mid + off) = part[1];
+          *reinterpret_cast<uint4*>(mid + kPTile + off) = part[2];
+        }
+        hand(&sh.k[st]);
+      }
+
+      if (MODE == kPWhole) {
+        if (!wait(&sh.z[st], round)) failed = true;
+        if (!wait(&sh.outs, c & 1)) failed = true;
+        tc::fence_after_sync();
+        // o[a][2 c + b]: tokens tt + 8 c and the next, value row jj + 8 b + 16 a
+        const int jj = 32 * qd + (lane >> 2), tt = 16 * hh + 2 * (lane & 3);
+        float2 o[2][4];
+        {
+          float x[2][8], y[2][8];
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            tmem_ld_16x16(tq + ((uint32_t)(16 * a) << 16) + kPColO1 + 16 * hh, x[a]);
+            tmem_ld_16x16(tq + ((uint32_t)(16 * a) << 16) + kPColO2 + 16 * hh, y[a]);
+          }
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 e = *reinterpret_cast<const float2*>(&sh.E[at][tt + 8 * i]);
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+                o[a][2 * i + b] = fma2(make_float2(x[a][4 * i + 2 * b], x[a][4 * i + 2 * b + 1]), e,
+                                       make_float2(y[a][4 * i + 2 * b], y[a][4 * i + 2 * b + 1]));
+          }
+        }
+        if (sh.any_bad[at])
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int bad = sh.bad[at][jj + 16 * (i >> 2) + 8 * (i & 1)], t = tt + 8 * ((i >> 1) & 1);
+            if (t >= bad) o[i >> 2][i & 3].x = __int_as_float(0x7fc00000);
+            if (t + 1 >= bad) o[i >> 2][i & 3].y = __int_as_float(0x7fc00000);
+          }
+        if (CORE)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int t = tt + 8 * ((i >> 1) & 1);
+            float* to = p.core_out + ((int64_t)(s.begin + c * kTc + t) * p.Hv + h) * kTd + jj + 16 * (i >> 2) + 8 * (i & 1);
+            if (t < n) to[0] = o[i >> 2][i & 3].x;
+            if (t + 1 < n) to[p.Hv * kTd] = o[i >> 2][i & 3].y;
+          }
+        float2 inv[2];
+        if (GATED) {
+          // squares over the value rows: the lanes' rows, then the four quadrants
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float2 sq = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+              for (int b = 0; b < 2; ++b) sq = fma2(o[a][2 * i + b], o[a][2 * i + b], sq);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+              sq.x += __shfl_xor_sync(0xffffffffu, sq.x, d);
+              sq.y += __shfl_xor_sync(0xffffffffu, sq.y, d);
+            }
+            if (lane < 4) *reinterpret_cast<float2*>(&sh.red[qd][tt + 8 * i]) = sq;
+          }
+          // the four warps of these tokens; before the next chunk's squares
+          // every one of them has read these (its outputs are handed on)
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + hh) : "memory");
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float2 r = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const float2 x = *reinterpret_cast<const float2*>(&sh.red[w][tt + 8 * i]);
+              r.x += x.x, r.y += x.y;
+            }
+            inv[i] = make_float2(rsqrtf(r.x * (1.f / kTd) + p.rms_eps), rsqrtf(r.y * (1.f / kTd) + p.rms_eps));
+          }
+        }
+        // blocks (value rows b of half a) x (token blocks 0, 1)
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          const int t = 16 * hh + 8 * (lane >> 4) + (lane & 7), c8 = 4 * qd + 2 * a + ((lane >> 3) & 1);
+          const uint32_t to = smem_u32(sm + kPO + st * kPTile) + (c8 >> 3) * 8192 + t * 128 + (((c8 & 7) ^ (t & 7)) << 4);
+          uint32_t r[4];
+          if (GATED) {
+            ldmatrix_t4(to, r);
+            const float w0 = sh.w[jj + 16 * a], w1 = sh.w[jj + 16 * a + 8];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const float2 z = unpack2(r[m]);
+              const float2 e = mul2(z, -kLog2e);
+              const float2 den = make_float2(1.f + exp2_fast(e.x), 1.f + exp2_fast(e.y));
+              const float2 silu = make_float2(__fdividef(z.x, den.x), __fdividef(z.y, den.y));
+              const float2 g = fma2(silu, mul2(inv[m >> 1], m & 1 ? w1 : w0), make_float2(-0.f, -0.f));
+              o[a][m] = fma2(o[a][m], g, make_float2(-0.f, -0.f));
+            }
+          }
+#pragma unroll
+          for (int m = 0; m < 4; ++m) r[m] = pack2(o[a][m]);
+          stmatrix_t4(to, r);
+        }
+        hand(&sh.o[st]);
+        take_delta(c);
+        if (c + 1 < chunks) put_state();
+      } else if (c > 0) {
+        take_delta(c - 1);
+        hand(&sh.o[st ^ 1]);
+      }
+    }
+    if (MODE == kPLocal) take_delta(chunks - 1);
+    if (!failed && !*abort_flag && (MODE == kPLocal || s.index + 1 == s.parts)) {
+      float* to = MODE == kPLocal ? sg.states + (int64_t)blockIdx.x * (kTd * kTd) : gS;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        store8(to + at0 + 8 * e, make_float4(S[4 * e].x, S[4 * e].y, S[4 * e + 1].x, S[4 * e + 1].y),
+               make_float4(S[4 * e + 2].x, S[4 * e + 2].y, S[4 * e + 3].x, S[4 * e + 3].y));
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kPMma) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tb, kPCols);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_decay_pipe(const DecayArgs& p, const DecaySegments& sg, cudaStream_t stream) {
+  const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUtensorMap mq, mk, mv, mz{}, mo{};  // the maps of what is not there are never used
+  const int64_t vw = (int64_t)p.Hv * kTd;
+  if (!tc::make_map_2d(&mq, p.q, p.T, (int64_t)p.Hk * kTd, p.q_stride, 2, bf, 64, kTc, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !tc::make_map_2d(&mk, p.k, p.T, (int64_t)p.Hk * kTd, p.k_stride, 2, bf, 64, kTc, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !tc::make_map_2d(&mv, p.v, p.T, vw, p.v_stride, 2, bf, 64, kTc, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      (p.z != nullptr && !tc::make_map_2d(&mz, p.z, p.T, vw, p.z_stride, 2, bf, 64, kTc, CU_TENSOR_MAP_SWIZZLE_128B)) ||
+      (p.out != nullptr && !tc::make_map_2d(&mo, p.out, p.T, vw, vw, 2, bf, 64, kTc, CU_TENSOR_MAP_SWIZZLE_128B)))
+    return cudaErrorInvalidValue;
+  const unsigned grid = (unsigned)(sg.slots * p.Hv);
+  const auto run = [&](auto* kernel) {
+    constexpr int smem = (int)kPSmem + 1024;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kPThreads, smem, stream>>>(p, sg, mq, mk, mv, mz, mo);
+    return cudaGetLastError();
+  };
+  if (sg.states != nullptr) {
+    const cudaError_t e = run(decay_pipe_kernel<kPLocal, false, false>);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.core_out != nullptr)
+    return p.z != nullptr ? run(decay_pipe_kernel<kPWhole, true, true>) : run(decay_pipe_kernel<kPWhole, true, false>);
+  return p.z != nullptr ? run(decay_pipe_kernel<kPWhole, false, true>) : run(decay_pipe_kernel<kPWhole, false, false>);
+}
+
+}  // namespace gdn
+
+GDN_DEFINE_ERROR_READER(decay_pipe)

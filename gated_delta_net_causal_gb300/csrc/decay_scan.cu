@@ -230,7 +230,7 @@ cudaError_t launch_scan_t(const DecayArgs& p, const DecaySegments& sg, int32_t D
 // tokens (whatever D: both go with the state's size), so n tokens in segments
 // of m cost 2 m + 2 n / m, least at m = sqrt(n).
 int32_t decay_segment_len(int32_t N, int64_t T, int32_t Hv, bool chunks) {
-  constexpr int64_t kCtas = 2 * 152;
+  const int64_t kCtas = chunks ? 152 : 304;
   const int64_t more = kCtas / Hv - N;  // segments beyond one for each sequence
   const int64_t unit = chunks ? 64 : kTile;
   if (more < 1 || T <= (chunks ? 64 : 32)) return (int32_t)T + 1;

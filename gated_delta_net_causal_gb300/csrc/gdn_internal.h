@@ -207,6 +207,8 @@ cudaError_t launch_decay_scan(const DecayArgs& p, const DecaySegments& sg, int32
 // whether it takes this state, too
 bool decay_tc_supported(const DecayArgs& p);
 cudaError_t launch_decay_tc(const DecayArgs& p, const DecaySegments& sg, cudaStream_t stream);
+cudaError_t launch_decay_pipe(const DecayArgs& p, const DecaySegments& sg, cudaStream_t stream);  // decay_pipe.cu
+cudaError_t read_error_decay_pipe(int32_t* status, bool clear);
 cudaError_t read_error_decay_tc(int32_t* status, bool clear);
 cudaError_t launch_add_rmsnorm(const AddRmsNormArgs& p, int32_t dtype, cudaStream_t stream);
 cudaError_t launch_linear_fp8(const LinearFp8Args& p, const void* x, int64_t x_stride, const void* w,
