@@ -2,7 +2,6 @@
 // Nothing is enqueued unless every check passes.
 #include <math.h>
 #include <stdint.h>
-#include <stdlib.h>
 
 #include "gdn.h"
 #include "gdn_internal.h"
@@ -673,7 +672,7 @@ gdn_status decay_plan(const gdn_dims* dims, int32_t num_seqs, int64_t total_toke
   *bytes = 0;
   *decays_at = 0;
   sg->len = gdn::decay_segment_len(num_seqs, total_tokens, dims->n_v_heads,
-                                   gdn::decay_tc_fits(dims->io_dtype, dims->head_dim));
+                                   gdn::decay_tc_fits(dims->io_dtype, dims->head_dim, num_seqs, total_tokens));
   sg->slots = total_tokens / sg->len + num_seqs;
   sg->states = nullptr;
   sg->decays = nullptr;
@@ -746,8 +745,8 @@ gdn_status gdn_decay_prefill(const gdn_dims* dims, int32_t num_seqs, const int32
     sg.len = (int32_t)total_tokens + 1;
     sg.slots = num_seqs;
   }
-  if (gdn::decay_tc_fits(dims->io_dtype, dims->head_dim) && gdn::decay_tc_supported(p))
-    return cuda_status((getenv("GDN_OLD") ? gdn::launch_decay_tc : gdn::launch_decay_pipe)(p, sg, static_cast<cudaStream_t>(stream)));
+  if (gdn::decay_tc_fits(dims->io_dtype, dims->head_dim, num_seqs, total_tokens) && gdn::decay_tc_supported(p))
+    return cuda_status(gdn::launch_decay_tc(p, sg, static_cast<cudaStream_t>(stream)));
   return cuda_status(gdn::launch_decay_scan(p, sg, dims->io_dtype, dims->head_dim, static_cast<cudaStream_t>(stream)));
 }
 
@@ -853,7 +852,7 @@ gdn_status gdn_device_error(int32_t* status, int32_t clear) {
                                                gdn::read_error_prefill_tc,
                                                gdn::read_error_prefill_cp, gdn::read_error_diag,
                                                gdn::read_error_linear, gdn::read_error_decay_step,
-                                               gdn::read_error_decay_scan, gdn::read_error_decay_tc, gdn::read_error_decay_pipe,
+                                               gdn::read_error_decay_scan, gdn::read_error_decay_tc,
                                                gdn::read_error_linear_fp8,
                                                gdn::read_error_add_rmsnorm};
   for (auto rd : readers) {

@@ -220,8 +220,8 @@ cudaError_t launch_scan_t(const DecayArgs& p, const DecaySegments& sg, int32_t D
 }  // namespace
 
 // Sized for the 152 SMs of the one target, so that a workspace asked for on
-// one thread fits the call on another: as many segments as give every SM two
-// CTAs and no CTA a second turn ((T / len + N) Hv <= 304), none where the
+// one thread fits the call on another: as many segments as give every SM one
+// CTA (token by token: two) and no CTA a second turn, none where the
 // (sequence, V head) pairs come near that by themselves. With few heads that
 // would be many short ones, and the last of them reads the states that all
 // others add: on the tensor cores a chunk of 64 tokens costs about as much as
@@ -231,7 +231,7 @@ cudaError_t launch_scan_t(const DecayArgs& p, const DecaySegments& sg, int32_t D
 // of m cost 2 m + 2 n / m, least at m = sqrt(n).
 int32_t decay_segment_len(int32_t N, int64_t T, int32_t Hv, bool chunks) {
   const int64_t kCtas = chunks ? 152 : 304;
-  const int64_t more = kCtas / Hv - N;  // segments beyond one for each sequence
+  const int64_t more = (2 * kCtas / Hv - N) / 2;  // a sequence's last segment is half full on average
   const int64_t unit = chunks ? 64 : kTile;
   if (more < 1 || T <= (chunks ? 64 : 32)) return (int32_t)T + 1;
   int64_t len = ((T + more - 1) / more + unit - 1) / unit * unit;  // below T + unit

@@ -18,13 +18,29 @@
 // the outputs: one part each where out alone is asked for, whose own rounding
 // is as large (together 1.4 times it), two (2^-17) where core_out is.
 //
-// An MMA of these sizes holds the tensor pipe for about 73 cycles whatever
-// its M and N, so what counts is their number: 32 a chunk (44 with core_out).
-// A CTA takes 104 KB of shared memory and 256 TMEM columns, so two share an SM
-// and one's loads, exponentials and stores run under the other's products.
-// The outputs leave TMEM as 8 x 8 blocks, are normed and gated in registers
-// (z comes by TMA as they go, transposed in shared memory) and whole chunks
-// are stored by TMA while dS is computed.
+// A pipeline of one CTA per SM, whose warps hand each other tiles through
+// mbarriers instead of meeting at barriers. Sixteen warps compute; per chunk c
+// they go through
+//   P(c)   from the scores, which were issued a chunk ahead
+//   K'(c)  in its parts
+//   the outputs, from O1(c) and O2(c)
+//   S      from dS(c), and its bf16 copy for O1(c + 1)
+// while the tensor cores run O2(c), dS(c), the scores of c + 1 and O1(c + 1),
+// each as soon as its operands are there: O2 runs under K', dS under the
+// outputs, the rest under everything. One warp issues the MMAs, one loads, one
+// sums the log decays and one stores the outputs and loads z into their
+// places. q, k, v, z and the outputs have two stages, and TMEM holds every
+// accumulator side by side. The outputs leave TMEM as 8 x 8 blocks, are normed
+// and gated in registers, transposed in shared memory and stored by TMA.
+//
+// What bounds it: a chunk of a head takes about 4300 cycles (8 x 1024 tokens,
+// 64 heads, no gate; 5500 with the gated norm, whose exponentials and
+// reciprocals are 1000 of the MUFU's), where its 32 MMAs hold the tensor pipe
+// for 2300 and its tiles the shared memory for 2700. 8 ragged prompts of
+// 34,482 tokens in all, 64 heads: 564 us, 2640 GB/s; one of 4096 tokens, 32
+// heads: 88 us. The same chunks with two CTAs an SM that meet at barriers took
+// 630 and 105 us.
+//
 // Exponents are differences of sums of up to 64 log decays, which a decay of
 // -100 a token makes large where the difference is small; the sums are held
 // as two floats each.
@@ -33,447 +49,649 @@
 // it: such elements of v are replaced by 0 before the product and make NaN in
 // their value row of the outputs from their token on, and of the state.
 //
-// Segments (decay_common.cuh) run as in decay_scan.cu: a first pass adds up
-// dS alone, the second starts each segment from what those before it leave.
-#include "decay_tc.cuh"
+// Segments (decay_common.cuh) run as in decay_scan.cu: a first pass
+// (kPLocal) adds up dS alone, with two stages of K' and of the accumulator
+// too; the second starts each segment from what those before it leave.
+//
+// A wait that gives up raises the CTA's abort flag; every role then runs
+// through its remaining waits at once and the kernel ends.
+#include <cuda.h>
+
+#include "decay_common.cuh"
+#include "tc_common.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kTThreads = 256;
-constexpr int kGateWarp = 1, kStoreWarp = 2, kDeltaWarp = 6;
-enum { kTWhole = 0, kTLocal = 1 };
+constexpr int kTc = 64;  // tokens per chunk
+constexpr int kTd = 128;
+
+// Descriptor of a tile [k][mn] of 16-bit elements read with k as the
+// contraction (MN-major, 128-byte swizzle): boxes of 64 mn columns 8 KB apart,
+// eight k rows in 1024 bytes, so that 16 of k advance it by 2048.
+__device__ __forceinline__ uint64_t sdesc_mn128(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr & 0x3FFFF) >> 4);
+  d |= (uint64_t)(8192 >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+constexpr uint32_t kTransA = 1u << 15, kTransB = 1u << 16;
+
+// Four 8 x 8 blocks of 16-bit elements between shared memory and registers,
+// transposed: lane l gives the address of row l % 8 of block l / 8, and its
+// register m holds elements (2 (l % 4), l / 4) and (2 (l % 4) + 1, l / 4) of
+// block m as (shared row, shared column).
+__device__ __forceinline__ void ldmatrix_t4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void stmatrix_t4(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// two floats to packed bf16 (x in the low half)
+__device__ __forceinline__ uint32_t pack2(float2 a) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(a.y), "f"(a.x));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint32_t r) {
+  return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+}
+// the same, leaving in a what the rounding dropped
+__device__ __forceinline__ uint32_t split2(float2& a) {
+  const uint32_t r = pack2(a);
+  a = fma2(unpack2(r), make_float2(-1.f, -1.f), a);
+  return r;
+}
+// the same with the hi part cut off instead of rounded: no conversion, and
+// what is left is exact too
+__device__ __forceinline__ uint32_t cut2(float2& a) {
+  const uint32_t x = __float_as_uint(a.x), y = __float_as_uint(a.y);
+  a = fma2(make_float2(__uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u)), make_float2(-1.f, -1.f), a);
+  return __byte_perm(x, y, 0x7632);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float b) { return fma2(a, make_float2(b, b), make_float2(-0.f, -0.f)); }
+
+// a + b as two floats
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  const float s = a.hi + b.hi;
+  const float t = s - a.hi;
+  const float e = (a.hi - (s - t)) + (b.hi - t);
+  const float l = e + (a.lo + b.lo);
+  const float h = s + l;
+  return Two{h, l - (h - s)};
+}
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLog2eLo = 1.9259629911e-8f;  // log2(e) less its fp32 rounding
+__device__ __forceinline__ Two to_log2(float g) {
+  const float h = g * kLog2e;
+  return Two{h, fmaf(g, kLog2e, -h) + g * kLog2eLo};
+}
+
+constexpr int kPCompute = 16;  // compute warps: TMEM lane quadrant warp % 4, column quarter warp / 4
+constexpr int kPMma = 16, kPLoad = 17, kPGates = 18, kPStore = 19;
+constexpr int kPThreads = 32 * 20;
+enum { kPWhole = 0, kPLocal = 1 };
 
 // shared memory, from a 1024-byte boundary; tiles of 64 tokens x 128 columns
 // are two boxes of 64 columns, 128-byte swizzled rows
-constexpr uint32_t kOffQ = 0;
-constexpr uint32_t kOffK = 16384;    // K, then K' hi in place
-constexpr uint32_t kOffMid = 32768;  // K' mid
-constexpr uint32_t kOffLo = 49152;   // K' lo
-constexpr uint32_t kOffV = 65536;
-constexpr uint32_t kOffO = 81920;    // z, then the outputs in its place
-constexpr uint32_t kOffP = 98304;    // P [64 t][64 s] SW128, with core_out its low part behind it
-constexpr uint32_t kTile16 = 16384;
-// the first pass has no q, P or outputs: their place is a second stage of K and V
-__device__ __forceinline__ uint32_t k_at(int stage) { return stage ? kOffO : kOffK; }
-__device__ __forceinline__ uint32_t v_at(int stage) { return stage ? kOffQ : kOffV; }
-constexpr uint32_t tc_smem(bool core) { return kOffP + (core ? 16384 : 8192); }
+constexpr uint32_t kPTile = 16384;
+constexpr uint32_t kPQ = 0;            // [2]
+constexpr uint32_t kPK = 2 * kPTile;   // [2] K, then K' hi in place
+constexpr uint32_t kPV = 4 * kPTile;   // [2]
+constexpr uint32_t kPMid = 6 * kPTile;  // K' mid, K' lo
+constexpr uint32_t kPP = 8 * kPTile;   // P and its low part; first pass: the second K' mid and lo
+constexpr uint32_t kPO = 9 * kPTile;   // [2] z, then the outputs in its place
+constexpr uint32_t kPSmem = 11 * kPTile;
+__device__ __forceinline__ uint32_t mid_at(int stage) { return stage ? kPO : kPMid; }
 
 // TMEM columns
-constexpr uint32_t kColS = 0;    // S hi (64 packed columns), S lo (64)
-constexpr uint32_t kColX = 128;  // scores (64), then O2; dS (128) once O1 and O2 are read
-constexpr uint32_t kColO1 = 192;
-constexpr uint32_t kCols = 256;
+constexpr uint32_t kPColS = 0;     // S hi (64 packed columns), S lo (64)
+constexpr uint32_t kPColSc = 128;  // scores
+constexpr uint32_t kPColO2 = 192;
+constexpr uint32_t kPColO1 = 256;
+constexpr uint32_t kPColKv = 320;  // dS; first pass: at 0 and 128
+constexpr uint32_t kPCols = 512;
+
+// 16 lanes x 16 columns: thread lane holds rows lane/4 and lane/4 + 8, columns
+// 8 c + 2 (lane % 4) and the next, at v[4 c], v[4 c + 1] and v[4 c + 2], v[4 c + 3]
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 
 struct TcShared {
-  Two G[2][kTc];    // sums of a chunk's log2 decays, by chunk parity
-  float E[kTc];     // scale e^(G_t)
-  float dk[kTc];    // e^(G_n - G_s), 0 past the chunk's tokens
-  float w[kTd];       // the norm's weights
+  Two G[4][kTc];     // by chunk % 4: sums of log2 decays
+  float E[4][kTc];   // scale e^(G_t)
+  float dk[4][kTc];  // e^(G_n - G_s), 0 past the chunk's tokens
+  Decay whole[4];    // e^(G_n)
+  int bad[4][kTd];   // first token with a non-finite v in this value row, or kTc
+  int any_bad[4];
   float red[4][kTc];  // squares of the outputs by TMEM lane quadrant
-  int bad[2][kTd];  // by chunk parity: first token with a non-finite v in this value row, or kTc
-  int any_bad[2];
+  float w[kTd];       // the norm's weights
   int abort;
   uint32_t tmem;
-  uint64_t load_q, load_kv[2], load_z, scores, outs, delta;  // mbarriers
+  // by chunk % 2, but gates by chunk % 4
+  uint64_t full[2], empty[2], z[2], gates[4], p[2], k[2], o[2];
+  uint64_t s, scores, outs, delta[2];
 };
 
 template <int MODE, bool CORE, bool GATED>
-__global__ void __launch_bounds__(kTThreads, 2)
+__global__ void __launch_bounds__(kPThreads, 1)
     decay_tc_kernel(const DecayArgs p, const DecaySegments sg, const __grid_constant__ CUtensorMap tm_q,
-                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                    const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_o) {
+                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_o) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ TcShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int qd = warp & 3, hh = warp >> 2;  // TMEM lane quadrant, column half
-  const int j = 32 * qd + lane;             // this thread's value row
   const int slot = blockIdx.x / (unsigned)p.Hv;  // a segment's V heads side by side: they share q, k in L2
   const int h = blockIdx.x % (unsigned)p.Hv;
   const int kh = k_head_of(p.map, h, p.Hk, p.rep);
   DecaySegment s;
   if (!find_segment(p, sg, slot, lane, &s)) return;
-  if (MODE == kTLocal && s.index + 1 == s.parts) return;
+  if (MODE == kPLocal && s.index + 1 == s.parts) return;
+  const int chunks = (s.end - s.begin + kTc - 1) / kTc;
 
-  if (warp == 0) {
-    tc::tmem_alloc(&sh.tmem, kCols);
+  if (warp == kPMma) {
+    tc::tmem_alloc(&sh.tmem, kPCols);
     tc::tmem_relinquish();
   }
   if (tid == 0) {
-    mbar_init(&sh.load_q, 1);
-    mbar_init(&sh.load_kv[0], 1);
-    mbar_init(&sh.load_kv[1], 1);
-    mbar_init(&sh.load_z, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.z[i], 1);
+      mbar_init(&sh.p[i], kPCompute);
+      mbar_init(&sh.k[i], kPCompute);
+      mbar_init(&sh.o[i], kPCompute);
+      mbar_init(&sh.delta[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh.gates[i], 1);
+      sh.any_bad[i] = 0;
+    }
+    mbar_init(&sh.s, kPCompute);
     mbar_init(&sh.scores, 1);
-    mbar_init(&sh.outs, 2);  // O1 and O2
-    mbar_init(&sh.delta, 1);
+    mbar_init(&sh.outs, 1);
     sh.abort = 0;
-    sh.any_bad[0] = sh.any_bad[1] = 0;
     fence_mbar_init();
   }
-  if (tid < 2 * kTd) (&sh.bad[0][0])[tid] = kTc;
+  if (tid < 4 * kTd) (&sh.bad[0][0])[tid] = kTc;
   if (GATED && tid < kTd) sh.w[tid] = p.norm_w[tid];
-  volatile int* abort_flag = &sh.abort;
-
-  // the state: columns 64 hh .. 64 hh + 63 of row j
-  float2 S[32];
-  float* gS = p.state + ((int64_t)s.seq * p.Hv + h) * (int64_t)(kTd * kTd);
-  const int at0 = j * kTd + 64 * hh;
-  {
-    const DecaySlots ws(p, sg, s, h, kTd * kTd);
-    float* keep = sg.states + ((int64_t)(s.slot + s.parts - 1) * p.Hv + h) * (kTd * kTd);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float4 x[8];
-      if (MODE == kTLocal) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (s.index == 0) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) load8(gS + at0 + 32 * c + 8 * e, x[2 * e], x[2 * e + 1]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) store8(keep + at0 + 32 * c + 8 * e, x[2 * e], x[2 * e + 1]);
-        }
-      } else if (s.parts == 1) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) load8(gS + at0 + 32 * c + 8 * e, x[2 * e], x[2 * e + 1]);
-      } else {
-        ws.start8<4>(s.index, s.parts, at0 + 32 * c, x);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        S[16 * c + 2 * e] = make_float2(x[e].x, x[e].y);
-        S[16 * c + 2 * e + 1] = make_float2(x[e].z, x[e].w);
-      }
-    }
-  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tb = sh.tmem, tq = tb + ((uint32_t)(32 * qd) << 16);
+  const uint32_t tb = sh.tmem;
+  volatile int* abort_flag = &sh.abort;
+  const auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, abort_flag); };
+  const auto tokens = [&](int c) { return s.end - s.begin - c * kTc < kTc ? s.end - s.begin - c * kTc : kTc; };
 
-  // columns 64 hh + 32 c .. + 31 of S as the A operand of O1: packed pairs,
-  // and with core_out what their rounding left
-  auto put_state = [&](int c) {
-    uint32_t hi[16];
-    if (CORE) {
-      uint32_t lo[16];
+  if (warp == kPMma) {
+    // ---------------------------------------------------------------- MMAs
+    const uint32_t id_s = tc::idesc(tc::kBF16, 64, 64), id_o1 = tc::idesc(tc::kBF16, 128, 64);
+    const uint32_t id_o2 = id_o1 | kTransA, id_d = tc::idesc(tc::kBF16, 128, 128) | kTransA | kTransB;
+    const uint64_t dP = tc::sdesc_sw128(smem_u32(sm + kPP));
+    const auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok); };
+    const auto issue_scores = [&](int st) {
+      const uint64_t dQ = tc::sdesc_sw128(smem_u32(sm + kPQ + st * kPTile));
+      const uint64_t dK = tc::sdesc_sw128(smem_u32(sm + kPK + st * kPTile));
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float2 a = S[16 * c + e];
-        hi[e] = split2(a);
-        lo[e] = pack2(a);
-      }
-      tc::tmem_st16u(tq + kColS + 64 + 32 * hh + 16 * c, lo);
-    } else {
+      for (int i = 0; i < 8; ++i)
+        tc::mma_f16_elect(tb + kPColSc, tc::sdesc_at(dQ, 64, i), tc::sdesc_at(dK, 64, i), id_s, i > 0);
+      tc::mma_commit_elect(&sh.scores);
+    };
+    const auto issue_o1 = [&](int st) {
+      const uint64_t dQ = tc::sdesc_sw128(smem_u32(sm + kPQ + st * kPTile));
 #pragma unroll
-      for (int e = 0; e < 16; ++e) hi[e] = pack2(S[16 * c + e]);
+      for (int i = 0; i < (CORE ? 16 : 8); ++i)
+        tc::mma_f16_ts_elect(tb + kPColO1, tb + kPColS + 8 * i, tc::sdesc_at(dQ, 64, i & 7), id_o1, i > 0);
+    };
+    bool ok = true;
+    if (MODE == kPWhole) {
+      ok = all(wait(&sh.full[0], 0));
+      if (ok) issue_scores(0);
+      ok = ok && all(wait(&sh.s, 0));
+      tc::fence_after_sync();
+      if (ok) issue_o1(0);
     }
-    tc::tmem_st16u(tq + kColS + 32 * hh + 16 * c, hi);
-  };
-  uint32_t q_loads = 0, kv_loads = 0, z_loads = 0;  // thread 0's, z the store warp's lane 0's
-  auto load_q = [&](int t0) {
-    ++q_loads;
-    mbar_arrive_expect_tx(&sh.load_q, kTile16);
-    for (int b = 0; b < 2; ++b) tc::tma_load_2d(sm + kOffQ + 8192 * b, &tm_q, kh * kTd + 64 * b, t0, &sh.load_q);
-  };
-  auto load_kv = [&](int t0, int stage) {
-    ++kv_loads;
-    mbar_arrive_expect_tx(&sh.load_kv[stage], 2 * kTile16);
-    for (int b = 0; b < 2; ++b) {
-      tc::tma_load_2d(sm + k_at(stage) + 8192 * b, &tm_k, kh * kTd + 64 * b, t0, &sh.load_kv[stage]);
-      tc::tma_load_2d(sm + v_at(stage) + 8192 * b, &tm_v, h * kTd + 64 * b, t0, &sh.load_kv[stage]);
-    }
-  };
-  auto load_z = [&](int t0) {
-    ++z_loads;
-    mbar_arrive_expect_tx(&sh.load_z, kTile16);
-    for (int b = 0; b < 2; ++b) tc::tma_load_2d(sm + kOffO + 8192 * b, &tm_z, h * kTd + 64 * b, t0, &sh.load_z);
-  };
-  // log decays of tokens 2 lane and 2 lane + 1 of a chunk, and its gates (warp 1)
-  float g0 = 0.f, g1 = 0.f;
-  Two total{0.f, 0.f}, gn{0.f, 0.f};  // log2, of the segment and the chunk
-  auto fetch_g = [&](int t0) {
-    const int t = t0 + 2 * lane;
-    const float* g = p.g + t * p.g_stride + h;
-    g0 = t < s.end ? g[0] : 0.f;
-    g1 = t + 1 < s.end ? g[p.g_stride] : 0.f;
-  };
-  auto put_sums = [&](Two* to) {
-    // inclusive sums over the chunk, as two floats; tokens past the chunk's
-    // have log decay 0, so lane 31 ends with G_n
-    const Two first = to_log2(decay_log(g0));
-    Two incl = add2(first, to_log2(decay_log(g1)));
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const Two o{__shfl_up_sync(0xffffffffu, incl.hi, d), __shfl_up_sync(0xffffffffu, incl.lo, d)};
-      if (lane >= d) incl = add2(incl, o);
-    }
-    const Two prev{__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
-    to[2 * lane] = lane > 0 ? add2(prev, first) : first;
-    to[2 * lane + 1] = incl;
-    if (MODE == kTLocal) gn = Two{__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)};
-  };
-  const auto tokens = [&](int t0) { return s.end - t0 < kTc ? s.end - t0 : kTc; };
-
-  if (tid == 0) {
-    load_kv(s.begin, 0);
-    if (MODE == kTLocal && s.begin + kTc < s.end) load_kv(s.begin + kTc, 1);
-    if (MODE == kTWhole) load_q(s.begin);
-  }
-  if (GATED && warp == kStoreWarp && lane == 0) load_z(s.begin);
-  if (warp == 1) {
-    fetch_g(s.begin);
-    put_sums(sh.G[0]);
-    total = gn;
-    fetch_g(s.begin + kTc);
-  }
-  if (MODE == kTWhole) {
-    put_state(0);
-    put_state(1);
-    tc::tmem_wait_st();
-  }
-  const uint64_t dQ = tc::sdesc_sw128(smem_u32(sm + kOffQ)), dK = tc::sdesc_sw128(smem_u32(sm + kOffK));
-  const uint64_t dP = tc::sdesc_sw128(smem_u32(sm + kOffP));
-  const uint64_t dMid = sdesc_mn128(smem_u32(sm + kOffMid));
-  bool failed = false;
-  uint32_t phase = 0, round = 0;  // parities of the chunk and, in the first pass, of its stage
-  // #1: the state operand is in TMEM, the gates in shared memory
-  tc::fence_before_sync();
-  __syncthreads();
-
-  for (int t0 = s.begin; t0 < s.end; t0 += kTc, phase ^= 1, round ^= phase ^ 1) {
-    const int n = tokens(t0);
-    const bool more = t0 + kTc < s.end;
-    const Two* G = sh.G[phase];
-    const int stage = MODE == kTLocal ? (int)phase : 0;
-    unsigned char *kt = sm + k_at(stage), *vt = sm + v_at(stage);
-    const uint64_t dV = sdesc_mn128(smem_u32(vt));
-    // the buffers are single: the next chunk's tiles come into L2 meanwhile, so
-    // that its loads, issued late in this chunk, are short
-    if (MODE == kTWhole && warp == 7 && lane == 0 && more) {
-      for (int b = 0; b < 2; ++b) {
-        tc::tma_prefetch_2d(&tm_k, kh * kTd + 64 * b, t0 + kTc);
-        tc::tma_prefetch_2d(&tm_v, h * kTd + 64 * b, t0 + kTc);
-        tc::tma_prefetch_2d(&tm_q, kh * kTd + 64 * b, t0 + kTc);
-        if (GATED) tc::tma_prefetch_2d(&tm_z, h * kTd + 64 * b, t0 + kTc);
-      }
-    }
-    if (!mbar_wait_bounded(&sh.load_kv[stage], MODE == kTLocal ? round : phase, abort_flag)) failed = true;
-    if (MODE == kTWhole) {
-      if (!mbar_wait_bounded(&sh.load_q, phase, abort_flag)) failed = true;
-      if (warp == 0) {
+    for (int c = 0; ok && c < chunks; ++c) {
+      const int st = c & 1;
+      const uint32_t round = (c >> 1) & 1;
+      const uint64_t dV = sdesc_mn128(smem_u32(sm + kPV + st * kPTile));
+      if (MODE == kPWhole) {
+        ok = all(wait(&sh.p[st], round));
+        if (!ok) break;
         tc::fence_after_sync();
-        const uint32_t id = tc::idesc(tc::kBF16, 64, 64);
-#pragma unroll 1
-        for (int k = 0; k < 8; ++k)
-          tc::mma_f16_elect(tb + kColX, tc::sdesc_at(dQ, 64, k), tc::sdesc_at(dK, 64, k), id, k > 0);
-        tc::mma_commit_elect(&sh.scores);
-      } else if (warp == 2) {
-        tc::fence_after_sync();
-        const uint32_t id = tc::idesc(tc::kBF16, 128, 64);
-#pragma unroll 1
-        for (int k = 0; k < (CORE ? 16 : 8); ++k)
-          tc::mma_f16_ts_elect(tb + kColO1, tb + kColS + 8 * k, tc::sdesc_at(dQ, 64, k & 7), id, k > 0);
+#pragma unroll
+        for (int i = 0; i < (CORE ? 8 : 4); ++i)
+          tc::mma_f16_elect(tb + kPColO2, dV + ((i & 3) * 2048 >> 4), dP + (((i >> 2) * 8192 + (i & 3) * 32) >> 4), id_o2,
+                            i > 0);
         tc::mma_commit_elect(&sh.outs);
       }
-    }
-    if (warp == kGateWarp) {
-      const Two gl = G[kTc - 1];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = lane + 32 * i;
-        const Two a = G[t];
-        if (MODE == kTWhole) sh.E[t] = p.scale * exp2_fast(a.hi + a.lo);
-        sh.dk[t] = t < n ? exp2_fast((gl.hi - a.hi) + (gl.lo - a.lo)) : 0.f;
-      }
-    }
-    // v: rows past the chunk's tokens are another sequence's (or stale): 0
-    // there; non-finite elements are noted and replaced by 0
-    if (MODE == kTWhole || n < kTc) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int u = tid + i * kTThreads, row = u >> 4, c16 = u & 15;
-        uint4* at = reinterpret_cast<uint4*>(vt + (c16 >> 3) * 8192 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4));
-        uint4 x = *at;
-        uint32_t* w = &x.x;
-        uint32_t hit = 0;  // an exponent of all ones carries into the sign's place
-#pragma unroll
-        for (int e = 0; e < 4; ++e) hit |= (w[e] & 0x7f807f80u) + 0x00800080u;
-        if (row >= n) {
-          *at = make_uint4(0, 0, 0, 0);
-        } else if (MODE == kTWhole && (hit & 0x80008000u) != 0) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (((w[e >> 1] >> (16 * (e & 1))) & 0x7f80u) == 0x7f80u) {
-              atomicMin(&sh.bad[phase][8 * c16 + e], row);
-              w[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
-            }
-          *at = x;
-          sh.any_bad[phase] = 1;
-        }
-      }
-    }
-
-    if (MODE == kTWhole) {
-      if (!mbar_wait_bounded(&sh.scores, phase, abort_flag)) failed = true;
+      ok = all(wait(&sh.k[st], round));
+      if (!ok) break;
       tc::fence_after_sync();
-      float x[16];
-      tmem_ld_16x32(tq + kColX + 32 * hh, x);
-      tc::tmem_wait_ld();
-      const int ta = 16 * qd + (lane >> 2), s0 = 32 * hh + 2 * (lane & 3);  // rows ta and ta + 8
-      const Two ga = G[ta], gb = G[ta + 8];
-      unsigned char* pp = sm + kOffP + ta * 128 + 4 * (lane & 3);  // the rows are eight apart: the same swizzle
+      const uint64_t dK0 = sdesc_mn128(smem_u32(sm + kPK + st * kPTile));
+      const uint64_t dK1 = sdesc_mn128(smem_u32(sm + (MODE == kPLocal ? mid_at(st) : kPMid)));
+      const uint32_t acc = tb + (MODE == kPLocal ? 128u * st : kPColKv);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int sc = s0 + 8 * c;
-        const Two u0 = G[sc], u1 = G[sc + 1];
-        float2 y = make_float2(x[4 * c] * exp2_fast((ga.hi - u0.hi) + (ga.lo - u0.lo)),
-                               x[4 * c + 1] * exp2_fast((ga.hi - u1.hi) + (ga.lo - u1.lo)));
-        float2 z = make_float2(x[4 * c + 2] * exp2_fast((gb.hi - u0.hi) + (gb.lo - u0.lo)),
-                               x[4 * c + 3] * exp2_fast((gb.hi - u1.hi) + (gb.lo - u1.lo)));
-        y = mul2(y, p.scale);
-        z = mul2(z, p.scale);
-        if (sc > ta) y.x = 0.f;
-        if (sc + 1 > ta) y.y = 0.f;
-        if (sc > ta + 8) z.x = 0.f;
-        if (sc + 1 > ta + 8) z.y = 0.f;
-        unsigned char* at = pp + (((4 * hh + c) ^ (ta & 7)) << 4);
-        *reinterpret_cast<uint32_t*>(at) = CORE ? split2(y) : pack2(y);
-        *reinterpret_cast<uint32_t*>(at + 1024) = CORE ? split2(z) : pack2(z);
-        if (CORE) {
-          *reinterpret_cast<uint32_t*>(at + 8192) = pack2(y);
-          *reinterpret_cast<uint32_t*>(at + 8192 + 1024) = pack2(z);
-        }
+      for (int i = 0; i < 12; ++i)
+        tc::mma_f16_elect(acc, dV + ((i & 3) * 2048 >> 4),
+                          (i < 4 ? dK0 : dK1 + (i < 8 ? 0 : kPTile >> 4)) + ((i & 3) * 2048 >> 4), id_d, i > 0);
+      tc::mma_commit_elect(&sh.delta[MODE == kPLocal ? st : 0]);
+      tc::mma_commit_elect(&sh.empty[st]);
+      if (MODE == kPWhole && c + 1 < chunks) {
+        ok = all(wait(&sh.full[st ^ 1], ((c + 1) >> 1) & 1));
+        if (!ok) break;
+        issue_scores(st ^ 1);
+        ok = all(wait(&sh.s, (c + 1) & 1));
+        if (!ok) break;
+        tc::fence_after_sync();
+        issue_o1(st ^ 1);
       }
+    }
+  } else if (warp == kPLoad) {
+    // --------------------------------------------------------------- loads
+    if (lane == 0) {
+      const auto load = [&](int c) {
+        const int st = c & 1, t0 = s.begin + c * kTc;
+        mbar_arrive_expect_tx(&sh.full[st], (MODE == kPWhole ? 3 : 2) * kPTile);
+        for (int b = 0; b < 2; ++b) {
+          if (MODE == kPWhole)
+            tc::tma_load_2d(sm + kPQ + st * kPTile + 8192 * b, &tm_q, kh * kTd + 64 * b, t0, &sh.full[st]);
+          tc::tma_load_2d(sm + kPK + st * kPTile + 8192 * b, &tm_k, kh * kTd + 64 * b, t0, &sh.full[st]);
+          tc::tma_load_2d(sm + kPV + st * kPTile + 8192 * b, &tm_v, h * kTd + 64 * b, t0, &sh.full[st]);
+        }
+      };
+      load(0);
+      int n = 1;
+      for (; n < chunks; ++n) {
+        if (n >= 2 && !wait(&sh.empty[n & 1], ((n >> 1) - 1) & 1)) break;
+        load(n);
+      }
+      // none may be in flight when the CTA ends: load i went to stage i % 2
+      mbar_wait(&sh.full[0], ((n + 1) / 2 - 1) & 1);
+      if (n > 1) mbar_wait(&sh.full[1], (n / 2 - 1) & 1);
+    }
+  } else if (warp == kPGates) {
+    // ------------------------------------------------- sums of log decays
+    // A buffer is written again four chunks later; o(c) seen means that every
+    // warp has left chunk c - 1 (in the first pass: that the state has taken
+    // chunk c). The compute warps cannot reach o(c + 2) before gates(c + 2),
+    // given after o(c) was seen, so none is missed.
+    float g0 = 0.f, g1 = 0.f;  // log decays of tokens 2 lane and 2 lane + 1 of a chunk
+    const auto fetch_g = [&](int c) {
+      const int t = s.begin + c * kTc + 2 * lane;
+      const float* g = p.g + t * p.g_stride + h;
+      g0 = t < s.end ? g[0] : 0.f;
+      g1 = t + 1 < s.end ? g[p.g_stride] : 0.f;
+    };
+    Two total{0.f, 0.f};  // of the segment, log2
+    fetch_g(0);
+    for (int c = 0; c < chunks; ++c) {
+      if (MODE == kPWhole && c >= 2) __all_sync(0xffffffffu, wait(&sh.o[c & 1], ((c - 2) >> 1) & 1));
+      if (MODE == kPLocal && c >= 3) __all_sync(0xffffffffu, wait(&sh.o[(c - 3) & 1], ((c - 3) >> 1) & 1));
+      // inclusive sums over the chunk, as two floats; tokens past the chunk's
+      // have log decay 0, so lane 31 ends with G_n
+      const int at = c & 3, n = tokens(c);
+      const Two first = to_log2(decay_log(g0));
+      Two incl = add2(first, to_log2(decay_log(g1)));
+      fetch_g(c + 1);
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const Two o{__shfl_up_sync(0xffffffffu, incl.hi, d), __shfl_up_sync(0xffffffffu, incl.lo, d)};
+        if (lane >= d) incl = add2(incl, o);
+      }
+      const Two prev{__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+      const Two a = lane > 0 ? add2(prev, first) : first, b = incl;
+      const Two gn{__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)};
+      if (MODE == kPWhole) {
+        sh.G[at][2 * lane] = a;
+        sh.G[at][2 * lane + 1] = b;
+        sh.E[at][2 * lane] = p.scale * exp2_fast(a.hi + a.lo);
+        sh.E[at][2 * lane + 1] = p.scale * exp2_fast(b.hi + b.lo);
+        for (int i = lane; i < kTd; i += 32) sh.bad[at][i] = kTc;
+        if (lane == 0) sh.any_bad[at] = 0;
+      } else {
+        total = add2(total, gn);
+      }
+      sh.dk[at][2 * lane] = 2 * lane < n ? exp2_fast((gn.hi - a.hi) + (gn.lo - a.lo)) : 0.f;
+      sh.dk[at][2 * lane + 1] = 2 * lane + 1 < n ? exp2_fast((gn.hi - b.hi) + (gn.lo - b.lo)) : 0.f;
+      if (lane == 0) sh.whole[at] = decay_factor((gn.hi + gn.lo) * kLn2);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.gates[at]);
+    }
+    if (MODE == kPLocal && lane == 0 && !*abort_flag) sg.decays[blockIdx.x] = exp2f(total.hi + total.lo);
+  } else if (warp == kPStore) {
+    // ------------------------------------------------------ z in, outputs out
+    // (as for the gates: z(c + 2), or its place, is given after o(c) was seen)
+    if (MODE == kPWhole) {
+      uint32_t n_z = 0;
+      const auto give_z = [&](int c) {
+        const int st = c & 1;
+        if (GATED) {
+          ++n_z;
+          mbar_arrive_expect_tx(&sh.z[st], kPTile);
+          for (int b = 0; b < 2; ++b)
+            tc::tma_load_2d(sm + kPO + st * kPTile + 8192 * b, &tm_z, h * kTd + 64 * b, s.begin + c * kTc, &sh.z[st]);
+        } else {
+          mbar_arrive(&sh.z[st]);
+        }
+      };
+      if (lane == 0) {
+        give_z(0);
+        if (chunks > 1) give_z(1);
+      }
+      for (int c = 0; c < chunks; ++c) {
+        const int st = c & 1;
+        const bool ok = __all_sync(0xffffffffu, wait(&sh.o[st], (c >> 1) & 1));
+        const int n = tokens(c), t0 = s.begin + c * kTc;
+        const unsigned char* tile = sm + kPO + st * kPTile;
+        if (ok && (!CORE || p.out != nullptr)) {
+          if (n == kTc) {
+            if (lane == 0) {
+              for (int b = 0; b < 2; ++b) tc::tma_store_2d(&tm_o, h * kTd + 64 * b, t0, tile + 8192 * b);
+              bulk_commit();
+              bulk_wait_read_all();
+            }
+          } else {  // a last, shorter chunk: its rows alone
+            for (int u = lane; u < 16 * n; u += 32) {
+              const int t = u >> 4, c8 = u & 15;
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + ((int64_t)(t0 + t) * p.Hv + h) * kTd + 8 * c8) =
+                  *reinterpret_cast<const uint4*>(tile + (c8 >> 3) * 8192 + t * 128 + (((c8 & 7) ^ (t & 7)) << 4));
+            }
+          }
+        }
+        if (lane == 0 && c + 2 < chunks) give_z(c + 2);
+      }
+      if (lane == 0) {
+        if (GATED) {
+          mbar_wait(&sh.z[0], ((n_z + 1) / 2 - 1) & 1);
+          if (n_z > 1) mbar_wait(&sh.z[1], (n_z / 2 - 1) & 1);
+        }
+        bulk_wait_all();
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- compute
+    const int qd = warp & 3, hh = warp >> 2;
+    const int j = 32 * qd + lane;  // this thread's value row; columns 32 hh .. 32 hh + 31 of the state
+    const uint32_t tq = tb + ((uint32_t)(32 * qd) << 16);
+    float2 S[16];
+    float* gS = p.state + ((int64_t)s.seq * p.Hv + h) * (int64_t)(kTd * kTd);
+    const int at0 = j * kTd + 32 * hh;
+    {
+      float4 x[8];
+      if (MODE == kPLocal) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s.index == 0) {
+          float* keep = sg.states + ((int64_t)(s.slot + s.parts - 1) * p.Hv + h) * (kTd * kTd);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) load8(gS + at0 + 8 * e, x[2 * e], x[2 * e + 1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) store8(keep + at0 + 8 * e, x[2 * e], x[2 * e + 1]);
+        }
+      } else if (s.parts == 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) load8(gS + at0 + 8 * e, x[2 * e], x[2 * e + 1]);
+      } else {
+        DecaySlots(p, sg, s, h, kTd * kTd).start8<4>(s.index, s.parts, at0, x);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        S[2 * e] = make_float2(x[e].x, x[e].y);
+        S[2 * e + 1] = make_float2(x[e].z, x[e].w);
+      }
+    }
+    bool failed = false;
+    // all of the warp's tile is in place for the tensor cores or for TMA
+    const auto hand = [&](uint64_t* bar) {
       fence_proxy_async_smem();
       tc::fence_before_sync();
-      __syncthreads();  // #2: P and v are in shared memory, the scores are read
-      if (warp == 4) {
-        tc::fence_after_sync();
-        const uint32_t id = tc::idesc(tc::kBF16, 128, 64) | kTransA;
-#pragma unroll 1
-        for (int k = 0; k < (CORE ? 8 : 4); ++k)
-          tc::mma_f16_elect(tb + kColX, dV + ((k & 3) * 2048 >> 4), dP + (((k >> 2) * 8192 + (k & 3) * 32) >> 4), id,
-                            k > 0);
-        tc::mma_commit_elect(&sh.outs);
-      }
-    } else {
-      if (n < kTc) fence_proxy_async_smem();
-      __syncthreads();  // dk is in shared memory
-    }
-
-    // K' = e^(G_n - G_s) k in three parts, the first in place of K
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    // S as the A operand of O1: packed pairs, and with core_out what their rounding left
+    const auto put_state = [&]() {
+      uint32_t hi[16];
+      if (CORE) {
+        uint32_t lo[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int u = tid + i * kTThreads, row = u >> 4, c16 = u & 15;
-      const uint32_t off = (c16 >> 3) * 8192 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4);
-      uint4 x = *reinterpret_cast<const uint4*>(kt + off);
-      if (row >= n) x = make_uint4(0, 0, 0, 0);  // another sequence's: may be a NaN
-      const uint32_t* w = &x.x;
-      const float d = sh.dk[row];
-      uint4 part[3];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float2 a = mul2(unpack2(w[e]), d);
-        (&part[0].x)[e] = cut2(a);
-        (&part[1].x)[e] = cut2(a);
-        (&part[2].x)[e] = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x7632);
-      }
-      *reinterpret_cast<uint4*>(kt + off) = part[0];
-      *reinterpret_cast<uint4*>(sm + kOffMid + off) = part[1];
-      *reinterpret_cast<uint4*>(sm + kOffLo + off) = part[2];
-    }
-    fence_proxy_async_smem();
-    if (MODE == kTWhole) {  // for the next chunk, which writes them after #1
-      if (tid < kTd) sh.bad[phase ^ 1][tid] = kTc;
-      if (tid == 0) sh.any_bad[phase ^ 1] = 0;
-    }
-    if (MODE == kTWhole) {
-      if (!mbar_wait_bounded(&sh.outs, phase, abort_flag)) failed = true;
-      tc::fence_after_sync();
-      if (tid == 0 && more) load_q(t0 + kTc);
-      if (GATED && !mbar_wait_bounded(&sh.load_z, phase, abort_flag)) failed = true;
-      // a lane holds value rows jj + 8 b + 16 a (a, b of 0, 1) and tokens
-      // tt + 8 c, tt + 8 c + 1 (c of 0..3)
-      const int jj = 32 * qd + (lane >> 2), tt = 32 * hh + 2 * (lane & 3);
-      // o[2 c + b]: tokens tt + 8 c and the next, value row jj + 8 b + 16 a
-      auto read_half = [&](int a, float2 (&o)[8]) {
-        float x[16], y[16];
-        tmem_ld_16x32(tq + ((uint32_t)(16 * a) << 16) + kColO1 + 32 * hh, x);
-        tmem_ld_16x32(tq + ((uint32_t)(16 * a) << 16) + kColX + 32 * hh, y);
-        tc::tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float2 e = *reinterpret_cast<const float2*>(&sh.E[tt + 8 * c]);
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-            o[2 * c + b] = fma2(make_float2(x[4 * c + 2 * b], x[4 * c + 2 * b + 1]), e,
-                                make_float2(y[4 * c + 2 * b], y[4 * c + 2 * b + 1]));
+        for (int e = 0; e < 16; ++e) {
+          float2 a = S[e];
+          hi[e] = split2(a);
+          lo[e] = pack2(a);
         }
-        if (sh.any_bad[phase])
+        tc::tmem_st16u(tq + kPColS + 64 + 16 * hh, lo);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) hi[e] = pack2(S[e]);
+      }
+      tc::tmem_st16u(tq + kPColS + 16 * hh, hi);
+      tc::tmem_wait_st();
+      hand(&sh.s);
+    };
+    // S <- e^(G_n) S + dS of chunk c
+    const auto take_delta = [&](int c) {
+      const Decay a = sh.whole[c & 3];
+      const uint32_t parity = MODE == kPLocal ? (c >> 1) & 1 : c & 1;
+      if (!wait(&sh.delta[MODE == kPLocal ? c & 1 : 0], parity)) failed = true;
+      tc::fence_after_sync();
+      float d[32];
+      const uint32_t col = tq + (MODE == kPLocal ? 128u * (c & 1) : kPColKv) + 32 * hh;
+      tc::tmem_ld16(col, *reinterpret_cast<float(*)[16]>(d));
+      tc::tmem_ld16(col + 16, *reinterpret_cast<float(*)[16]>(d + 16));
+      tc::tmem_wait_ld();
+      const float2 f = make_float2(a.factor, a.factor), keep = make_float2(a.keep, a.keep);
+      if (a.keep != 0.f) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) S[e] = fma2(f, S[e], fma2(keep, S[e], make_float2(d[2 * e], d[2 * e + 1])));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) S[e] = fma2(f, S[e], make_float2(d[2 * e], d[2 * e + 1]));
+      }
+      if (MODE == kPWhole && sh.any_bad[c & 3] && sh.bad[c & 3][j] < kTc)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) S[e] = make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
+    };
+    if (MODE == kPWhole) put_state();
+
+    for (int c = 0; c < chunks; ++c) {
+      const int n = tokens(c), st = c & 1, at = c & 3;
+      const uint32_t round = (c >> 1) & 1;
+      const Two* G = sh.G[at];
+      if (!wait(&sh.gates[at], (c >> 2) & 1)) failed = true;
+      if (!wait(&sh.full[st], round)) failed = true;
+      unsigned char* kt = sm + kPK + st * kPTile;
+      if (MODE == kPWhole) {
+        // v: rows past the chunk's tokens are another sequence's (or stale): 0
+        // there; non-finite elements are noted and replaced by 0
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int u = tid + i * 32 * kPCompute, row = u >> 4, c16 = u & 15;
+          uint4* v = reinterpret_cast<uint4*>(sm + kPV + st * kPTile + (c16 >> 3) * 8192 + row * 128 +
+                                              (((c16 & 7) ^ (row & 7)) << 4));
+          uint4 x = *v;
+          uint32_t* w = &x.x;
+          uint32_t hit = 0;  // an exponent of all ones carries into the sign's place
+#pragma unroll
+          for (int e = 0; e < 4; ++e) hit |= (w[e] & 0x7f807f80u) + 0x00800080u;
+          if (row >= n) {
+            *v = make_uint4(0, 0, 0, 0);
+          } else if ((hit & 0x80008000u) != 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (((w[e >> 1] >> (16 * (e & 1))) & 0x7f80u) == 0x7f80u) {
+                atomicMin(&sh.bad[at][8 * c16 + e], row);
+                w[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+              }
+            *v = x;
+            sh.any_bad[at] = 1;
+          }
+        }
+        // P: a lane has rows ta and ta + 8, columns s0 + 8 c and the next
+        const int ta = 16 * qd + (lane >> 2), s0 = 16 * hh + 2 * (lane & 3);
+        if (!wait(&sh.scores, c & 1)) failed = true;
+        tc::fence_after_sync();
+        float x[8];
+        tmem_ld_16x16(tq + kPColSc + 16 * hh, x);
+        tc::tmem_wait_ld();
+        const Two ga = G[ta], gb = G[ta + 8];
+        unsigned char* pp = sm + kPP + ta * 128 + 4 * (lane & 3);  // the rows are eight apart: the same swizzle
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int sc = s0 + 8 * i;
+          const Two u0 = G[sc], u1 = G[sc + 1];
+          float2 y = make_float2(x[4 * i] * exp2_fast((ga.hi - u0.hi) + (ga.lo - u0.lo)),
+                                 x[4 * i + 1] * exp2_fast((ga.hi - u1.hi) + (ga.lo - u1.lo)));
+          float2 z = make_float2(x[4 * i + 2] * exp2_fast((gb.hi - u0.hi) + (gb.lo - u0.lo)),
+                                 x[4 * i + 3] * exp2_fast((gb.hi - u1.hi) + (gb.lo - u1.lo)));
+          y = mul2(y, p.scale);
+          z = mul2(z, p.scale);
+          if (sc > ta) y.x = 0.f;
+          if (sc + 1 > ta) y.y = 0.f;
+          if (sc > ta + 8) z.x = 0.f;
+          if (sc + 1 > ta + 8) z.y = 0.f;
+          unsigned char* to = pp + (((2 * hh + i) ^ (ta & 7)) << 4);
+          *reinterpret_cast<uint32_t*>(to) = CORE ? split2(y) : pack2(y);
+          *reinterpret_cast<uint32_t*>(to + 1024) = CORE ? split2(z) : pack2(z);
+          if (CORE) {
+            *reinterpret_cast<uint32_t*>(to + 8192) = pack2(y);
+            *reinterpret_cast<uint32_t*>(to + 8192 + 1024) = pack2(z);
+          }
+        }
+        hand(&sh.p[st]);
+      }
+
+      // K' = e^(G_n - G_s) k in three parts, the first in place of K
+      {
+        unsigned char* mid = sm + (MODE == kPLocal ? mid_at(st) : kPMid);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int u = tid + i * 32 * kPCompute, row = u >> 4, c16 = u & 15;
+          const uint32_t off = (c16 >> 3) * 8192 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4);
+          uint4 x = *reinterpret_cast<const uint4*>(kt + off);
+          if (row >= n) x = make_uint4(0, 0, 0, 0);  // another sequence's: may be a NaN
+          const uint32_t* w = &x.x;
+          const float d = sh.dk[at][row];
+          uint4 part[3];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float2 a = mul2(unpack2(w[e]), d);
+            (&part[0].x)[e] = cut2(a);
+            (&part[1].x)[e] = cut2(a);
+            (&part[2].x)[e] = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x7632);
+          }
+          *reinterpret_cast<uint4*>(kt + off) = part[0];
+          *reinterpret_cast<uint4*>(mid + off) = part[1];
+          *reinterpret_cast<uint4*>(mid + kPTile + off) = part[2];
+        }
+        hand(&sh.k[st]);
+      }
+
+      if (MODE == kPWhole) {
+        if (!wait(&sh.z[st], round)) failed = true;
+        if (!wait(&sh.outs, c & 1)) failed = true;
+        tc::fence_after_sync();
+        // o[a][2 c + b]: tokens tt + 8 c and the next, value row jj + 8 b + 16 a
+        const int jj = 32 * qd + (lane >> 2), tt = 16 * hh + 2 * (lane & 3);
+        float2 o[2][4];
+        {
+          float x[2][8], y[2][8];
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            tmem_ld_16x16(tq + ((uint32_t)(16 * a) << 16) + kPColO1 + 16 * hh, x[a]);
+            tmem_ld_16x16(tq + ((uint32_t)(16 * a) << 16) + kPColO2 + 16 * hh, y[a]);
+          }
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 e = *reinterpret_cast<const float2*>(&sh.E[at][tt + 8 * i]);
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+                o[a][2 * i + b] = fma2(make_float2(x[a][4 * i + 2 * b], x[a][4 * i + 2 * b + 1]), e,
+                                       make_float2(y[a][4 * i + 2 * b], y[a][4 * i + 2 * b + 1]));
+          }
+        }
+        if (sh.any_bad[at])
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int bad = sh.bad[phase][jj + 16 * a + 8 * (i & 1)], t = tt + 8 * (i >> 1);
-            if (t >= bad) o[i].x = __int_as_float(0x7fc00000);
-            if (t + 1 >= bad) o[i].y = __int_as_float(0x7fc00000);
+            const int bad = sh.bad[at][jj + 16 * (i >> 2) + 8 * (i & 1)], t = tt + 8 * ((i >> 1) & 1);
+            if (t >= bad) o[i >> 2][i & 3].x = __int_as_float(0x7fc00000);
+            if (t + 1 >= bad) o[i >> 2][i & 3].y = __int_as_float(0x7fc00000);
           }
-      };
-      float2 inv[4];
-      if (GATED) {
-        float2 sq[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sq[c] = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          float2 o[8];
-          read_half(a, o);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sq[i >> 1] = fma2(o[i], o[i], sq[i >> 1]);
-        }
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            sq[c].x += __shfl_xor_sync(0xffffffffu, sq[c].x, d);
-            sq[c].y += __shfl_xor_sync(0xffffffffu, sq[c].y, d);
-          }
-        if (lane < 4)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) *reinterpret_cast<float2*>(&sh.red[qd][tt + 8 * c]) = sq[c];
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + hh) : "memory");
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float2 r = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const float2 x = *reinterpret_cast<const float2*>(&sh.red[w][tt + 8 * c]);
-            r.x += x.x, r.y += x.y;
-          }
-          inv[c] = make_float2(rsqrtf(r.x * (1.f / kTd) + p.rms_eps), rsqrtf(r.y * (1.f / kTd) + p.rms_eps));
-        }
-      }
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        float2 o[8];
-        read_half(a, o);
         if (CORE)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int t = tt + 8 * (i >> 1);
-            float* at = p.core_out + ((int64_t)(t0 + t) * p.Hv + h) * kTd + jj + 16 * a + 8 * (i & 1);
-            if (t < n) at[0] = o[i].x;
-            if (t + 1 < n) at[p.Hv * kTd] = o[i].y;
+            const int t = tt + 8 * ((i >> 1) & 1);
+            float* to = p.core_out + ((int64_t)(s.begin + c * kTc + t) * p.Hv + h) * kTd + jj + 16 * (i >> 2) + 8 * (i & 1);
+            if (t < n) to[0] = o[i >> 2][i & 3].x;
+            if (t + 1 < n) to[p.Hv * kTd] = o[i >> 2][i & 3].y;
           }
-        // blocks (rows jj block 0 and 1 of this half) x (token blocks 2 d, 2 d + 1)
+        float2 inv[2];
+        if (GATED) {
+          // squares over the value rows: the lanes' rows, then the four quadrants
 #pragma unroll
-        for (int d = 0; d < 2; ++d) {
-          const int t = 32 * hh + 16 * d + 8 * (lane >> 4) + (lane & 7), c8 = 4 * qd + 2 * a + ((lane >> 3) & 1);
-          const uint32_t at = smem_u32(sm + kOffO) + (c8 >> 3) * 8192 + t * 128 + (((c8 & 7) ^ (t & 7)) << 4);
+          for (int i = 0; i < 2; ++i) {
+            float2 sq = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+              for (int b = 0; b < 2; ++b) sq = fma2(o[a][2 * i + b], o[a][2 * i + b], sq);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+              sq.x += __shfl_xor_sync(0xffffffffu, sq.x, d);
+              sq.y += __shfl_xor_sync(0xffffffffu, sq.y, d);
+            }
+            if (lane < 4) *reinterpret_cast<float2*>(&sh.red[qd][tt + 8 * i]) = sq;
+          }
+          // the four warps of these tokens; before the next chunk's squares
+          // every one of them has read these (its outputs are handed on)
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + hh) : "memory");
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float2 r = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const float2 x = *reinterpret_cast<const float2*>(&sh.red[w][tt + 8 * i]);
+              r.x += x.x, r.y += x.y;
+            }
+            inv[i] = make_float2(rsqrtf(r.x * (1.f / kTd) + p.rms_eps), rsqrtf(r.y * (1.f / kTd) + p.rms_eps));
+          }
+        }
+        // blocks (value rows b of half a) x (token blocks 0, 1)
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          const int t = 16 * hh + 8 * (lane >> 4) + (lane & 7), c8 = 4 * qd + 2 * a + ((lane >> 3) & 1);
+          const uint32_t to = smem_u32(sm + kPO + st * kPTile) + (c8 >> 3) * 8192 + t * 128 + (((c8 & 7) ^ (t & 7)) << 4);
           uint32_t r[4];
           if (GATED) {
-            ldmatrix_t4(at, r);
+            ldmatrix_t4(to, r);
             const float w0 = sh.w[jj + 16 * a], w1 = sh.w[jj + 16 * a + 8];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
@@ -481,122 +699,47 @@ __global__ void __launch_bounds__(kTThreads, 2)
               const float2 e = mul2(z, -kLog2e);
               const float2 den = make_float2(1.f + exp2_fast(e.x), 1.f + exp2_fast(e.y));
               const float2 silu = make_float2(__fdividef(z.x, den.x), __fdividef(z.y, den.y));
-              const float2 g = fma2(silu, mul2(inv[2 * d + (m >> 1)], m & 1 ? w1 : w0), make_float2(-0.f, -0.f));
-              o[4 * d + m] = fma2(o[4 * d + m], g, make_float2(-0.f, -0.f));
+              const float2 g = fma2(silu, mul2(inv[m >> 1], m & 1 ? w1 : w0), make_float2(-0.f, -0.f));
+              o[a][m] = fma2(o[a][m], g, make_float2(-0.f, -0.f));
             }
           }
 #pragma unroll
-          for (int m = 0; m < 4; ++m) r[m] = pack2(o[4 * d + m]);
-          stmatrix_t4(at, r);
+          for (int m = 0; m < 4; ++m) r[m] = pack2(o[a][m]);
+          stmatrix_t4(to, r);
         }
-      }
-      fence_proxy_async_smem();
-    }
-    tc::fence_before_sync();
-    __syncthreads();  // #3: K' is in shared memory, the outputs are staged and their TMEM columns read
-    if (warp == kDeltaWarp) {
-      tc::fence_after_sync();
-      const uint32_t id = tc::idesc(tc::kBF16, 128, 128) | kTransA | kTransB;
-      const uint64_t dK0 = sdesc_mn128(smem_u32(kt));
-#pragma unroll 1
-      for (int k = 0; k < 12; ++k)
-        tc::mma_f16_elect(tb + kColX, dV + ((k & 3) * 2048 >> 4),
-                          (k < 4 ? dK0 : dMid + (k < 8 ? 0 : kTile16 >> 4)) + ((k & 3) * 2048 >> 4), id, k > 0);
-      tc::mma_commit_elect(&sh.delta);
-    } else if (warp == kGateWarp) {
-      if (more) {
-        // one decay for all tokens: full chunks share their sums, in both buffers after the second
-        if (p.g_stride != 0 || t0 == s.begin || tokens(t0 + kTc) < kTc) put_sums(sh.G[phase ^ 1]);
-        if (MODE == kTLocal) total = add2(total, gn);
-        fetch_g(t0 + 2 * kTc);
-      }
-    } else if (MODE == kTWhole && (!CORE || p.out != nullptr)) {
-      if (n == kTc) {
-        if (warp == kStoreWarp && lane == 0) {
-          for (int b = 0; b < 2; ++b) tc::tma_store_2d(&tm_o, h * kTd + 64 * b, t0, sm + kOffO + 8192 * b);
-          bulk_commit();
-          bulk_wait_read_all();
-        }
-      } else if (warp != 7) {
-        // a last, shorter chunk: its rows alone, by the warps 0, 2, 3, 4 and 5
-        const int first = warp == 0 ? 0 : warp - 1;
-        for (int u = first * 32 + lane; u < 16 * n; u += 5 * 32) {
-          const int t = u >> 4, c8 = u & 15;
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + ((int64_t)(t0 + t) * p.Hv + h) * kTd + 8 * c8) =
-              *reinterpret_cast<const uint4*>(sm + kOffO + (c8 >> 3) * 8192 + t * 128 + (((c8 & 7) ^ (t & 7)) << 4));
-        }
+        hand(&sh.o[st]);
+        take_delta(c);
+        if (c + 1 < chunks) put_state();
+      } else if (c > 0) {
+        take_delta(c - 1);
+        hand(&sh.o[st ^ 1]);
       }
     }
-    if (GATED && more && warp == kStoreWarp && lane == 0) load_z(t0 + kTc);
-    const Decay a = decay_factor((G[kTc - 1].hi + G[kTc - 1].lo) * kLn2);
-    if (!mbar_wait_bounded(&sh.delta, phase, abort_flag)) failed = true;
-    tc::fence_after_sync();
-    if (tid == 0 && (MODE == kTLocal ? t0 + 2 * kTc < s.end : more)) load_kv(t0 + (MODE == kTLocal ? 2 : 1) * kTc, stage);
-    {
-      const float2 f = make_float2(a.factor, a.factor), keep = make_float2(a.keep, a.keep);
-      const bool spoilt = MODE == kTWhole && sh.any_bad[phase] && sh.bad[phase][j] < kTc;
+    if (MODE == kPLocal) take_delta(chunks - 1);
+    if (!failed && !*abort_flag && (MODE == kPLocal || s.index + 1 == s.parts)) {
+      float* to = MODE == kPLocal ? sg.states + (int64_t)blockIdx.x * (kTd * kTd) : gS;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float d[32];
-        tc::tmem_ld16(tq + kColX + 64 * hh + 32 * c, *reinterpret_cast<float(*)[16]>(d));
-        tc::tmem_ld16(tq + kColX + 64 * hh + 32 * c + 16, *reinterpret_cast<float(*)[16]>(d + 16));
-        tc::tmem_wait_ld();
-        if (a.keep != 0.f) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            S[16 * c + e] = fma2(f, S[16 * c + e], fma2(keep, S[16 * c + e], make_float2(d[2 * e], d[2 * e + 1])));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) S[16 * c + e] = fma2(f, S[16 * c + e], make_float2(d[2 * e], d[2 * e + 1]));
-        }
-        if (spoilt)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) S[16 * c + e] = make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
-        if (MODE == kTWhole && more) put_state(c);
-      }
-      if (MODE == kTWhole && more) tc::tmem_wait_st();
+      for (int e = 0; e < 4; ++e)
+        store8(to + at0 + 8 * e, make_float4(S[4 * e].x, S[4 * e].y, S[4 * e + 1].x, S[4 * e + 1].y),
+               make_float4(S[4 * e + 2].x, S[4 * e + 2].y, S[4 * e + 3].x, S[4 * e + 3].y));
     }
-    tc::fence_before_sync();
-    // #1 of the next chunk: everything of this one is read
-    if (__syncthreads_or(failed)) break;
-  }
-
-  if (!failed && !*abort_flag) {
-    if (MODE == kTLocal || s.index + 1 == s.parts) {
-      float* to = MODE == kTLocal ? sg.states + (int64_t)blockIdx.x * (kTd * kTd) : gS;
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        store8(to + at0 + 8 * c, make_float4(S[4 * c].x, S[4 * c].y, S[4 * c + 1].x, S[4 * c + 1].y),
-               make_float4(S[4 * c + 2].x, S[4 * c + 2].y, S[4 * c + 3].x, S[4 * c + 3].y));
-    }
-    if (MODE == kTLocal && warp == 1 && lane == 0) sg.decays[blockIdx.x] = exp2f(total.hi + total.lo);
-  }
-  // no load may still be in flight when the CTA ends: after a wait that gave
-  // up the next chunk's may be
-  if (tid == 0) {
-    if (MODE == kTLocal) {  // load i goes to stage i % 2
-      mbar_wait(&sh.load_kv[0], ((kv_loads + 1) / 2 - 1) & 1);
-      if (kv_loads > 1) mbar_wait(&sh.load_kv[1], (kv_loads / 2 - 1) & 1);
-    } else {
-      mbar_wait(&sh.load_kv[0], (kv_loads - 1) & 1);
-    }
-    if (MODE == kTWhole) mbar_wait(&sh.load_q, (q_loads - 1) & 1);
-  }
-  if (MODE == kTWhole && warp == kStoreWarp && lane == 0) {
-    if (GATED) mbar_wait(&sh.load_z, (z_loads - 1) & 1);
-    bulk_wait_all();
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == kPMma) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tb, kCols);
+    tc::tmem_dealloc(tb, kPCols);
   }
 }
 
 }  // namespace
 
-bool decay_tc_fits(int32_t dtype, int32_t D) { return dtype == GDN_BF16 && D == kTd; }
+bool decay_tc_fits(int32_t dtype, int32_t D, int32_t N, int64_t T) {
+  // short sequences cost a CTA its start more than its chunk: up to 16 tokens
+  // on average the scan is faster (64 sequences of 8 tokens, 32 heads: 82
+  // against 131 us; of 16: 125 against 135; of 32: 219 against 142)
+  return dtype == GDN_BF16 && D == kTd && T > 16ll * N;
+}
 
 bool decay_tc_supported(const DecayArgs& p) {
   // states are read and written in 32-byte accesses
@@ -605,34 +748,29 @@ bool decay_tc_supported(const DecayArgs& p) {
 
 cudaError_t launch_decay_tc(const DecayArgs& p, const DecaySegments& sg, cudaStream_t stream) {
   const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  CUtensorMap mq, mk, mv, mz{}, mo{};
-  bool mz_ok, mo_ok;
+  CUtensorMap mq, mk, mv, mz{}, mo{};  // the maps of what is not there are never used
+  const int64_t vw = (int64_t)p.Hv * kTd;
   if (!tc::make_map_2d(&mq, p.q, p.T, (int64_t)p.Hk * kTd, p.q_stride, 2, bf, 64, kTc, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !tc::make_map_2d(&mk, p.k, p.T, (int64_t)p.Hk * kTd, p.k_stride, 2, bf, 64, kTc, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !tc::make_map_2d(&mv, p.v, p.T, (int64_t)p.Hv * kTd, p.v_stride, 2, bf, 64, kTc, CU_TENSOR_MAP_SWIZZLE_128B))
+      !tc::make_map_2d(&mv, p.v, p.T, vw, p.v_stride, 2, bf, 64, kTc, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      (p.z != nullptr && !tc::make_map_2d(&mz, p.z, p.T, vw, p.z_stride, 2, bf, 64, kTc, CU_TENSOR_MAP_SWIZZLE_128B)) ||
+      (p.out != nullptr && !tc::make_map_2d(&mo, p.out, p.T, vw, vw, 2, bf, 64, kTc, CU_TENSOR_MAP_SWIZZLE_128B)))
     return cudaErrorInvalidValue;
-  // z and out: the maps of those that are not there are never used
-  mz_ok = p.z == nullptr || tc::make_map_2d(&mz, p.z, p.T, (int64_t)p.Hv * kTd, p.z_stride, 2, bf, 64, kTc,
-                                            CU_TENSOR_MAP_SWIZZLE_128B);
-  mo_ok = p.out == nullptr || tc::make_map_2d(&mo, p.out, p.T, (int64_t)p.Hv * kTd, (int64_t)p.Hv * kTd, 2, bf, 64, kTc,
-                                              CU_TENSOR_MAP_SWIZZLE_128B);
-  if (!mz_ok || !mo_ok) return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)(sg.slots * p.Hv);
-  const auto run = [&](auto* kernel, bool core) {
-    const int smem = (int)tc_smem(core) + 1024;
+  const auto run = [&](auto* kernel) {
+    constexpr int smem = (int)kPSmem + 1024;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kTThreads, smem, stream>>>(p, sg, mq, mk, mv, mz, mo);
+    kernel<<<grid, kPThreads, smem, stream>>>(p, sg, mq, mk, mv, mz, mo);
     return cudaGetLastError();
   };
   if (sg.states != nullptr) {
-    const cudaError_t e = run(decay_tc_kernel<kTLocal, false, false>, false);
+    const cudaError_t e = run(decay_tc_kernel<kPLocal, false, false>);
     if (e != cudaSuccess) return e;
   }
   if (p.core_out != nullptr)
-    return p.z != nullptr ? run(decay_tc_kernel<kTWhole, true, true>, true) : run(decay_tc_kernel<kTWhole, true, false>, true);
-  return p.z != nullptr ? run(decay_tc_kernel<kTWhole, false, true>, false)
-                        : run(decay_tc_kernel<kTWhole, false, false>, false);
+    return p.z != nullptr ? run(decay_tc_kernel<kPWhole, true, true>) : run(decay_tc_kernel<kPWhole, true, false>);
+  return p.z != nullptr ? run(decay_tc_kernel<kPWhole, false, true>) : run(decay_tc_kernel<kPWhole, false, false>);
 }
 
 }  // namespace gdn

@@ -199,7 +199,7 @@ cudaError_t launch_linear(LinearArgs p, const void* x, int64_t x_stride, const v
 // tokens of a segment (decay_scan.cu); chunks: for the tensor-core kernel
 int32_t decay_segment_len(int32_t N, int64_t T, int32_t Hv, bool chunks);
 // whether the tensor-core kernel takes these sizes
-bool decay_tc_fits(int32_t dtype, int32_t D);
+bool decay_tc_fits(int32_t dtype, int32_t D, int32_t N, int64_t T);
 cudaError_t launch_decay_step(const DecayArgs& p, int32_t dtype, int32_t D, int32_t batch, cudaStream_t stream);
 cudaError_t launch_decay_scan(const DecayArgs& p, const DecaySegments& sg, int32_t dtype, int32_t D,
                               cudaStream_t stream);
@@ -207,8 +207,6 @@ cudaError_t launch_decay_scan(const DecayArgs& p, const DecaySegments& sg, int32
 // whether it takes this state, too
 bool decay_tc_supported(const DecayArgs& p);
 cudaError_t launch_decay_tc(const DecayArgs& p, const DecaySegments& sg, cudaStream_t stream);
-cudaError_t launch_decay_pipe(const DecayArgs& p, const DecaySegments& sg, cudaStream_t stream);  // decay_pipe.cu
-cudaError_t read_error_decay_pipe(int32_t* status, bool clear);
 cudaError_t read_error_decay_tc(int32_t* status, bool clear);
 cudaError_t launch_add_rmsnorm(const AddRmsNormArgs& p, int32_t dtype, cudaStream_t stream);
 cudaError_t launch_linear_fp8(const LinearFp8Args& p, const void* x, int64_t x_stride, const void* w,

@@ -189,6 +189,55 @@ def test_prefill_matches_the_recurrence(dtype, hk, hv, D, gated, tiled, token_de
     run_prefill(c, lengths)
 
 
+@pytest.mark.parametrize("gated", [True, False])
+@pytest.mark.parametrize("lengths", [[1, 0, 63, 64, 65, 130, 193], [700, 3]])
+def test_prefill_outputs_one_at_a_time(gated, lengths):
+    """out alone: the tensor-core kernel then rounds S and P to bf16, each 2^-8 of a factor of one product, so o is off
+    by at most 2^-8 of the magnitudes; the state is the same to the bit. core_out alone is the same as beside out."""
+    T = sum(lengths)
+    cu = np.concatenate([[0], np.cumsum(lengths)])
+    c = Case(31, 2, 4, 128, "bf16", T, len(lengths), gated=gated)
+    dcu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    S0 = c.state.clone()
+    gdn.gdn_decay_prefill(c.d, dcu, c.q, c.k, c.v, c.g, c.state, core_out=c.core, out=c.out, **c.gate())
+    S, core = S0.clone(), torch.empty_like(c.core)
+    gdn.gdn_decay_prefill(c.d, dcu, c.q, c.k, c.v, c.g, S, core_out=core)
+    assert torch.equal(S, c.state) and torch.equal(core, c.core)
+    S = S0.clone()
+    c.out.fill_(7.25)
+    gdn.gdn_decay_prefill(c.d, dcu, c.q, c.k, c.v, c.g, S, out=c.out, **c.gate())
+    assert torch.equal(S, c.state)
+    for n, length in enumerate(lengths):
+        if length:
+            a, b = cu[n], cu[n + 1]
+            o, _, do, mag, _, _ = c.reference(a, b, f64(S0[n]))
+            do = do + (2.0 ** -8 + SPLIT) * mag
+            y, dy = (ref.gated(o, f64(c.z[a:b]).reshape(o.shape), f64(c.w), 1e-6, c.dtype, do) if gated
+                     else (o, ref.rounded(o, c.dtype, do)))
+            ref.check(f64(c.out[a:b]), y, dy, f"sequence {n}")
+
+
+def test_prefill_state_aligned_to_16_bytes_alone():
+    """The tensor-core kernel wants 32; the call takes 16."""
+    lengths = [100, 60]
+    c = Case(32, 1, 2, 128, "bf16", 160, 2)
+    n = c.state.numel()
+    buf = torch.empty(n + 8, device="cuda")
+    at = 4 if buf.data_ptr() % 32 == 0 else 0
+    shifted = buf[at:at + n].view(c.state.shape)
+    shifted.copy_(c.state)
+    assert shifted.data_ptr() % 32 == 16
+    c.state = shifted
+    run_prefill(c, lengths)
+
+
+@pytest.mark.parametrize("N,L", [(40, 1), (40, 3), (33, 16), (20, 17), (70, 40)])
+def test_prefill_several_tokens_of_many_sequences(N, L):
+    """Both sides of the length from which chunks are used: several tokens of a decode step, short prompts."""
+    c = Case(33 + L, 2, 2, 128, "bf16", N * L, N)
+    run_prefill(c, [L] * N)
+
+
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f32", 64), ("f16", 128)])
 @pytest.mark.parametrize("workspace", ["auto", None])
 def test_prefill_long_sequences(dtype, D, workspace):
