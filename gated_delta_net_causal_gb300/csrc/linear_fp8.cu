@@ -59,7 +59,7 @@ __device__ __forceinline__ void store8(T* dst, const float* x, int n, bool wide)
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kFThreads, 2)
+__global__ void __launch_bounds__(kFThreads, 4)
     linear_fp8_band_kernel(const LinearFp8Args p, const BandPlan plan, const __grid_constant__ CUtensorMap tm_x,
                            const __grid_constant__ CUtensorMap tm_w) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -405,16 +405,22 @@ cudaError_t launch_band(const LinearFp8Args& p, const void* x, int64_t x_stride,
     return cudaErrorInvalidValue;
   const int bands = (p.N + kFBand - 1) / kFBand, nk = (p.K + kFK - 1) / kFK;
   const int64_t tiles = (p.M + kFM - 1) / kFM;
-  // as many K splits as keep every CTA slot busy in one wave, each of two K steps at least
+  // Two CTAs of 96 KB an SM and as many K splits as keep them busy in one wave,
+  // each of two K steps at least (12352 x 2048, 64 rows: 10.6 us; three CTAs of
+  // 64 KB 11.5, four of 48 KB 17.9). Where the bands fill several waves, four
+  // CTAs of 54 KB in all, so that one starts and stores under the others'
+  // streams (65536 x 2048: one row 27.7 us against 41.9, 128 rows 37.0 against
+  // 42.4; three CTAs 33.5 and 36.8).
+  const bool waves = bands * tiles >= 4 * sm_count();
   int64_t splits = 2 * sm_count() / (bands * tiles);
   if (splits > nk / 2) splits = nk / 2;
   if (splits > kFMaxSplits) splits = kFMaxSplits;
   plan.splits = splits < 1 ? 1 : (int)splits;
   const uint32_t x_tile = ((uint32_t)plan.box_rows * kFK + 1023) / 1024 * 1024, stage_bytes = x_tile + kFWTile;
-  const int fit = (int)(96 * 1024 / stage_bytes);
-  plan.stages = fit < kFMaxStages ? fit : kFMaxStages;
-  // the MMA reads kFM rows from a stage's start
-  const uint32_t smem = (uint32_t)plan.stages * stage_bytes + (kFM * kFK - x_tile) + 1024;
+  const uint32_t extra = (kFM * kFK - x_tile) + 1024;  // the MMA reads kFM rows from a stage's start; alignment
+  const int fit = (int)((waves ? 54 * 1024 - extra : 96 * 1024) / stage_bytes);
+  plan.stages = fit < 2 ? 2 : (fit < kFMaxStages ? fit : kFMaxStages);  // two hold a split's fp32 tile, too
+  const uint32_t smem = (uint32_t)plan.stages * stage_bytes + extra;
   auto kern = linear_fp8_band_kernel<T>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;

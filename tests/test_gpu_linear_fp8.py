@@ -61,6 +61,11 @@ def test_layer_sizes(M, N, K):
     run(7, M, N, K)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 40960, 128), (16, 38913, 400), (50, 39000, 656), (128, 41000, 256)])
+def test_bands_of_several_waves(M, N, K):
+    run(8, M, N, K, y_pad=8)
+
+
 def test_largest_codes_and_zeros():
     """All 448: every sum is K 448^2, the largest that fp32 sums of codes reach; and all zeros."""
     for M in (2, 130):
