@@ -41,13 +41,13 @@ __device__ __forceinline__ uint32_t e4m3x2(float x, float y) {
 
 // what the values of a row become once its reductions are there
 struct RowScale {
-  float inv, inv_q, scale;
+  float inv, scale, inv_scale;
 };
 __device__ __forceinline__ RowScale row_scale(const AddRmsNormArgs& p, float ss, float top) {
   RowScale r;
   r.inv = p.norm_w == nullptr ? 1.f : 1.f / sqrtf(ss / (float)p.cols + p.eps);
   r.scale = fmaxf(top * r.inv / kE4m3Max, kScaleFloor);
-  r.inv_q = r.inv / r.scale;
+  r.inv_scale = 1.f / r.scale;  // not inv / scale: a row of zeros would make that infinite
   return r;
 }
 // Elements 2 k and 2 k + 1 of a vector in fp32 (the second is 0 where VEC is 1)
@@ -129,14 +129,13 @@ __device__ __forceinline__ void give(const AddRmsNormArgs& p, int64_t row, int i
   constexpr int N2 = (VEC + 1) / 2;
   float2 t[N2];
 #pragma unroll
-  for (int k = 0; k < N2; ++k) t[k] = times(pair<VEC>(s, k), w.v[k]);
+  for (int k = 0; k < N2; ++k) t[k] = times(times(pair<VEC>(s, k), w.v[k]), make_float2(r.inv, r.inv));
   if (p.out != nullptr) {
     Pack<T, VEC> c;
 #pragma unroll
     for (int k = 0; k < N2; ++k) {
-      const float2 y = times(t[k], make_float2(r.inv, r.inv));
-      c.v[2 * k] = from_f32<T>(y.x);
-      if (VEC > 1) c.v[VEC > 1 ? 2 * k + 1 : 0] = from_f32<T>(y.y);
+      c.v[2 * k] = from_f32<T>(t[k].x);
+      if (VEC > 1) c.v[VEC > 1 ? 2 * k + 1 : 0] = from_f32<T>(t[k].y);
     }
     reinterpret_cast<Pack<T, VEC>*>(static_cast<T*>(p.out) + row * p.out_stride)[i] = c;
   }
@@ -144,7 +143,7 @@ __device__ __forceinline__ void give(const AddRmsNormArgs& p, int64_t row, int i
     uint32_t q[N2];
 #pragma unroll
     for (int k = 0; k < N2; ++k) {
-      const float2 y = times(t[k], make_float2(r.inv_q, r.inv_q));
+      const float2 y = times(t[k], make_float2(r.inv_scale, r.inv_scale));
       q[k] = e4m3x2(y.x, y.y);
     }
     uint8_t* oq = static_cast<uint8_t*>(p.out_q) + row * p.out_q_stride + (int64_t)i * VEC;

@@ -24,7 +24,9 @@ def rows_of(gen, rows, cols, stride, dtype, std=1.0):
 
 def verify(x, r, w, eps, dtype, s, y, q, scale):
     """Outputs (None where not asked for) of the formula; the mean's fp32 sum and the products are allowed
-    (cols / 32 + 40) u of the value: a lane sums at most cols / 32 squares, the rest are single operations."""
+    (cols / 32 + 40) u of the value: a lane sums at most cols / 32 squares, the rest are single operations. Where the
+    product s w is below fp32's normal range it is off by half of its smallest step, 2^-150, instead, and what
+    multiplies it then is at most eps^(-1/2)."""
     cols = x.shape[1]
     X = f64(x) + (0 if r is None else f64(r))
     if s is not None:
@@ -33,16 +35,18 @@ def verify(x, r, w, eps, dtype, s, y, q, scale):
     elif r is not None:
         X = f64((x.float() + r.float()).to(x.dtype))
     rel = (cols / 32 + 40) * U
+    low = 0.0 if w is None else 1.01 * 2.0 ** -150 / np.sqrt(eps)
     Y = X if w is None else X / np.sqrt((X * X).mean(-1, keepdims=True) + eps) * f64(w)
     if y is not None:
-        check(f64(y), Y, (HALF_STEP[dtype] + 1.01 * rel) * np.abs(Y) + TINY[dtype], "out")
+        check(f64(y), Y, (HALF_STEP[dtype] + 1.01 * rel) * np.abs(Y) + TINY[dtype] + low, "out")
     if q is not None:
         sc = np.maximum(np.abs(Y).max(-1) / 448, 2.0 ** -126)
         check(f64(scale), sc, rel * sc, "out_scale")
         code = Y / sc[:, None]
         assert np.abs(f64(q)).max() <= 448
         # half a step: 2^-4 of the value, or half of e4m3's smallest step 2^-9
-        check(f64(q), code, np.maximum(2.0 ** -4 * np.abs(code), 2.0 ** -10) + 3 * rel * np.abs(code), "out_q")
+        check(f64(q), code, np.maximum(2.0 ** -4 * np.abs(code), 2.0 ** -10) + 3 * rel * np.abs(code) + low / sc[:, None],
+              "out_q")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
@@ -145,6 +149,23 @@ def test_zero_tiny_and_large_rows():
     assert (np.abs(f64(q)[1] * f64(sc)[1, None] - 1e-38) <= 2.0 ** -4 * 1e-38).all()
     gdn.gdn_add_rmsnorm(x, torch.ones(256, device="cuda"), out=y, eps=0.0 + 1e-6)
     assert not f64(y)[0].any() and np.allclose(f64(y)[3], 1.0, rtol=1e-5)
+
+
+@pytest.mark.parametrize("rows", [3, 2000])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_codes_of_zero_and_tiny_normed_rows(dtype, rows):
+    """Zeros (a padded row) and rows so small that their inverse root over their scale passes fp32's range."""
+    x = torch.randn((rows, 512), generator=torch.Generator().manual_seed(2))
+    x[0] = 0.0
+    x[1] *= 1e-37
+    x[rows - 1] = 0.0
+    x[rows - 1, 5] = 2e-37
+    x = x.to(DT[dtype]).cuda()
+    w = (1 + 0.3 * torch.randn(512, generator=torch.Generator().manual_seed(3))).cuda()
+    y, q, sc = torch.empty_like(x), torch.empty(x.shape, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(rows, device="cuda")
+    gdn.gdn_add_rmsnorm(x, w, out=y, out_q=q, out_scale=sc)
+    verify(x, None, w, 1e-6, dtype, None, y, q, sc)
+    assert not f64(q)[0].any() and not f64(y)[0].any()
 
 
 def test_nan_and_infinity_stay_in_their_rows():
