@@ -268,9 +268,10 @@ __global__ void __launch_bounds__(NT) add_rmsnorm_ring_kernel(const AddRmsNormAr
       bulk_load(ring + (size_t)s * slot_bytes + bytes, static_cast<const T*>(p.residual) + row * p.residual_stride, bytes,
                 &full[s]);
   };
+  int64_t fills = 0;  // thread 0's
   if (tid == 0)
-    for (int s = 0; s < slots && blockIdx.x + (int64_t)s * gridDim.x < p.rows; ++s)
-      fill(s, blockIdx.x + (int64_t)s * gridDim.x);
+    for (; fills < slots && blockIdx.x + fills * gridDim.x < p.rows; ++fills)
+      fill((int)fills, blockIdx.x + fills * gridDim.x);
   Weights<VEC> w[NV];
 #pragma unroll
   for (int n = 0; n < NV; ++n)
@@ -298,7 +299,10 @@ __global__ void __launch_bounds__(NT) add_rmsnorm_ring_kernel(const AddRmsNormAr
     // every thread has read the row
     if (tid == 0 && !*abort_flag) {
       const int64_t next = row + (int64_t)slots * gridDim.x;
-      if (next < p.rows) fill(slot, next);
+      if (next < p.rows) {
+        fill(slot, next);
+        ++fills;
+      }
     }
     if (ok) {
       const RowScale sc = row_scale(p, ss, top);
@@ -312,6 +316,9 @@ __global__ void __launch_bounds__(NT) add_rmsnorm_ring_kernel(const AddRmsNormAr
       phase ^= 1;
     }
   }
+  // after a wait that gave up: no copy may be in flight when the CTA ends
+  if (tid == 0 && *abort_flag)
+    for (int s = 0; s < slots && s < fills; ++s) mbar_wait(&full[s], ((fills - s + slots - 1) / slots - 1) & 1);
 }
 
 int norm_sms() {

@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // given after o(c) was seen, so none is missed.
     float g0 = 0.f, g1 = 0.f;  // log decays of tokens 2 lane and 2 lane + 1 of a chunk
     const auto fetch_g = [&](int c) {
-      const int t = s.begin + c * kTc + 2 * lane;
+      const int64_t t = (int64_t)s.begin + c * kTc + 2 * lane;
       const float* g = p.g + t * p.g_stride + h;
       g0 = t < s.end ? g[0] : 0.f;
       g1 = t + 1 < s.end ? g[p.g_stride] : 0.f;

@@ -303,6 +303,30 @@ def test_prefill_nan_stays_behind_its_token():
     assert torch.isnan(c.core[140]).all() and torch.isnan(c.state[1]).all()
 
 
+@pytest.mark.parametrize("dtype,D,workspace", [("bf16", 128, "auto"), ("bf16", 128, None), ("f16", 128, "auto"),
+                                               ("f32", 64, "auto"), ("bf16", 96, None)])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_prefill_bad_neighbours(dtype, D, workspace, what):
+    """Every other sequence and the rows behind the last one hold nothing finite, their decays included: what a tile
+    reads past a sequence's end must not reach it."""
+    lengths = [100, 40, 65, 3, 1, 70, 300, 20, 5]
+    cu = np.concatenate([[0], np.cumsum(lengths)])
+    T = int(cu[-1]) + 40
+    c = Case(23, 1, 2, D, dtype, T, len(lengths))
+    for n in range(1, len(lengths), 2):
+        c.act[cu[n]:cu[n + 1]] = what
+        c.g[cu[n]:cu[n + 1]] = float("nan")
+    c.act[cu[-1]:] = what
+    c.g[cu[-1]:] = float("nan")
+    S0 = f64(c.state)
+    gdn.gdn_decay_prefill(c.d, torch.tensor(cu, dtype=torch.int32, device="cuda"), c.q, c.k, c.v, c.g, c.state,
+                          core_out=c.core, out=c.out, workspace=workspace, **c.gate())
+    for n in range(0, len(lengths), 2):
+        c.check(cu[n], cu[n + 1], S0[n], c.state[n], f"sequence {n}", SPLIT if dtype == "bf16" and D == 128 else 0.0)
+    assert (c.core[cu[-1]:] == 7.25).all() and (c.out[cu[-1]:].float() == 7.25).all()
+    assert gdn.gdn_device_error() == 0
+
+
 def test_prefill_infinite_value_spoils_its_value_row_alone():
     """An infinity in one element of v makes that value row non-finite from its token on, and nothing else."""
     T = 140
