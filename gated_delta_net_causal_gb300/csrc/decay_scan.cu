@@ -231,7 +231,9 @@ cudaError_t launch_scan_t(const DecayArgs& p, const DecaySegments& sg, int32_t D
 // of m cost 2 m + 2 n / m, least at m = sqrt(n).
 int32_t decay_segment_len(int32_t N, int64_t T, int32_t Hv, bool chunks) {
   const int64_t kCtas = chunks ? 152 : 304;
-  const int64_t more = (2 * kCtas / Hv - N) / 2;  // a sequence's last segment is half full on average
+  // a sequence's last segment is half full on average; a lone one's is full
+  // (4096 tokens, 48 heads: 144 -> 106 us, 64 heads: 179 -> 147 us)
+  const int64_t more = N == 1 ? kCtas / Hv : (2 * kCtas / Hv - N) / 2;
   const int64_t unit = chunks ? 64 : kTile;
   if (more < 1 || T <= (chunks ? 64 : 32)) return (int32_t)T + 1;
   int64_t len = ((T + more - 1) / more + unit - 1) / unit * unit;  // below T + unit
