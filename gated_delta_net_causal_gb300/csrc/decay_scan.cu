@@ -221,24 +221,37 @@ cudaError_t launch_scan_t(const DecayArgs& p, const DecaySegments& sg, int32_t D
 
 // Sized for the 152 SMs of the one target, so that a workspace asked for on
 // one thread fits the call on another: as many segments as give every SM one
-// CTA (token by token: two) and no CTA a second turn, none where the
-// (sequence, V head) pairs come near that by themselves. With few heads that
-// would be many short ones, and the last of them reads the states that all
-// others add: on the tensor cores a chunk of 64 tokens costs about as much as
-// seven such states, so n chunks in segments of m cost m + n / (7 m), least
-// at m = sqrt(n / 7); token by token a state costs about as much as two
-// tokens (whatever D: both go with the state's size), so n tokens in segments
-// of m cost 2 m + 2 n / m, least at m = sqrt(n).
+// CTA (token by token: two) and no CTA a second turn, as many to a sequence if
+// they are alike, else (and token by token, but for a lone sequence) with room
+// for a half full last one of each. With few heads that would be many short
+// ones, and the last of them reads the states that all others add: on the
+// tensor cores a chunk of 64 tokens costs about as much as seven such states,
+// so n chunks in segments of m cost m + n / (7 m), least at m = sqrt(n / 7);
+// token by token a state costs about as much as two tokens (whatever D: both
+// go with the state's size), so n tokens in segments of m cost 2 m + 2 n / m,
+// least at m = sqrt(n).
+// On the tensor cores n chunks take 8 + 2.65 n us in one pass and 17 + 4.2 m +
+// 0.5 n / m in two over segments of m, so short prompts and those of many
+// heads stay whole (one prompt, 32 heads, one pass and two: 128 tokens 13 and
+// 20 us, 512 tokens 29 and 26, 2048 tokens 93 and 50).
 int32_t decay_segment_len(int32_t N, int64_t T, int32_t Hv, bool chunks) {
-  const int64_t kCtas = chunks ? 152 : 304;
-  // a sequence's last segment is half full on average; a lone one's is full
-  // (4096 tokens, 48 heads: 144 -> 106 us, 64 heads: 179 -> 147 us)
-  const int64_t more = N == 1 ? kCtas / Hv : (2 * kCtas / Hv - N) / 2;
-  const int64_t unit = chunks ? 64 : kTile;
-  if (more < 1 || T <= (chunks ? 64 : 32)) return (int32_t)T + 1;
-  int64_t len = ((T + more - 1) / more + unit - 1) / unit * unit;  // below T + unit
-  const int64_t n = (T + unit - 1) / unit, per = chunks ? 7 : 8;   // 8 tokens a unit: m^2 >= T
-  while (per * (len / unit) * (len / unit) < n) len += unit;
+  const int32_t whole = (int32_t)T + 1;
+  if (T == 0) return whole;
+  if (chunks) {
+    const int64_t n = (T + 63) / 64, sms = 152 / Hv, each = sms / N;
+    const int64_t more = each >= 2 ? N * each : sms - N / 2;
+    if (more < 1) return whole;
+    int64_t len = (n + more - 1) / more;
+    while (7 * N * len * len < n) ++len;
+    // the longest sequence, times N: more than the mean where they may be unlike
+    const int64_t longest = N == 1 ? n : each >= 2 ? n + n / 4 : 2 * n;
+    return 53 * longest > (84 * len + 180) * N + 10 * n / len ? (int32_t)(64 * len) : whole;
+  }
+  const int64_t more = N == 1 ? 304 / Hv : (608 / Hv - N) / 2;
+  if (more < 1 || T <= 32) return whole;
+  int64_t len = ((T + more - 1) / more + kTile - 1) / kTile * kTile;  // below T + kTile
+  const int64_t n = (T + kTile - 1) / kTile;
+  while (8 * (len / kTile) * (len / kTile) < n) len += kTile;  // 8 tokens a tile: m^2 >= T
   return (int32_t)len;
 }
 
