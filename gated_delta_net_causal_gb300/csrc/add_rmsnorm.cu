@@ -6,6 +6,9 @@
 // in fp32. With t = s w, max|y| is max|t| times the inverse root, so both
 // reductions of a row go through one barrier and its values stay in
 // registers between: x and r are read once, each output is written once.
+// Bound by those bytes: 8192 rows of 8192 bf16 with a residual to e4m3, 81 us,
+// 5.8 TB/s (a copy: 6.8; one row a CTA without the ring below: 122 us); 999
+// rows of 2051 fp16, which allow no wide accesses, 10.2 us.
 #include <type_traits>
 
 #include "gdn_common.cuh"

@@ -6,6 +6,9 @@
 // loads before it uses any, so a CTA has 64 KB in flight and the CTAs
 // resident on an SM cover each other's compute and stores. The rows of a
 // state are independent but for the norm, which takes one barrier.
+// Measured: 128 sequences x 48 heads 119 us, 6.8 TB/s (a copy: 6.8); 64 rows of
+// a pool, 32 heads, 44.5 us, 6.1 TB/s. States are read and written once: loads
+// and stores marked so (ordinary stores: 125 and 47 us).
 #include "decay_common.cuh"
 
 namespace gdn {

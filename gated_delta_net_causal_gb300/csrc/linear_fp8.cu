@@ -11,6 +11,9 @@
 // distributed shared memory, so the result does not depend on which ran
 // first. K past the end of a row reads as zeros.
 //
+// Measured, 12352 x 2048: one row and 64 rows 12.3 us a call (10.6 us as
+// graph nodes, 2.4 TB/s): the ramp of 193 CTAs that each stream 128 KB.
+//
 // linear_fp8_tile_kernel: 256 x 256 tiles for prompts, each on a pair of CTAs
 // (cta_group::2). An MMA of N = 256 holds the tensor pipe as long as its work
 // takes (one of N = 64 more than twice as long), about 124 cycles a K step of
@@ -20,7 +23,8 @@
 // in either CTA, 16 KB. Persistent: warp 0 loads, warp 1 of the first CTA
 // issues the MMAs, four warps of each scale and store the previous tile's 128
 // rows out of the other half of TMEM, through swizzled shared memory and TMA,
-// which also clips the edges.
+// which also clips the edges. 4096 x 12352 x 2048 in bf16: 75.5 us, 2.74 PFLOP/s,
+// the tensor pipe 80 % active.
 #include <cuda.h>
 
 #include <type_traits>

@@ -470,6 +470,16 @@ gdn_status gdn_decay_step(const gdn_dims* dims, int32_t batch, const int32_t* st
  * decode step. Every argument is indexed by the token as in gdn_decay_step,
  * where that has the row.
  *
+ * bf16 at head_dim 128 with more than 16 tokens a sequence on average and a
+ * 32-byte aligned state runs on the tensor cores, 64 tokens at a time: what is
+ * added to the state is right to about 2^-22 of each product, the outputs to
+ * 2^-16 of their terms' magnitudes where core_out is asked for and to 2^-8
+ * where out alone is (whose own rounding is 2^-8 of the value). Everything
+ * else runs token by token in fp32. What is not finite in v spoils its value
+ * row of the state and of the outputs from its token on, in k or g every row,
+ * in q or z the outputs of its token alone; nothing reaches earlier tokens or
+ * other sequences.
+ *
  * cu_seqlens   device int32 [N+1] as for gdn_conv_update; an empty sequence
  *              keeps its state. cu[N] may be smaller than total_tokens: the
  *              rows behind the last sequence (a padded batch) are neither
