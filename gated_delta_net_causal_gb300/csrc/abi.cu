@@ -671,8 +671,8 @@ gdn_status decay_plan(const gdn_dims* dims, int32_t num_seqs, int64_t total_toke
   const int64_t Hv = dims->n_v_heads, D = dims->head_dim;
   *bytes = 0;
   *decays_at = 0;
-  sg->len = gdn::decay_segment_len(num_seqs, total_tokens, dims->n_v_heads,
-                                   gdn::decay_tc_fits(dims->io_dtype, dims->head_dim, num_seqs, total_tokens));
+  gdn::decay_cut(num_seqs, total_tokens, dims->n_v_heads, dims->head_dim,
+                 gdn::decay_tc_fits(dims->io_dtype, dims->head_dim, num_seqs, total_tokens), sg);
   sg->slots = total_tokens / sg->len + num_seqs;
   sg->states = nullptr;
   sg->decays = nullptr;
@@ -742,7 +742,7 @@ gdn_status gdn_decay_prefill(const gdn_dims* dims, int32_t num_seqs, const int32
     sg.states = static_cast<float*>(workspace);
     sg.decays = reinterpret_cast<float*>(static_cast<char*>(workspace) + decays_at);
   } else {  // one segment per sequence
-    sg.len = (int32_t)total_tokens + 1;
+    sg.len = sg.whole = (int32_t)total_tokens + 1;
     sg.slots = num_seqs;
   }
   if (gdn::decay_tc_fits(dims->io_dtype, dims->head_dim, num_seqs, total_tokens) && gdn::decay_tc_supported(p))

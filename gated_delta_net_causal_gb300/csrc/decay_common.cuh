@@ -122,8 +122,8 @@ __device__ __forceinline__ void store8(float* p, float4 a, float4 b) {
 }
 
 // ------------------------------------------------------------- segments
-// The packed tokens of a call are cut into segments of at most sg.len tokens,
-// each inside one sequence. Segment i of sequence n has slot
+// Sequences of more than sg.whole tokens are cut into segments of sg.len, the
+// others are one segment each. Segment i of sequence n has slot
 //   floor(cu[n] / len) + n + i,
 // which is increasing and never reaches the next sequence's first slot
 // (ceil((b - a) / len) <= floor(b / len) - floor(a / len) + 1), so
@@ -162,14 +162,15 @@ __device__ __forceinline__ bool find_segment(const DecayArgs& p, const DecaySegm
     count = count - at * step < step ? count - at * step : step;
   }
   const int begin = seq_bound(p, lo), end = seq_end(p, lo, begin);
+  const int length = end - begin;
   out->slot = begin / sg.len + lo;
+  out->parts = length <= sg.whole ? (length > 0 ? 1 : 0) : 1 + (length - 1) / sg.len;
   const int i = slot - out->slot;
-  if (i < 0 || i >= (end - begin + sg.len - 1) / sg.len) return false;
+  if (i < 0 || i >= out->parts) return false;
   out->seq = lo;
   out->index = i;
-  out->parts = (end - begin + sg.len - 1) / sg.len;
   out->begin = begin + i * sg.len;
-  out->end = end - out->begin <= sg.len ? end : out->begin + sg.len;
+  out->end = i + 1 == out->parts ? end : out->begin + sg.len;
   return true;
 }
 

@@ -19,6 +19,7 @@
 // Bound by the FMAs and shuffles of its few warps, and by the chain: fp32, 1024
 // tokens, 32 heads 148 us (520 in one pass); 208 tokens of three sequences,
 // 4 heads of 64, 9 and 11 us for the two passes.
+#include <algorithm>
 #include <type_traits>
 
 #include "decay_common.cuh"
@@ -39,7 +40,7 @@ struct ScanSmem {
 };
 
 template <typename T, int D, int MODE, bool FEW>
-__global__ void __launch_bounds__(DecayGeom<D, FEW>::THREADS, FEW ? 1 : 512 / DecayGeom<D>::THREADS)
+__global__ void __launch_bounds__(DecayGeom<D, FEW>::THREADS, FEW ? 1 : (D == 32 ? 768 : 512) / DecayGeom<D>::THREADS)
     decay_scan_kernel(const DecayArgs p, const DecaySegments sg) {
   using G = DecayGeom<D, FEW>;
   constexpr int LPR = G::LPR, NV4 = G::NV4, RPL = G::RPL, RPW = G::RPW, NT = G::THREADS;
@@ -122,12 +123,60 @@ __global__ void __launch_bounds__(DecayGeom<D, FEW>::THREADS, FEW ? 1 : 512 / De
       if (tid == 0) sm.near[buf] = near;
     }
   };
+  // outputs of a tile: token tt to warp tt % WARPS, each lane COLS columns; z
+  // comes in while the tile runs, and a warp's tokens go side by side
+  constexpr int COLS = D / 32, TOKENS = (kTile + G::WARPS - 1) / G::WARPS;
+  struct alignas(COLS == 3 ? sizeof(T) : COLS * sizeof(T)) Columns {
+    T v[COLS];
+  };
+  float nw[COLS];
+#pragma unroll
+  for (int e = 0; e < COLS; ++e) nw[e] = MODE == kWhole && p.z != nullptr ? p.norm_w[lane * COLS + e] : 0.f;
+  Columns zr[TOKENS];
+  auto fetch_z = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < TOKENS; ++i) {
+      const int tt = warp + i * G::WARPS;
+      if (p.z != nullptr && tt < kTile && t0 + tt < s.end)
+        zr[i] = reinterpret_cast<const Columns*>(static_cast<const T*>(p.z) + (int64_t)(t0 + tt) * p.z_stride + h * D)[lane];
+    }
+  };
   auto write_tile = [&](int buf, int t0) {
-    for (int tt = warp; tt < kTile && t0 + tt < s.end; tt += G::WARPS) {
-      const int64_t t = (int64_t)t0 + tt, orow = (t * p.Hv + h) * D;
-      decay_write_row<T, D>(sm.o[buf][tt], p.core_out == nullptr ? nullptr : p.core_out + orow,
-                            p.z == nullptr ? nullptr : static_cast<const T*>(p.z) + t * p.z_stride + h * D, p.norm_w,
-                            p.out == nullptr ? nullptr : static_cast<T*>(p.out) + orow, p.rms_eps, lane);
+    float o[TOKENS][COLS], ss[TOKENS];
+#pragma unroll
+    for (int i = 0; i < TOKENS; ++i) {
+      const int tt = warp + i * G::WARPS;
+      ss[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < COLS; ++e) {
+        o[i][e] = tt < kTile ? sm.o[buf][tt < kTile ? tt : 0][lane * COLS + e] : 0.f;
+        ss[i] += o[i][e] * o[i][e];
+      }
+    }
+    if (p.z != nullptr) {
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < TOKENS; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], d);
+    }
+#pragma unroll
+    for (int i = 0; i < TOKENS; ++i) {
+      const int tt = warp + i * G::WARPS;
+      if (tt >= kTile || t0 + tt >= s.end) continue;
+      const int64_t orow = ((int64_t)(t0 + tt) * p.Hv + h) * D;
+      if (p.core_out != nullptr) {
+#pragma unroll
+        for (int e = 0; e < COLS; ++e) p.core_out[orow + lane * COLS + e] = o[i][e];
+      }
+      if (p.out == nullptr) continue;
+      const float inv = 1.f / sqrtf(ss[i] / (float)D + p.rms_eps);
+      Columns c;
+#pragma unroll
+      for (int e = 0; e < COLS; ++e) {
+        const float y = p.z == nullptr ? o[i][e] : o[i][e] * inv * nw[e] * silu_f(to_f32(zr[i].v[e]));
+        c.v[e] = from_f32<T>(y);
+      }
+      reinterpret_cast<Columns*>(static_cast<T*>(p.out) + orow)[lane] = c;
     }
   };
 
@@ -137,6 +186,7 @@ __global__ void __launch_bounds__(DecayGeom<D, FEW>::THREADS, FEW ? 1 : 512 / De
   int buf = 0;
   for (int t0 = s.begin; t0 < s.end; t0 += kTile, buf ^= 1) {
     if (t0 + kTile < s.end) fetch(t0 + kTile);
+    if (MODE == kWhole) fetch_z(t0);
     const int n = s.end - t0 < kTile ? s.end - t0 : kTile;
     const auto token = [&](int tt, auto near) {
       const Decay decay = sm.decay[buf][tt];
@@ -237,25 +287,37 @@ cudaError_t launch_scan_t(const DecayArgs& p, const DecaySegments& sg, int32_t D
 // 0.5 n / m in two over segments of m, so short prompts and those of many
 // heads stay whole (one prompt, 32 heads, one pass and two: 128 tokens 13 and
 // 20 us, 512 tokens 29 and 26, 2048 tokens 93 and 50).
-int32_t decay_segment_len(int32_t N, int64_t T, int32_t Hv, bool chunks) {
-  const int32_t whole = (int32_t)T + 1;
-  if (T == 0) return whole;
+// Token by token many (sequence, V head) pairs hide long ones among them, whose
+// chain of tokens outlasts the rest: sequences of half more tokens than an even
+// share of the SMs' work are then cut, too (fp32, 64 heads, 13 sequences of
+// 9782 tokens in all, the longest 3660: 1574 us and uncut 2251 at head_dim 64,
+// 2501 and 2805 at 128; 20 of 1000 tokens, which nothing cuts, 1484 and 1466,
+// for the first pass that finds nothing to do).
+void decay_cut(int32_t N, int64_t T, int32_t Hv, int32_t D, bool chunks, DecaySegments* sg) {
+  sg->len = sg->whole = (int32_t)T + 1;
+  if (T == 0) return;
   if (chunks) {
     const int64_t n = (T + 63) / 64, sms = 152 / Hv, each = sms / N;
     const int64_t more = each >= 2 ? N * each : sms - N / 2;
-    if (more < 1) return whole;
+    if (more < 1) return;
     int64_t len = (n + more - 1) / more;
     while (7 * N * len * len < n) ++len;
     // the longest sequence, times N: more than the mean where they may be unlike
     const int64_t longest = N == 1 ? n : each >= 2 ? n + n / 4 : 2 * n;
-    return 53 * longest > (84 * len + 180) * N + 10 * n / len ? (int32_t)(64 * len) : whole;
+    if (53 * longest > (84 * len + 180) * N + 10 * n / len) sg->len = sg->whole = (int32_t)(64 * len);
+    return;
   }
-  const int64_t more = N == 1 ? 304 / Hv : (608 / Hv - N) / 2;
-  if (more < 1 || T <= 32) return whole;
-  int64_t len = ((T + more - 1) / more + kTile - 1) / kTile * kTile;  // below T + kTile
+  const int64_t more = N == 1 ? 304 / Hv : (608 / Hv - N) / 2, share = T * Hv / 304;
+  const bool few = more >= (N == 1 || D > 64 ? 1 : 4);
+  if (T <= 32 || (!few && (T <= 512 || N * (int64_t)Hv > 8192))) return;
+  int64_t len = few ? (T + more - 1) / more : share / 2;
+  len = (len + kTile - 1) / kTile * kTile;  // below T + kTile
   const int64_t n = (T + kTile - 1) / kTile;
   while (8 * (len / kTile) * (len / kTile) < n) len += kTile;  // 8 tokens a tile: m^2 >= T
-  return (int32_t)len;
+  const int64_t whole = few ? len : std::max(len, share + share / 2);
+  if (whole >= T) return;
+  sg->len = (int32_t)len;
+  sg->whole = (int32_t)whole;
 }
 
 cudaError_t launch_decay_scan(const DecayArgs& p, const DecaySegments& sg, int32_t dtype, int32_t D,

@@ -129,7 +129,8 @@ struct DecayArgs {
 
 // The segments that a prefill is cut into (decay_common.cuh)
 struct DecaySegments {
-  int32_t len;    // tokens a segment holds at most, for the tensor-core kernel a multiple of 64 where there are several
+  int32_t len;    // tokens of a segment where there are several, for the tensor-core kernel a multiple of 64
+  int32_t whole;  // longer sequences are cut, >= len
   int64_t slots;  // floor(T / len) + N
   float* states;  // [slots][Hv][D][D] or null: one segment per sequence
   float* decays;  // [slots][Hv] factors of the state over a segment
@@ -196,8 +197,8 @@ int64_t linear_workspace_bytes(int32_t M, int32_t N, int32_t K);
 bool linear_supported();
 cudaError_t launch_linear(LinearArgs p, const void* x, int64_t x_stride, const void* w, void* workspace,
                           cudaStream_t stream);
-// tokens of a segment (decay_scan.cu); chunks: for the tensor-core kernel
-int32_t decay_segment_len(int32_t N, int64_t T, int32_t Hv, bool chunks);
+// len and whole for these sizes (decay_scan.cu); chunks: for the tensor-core kernel
+void decay_cut(int32_t N, int64_t T, int32_t Hv, int32_t D, bool chunks, DecaySegments* sg);
 // whether the tensor-core kernel takes these sizes
 bool decay_tc_fits(int32_t dtype, int32_t D, int32_t N, int64_t T);
 cudaError_t launch_decay_step(const DecayArgs& p, int32_t dtype, int32_t D, int32_t batch, cudaStream_t stream);

@@ -249,6 +249,16 @@ def test_prefill_long_sequences(dtype, D, workspace):
     run_prefill(c, lengths, workspace=workspace)
 
 
+@pytest.mark.parametrize("dtype,D", [("f32", 32), ("f16", 64), ("bf16", 96), ("f32", 128)])
+def test_prefill_one_long_sequence_among_many(dtype, D):
+    """More (sequence, head) pairs than SMs, and one sequence that outlasts the rest: it alone is cut."""
+    lengths = [3, 0, 9, 700] + [5, 1, 40, 0, 72, 2] * 6
+    c = Case(35, 4, 16, D, dtype, sum(lengths) + 3, len(lengths), rate=0.05)
+    assert gdn.gdn_decay_prefill_workspace_size(c.d, len(lengths), sum(lengths) + 3) > 0
+    run_prefill(c, lengths)
+    run_prefill(c, lengths, workspace=None)
+
+
 def test_prefill_many_sequences():
     """More sequences than one probe of the search covers, most of them short or empty."""
     rng = np.random.default_rng(3)
