@@ -409,17 +409,22 @@ cudaError_t launch_band(const LinearFp8Args& p, const void* x, int64_t x_stride,
     return cudaErrorInvalidValue;
   const int bands = (p.N + kFBand - 1) / kFBand, nk = (p.K + kFK - 1) / kFK;
   const int64_t tiles = (p.M + kFM - 1) / kFM;
-  // Two CTAs of 96 KB an SM and as many K splits as keep them busy in one wave,
-  // each of two K steps at least (12352 x 2048, 64 rows: 10.6 us; three CTAs of
-  // 64 KB 11.5, four of 48 KB 17.9). Where the bands fill several waves, four
-  // CTAs of 54 KB in all, so that one starts and stores under the others'
-  // streams (65536 x 2048: one row 27.7 us against 41.9, 128 rows 37.0 against
-  // 42.4; three CTAs 33.5 and 36.8).
+  // Two CTAs of 96 KB an SM (12352 x 2048, 64 rows: 10.6 us; three CTAs of 64 KB
+  // 11.5, four of 48 KB 17.9) and as many K splits as still run in one wave,
+  // each of two K steps at least, of eight from 32 rows on, whose fp32 tiles are
+  // as large as a K step (2048 x 4096, 128 rows: eight splits 13.2 us, four 9.7;
+  // one row 7.5 and 8.2). A cluster lies in one GPC of 18 or 20 SMs, so
+  // fewer of them run at once than the SMs have places (3808 x 3984, three
+  // rows: 60 clusters of four 9.3 us, of five 15.0).
+  // Where the bands fill several waves, four CTAs of 54 KB in all, so that one
+  // starts and stores under the others' streams (65536 x 2048: one row 27.7 us
+  // against 41.9, 128 rows 37.0 against 42.4; three CTAs 33.5 and 36.8).
   const bool waves = bands * tiles >= 4 * sm_count();
-  int64_t splits = 2 * sm_count() / (bands * tiles);
-  if (splits > nk / 2) splits = nk / 2;
+  const auto clusters = [](int s) { return s == 1 ? INT64_MAX : s == 2 ? 152 : 8ll * (36 / s); };
+  int splits = nk / (p.M < 32 ? 2 : 8);
   if (splits > kFMaxSplits) splits = kFMaxSplits;
-  plan.splits = splits < 1 ? 1 : (int)splits;
+  while (splits > 1 && bands * tiles > clusters(splits)) --splits;
+  plan.splits = splits < 1 ? 1 : splits;
   const uint32_t x_tile = ((uint32_t)plan.box_rows * kFK + 1023) / 1024 * 1024, stage_bytes = x_tile + kFWTile;
   const uint32_t extra = (kFM * kFK - x_tile) + 1024;  // the MMA reads kFM rows from a stage's start; alignment
   const int fit = (int)((waves ? 54 * 1024 - extra : 96 * 1024) / stage_bytes);
