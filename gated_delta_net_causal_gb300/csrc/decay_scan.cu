@@ -286,7 +286,9 @@ cudaError_t launch_scan_t(const DecayArgs& p, const DecaySegments& sg, int32_t D
 // On the tensor cores n chunks take 8 + 2.65 n us in one pass and 17 + 4.2 m +
 // 0.5 n / m in two over segments of m, so short prompts and those of many
 // heads stay whole (one prompt, 32 heads, one pass and two: 128 tokens 13 and
-// 20 us, 512 tokens 29 and 26, 2048 tokens 93 and 50).
+// 20 us, 512 tokens 29 and 26, 2048 tokens 93 and 50). Where that holds for
+// sequences of the mean length, one of three times that may still gain: those
+// above the mean by a quarter are cut alone.
 // Token by token many (sequence, V head) pairs hide long ones among them, whose
 // chain of tokens outlasts the rest: sequences of half more tokens than an even
 // share of the SMs' work are then cut, too (fp32, 64 heads, 13 sequences of
@@ -302,9 +304,12 @@ void decay_cut(int32_t N, int64_t T, int32_t Hv, int32_t D, bool chunks, DecaySe
     if (more < 1) return;
     int64_t len = (n + more - 1) / more;
     while (7 * N * len * len < n) ++len;
-    // the longest sequence, times N: more than the mean where they may be unlike
-    const int64_t longest = N == 1 ? n : each >= 2 ? n + n / 4 : 2 * n;
-    if (53 * longest > (84 * len + 180) * N + 10 * n / len) sg->len = sg->whole = (int32_t)(64 * len);
+    if (each >= 2 && 53 * n > (84 * len + 180) * N + 10 * n / len) {
+      sg->len = sg->whole = (int32_t)(64 * len);
+    } else if (53 * std::min(N * n, 3 * n) > (31 * len + 180) * N + 53 * n + 10 * n / len) {
+      sg->len = (int32_t)(64 * len);
+      sg->whole = (int32_t)std::min<int64_t>(64 * std::max(len, (5 * n + 4 * N - 1) / (4 * N)), T);
+    }
     return;
   }
   const int64_t more = N == 1 ? 304 / Hv : (608 / Hv - N) / 2, share = T * Hv / 304;
