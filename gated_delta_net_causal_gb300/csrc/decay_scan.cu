@@ -84,7 +84,9 @@ __global__ void __launch_bounds__(DecayGeom<D, FEW>::THREADS, FEW ? 1 : (D == 32
 
   // staging: unit u of a tile is four elements; units of q, k, v in turn
   constexpr int UNITS = kTile * D / 4, PER = (3 * UNITS + NT - 1) / NT;
-  float4 pre[PER];
+  // as they lie in memory: converting them here would wait for each load
+  using Raw = typename std::conditional<sizeof(T) == 4, float4, uint2>::type;
+  Raw pre[PER];
   float pre_g = 0.f;
   auto fetch = [&](int t0) {
 #pragma unroll
@@ -95,7 +97,7 @@ __global__ void __launch_bounds__(DecayGeom<D, FEW>::THREADS, FEW ? 1 : (D == 32
         const T* src = which == 0   ? static_cast<const T*>(p.q) + (int64_t)(t0 + tt) * p.q_stride + kh * D + c
                        : which == 1 ? static_cast<const T*>(p.k) + (int64_t)(t0 + tt) * p.k_stride + kh * D + c
                                     : static_cast<const T*>(p.v) + (int64_t)(t0 + tt) * p.v_stride + h * D + c;
-        pre[i] = load4(src);
+        pre[i] = *reinterpret_cast<const Raw*>(src);
       }
     }
     if (tid < kTile && t0 + tid < s.end) pre_g = p.g[(int64_t)(t0 + tid) * p.g_stride + h];
@@ -108,7 +110,7 @@ __global__ void __launch_bounds__(DecayGeom<D, FEW>::THREADS, FEW ? 1 : (D == 32
       const int which = u / UNITS, r = u - which * UNITS;
       if (which < 3) {
         float* dst = (which == 0 ? &sm.q[buf][0][0] : which == 1 ? &sm.k[buf][0][0] : &sm.v[buf][0][0]) + 4 * r;
-        *reinterpret_cast<float4*>(dst) = pre[i];
+        *reinterpret_cast<float4*>(dst) = load4(reinterpret_cast<const T*>(&pre[i]));
       }
     }
     if (warp == 0) {
