@@ -107,6 +107,19 @@ def test_many_rows(dtype, rows, cols, stride, residual):
     assert gdn.gdn_device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("cols,stride", [(3001, 3001), (4097, 4104), (5000, 5003), (8191, 8192), (8192, 8193), (8193, 8193)])
+def test_rows_without_wide_accesses(dtype, cols, stride):
+    """Around the lengths up to which such a row stays in registers."""
+    gen = torch.Generator().manual_seed(cols)
+    x, r = rows_of(gen, 5, cols, stride, dtype), rows_of(gen, 5, cols, stride, dtype, 3.0)
+    w = (1 + 0.3 * torch.randn(cols, generator=gen)).cuda()
+    y, q, sc = torch.empty_like(x), torch.empty((5, cols), dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(5, device="cuda")
+    x0, r0 = x.clone(), r.clone()
+    gdn.gdn_add_rmsnorm(x, w, residual=r, sum_out=r, out=y, out_q=q, out_scale=sc)
+    verify(x0, r0, w, 1e-6, dtype, r, y, q, sc)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("cols", [100, 2048, 20000])
 def test_without_residual_or_weight(dtype, cols):
