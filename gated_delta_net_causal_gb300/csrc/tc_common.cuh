@@ -309,12 +309,6 @@ __device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const void* tma
       : "memory");
 }
 
-// The same box into L2 alone, for a load to come.
-__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int x, int y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tmap), "r"(x), "r"(y)
-               : "memory");
-}
-
 // 2-D tiled store of a box from shared memory (16-byte aligned source),
 // tracked by the executing thread's bulk async-groups (commit, then
 // wait_group). Rows or columns outside the tensor are not written. The box
