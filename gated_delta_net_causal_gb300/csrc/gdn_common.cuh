@@ -270,10 +270,6 @@ __device__ __forceinline__ uint32_t map_shared_rank(uint32_t smem_addr, uint32_t
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(smem_addr), "r"(rank));
   return out;
 }
-// Arrive on a barrier of another CTA of the cluster (address from mapa).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 // Asynchronous 4-byte store into another CTA's shared memory that completes
 // 4 transaction bytes on that CTA's mbarrier (both addresses from mapa).
 __device__ __forceinline__ void st_async_cluster_f32(uint32_t remote_addr, float v,

@@ -32,6 +32,7 @@
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
 #include "tc_common.cuh"
+#include "tc_fp8.cuh"
 
 namespace gdn {
 namespace {

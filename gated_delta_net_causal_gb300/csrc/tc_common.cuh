@@ -60,7 +60,6 @@ __device__ __forceinline__ uint64_t sdesc_at(uint64_t base, int rows, int s) {
 }
 
 enum : uint32_t { kF16 = 0, kBF16 = 1, kTF32 = 2 };
-constexpr uint32_t kE4M3 = 0;  // operand format of kind::f8f6f4
 
 // Instruction descriptor for kind::f16 / kind::tf32 with fp32 accumulation,
 // both operands K-major: D format (bits 4-5) = F32, A/B formats in bits 7-9 /
@@ -154,51 +153,6 @@ __device__ __forceinline__ void mma_f16_elect(uint32_t d_tmem, uint64_t a, uint6
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a), "l"(b), "r"(id), "r"((uint32_t)accumulate)
       : "memory");
-}
-// The same with 8-bit floating operands (32 of K in an instruction). The
-// instruction descriptor's operand formats are kE4M3.
-__device__ __forceinline__ void mma_f8_elect(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id,
-                                             bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred e, p;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(id), "r"((uint32_t)accumulate)
-      : "memory");
-}
-// The same over a pair of CTAs (a cluster of two): A and B each half in either
-// CTA's shared memory at the same place, D's upper half of the rows in the
-// second CTA's TMEM. Issued by the first CTA alone.
-__device__ __forceinline__ void mma_f8_pair_elect(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id,
-                                                  bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred e, p;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(id), "r"((uint32_t)accumulate)
-      : "memory");
-}
-// Arrive on the barrier at this place in both CTAs once the pair's MMAs issued
-// so far have completed.
-__device__ __forceinline__ void mma_commit_pair_elect(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
-          smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
-}
-// TMEM of a pair: one warp of each CTA allocates, and frees, its half.
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 // two consecutive k-steps into one accumulator (the second accumulates)
 // issued by one elected lane of a converged warp
@@ -296,16 +250,6 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const void* tmap, in
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(smem_dst)),
       "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
-}
-
-// The same, completing on a barrier of either CTA of a pair (an address of
-// the cluster's shared memory).
-__device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const void* tmap, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(smem_dst)),
-      "l"(tmap), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
 
