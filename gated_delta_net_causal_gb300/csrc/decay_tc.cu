@@ -10,13 +10,15 @@
 // so no chunk waits on anything but the state before it. The products, with
 // value rows j or tokens t on the 128 or 64 MMA rows:
 //   scores  [t][s] = Q K^T               both tiles as TMA loads them
-//   O1      [j][t] = S Q^T               S from TMEM, rounded to bf16
-//   O2      [j][t] = V^T P^T             V read transposed, P rounded to bf16
+//   O1      [j][t] = S Q^T               S from TMEM as bf16 hi + lo
+//   O2      [j][t] = V^T P^T             V read transposed, P as bf16 hi + lo
 //   dS      [j][i] = V^T K'              K' = e^(G_n - G_s) k as bf16 hi + mid + lo
 // q, k and v are exact in bf16. What is added to the state has three bf16
 // parts (2^-24 of a factor), as the state is kept in fp32. S and P only reach
-// the outputs: one part each where out alone is asked for, whose own rounding
-// is as large (together 1.4 times it), two (2^-17) where core_out is.
+// the outputs: two parts (2^-17 of a factor). One part would be off by 2^-8 of
+// the terms' magnitudes, which is far more than the rounding of a 16-bit out
+// where terms cancel; the second costs 10 % with the gated norm and 17 %
+// without (88 and 553 us below), most of it the conversions of S.
 //
 // A pipeline of one CTA per SM, whose warps hand each other tiles through
 // mbarriers instead of meeting at barriers. Sixteen warps compute; per chunk c
@@ -33,13 +35,13 @@
 // accumulator side by side. The outputs leave TMEM as 8 x 8 blocks, are normed
 // and gated in registers, transposed in shared memory and stored by TMA.
 //
-// What bounds it: a chunk of a head takes about 4300 cycles (8 x 1024 tokens,
-// 64 heads, no gate; 5500 with the gated norm, whose exponentials and
-// reciprocals are 1000 of the MUFU's), where its 32 MMAs hold the tensor pipe
-// for 2300 and its tiles the shared memory for 2700. 8 ragged prompts of
-// 34,482 tokens in all, 64 heads: 564 us, 2640 GB/s; one of 4096 tokens, 32
-// heads: 88 us. The same chunks with two CTAs an SM that meet at barriers took
-// 630 and 105 us.
+// What bounds it: a chunk of a head takes about 5000 cycles (8 x 1024 tokens,
+// 64 heads, no gate; 6300 with the gated norm, whose exponentials and
+// reciprocals are 1000 of the MUFU's), a chain of phases of the same warps in
+// which no unit is full. 8 ragged prompts of 34,482 tokens in all, 64 heads:
+// 650 us, 2290 GB/s; one of 4096 tokens, 32 heads: 96 us. With one part of S
+// and P, the same chunks with two CTAs an SM that meet at barriers took 630
+// and 105 us against 564 and 88.
 //
 // Exponents are differences of sums of up to 64 log decays, which a decay of
 // -100 a token makes large where the difference is small; the sums are held
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const auto issue_o1 = [&](int st) {
       const uint64_t dQ = tc::sdesc_sw128(smem_u32(sm + kPQ + st * kPTile));
 #pragma unroll
-      for (int i = 0; i < (CORE ? 16 : 8); ++i)
+      for (int i = 0; i < 16; ++i)
         tc::mma_f16_ts_elect(tb + kPColO1, tb + kPColS + 8 * i, tc::sdesc_at(dQ, 64, i & 7), id_o1, i > 0);
     };
     bool ok = true;
@@ -285,7 +287,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (!ok) break;
         tc::fence_after_sync();
 #pragma unroll
-        for (int i = 0; i < (CORE ? 8 : 4); ++i)
+        for (int i = 0; i < 8; ++i)
           tc::mma_f16_elect(tb + kPColO2, dV + ((i & 3) * 2048 >> 4), dP + (((i >> 2) * 8192 + (i & 3) * 32) >> 4), id_o2,
                             i > 0);
         tc::mma_commit_elect(&sh.outs);
@@ -474,22 +476,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    // S as the A operand of O1: packed pairs, and with core_out what their rounding left
+    // S as the A operand of O1: packed pairs, and what their rounding left
     const auto put_state = [&]() {
-      uint32_t hi[16];
-      if (CORE) {
-        uint32_t lo[16];
+      uint32_t hi[16], lo[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float2 a = S[e];
-          hi[e] = split2(a);
-          lo[e] = pack2(a);
-        }
-        tc::tmem_st16u(tq + kPColS + 64 + 16 * hh, lo);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) hi[e] = pack2(S[e]);
+      for (int e = 0; e < 16; ++e) {
+        float2 a = S[e];
+        hi[e] = split2(a);
+        lo[e] = pack2(a);
       }
+      tc::tmem_st16u(tq + kPColS + 64 + 16 * hh, lo);
       tc::tmem_st16u(tq + kPColS + 16 * hh, hi);
       tc::tmem_wait_st();
       hand(&sh.s);
@@ -576,12 +572,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
           if (sc > ta + 8) z.x = 0.f;
           if (sc + 1 > ta + 8) z.y = 0.f;
           unsigned char* to = pp + (((2 * hh + i) ^ (ta & 7)) << 4);
-          *reinterpret_cast<uint32_t*>(to) = CORE ? split2(y) : pack2(y);
-          *reinterpret_cast<uint32_t*>(to + 1024) = CORE ? split2(z) : pack2(z);
-          if (CORE) {
-            *reinterpret_cast<uint32_t*>(to + 8192) = pack2(y);
-            *reinterpret_cast<uint32_t*>(to + 8192 + 1024) = pack2(z);
-          }
+          *reinterpret_cast<uint32_t*>(to) = split2(y);
+          *reinterpret_cast<uint32_t*>(to + 1024) = split2(z);
+          *reinterpret_cast<uint32_t*>(to + 8192) = pack2(y);
+          *reinterpret_cast<uint32_t*>(to + 8192 + 1024) = pack2(z);
         }
         hand(&sh.p[st]);
       }

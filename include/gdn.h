@@ -473,9 +473,9 @@ gdn_status gdn_decay_step(const gdn_dims* dims, int32_t batch, const int32_t* st
  * bf16 at head_dim 128 with more than 16 tokens a sequence on average and a
  * 32-byte aligned state runs on the tensor cores, 64 tokens at a time: what is
  * added to the state is right to about 2^-22 of each product, the outputs to
- * 2^-16 of their terms' magnitudes where core_out is asked for and to 2^-8
- * where out alone is (whose own rounding is 2^-8 of the value). Everything
- * else runs token by token in fp32. What is not finite in v spoils its value
+ * 2^-16 of their terms' magnitudes before their rounding; out is the same
+ * whether core_out is asked for or not. Everything else runs token by token in
+ * fp32. What is not finite in v spoils its value
  * row of the state and of the outputs from its token on, in k or g every row,
  * in q or z the outputs of its token alone; nothing reaches earlier tokens or
  * other sequences.
