@@ -187,6 +187,19 @@ def _stream(stream) -> Optional[int]:
     return int(stream) or None
 
 
+def _scratch(need: int, device, stream) -> torch.Tensor:
+    """A workspace that is dropped when the call returns, allocated on the stream that the call's kernels run on: what
+    that stream allocates next is ordered behind them, and they behind what used the block before. (A block of the
+    current stream's would be neither, for a call on another one.)"""
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = int(stream)  # 0 and 1: the legacy default stream
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw > 1 else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=device)
+
+
 def _io(d: GdnDims):
     return _GDN_TO_TORCH[d.io_dtype]
 
@@ -347,14 +360,7 @@ def gdn_prefill_chunked(d: GdnDims, cu_seqlens, q, k, v, a, b, decay_param, dt_b
         if workspace != "auto":
             raise ValueError("workspace must be 'auto', None or a CUDA tensor")
         need = gdn_prefill_workspace_size(d, n, total, flags)
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            if isinstance(stream, torch.cuda.Stream):
-                # freed when this call returns: keep it from being reused
-                # before the kernels on that stream are done with it
-                workspace.record_stream(stream)
-        else:
-            workspace = None
+        workspace = _scratch(need, q.device, stream) if need > 0 else None
     if workspace is not None:
         ws_ptr = _ptr(workspace, "workspace", torch.uint8)
         ws_bytes = workspace.numel()
@@ -443,7 +449,7 @@ def gdn_linear(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, bias: Optional
     _need(bias, "bias", N)
     need = gdn_linear_workspace_size(M, N, K)
     if isinstance(workspace, str) and workspace == "auto":
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need > 0 else None
+        workspace = _scratch(need, x.device, stream) if need > 0 else None
     _need(workspace, "workspace", need)
     ws_ptr = _ptr(workspace, "workspace", torch.uint8) if workspace is not None else None
     _check(library().gdn_linear(int(M), int(N), int(K), x.data_ptr(), int(x.stride(0)), _ptr(w, "w", bf),
@@ -481,7 +487,7 @@ def gdn_decode_layer(d: GdnDims, x: torch.Tensor, w_in, w_out, conv_w, decay_par
     _need(y, "y", batch * hidden)
     need = gdn_decode_layer_workspace_size(d, hidden, batch)
     if isinstance(workspace, str) and workspace == "auto":
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _scratch(need, x.device, stream)
     _need(workspace, "workspace", need)
     wts = GdnLayerWeights(_ptr(w_in, "w_in", bf), _ptr(b_in, "b_in", f32), _ptr(w_out, "w_out", bf),
                           _ptr(b_out, "b_out", f32), _ptr(conv_w, "conv_w", bf),
@@ -602,10 +608,7 @@ def gdn_decay_prefill(d: GdnDims, cu_seqlens, q, k, v, g, state, core_out=None, 
         if workspace != "auto":
             raise ValueError("workspace must be 'auto', None or a CUDA tensor")
         need = gdn_decay_prefill_workspace_size(d, n, rows)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
-        if workspace is not None and isinstance(stream, torch.cuda.Stream):
-            # freed when this call returns: not reused before that stream is done with it
-            workspace.record_stream(stream)
+        workspace = _scratch(need, q.device, stream) if need > 0 else None
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         ws_bytes = workspace.numel()
