@@ -502,9 +502,11 @@ def gdn_decode_layer(d: GdnDims, x: torch.Tensor, w_in, w_out, conv_w, decay_par
 
 
 # The calls below are short (a launch takes about 4 us of host time), so their checks read each tensor's properties
-# once and the current stream comes from the binding that torch's own code generators use.
-_current_device = torch._C._cuda_getDevice
-_current_raw_stream = torch._C._cuda_getCurrentRawStream
+# once and the current stream comes from the binding that torch's own code generators use (a build of torch without
+# CUDA has neither: there the public calls say so when one of these is used).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_current_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                       or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
 
 
 def _stream_on(stream, dev: int) -> Optional[int]:
