@@ -333,9 +333,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (n >= 2 && !wait(&sh.empty[n & 1], ((n >> 1) - 1) & 1)) break;
         load(n);
       }
-      // none may be in flight when the CTA ends: load i went to stage i % 2
+      // none may be in flight when the CTA ends: load i went to stage i % 2;
+      // nor the arrivals that give the last stages back, the MMA warp's last
+      // commits, which nothing else waits for
       mbar_wait(&sh.full[0], ((n + 1) / 2 - 1) & 1);
       if (n > 1) mbar_wait(&sh.full[1], (n / 2 - 1) & 1);
+      wait(&sh.empty[0], ((chunks + 1) / 2 - 1) & 1);
+      if (chunks > 1) wait(&sh.empty[1], (chunks / 2 - 1) & 1);
     }
   } else if (warp == kPGates) {
     // ------------------------------------------------- sums of log decays
