@@ -49,9 +49,10 @@ struct BandPlan {
   int32_t splits, stages, box_rows;  // box_rows: rows of x per load
 };
 
+// the first n of eight elements, in 16-byte accesses where all of them are (dst on 16 bytes)
 template <typename T>
-__device__ __forceinline__ void store8(T* dst, const float* x, int n, bool wide) {
-  if (wide && n >= 8) {
+__device__ __forceinline__ void store8(T* dst, const float* x, int n) {
+  if (n >= 8) {
     alignas(16) T v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = from_f32<T>(x[e]);
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kFThreads, 4)
     if (left <= 0) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) x8[e] = fmaf(x8[e] * xs, s_scale[8 * g8 + e], s_bias[8 * g8 + e]);
-    store8<T>(static_cast<T*>(p.y) + (m0 + r) * p.y_stride + n, x8, left, true);
+    store8<T>(static_cast<T*>(p.y) + (m0 + r) * p.y_stride + n, x8, left);
   };
   if (plan.splits == 1) {
     if (m < rows && !*abort_flag)
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           if (m < p.M) {
             T* row = static_cast<T*>(p.y) + m * p.y_stride + n0 + c0;
 #pragma unroll
-            for (int c = 0; c < kCols; c += 8) store8<T>(row + c, v + c, left - c, true);
+            for (int c = 0; c < kCols; c += 8) store8<T>(row + c, v + c, left - c);
           }
           continue;
         }
