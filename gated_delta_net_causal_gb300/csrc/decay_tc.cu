@@ -18,7 +18,10 @@
 // the outputs: two parts (2^-17 of a factor). One part would be off by 2^-8 of
 // the terms' magnitudes, which is far more than the rounding of a 16-bit out
 // where terms cancel; the second costs 10 % with the gated norm and 17 %
-// without (88 and 553 us below), most of it the conversions of S.
+// without (88 and 553 us below), most of it the conversions of S. The MMAs cut
+// their sums off at fp32's last bits, so the smallest parts are added first:
+// with them last sums of positive terms came out up to 2^-18.6 of themselves
+// too small, so up to 2^-22.
 //
 // A pipeline of one CTA per SM, whose warps hand each other tiles through
 // mbarriers instead of meeting at barriers. Sixteen warps compute; per chunk c
@@ -268,7 +271,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const uint64_t dQ = tc::sdesc_sw128(smem_u32(sm + kPQ + st * kPTile));
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        tc::mma_f16_ts_elect(tb + kPColO1, tb + kPColS + 8 * i, tc::sdesc_at(dQ, 64, i & 7), id_o1, i > 0);
+        tc::mma_f16_ts_elect(tb + kPColO1, tb + kPColS + 8 * (i ^ 8), tc::sdesc_at(dQ, 64, i & 7), id_o1, i > 0);
     };
     bool ok = true;
     if (MODE == kPWhole) {
@@ -288,8 +291,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         tc::fence_after_sync();
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          tc::mma_f16_elect(tb + kPColO2, dV + ((i & 3) * 2048 >> 4), dP + (((i >> 2) * 8192 + (i & 3) * 32) >> 4), id_o2,
-                            i > 0);
+          tc::mma_f16_elect(tb + kPColO2, dV + ((i & 3) * 2048 >> 4), dP + (((1 - (i >> 2)) * 8192 + (i & 3) * 32) >> 4),
+                            id_o2, i > 0);
         tc::mma_commit_elect(&sh.outs);
       }
       ok = all(wait(&sh.k[st], round));
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
       for (int i = 0; i < 12; ++i)
         tc::mma_f16_elect(acc, dV + ((i & 3) * 2048 >> 4),
-                          (i < 4 ? dK0 : dK1 + (i < 8 ? 0 : kPTile >> 4)) + ((i & 3) * 2048 >> 4), id_d, i > 0);
+                          (i < 4 ? dK1 + (kPTile >> 4) : i < 8 ? dK1 : dK0) + ((i & 3) * 2048 >> 4), id_d, i > 0);
       tc::mma_commit_elect(&sh.delta[MODE == kPLocal ? st : 0]);
       tc::mma_commit_elect(&sh.empty[st]);
       if (MODE == kPWhole && c + 1 < chunks) {
