@@ -17,11 +17,11 @@
 // parts (2^-24 of a factor), as the state is kept in fp32. S and P only reach
 // the outputs: two parts (2^-17 of a factor). One part would be off by 2^-8 of
 // the terms' magnitudes, which is far more than the rounding of a 16-bit out
-// where terms cancel; the second costs 10 % with the gated norm and 17 %
-// without (88 and 553 us below), most of it the conversions of S. The MMAs cut
-// their sums off at fp32's last bits, so the smallest parts are added first:
-// with them last sums of positive terms came out up to 2^-18.6 of themselves
-// too small, so up to 2^-22.
+// where terms cancel; the second costs 6 % with the gated norm and 14 %
+// without (88 and 553 us with one), most of it the conversions of S. The MMAs
+// cut their sums off at fp32's last bits, so the smallest parts are added
+// first: with them last sums of positive terms came out up to 2^-18.6 of
+// themselves too small, so up to 2^-22.
 //
 // A pipeline of one CTA per SM, whose warps hand each other tiles through
 // mbarriers instead of meeting at barriers. Sixteen warps compute; per chunk c
@@ -42,7 +42,7 @@
 // 64 heads, no gate; 6300 with the gated norm, whose exponentials and
 // reciprocals are 1000 of the MUFU's), a chain of phases of the same warps in
 // which no unit is full. 8 ragged prompts of 34,482 tokens in all, 64 heads:
-// 650 us, 2290 GB/s; one of 4096 tokens, 32 heads: 96 us. With one part of S
+// 631 us, 2360 GB/s; one of 4096 tokens, 32 heads: 93 us. With one part of S
 // and P, the same chunks with two CTAs an SM that meet at barriers took 630
 // and 105 us against 564 and 88.
 //
@@ -251,6 +251,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const uint32_t tb = sh.tmem;
   volatile int* abort_flag = &sh.abort;
   const auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, abort_flag); };
+  // the arrivals that give the last stages back are the MMA warp's last
+  // commits: none may be under way when the CTA ends. For a warp that has seen
+  // the phases before them (the load warp has, and the store warp with the
+  // last o; the store warp's wait costs nothing: 93 us for one prompt, the
+  // load warp's 98)
+  const auto wait_given_back = [&]() {
+    wait(&sh.empty[0], ((chunks + 1) / 2 - 1) & 1);
+    if (chunks > 1) wait(&sh.empty[1], (chunks / 2 - 1) & 1);
+  };
   const auto tokens = [&](int c) { return s.end - s.begin - c * kTc < kTc ? s.end - s.begin - c * kTc : kTc; };
 
   if (warp == kPMma) {
@@ -336,13 +345,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (n >= 2 && !wait(&sh.empty[n & 1], ((n >> 1) - 1) & 1)) break;
         load(n);
       }
-      // none may be in flight when the CTA ends: load i went to stage i % 2;
-      // nor the arrivals that give the last stages back, the MMA warp's last
-      // commits, which nothing else waits for
+      // none may be in flight when the CTA ends: load i went to stage i % 2
       mbar_wait(&sh.full[0], ((n + 1) / 2 - 1) & 1);
       if (n > 1) mbar_wait(&sh.full[1], (n / 2 - 1) & 1);
-      wait(&sh.empty[0], ((chunks + 1) / 2 - 1) & 1);
-      if (chunks > 1) wait(&sh.empty[1], (chunks / 2 - 1) & 1);
+      if (MODE == kPLocal) wait_given_back();
     }
   } else if (warp == kPGates) {
     // ------------------------------------------------- sums of log decays
@@ -442,6 +448,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         bulk_wait_all();
       }
+      wait_given_back();
     }
   } else {
     // ------------------------------------------------------------- compute
