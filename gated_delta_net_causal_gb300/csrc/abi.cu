@@ -674,13 +674,14 @@ gdn_status decay_plan(const gdn_dims* dims, int32_t num_seqs, int64_t total_toke
   gdn::decay_cut(num_seqs, total_tokens, dims->n_v_heads, dims->head_dim,
                  gdn::decay_tc_fits(dims->io_dtype, dims->head_dim, num_seqs, total_tokens), sg);
   sg->slots = total_tokens / sg->len + num_seqs;
+  sg->kept = total_tokens / sg->len + (total_tokens / sg->whole < num_seqs ? total_tokens / sg->whole : num_seqs);
   sg->states = nullptr;
   sg->decays = nullptr;
   int64_t tmp = 0;
   if (!mul_ok(sg->slots, Hv, &tmp) || tmp > INT32_MAX) return GDN_ERR_EXTENT;
   if (sg->len < total_tokens) {
-    *decays_at = tmp * D * D * 4;  // tmp <= 2^31, D <= 128: no overflow
-    *bytes = *decays_at + tmp * 4;
+    *decays_at = sg->kept * Hv * D * D * 4;  // kept <= slots, slots Hv < 2^31, D <= 128: no overflow
+    *bytes = *decays_at + sg->kept * Hv * 4;
   }
   return GDN_OK;
 }
@@ -744,6 +745,7 @@ gdn_status gdn_decay_prefill(const gdn_dims* dims, int32_t num_seqs, const int32
   } else {  // one segment per sequence
     sg.len = sg.whole = (int32_t)total_tokens + 1;
     sg.slots = num_seqs;
+    sg.kept = 0;
   }
   if (gdn::decay_tc_fits(dims->io_dtype, dims->head_dim, num_seqs, total_tokens) && gdn::decay_tc_supported(p))
     return cuda_status(gdn::launch_decay_tc(p, sg, static_cast<cudaStream_t>(stream)));

@@ -129,6 +129,12 @@ __device__ __forceinline__ void store8(float* p, float4 a, float4 b) {
 // (ceil((b - a) / len) <= floor(b / len) - floor(a / len) + 1), so
 // floor(T / len) + N slots hold every segment, the host need not know the
 // lengths, and a slot finds its sequence by a search over cu_seqlens.
+// In the workspace only the sequences that are cut have slots. Each of them
+// is longer than whole, so they can be told apart by floor(cu[n] / whole), too:
+// where that is fewer than N, segment i has workspace slot
+//   floor(cu[n] / len) + floor(cu[n] / whole) + i
+// (the next cut sequence begins more than whole later), below
+// floor(T / len) + floor(T / whole), whatever cu holds.
 
 __device__ __forceinline__ int seq_bound(const DecayArgs& p, int n) {
   const int c = p.cu_seqlens[n];
@@ -142,7 +148,7 @@ __device__ __forceinline__ int seq_end(const DecayArgs& p, int n, int begin) {
 struct DecaySegment {
   int seq;
   int index, parts;    // which of the sequence's segments, and how many it has
-  int slot;            // of its first segment
+  int kept;            // of its first segment in the workspace, if it has several
   int begin, end;      // tokens
 };
 
@@ -163,9 +169,9 @@ __device__ __forceinline__ bool find_segment(const DecayArgs& p, const DecaySegm
   }
   const int begin = seq_bound(p, lo), end = seq_end(p, lo, begin);
   const int length = end - begin;
-  out->slot = begin / sg.len + lo;
+  out->kept = begin / sg.len + (sg.whole > p.T / p.N ? begin / sg.whole : lo);
   out->parts = length <= sg.whole ? (length > 0 ? 1 : 0) : 1 + (length - 1) / sg.len;
-  const int i = slot - out->slot;
+  const int i = slot - (begin / sg.len + lo);
   if (i < 0 || i >= out->parts) return false;
   out->seq = lo;
   out->index = i;
@@ -174,8 +180,8 @@ __device__ __forceinline__ bool find_segment(const DecayArgs& p, const DecaySegm
   return true;
 }
 
-// The first pass over a sequence of several segments leaves in slot m of the
-// workspace what segment m adds to the state (segment 0: the state after it)
+// The first pass over a sequence of several segments leaves in its slot m of
+// the workspace what segment m adds to the state (segment 0: the state after it)
 // and in decays[m] what it multiplies the state by. The last segment is not
 // in that pass; its slot keeps a copy of the state before the call, which
 // the call overwrites. These read and write four elements at `at` of V head
@@ -187,9 +193,9 @@ struct DecaySlots {
   int32_t dstep;
   __device__ __forceinline__ DecaySlots(const DecayArgs& p, const DecaySegments& sg, const DecaySegment& s, int h,
                                         int dd) {
-    base = sg.states + ((int64_t)s.slot * p.Hv + h) * dd;
+    base = sg.states + ((int64_t)s.kept * p.Hv + h) * dd;
     step = (int64_t)p.Hv * dd;
-    decay = sg.decays + ((int64_t)s.slot * p.Hv + h);
+    decay = sg.decays + ((int64_t)s.kept * p.Hv + h);
     dstep = p.Hv;
   }
   // n times eight elements from `at`, for a thread that holds part of a row:

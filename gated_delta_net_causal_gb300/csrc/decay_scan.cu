@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(DecayGeom<D, FEW>::THREADS, FEW ? 1 : (D == 32
   const DecaySlots ws(p, sg, s, h, D * D);
   const int at0 = (warp * G::WROWS + rq) * D + 4 * sub;
   if (MODE == kLocal) {
-    float* keep = sg.states + ((int64_t)(s.slot + s.parts - 1) * p.Hv + h) * (D * D);
+    float* keep = sg.states + ((int64_t)(s.kept + s.parts - 1) * p.Hv + h) * (D * D);
 #pragma unroll
     for (int u = 0; u < RPL; ++u)
 #pragma unroll
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(DecayGeom<D, FEW>::THREADS, FEW ? 1 : (D == 32
   }
 
   if (MODE == kLocal || s.index + 1 == s.parts) {
-    float* to = MODE == kLocal ? sg.states + (int64_t)blockIdx.x * (D * D) : gS;
+    float* to = MODE == kLocal ? sg.states + ((int64_t)(s.kept + s.index) * p.Hv + h) * (D * D) : gS;
 #pragma unroll
     for (int u = 0; u < RPL; ++u)
 #pragma unroll
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(DecayGeom<D, FEW>::THREADS, FEW ? 1 : (D == 32
   }
   if (MODE == kLocal && warp == 0) {
     total = group_sum<32>(tid < kTile ? total : 0.f);
-    if (lane == 0) sg.decays[blockIdx.x] = expf(total);
+    if (lane == 0) sg.decays[(int64_t)(s.kept + s.index) * p.Hv + h] = expf(total);
   }
 }
 

@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.gates[at]);
     }
-    if (MODE == kPLocal && lane == 0 && !*abort_flag) sg.decays[blockIdx.x] = exp2f(total.hi + total.lo);
+    if (MODE == kPLocal && lane == 0 && !*abort_flag) sg.decays[(int64_t)(s.kept + s.index) * p.Hv + h] = exp2f(total.hi + total.lo);
   } else if (warp == kPStore) {
     // ------------------------------------------------------ z in, outputs out
     // (as for the gates: z(c + 2), or its place, is given after o(c) was seen)
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (s.index == 0) {
-          float* keep = sg.states + ((int64_t)(s.slot + s.parts - 1) * p.Hv + h) * (kTd * kTd);
+          float* keep = sg.states + ((int64_t)(s.kept + s.parts - 1) * p.Hv + h) * (kTd * kTd);
 #pragma unroll
           for (int e = 0; e < 4; ++e) load8(gS + at0 + 8 * e, x[2 * e], x[2 * e + 1]);
 #pragma unroll
@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     if (MODE == kPLocal) take_delta(chunks - 1);
     if (!failed && !*abort_flag && (MODE == kPLocal || s.index + 1 == s.parts)) {
-      float* to = MODE == kPLocal ? sg.states + (int64_t)blockIdx.x * (kTd * kTd) : gS;
+      float* to = MODE == kPLocal ? sg.states + ((int64_t)(s.kept + s.index) * p.Hv + h) * (kTd * kTd) : gS;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         store8(to + at0 + 8 * e, make_float4(S[4 * e].x, S[4 * e].y, S[4 * e + 1].x, S[4 * e + 1].y),

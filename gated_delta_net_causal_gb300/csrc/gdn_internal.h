@@ -131,9 +131,10 @@ struct DecayArgs {
 struct DecaySegments {
   int32_t len;    // tokens of a segment where there are several, for the tensor-core kernel a multiple of 64
   int32_t whole;  // longer sequences are cut, >= len
-  int64_t slots;  // floor(T / len) + N
-  float* states;  // [slots][Hv][D][D] or null: one segment per sequence
-  float* decays;  // [slots][Hv] factors of the state over a segment
+  int64_t slots;  // of segments: floor(T / len) + N
+  int64_t kept;   // of the workspace: floor(T / len) + min(N, floor(T / whole))
+  float* states;  // [kept][Hv][D][D] or null: one segment per sequence
+  float* decays;  // [kept][Hv] factors of the state over a segment
 };
 
 struct AddRmsNormArgs {
