@@ -40,6 +40,24 @@ Range range_of(const void* p, int64_t bytes) {
 }
 bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo; }
 
+// rows of `width` bytes, `stride` bytes apart; none where ptr is NULL
+struct Rows {
+  Range all;
+  uintptr_t stride, width;
+};
+Rows rows_of(const void* p, int64_t rows, int64_t stride, int64_t width) {
+  return Rows{range_of(p, p != nullptr && rows > 0 ? (rows - 1) * stride + width : 0), (uintptr_t)stride,
+              (uintptr_t)width};
+}
+// Column slices of one wider buffer (the same stride) overlap only where their
+// columns do; else the whole ranges decide.
+bool overlap(const Rows& a, const Rows& b) {
+  if (!overlap(a.all, b.all)) return false;
+  if (a.stride != b.stride) return true;
+  const uintptr_t s = a.stride, at = (b.all.lo % s + s - a.all.lo % s) % s;  // b's first column in a's rows
+  return at < a.width || at + b.width > s;
+}
+
 gdn_status check_dims(const gdn_dims* d) {
   if (d == nullptr) return GDN_ERR_INVALID_ARG;
   if (d->n_k_heads < 1 || d->n_v_heads < 1) return GDN_ERR_INVALID_ARG;
@@ -775,12 +793,12 @@ gdn_status gdn_add_rmsnorm(int64_t rows, int64_t cols, int32_t io_dtype, const v
   for (int64_t st : strides)
     if (!mul_ok(rows, st, &tmp) || !mul_ok(tmp, es, &tmp)) return GDN_ERR_EXTENT;
   const auto span = [&](const void* ptr, int64_t stride, int64_t size) {
-    return range_of(ptr, ptr != nullptr ? ((rows - 1) * stride + cols) * size : 0);
+    return rows_of(ptr, rows, stride * size, cols * size);
   };
-  const Range rx = span(x, x_stride, es), rr = span(residual, residual_stride, es);
-  const Range rw = range_of(norm_w, norm_w ? cols * 4 : 0);
-  const Range outs[] = {span(sum_out, sum_stride, es), span(out, out_stride, es), span(out_q, out_q_stride, 1),
-                        range_of(out_scale, out_scale ? rows * 4 : 0)};
+  const Rows rx = span(x, x_stride, es), rr = span(residual, residual_stride, es);
+  const Rows rw = rows_of(norm_w, 1, cols * 4, cols * 4);
+  const Rows outs[] = {span(sum_out, sum_stride, es), span(out, out_stride, es), span(out_q, out_q_stride, 1),
+                       rows_of(out_scale, 1, rows * 4, rows * 4)};
   for (int i = 0; i < 4; ++i) {
     const bool same_x = i == 0 && sum_out == x && sum_stride == x_stride;
     const bool same_r = i == 0 && sum_out == residual && sum_stride == residual_stride;

@@ -529,7 +529,8 @@ gdn_status gdn_decay_prefill_workspace_size(const gdn_dims* dims, int32_t num_se
  * out          [rows][out_stride] io dtype, or NULL.
  * out_q        [rows][out_q_stride] e4m3 bytes, or NULL; out_scale [rows]
  *              fp32, needed with out_q. At least one of sum_out, out, out_q.
- * No output may overlap another output or an input, but for sum_out as above.
+ * No output may overlap another output or an input, but for sum_out as above;
+ * column slices of one wider buffer (rows as many bytes apart) do not.
  */
 gdn_status gdn_add_rmsnorm(int64_t rows, int64_t cols, int32_t io_dtype, const void* x,
                            int64_t x_stride, const void* residual, int64_t residual_stride,
