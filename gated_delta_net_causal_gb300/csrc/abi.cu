@@ -713,9 +713,10 @@ gdn_status gdn_decay_step(const gdn_dims* dims, int32_t batch, const int32_t* st
                           void* stream) {
   gdn_status st = check_dims(dims);
   if (st != GDN_OK) return st;
-  if (batch < 0 || num_slots < 0 || (state_slots == nullptr && num_slots != batch)) return GDN_ERR_INVALID_ARG;
+  if (batch < 0 || num_slots < 0) return GDN_ERR_INVALID_ARG;
+  if (batch == 0) return GDN_OK;  // (the table of no rows may have no address)
+  if (state_slots == nullptr && num_slots != batch) return GDN_ERR_INVALID_ARG;
   if (batch > kMaxGridY) return GDN_ERR_EXTENT;
-  if (batch == 0) return GDN_OK;
   gdn::DecayArgs p{};
   st = check_decay(dims, batch, num_slots, state_slots, batch, q, q_stride, k, k_stride, v, v_stride, g, g_stride,
                    scale, state, core_out, z, z_stride, norm_w, out, nullptr, 0, &p);
