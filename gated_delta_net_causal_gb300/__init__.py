@@ -655,7 +655,7 @@ def gdn_add_rmsnorm(x: torch.Tensor, norm_w: Optional[torch.Tensor] = None, resi
 
 def gdn_linear_fp8(x: torch.Tensor, x_scale, w, w_scale, y: torch.Tensor, bias=None, stream=None) -> torch.Tensor:
     """y[m][n] = x_scale[m] w_scale[n] sum_k x[m][k] w[n][k] + bias[n]: x [M][K] and w [N][K] torch.float8_e4m3fn
-    (rows of x and y may be strided), scales and bias fp32, y float16, bfloat16 or float32."""
+    (rows of x and y may be strided, there may be none), scales and bias fp32, y float16, bfloat16 or float32."""
     f8, f32, io = torch.float8_e4m3fn, torch.float32, y.dtype
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w must be 2-D")
@@ -668,10 +668,11 @@ def gdn_linear_fp8(x: torch.Tensor, x_scale, w, w_scale, y: torch.Tensor, bias=N
     yp, ys = _rows(y, "y", io, M, N, dev)
     if M == 1:
         ys = (N + 7) // 8 * 8  # the one row's stride is never used
-    st = library().gdn_linear_fp8(
-        M, N, K, xp, xs, _dense(x_scale, "x_scale", f32, M, dev), _dense(w, "w", f8, N * K, dev),
-        _dense(w_scale, "w_scale", f32, N, dev), None if bias is None else _dense(bias, "bias", f32, N, dev),
-        _TORCH_TO_GDN[io], yp, ys, _stream_on(stream, dev))
+    operands = (_dense(x_scale, "x_scale", f32, M, dev), _dense(w, "w", f8, N * K, dev),
+                _dense(w_scale, "w_scale", f32, N, dev), None if bias is None else _dense(bias, "bias", f32, N, dev))
+    if M == 0:  # an empty batch: nothing to launch
+        return y
+    st = library().gdn_linear_fp8(M, N, K, xp, xs, *operands, _TORCH_TO_GDN[io], yp, ys, _stream_on(stream, dev))
     if st:
         _check(st, "gdn_linear_fp8")
     return y
