@@ -447,7 +447,8 @@ gdn_status gdn_decode_layer_workspace_size(const gdn_dims* dims, int32_t hidden,
  * v            row b, V head h at v[b*v_stride + h*D + j].
  * g            fp32 log decay of (b, h) at g[b*g_stride + h]; g_stride 0 (one
  *              decay per head for every row) or >= Hv. g = -inf resets the
- *              state; positive values grow it.
+ *              state (entries that are not finite stay so, as 0 times them);
+ *              positive values grow it.
  * scale        factor of the output, finite (1/sqrt(D) for scaled attention).
  * state        [num_slots][Hv][D][D] fp32 S[.][h][j][i], in place.
  * core_out     [B][Hv][D] fp32 o, or NULL.
@@ -478,7 +479,10 @@ gdn_status gdn_decay_step(const gdn_dims* dims, int32_t batch, const int32_t* st
  * fp32. What is not finite in v spoils its value
  * row of the state and of the outputs from its token on, in k or g every row,
  * in q or z the outputs of its token alone; nothing reaches earlier tokens or
- * other sequences.
+ * other sequences. Decays of 64 tokens, or of a segment of a long sequence, are
+ * also multiplied up: where g grows the state by more than fp32's range over
+ * such a stretch (its sum passes 88) the state may overflow in rows that are
+ * small or zero, too.
  *
  * cu_seqlens   device int32 [N+1] as for gdn_conv_update; an empty sequence
  *              keeps its state. cu[N] may be smaller than total_tokens: the
