@@ -38,8 +38,8 @@
 // accumulator side by side. The outputs leave TMEM as 8 x 8 blocks, are normed
 // and gated in registers, transposed in shared memory and stored by TMA.
 //
-// What bounds it: a chunk of a head takes about 5000 cycles (8 x 1024 tokens,
-// 64 heads, no gate; 6300 with the gated norm, whose exponentials and
+// What bounds it: a chunk of a head takes about 4800 cycles (8 x 1024 tokens,
+// 64 heads, no gate; 6100 with the gated norm, whose exponentials and
 // reciprocals are 1000 of the MUFU's), a chain of phases of the same warps in
 // which no unit is full. 8 ragged prompts of 34,482 tokens in all, 64 heads:
 // 631 us, 2360 GB/s; one of 4096 tokens, 32 heads: 93 us. With one part of S
