@@ -27,6 +27,10 @@ GDN_F16, GDN_BF16, GDN_F32 = 0, 1, 2
 GDN_QK_PRENORMALIZED, GDN_GATES_PRECOMPUTED, GDN_PREFILL_CUDA_CORES = 1, 2, 4
 GDN_PREFILL_CARRY_WHOLE, GDN_PREFILL_CARRY_SLICED = 8, 16
 
+GDN_ROPE_HALF, GDN_ROPE_INTERLEAVED = 0, 1
+GDN_ROPE_PLAIN, GDN_ROPE_LINEAR, GDN_ROPE_BANDS, GDN_ROPE_RAMP = 0, 1, 2, 3
+GDN_ROPE_INVERSE = 1
+
 _TORCH_TO_GDN = {torch.float16: GDN_F16, torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
 _GDN_TO_TORCH = {v: k for k, v in _TORCH_TO_GDN.items()}
 
@@ -43,6 +47,12 @@ def dims(n_k_heads: int, n_v_heads: int, head_dim: int, map: int = GDN_MAP_GROUP
          rms_eps: float = 1e-6) -> GdnDims:
     dt = _TORCH_TO_GDN[io_dtype] if isinstance(io_dtype, torch.dtype) else int(io_dtype)
     return GdnDims(n_k_heads, n_v_heads, head_dim, map, decay, dt, l2_eps, rms_eps)
+
+
+class GdnRopeTable(ctypes.Structure):
+    """gdn_rope_table: a model's rotary positions (rope_spec makes one)."""
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("step", ctypes.c_uint64 * 64)]
 
 
 class GdnError(RuntimeError):
@@ -119,6 +129,22 @@ def library() -> ctypes.CDLL:
                                       vp]
         L.gdn_linear_fp8.restype = ctypes.c_int
         L.gdn_linear_fp8.argtypes = [i64, i32, i32, vp, i64, vp, vp, vp, vp, i32, vp, i64, vp]
+        f64 = ctypes.c_double
+        pt = ctypes.POINTER(GdnRopeTable)
+        L.gdn_rope_frequencies.restype = ctypes.c_int
+        L.gdn_rope_frequencies.argtypes = [i32, i32, f64, i32, f64, f64, f64, f64, f64, pt]
+        L.gdn_rope.restype = ctypes.c_int
+        L.gdn_rope.argtypes = [pd, pt, i64, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp]
+        L.gdn_attn_prefill.restype = ctypes.c_int
+        L.gdn_attn_prefill.argtypes = [pd, i32, vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, vp, ctypes.c_float, vp, vp,
+                                       vp, i64, vp]
+        L.gdn_attn_prefill_workspace_size.restype = ctypes.c_int
+        L.gdn_attn_prefill_workspace_size.argtypes = [pd, i32, i64, ctypes.POINTER(i64)]
+        L.gdn_attn_shared.restype = ctypes.c_int
+        L.gdn_attn_shared.argtypes = [pd, i32, vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, vp, i32, vp, vp, vp,
+                                      ctypes.c_float, vp, vp, vp, i64, vp]
+        L.gdn_attn_shared_workspace_size.restype = ctypes.c_int
+        L.gdn_attn_shared_workspace_size.argtypes = [pd, i32, i64, i32, ctypes.POINTER(i64)]
         _lib = L
     return _lib
 
@@ -678,6 +704,146 @@ def gdn_linear_fp8(x: torch.Tensor, x_scale, w, w_scale, y: torch.Tensor, bias=N
     return y
 
 
+def rope_spec(rotary_dim: int, layout: int = GDN_ROPE_HALF, base: float = 10000.0, scaling: int = GDN_ROPE_PLAIN,
+              factor: float = 1.0, original_length: float = 0.0, low: float = 0.0, high: float = 0.0,
+              amplitude: float = 1.0) -> GdnRopeTable:
+    """A model's rotary positions for gdn_rope, made once (gdn_rope_frequencies): the first rotary_dim elements of a
+    head rotate, by frequencies of the given base, scaled as the header says (low and high are turns over
+    original_length)."""
+    t = GdnRopeTable()
+    _check(library().gdn_rope_frequencies(int(rotary_dim), int(layout), base, int(scaling), factor, original_length, low,
+                                          high, amplitude, ctypes.byref(t)), "gdn_rope_frequencies")
+    return t
+
+
+def gdn_rope(d: GdnDims, table: GdnRopeTable, positions, q=None, q_out=None, k=None, k_out=None, v=None, v_out=None,
+             cache_rows=None, inverse: bool = False, stream=None):
+    """Rotary positions of q [T][Hq*D] into q_out and k [T][Hk*D] into k_out (d.n_v_heads query heads, d.n_k_heads key
+    heads; either may be None; in place where the same tensor is given twice). With cache_rows (int32 [T]) token t's key
+    goes to row cache_rows[t] of k_out [rows][Hk*D], and its value from v to that row of v_out; negative: nowhere.
+    positions: int32 [T]. inverse: rotates back (the gradient)."""
+    dev, io, dim = _current_device(), _io(d), d.head_dim
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k must be given")
+    rows = x.shape[0]
+    qw, kw = d.n_v_heads * dim, d.n_k_heads * dim
+    pp = _dense(positions, "positions", torch.int32, rows, dev)
+    cp, n = None, rows
+    if cache_rows is not None:
+        cp = _dense(cache_rows, "cache_rows", torch.int32, rows, dev)
+        if k_out is None:
+            raise ValueError("cache_rows needs k and k_out")
+        n = k_out.shape[0]
+    qp = kp = vp = qo = ko = vo = None
+    qs = ks = vs = qos = kos = vos = 0
+    if q is not None:
+        qp, qs = _rows(q, "q", io, rows, qw, dev)
+    if q_out is not None:
+        qo, qos = _rows(q_out, "q_out", io, rows, qw, dev)
+    if k is not None:
+        kp, ks = _rows(k, "k", io, rows, kw, dev)
+    if k_out is not None:
+        ko, kos = _rows(k_out, "k_out", io, n, kw, dev)
+    if v is not None:
+        vp, vs = _rows(v, "v", io, rows, kw, dev)
+    if v_out is not None:
+        vo, vos = _rows(v_out, "v_out", io, n, kw, dev)
+    st = library().gdn_rope(ctypes.byref(d), ctypes.byref(table), rows, pp, qp, qs, qo, qos, kp, ks, ko, kos, vp, vs, vo,
+                            vos, cp, n, GDN_ROPE_INVERSE if inverse else 0, _stream_on(stream, dev))
+    if st:
+        _check(st, "gdn_rope")
+    return q_out, k_out, v_out
+
+
+def gdn_attn_prefill_workspace_size(d: GdnDims, num_seqs: int, total_tokens: int) -> int:
+    n = ctypes.c_int64(0)
+    st = library().gdn_attn_prefill_workspace_size(ctypes.byref(d), num_seqs, total_tokens, ctypes.byref(n))
+    if st:
+        _check(st, "gdn_attn_prefill_workspace_size")
+    return n.value
+
+
+def gdn_attn_shared_workspace_size(d: GdnDims, num_seqs: int, total_tokens: int, num_groups: int) -> int:
+    n = ctypes.c_int64(0)
+    st = library().gdn_attn_shared_workspace_size(ctypes.byref(d), num_seqs, total_tokens, num_groups, ctypes.byref(n))
+    if st:
+        _check(st, "gdn_attn_shared_workspace_size")
+    return n.value
+
+
+def _attn_operands(d: GdnDims, n, q, k, v, kv_start, kv_len, dev):
+    """The operands that the attention calls share, from q to kv_len."""
+    io, dim, rows, kv = _io(d), d.head_dim, q.shape[0], k.shape[0]
+    kw = d.n_k_heads * dim
+    qp, qs = _rows(q, "q", io, rows, d.n_v_heads * dim, dev)
+    kp, ks = _rows(k, "k", io, kv, kw, dev)
+    vp, vs = _rows(v, "v", io, kv, kw, dev)
+    return (rows, qp, qs, kp, ks, vp, vs, kv,
+            None if kv_start is None else _dense(kv_start, "kv_start", torch.int32, n, dev),
+            None if kv_len is None else _dense(kv_len, "kv_len", torch.int32, n, dev))
+
+
+def _attn_outputs(d: GdnDims, rows, scale, out, lse, dev):
+    return (d.head_dim ** -0.5 if scale is None else scale,
+            _dense(out, "out", _io(d), rows * d.n_v_heads * d.head_dim, dev),
+            None if lse is None else _dense(lse, "lse", torch.float32, rows * d.n_v_heads, dev))
+
+
+def gdn_attn_prefill(d: GdnDims, cu_seqlens, q, k, v, out, lse=None, scale: Optional[float] = None, kv_start=None,
+                     kv_len=None, workspace="auto", stream=None):
+    """Causal attention over packed sequences (cu_seqlens int32 [N+1]; prompts, chunks of them or single tokens): q
+    [T][Hq*D] with Hq = d.n_v_heads, out [T][Hq][D], lse fp32 [T][Hq]; k, v [T][Hk*D] (Hk = d.n_k_heads), the tokens'
+    own, or with kv_start and kv_len (int32 [N]) [rows][Hk*D], of which sequence n has kv_len[n] from kv_start[n] on.
+    scale None: D ** -0.5. workspace: "auto" allocates it, None passes none (slow for long caches), or a CUDA uint8
+    tensor of at least gdn_attn_prefill_workspace_size bytes."""
+    dev = _current_device()
+    n = cu_seqlens.numel() - 1
+    cp = _dense(cu_seqlens, "cu_seqlens", torch.int32, n + 1, dev)
+    rows, *operands = _attn_operands(d, n, q, k, v, kv_start, kv_len, dev)
+    outputs = _attn_outputs(d, rows, scale, out, lse, dev)
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError("workspace must be 'auto', None or a CUDA tensor")
+        need = gdn_attn_prefill_workspace_size(d, n, rows)
+        workspace = _scratch(need, q.device, stream) if need > 0 else None
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        ws_bytes = workspace.numel()
+        ws_ptr = _dense(workspace, "workspace", torch.uint8, ws_bytes, dev)
+    st = library().gdn_attn_prefill(ctypes.byref(d), n, cp, rows, *operands, *outputs, ws_ptr, ws_bytes,
+                                    _stream_on(stream, dev))
+    if st:
+        _check(st, "gdn_attn_prefill")
+    return out, lse
+
+
+def gdn_attn_shared(d: GdnDims, cu_seqlens, q, k, v, kv_start, kv_len, group_cu, prefix_start, prefix_len, out, lse=None,
+                    scale: Optional[float] = None, workspace="auto", stream=None):
+    """gdn_attn_prefill over a cache where the tokens group_cu[j] to group_cu[j + 1] also see the prefix_len[j] rows of k
+    and v from prefix_start[j] on (group_cu int32 [G+1], prefix_start and prefix_len int32 [G])."""
+    dev = _current_device()
+    n, groups = cu_seqlens.numel() - 1, prefix_start.numel()
+    i32 = torch.int32
+    cp = _dense(cu_seqlens, "cu_seqlens", i32, n + 1, dev)
+    rows, *operands = _attn_operands(d, n, q, k, v, kv_start, kv_len, dev)
+    prefixes = (groups, _dense(group_cu, "group_cu", i32, groups + 1, dev),
+                _dense(prefix_start, "prefix_start", i32, groups, dev),
+                _dense(prefix_len, "prefix_len", i32, groups, dev))
+    outputs = _attn_outputs(d, rows, scale, out, lse, dev)
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError("workspace must be 'auto' or a CUDA tensor")
+        workspace = _scratch(gdn_attn_shared_workspace_size(d, n, rows, groups), q.device, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel()
+    ws_ptr = None if workspace is None else _dense(workspace, "workspace", torch.uint8, ws_bytes, dev)
+    st = library().gdn_attn_shared(ctypes.byref(d), n, cp, rows, *operands, *prefixes, *outputs, ws_ptr, ws_bytes,
+                                   _stream_on(stream, dev))
+    if st:
+        _check(st, "gdn_attn_shared")
+    return out, lse
+
+
 def gdn_selftest_wait_timeout(limit_ns: int, gave_up: torch.Tensor, stream=None):
     """A device-side bounded wait made to give up after limit_ns; gave_up is a
     CUDA int32 tensor of one element, set to 1 by the kernel."""
@@ -702,6 +868,9 @@ __all__ = ["GdnDims", "GdnError", "dims", "library", "status_string", "gdn_conv_
            "gdn_decode_layer_workspace_size", "GdnLayerWeights",
            "gdn_decay_step", "gdn_decay_prefill", "gdn_decay_prefill_workspace_size", "gdn_add_rmsnorm",
            "gdn_linear_fp8",
+           "GdnRopeTable", "rope_spec", "gdn_rope", "gdn_attn_prefill", "gdn_attn_prefill_workspace_size",
+           "gdn_attn_shared", "gdn_attn_shared_workspace_size", "GDN_ROPE_HALF", "GDN_ROPE_INTERLEAVED",
+           "GDN_ROPE_PLAIN", "GDN_ROPE_LINEAR", "GDN_ROPE_BANDS", "GDN_ROPE_RAMP", "GDN_ROPE_INVERSE",
            "gdn_qkv_features", "gdn_version", "gdn_host_pointer", "GDN_MAP_GROUPED", "GDN_MAP_TILED",
            "GDN_DECAY_LOG_RATE", "GDN_DECAY_NEGATIVE_RATE", "GDN_F16", "GDN_BF16", "GDN_F32",
            "GDN_QK_PRENORMALIZED", "GDN_GATES_PRECOMPUTED", "GDN_PREFILL_CUDA_CORES",

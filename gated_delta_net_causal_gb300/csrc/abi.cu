@@ -194,7 +194,7 @@ const char* gdn_status_string(int32_t status) {
   }
 }
 
-int32_t gdn_version(void) { return 500; }
+int32_t gdn_version(void) { return 600; }
 
 gdn_status gdn_host_pointer(const void* host, void** device) {
   if (host == nullptr || device == nullptr) return GDN_ERR_INVALID_ARG;
@@ -704,6 +704,99 @@ gdn_status decay_plan(const gdn_dims* dims, int32_t num_seqs, int64_t total_toke
   return GDN_OK;
 }
 
+// Softmax attention: sizes that every call of it checks first.
+gdn_status check_attn_sizes(const gdn_dims* dims, int32_t num_seqs, int64_t total_tokens) {
+  const gdn_status st = check_dims(dims);
+  if (st != GDN_OK) return st;
+  if (num_seqs < 0 || total_tokens < 0) return GDN_ERR_INVALID_ARG;
+  if (num_seqs > kMaxGridY || total_tokens > INT32_MAX - 1024) return GDN_ERR_EXTENT;
+  return dims->n_v_heads / dims->n_k_heads > 64 ? GDN_ERR_UNSUPPORTED : GDN_OK;
+}
+
+gdn::AttnSplit attn_split_of(const gdn_dims* dims, int64_t total_tokens) {
+  return gdn::attn_split(dims->io_dtype, total_tokens, dims->n_v_heads / dims->n_k_heads, dims->head_dim);
+}
+
+// gdn_attn_shared's workspace: that of the splits, then the prefixes' outputs
+// and logarithms of sums.
+struct AttnPrior {
+  int64_t o, lse, bytes;
+};
+AttnPrior attn_prior_at(const gdn_dims* dims, int64_t total_tokens) {
+  AttnPrior a{};
+  a.o = attn_split_of(dims, total_tokens).bytes;
+  const int64_t rows = total_tokens * dims->n_v_heads;  // < 2^31 2^16
+  a.lse = a.o + (rows * dims->head_dim * 4 + 255) / 256 * 256;
+  a.bytes = a.lse + (rows * 4 + 255) / 256 * 256;
+  return a;
+}
+
+// Checks what the calls share and fills *p; extra: further inputs.
+gdn_status check_attn(const gdn_dims* dims, int32_t num_seqs, const int32_t* cu_seqlens, int64_t total_tokens,
+                      const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                      int64_t v_stride, int64_t kv_rows, float scale, void* out, float* lse, void* workspace,
+                      int64_t ws_bytes, const Range* extra, const void* const* extra_ptrs, int n_extra,
+                      gdn::AttnArgs* p) {
+  const int64_t es = dtype_size(dims->io_dtype), Hq = dims->n_v_heads, Hk = dims->n_k_heads, D = dims->head_dim;
+  if (num_seqs == 0 || !cu_seqlens || !q || !out || kv_rows < 0 || (kv_rows > 0 && (!k || !v)))
+    return GDN_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !isfinite(scale)) return GDN_ERR_INVALID_ARG;
+  if (q_stride < Hq * D || k_stride < Hk * D || v_stride < Hk * D) return GDN_ERR_INVALID_ARG;
+  if (kv_rows > INT32_MAX - 1024) return GDN_ERR_EXTENT;
+  const int64_t strides[] = {q_stride, k_stride, v_stride};
+  for (int64_t st : strides) {
+    int64_t tmp = 0;
+    // a tensor map's stride is below 2^40 bytes
+    if (st >= (1ll << 37) || !mul_ok(st * es, total_tokens > kv_rows ? total_tokens : kv_rows, &tmp))
+      return GDN_ERR_EXTENT;
+    if (st * es % 16 != 0) return GDN_ERR_ALIGN;
+  }
+  // the units of the work (tiles of keys, of items, of heads) are counted in
+  // 64 bits: at most a tile of 64 keys for each token and key head
+  int64_t units = 0;
+  if (!mul_ok((total_tokens + num_seqs) * Hk, kv_rows / 64 + 2, &units)) return GDN_ERR_EXTENT;
+  const void* ptrs[] = {cu_seqlens, q, k, v, out, lse, workspace};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return GDN_ERR_ALIGN;
+  for (int i = 0; i < n_extra; ++i)
+    if (!aligned16(extra_ptrs[i])) return GDN_ERR_ALIGN;
+  if (workspace != nullptr && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return GDN_ERR_ALIGN;
+  const auto span = [&](const void* ptr, int64_t rows, int64_t stride, int64_t width) {
+    return range_of(ptr, ptr != nullptr && rows > 0 ? ((rows - 1) * stride + width) * es : 0);
+  };
+  const Range inputs[] = {span(q, total_tokens, q_stride, Hq * D), span(k, kv_rows, k_stride, Hk * D),
+                          span(v, kv_rows, v_stride, Hk * D), range_of(cu_seqlens, ((int64_t)num_seqs + 1) * 4)};
+  const Range outputs[] = {range_of(out, total_tokens * Hq * D * es),
+                           range_of(lse, lse != nullptr ? total_tokens * Hq * 4 : 0), range_of(workspace, ws_bytes)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& in : inputs)
+      if (overlap(outputs[i], in)) return GDN_ERR_ALIAS;
+    for (int j = 0; j < n_extra; ++j)
+      if (overlap(outputs[i], extra[j])) return GDN_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outputs[i], outputs[j])) return GDN_ERR_ALIAS;
+  }
+  p->q = q;
+  p->q_stride = q_stride;
+  p->k = k;
+  p->k_stride = k_stride;
+  p->v = v;
+  p->v_stride = v_stride;
+  p->cu_seqlens = cu_seqlens;
+  p->N = num_seqs;
+  p->T = (int32_t)total_tokens;
+  p->kv_rows = (int32_t)kv_rows;
+  p->causal = 1;
+  p->Hq = (int32_t)Hq;
+  p->Hk = (int32_t)Hk;
+  p->group = (int32_t)(Hq / Hk);
+  p->map = dims->map;
+  p->scale = scale;
+  p->out = out;
+  p->lse = lse;
+  return GDN_OK;
+}
+
 }  // namespace
 
 gdn_status gdn_decay_step(const gdn_dims* dims, int32_t batch, const int32_t* state_slots, int32_t num_slots,
@@ -769,6 +862,219 @@ gdn_status gdn_decay_prefill(const gdn_dims* dims, int32_t num_seqs, const int32
   if (gdn::decay_tc_fits(dims->io_dtype, dims->head_dim, num_seqs, total_tokens) && gdn::decay_tc_supported(p))
     return cuda_status(gdn::launch_decay_tc(p, sg, static_cast<cudaStream_t>(stream)));
   return cuda_status(gdn::launch_decay_scan(p, sg, dims->io_dtype, dims->head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_rope_frequencies(int32_t rotary_dim, int32_t layout, double base, int32_t scaling, double factor,
+                                double original_length, double low, double high, double amplitude,
+                                gdn_rope_table* table) {
+  const double two_pi = 6.283185307179586476925286766559;
+  if (table == nullptr || rotary_dim < 2 || rotary_dim > 128 || rotary_dim % 2 != 0) return GDN_ERR_INVALID_ARG;
+  if (layout != GDN_ROPE_HALF && layout != GDN_ROPE_INTERLEAVED) return GDN_ERR_INVALID_ARG;
+  if (scaling < GDN_ROPE_PLAIN || scaling > GDN_ROPE_RAMP) return GDN_ERR_INVALID_ARG;
+  if (!(base > 1.0) || !isfinite(base) || !isfinite((float)amplitude)) return GDN_ERR_INVALID_ARG;
+  if (scaling != GDN_ROPE_PLAIN && (!(factor > 0.0) || !isfinite(factor))) return GDN_ERR_INVALID_ARG;
+  const bool ranged = scaling == GDN_ROPE_BANDS || scaling == GDN_ROPE_RAMP;
+  if (ranged && (!(original_length > 0.0) || !isfinite(original_length) || !(low > 0.0) || !(high > low) ||
+                 !isfinite(high)))
+    return GDN_ERR_INVALID_ARG;
+  const double R = rotary_dim;
+  double first = 0.0, last = 0.0;
+  if (scaling == GDN_ROPE_RAMP) {
+    const auto at = [&](double turns) { return R * log(original_length / (two_pi * turns)) / (2.0 * log(base)); };
+    first = fmax(floor(at(high)), 0.0);
+    last = fmin(ceil(at(low)), R - 1.0);
+  }
+  gdn_rope_table t{};
+  t.rotary_dim = rotary_dim;
+  t.layout = layout;
+  t.amplitude = (float)amplitude;
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    const double b = pow(base, -2.0 * i / R);
+    double f = b;
+    if (scaling == GDN_ROPE_LINEAR) {
+      f = b / factor;
+    } else if (ranged) {
+      const double w = scaling == GDN_ROPE_BANDS ? (original_length * b / two_pi - low) / (high - low)
+                                                 : 1.0 - (i - first) / fmax(last - first, 0.001);
+      const double keep = w < 0.0 ? 0.0 : w > 1.0 ? 1.0 : w;
+      f = b * (keep + (1.0 - keep) / factor);
+    }
+    const double turns = f / two_pi;
+    t.step[i] = (uint64_t)ldexp(turns - floor(turns), 64);
+  }
+  *table = t;
+  return GDN_OK;
+}
+
+gdn_status gdn_rope(const gdn_dims* dims, const gdn_rope_table* table, int64_t tokens, const int32_t* positions,
+                    const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, const void* k,
+                    int64_t k_stride, void* k_out, int64_t k_out_stride, const void* v, int64_t v_stride, void* v_out,
+                    int64_t v_out_stride, const int32_t* cache_rows, int64_t num_rows, int32_t flags, void* stream) {
+  gdn_status st = check_dims(dims);
+  if (st != GDN_OK) return st;
+  if (table == nullptr || tokens < 0 || (flags & ~GDN_ROPE_INVERSE) != 0) return GDN_ERR_INVALID_ARG;
+  if (table->rotary_dim < 2 || table->rotary_dim > dims->head_dim || table->rotary_dim % 2 != 0 ||
+      (table->layout != GDN_ROPE_HALF && table->layout != GDN_ROPE_INTERLEAVED))
+    return GDN_ERR_INVALID_ARG;
+  if (tokens > INT32_MAX - 64) return GDN_ERR_EXTENT;
+  if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr) ||
+      (v == nullptr) != (v_out == nullptr))
+    return GDN_ERR_INVALID_ARG;
+  if (cache_rows == nullptr) num_rows = tokens;
+  if (num_rows < 0) return GDN_ERR_INVALID_ARG;
+  if (num_rows > INT32_MAX) return GDN_ERR_EXTENT;
+  if (tokens == 0) return GDN_OK;
+  if (positions == nullptr || (q == nullptr && k == nullptr)) return GDN_ERR_INVALID_ARG;
+  if (v != nullptr && (cache_rows == nullptr || k == nullptr)) return GDN_ERR_INVALID_ARG;
+  const int64_t es = dtype_size(dims->io_dtype);
+  const int64_t qw = (int64_t)dims->n_v_heads * dims->head_dim, kw = (int64_t)dims->n_k_heads * dims->head_dim;
+  const struct {
+    const void* p;
+    int64_t stride, width, rows;
+  } ops[] = {{q, q_stride, qw, tokens},         {k, k_stride, kw, tokens},          {v, v_stride, kw, tokens},
+             {q_out, q_out_stride, qw, tokens}, {k_out, k_out_stride, kw, num_rows}, {v_out, v_out_stride, kw, num_rows}};
+  Rows at[6];
+  for (int i = 0; i < 6; ++i) {
+    if (ops[i].p == nullptr) {
+      at[i] = rows_of(nullptr, 0, 16, 0);
+      continue;
+    }
+    int64_t tmp = 0;
+    if (ops[i].stride < ops[i].width) return GDN_ERR_INVALID_ARG;
+    if (!mul_ok(ops[i].stride, es, &tmp) || !mul_ok(tmp, ops[i].rows, &tmp)) return GDN_ERR_EXTENT;
+    if (ops[i].stride * es % 16 != 0 || !aligned16(ops[i].p)) return GDN_ERR_ALIGN;
+    at[i] = rows_of(ops[i].p, ops[i].rows, ops[i].stride * es, ops[i].width * es);
+  }
+  if (!aligned16(positions) || !aligned16(cache_rows)) return GDN_ERR_ALIGN;
+  const Rows tables[] = {rows_of(positions, 1, tokens * 4, tokens * 4),
+                         rows_of(cache_rows, 1, tokens * 4, tokens * 4)};
+  for (int o = 3; o < 6; ++o) {
+    for (int i = 0; i < o; ++i) {
+      const bool in_place = (i == 0 && o == 3 && q == q_out && q_stride == q_out_stride) ||
+                            (i == 1 && o == 4 && k == k_out && k_stride == k_out_stride && cache_rows == nullptr);
+      if (overlap(at[o], at[i]) && !in_place) return GDN_ERR_ALIAS;
+    }
+    for (const Rows& t : tables)
+      if (overlap(at[o].all, t.all)) return GDN_ERR_ALIAS;
+  }
+  gdn::RopeArgs p{};
+  p.positions = positions;
+  p.cache_rows = cache_rows;
+  p.num_rows = (int32_t)num_rows;
+  p.T = tokens;
+  p.q = q;
+  p.q_stride = q_stride;
+  p.q_out = q_out;
+  p.q_out_stride = q_out_stride;
+  p.k = k;
+  p.k_stride = k_stride;
+  p.k_out = k_out;
+  p.k_out_stride = k_out_stride;
+  p.v = v;
+  p.v_stride = v_stride;
+  p.v_out = v_out;
+  p.v_out_stride = v_out_stride;
+  p.Hq = dims->n_v_heads;
+  p.Hk = dims->n_k_heads;
+  p.D = dims->head_dim;
+  p.inverse = (flags & GDN_ROPE_INVERSE) != 0;
+  p.table = *table;
+  return cuda_status(gdn::launch_rope(p, dims->io_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_attn_prefill_workspace_size(const gdn_dims* dims, int32_t num_seqs, int64_t total_tokens,
+                                           int64_t* bytes) {
+  if (bytes == nullptr) return GDN_ERR_INVALID_ARG;
+  *bytes = 0;
+  const gdn_status st = check_attn_sizes(dims, num_seqs, total_tokens);
+  if (st != GDN_OK || total_tokens == 0) return st;
+  *bytes = attn_split_of(dims, total_tokens).bytes;
+  return GDN_OK;
+}
+
+gdn_status gdn_attn_shared_workspace_size(const gdn_dims* dims, int32_t num_seqs, int64_t total_tokens,
+                                          int32_t num_groups, int64_t* bytes) {
+  if (bytes == nullptr) return GDN_ERR_INVALID_ARG;
+  *bytes = 0;
+  gdn_status st = check_attn_sizes(dims, num_seqs, total_tokens);
+  if (st == GDN_OK) st = check_attn_sizes(dims, num_groups, 0);
+  if (st != GDN_OK || total_tokens == 0) return st;
+  *bytes = attn_prior_at(dims, total_tokens).bytes;
+  return GDN_OK;
+}
+
+gdn_status gdn_attn_prefill(const gdn_dims* dims, int32_t num_seqs, const int32_t* cu_seqlens, int64_t total_tokens,
+                            const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, int64_t kv_rows, const int32_t* kv_start, const int32_t* kv_len,
+                            float scale, void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                            void* stream) {
+  gdn_status st = check_attn_sizes(dims, num_seqs, total_tokens);
+  if (st != GDN_OK) return st;
+  if (total_tokens == 0) return GDN_OK;
+  if ((kv_start == nullptr) != (kv_len == nullptr) || (kv_start == nullptr && kv_rows != total_tokens))
+    return GDN_ERR_INVALID_ARG;
+  const gdn::AttnSplit s = attn_split_of(dims, total_tokens);
+  if (workspace != nullptr && workspace_bytes < s.bytes) return GDN_ERR_INVALID_ARG;
+  gdn::AttnArgs p{};
+  const Range extra[] = {range_of(kv_start, kv_start ? (int64_t)num_seqs * 4 : 0),
+                         range_of(kv_len, kv_len ? (int64_t)num_seqs * 4 : 0)};
+  const void* extra_ptrs[] = {kv_start, kv_len};
+  st = check_attn(dims, num_seqs, cu_seqlens, total_tokens, q, q_stride, k, k_stride, v, v_stride, kv_rows, scale, out,
+                  lse, workspace, workspace != nullptr ? s.bytes : 0, extra, extra_ptrs, 2, &p);
+  if (st != GDN_OK) return st;
+  p.kv_start = kv_start;
+  p.kv_len = kv_len;
+  return cuda_status(
+      gdn::launch_attn(p, s, workspace, dims->io_dtype, dims->head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_attn_shared(const gdn_dims* dims, int32_t num_seqs, const int32_t* cu_seqlens, int64_t total_tokens,
+                           const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, int64_t kv_rows, const int32_t* kv_start, const int32_t* kv_len,
+                           int32_t num_groups, const int32_t* group_cu, const int32_t* prefix_start,
+                           const int32_t* prefix_len, float scale, void* out, float* lse, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  gdn_status st = check_attn_sizes(dims, num_seqs, total_tokens);
+  if (st == GDN_OK) st = check_attn_sizes(dims, num_groups, 0);
+  if (st != GDN_OK) return st;
+  if (total_tokens == 0) return GDN_OK;
+  if (!kv_start || !kv_len) return GDN_ERR_INVALID_ARG;
+  if (num_groups > 0 && (!group_cu || !prefix_start || !prefix_len)) return GDN_ERR_INVALID_ARG;
+  const gdn::AttnSplit s = attn_split_of(dims, total_tokens);
+  const AttnPrior at = attn_prior_at(dims, total_tokens);
+  if (workspace == nullptr || workspace_bytes < at.bytes) return GDN_ERR_INVALID_ARG;
+  gdn::AttnArgs p{};
+  const bool any = num_groups > 0;
+  const Range extra[] = {range_of(kv_start, (int64_t)num_seqs * 4), range_of(kv_len, (int64_t)num_seqs * 4),
+                         range_of(group_cu, any ? (int64_t)num_groups * 4 + 4 : 0),
+                         range_of(prefix_start, any ? (int64_t)num_groups * 4 : 0),
+                         range_of(prefix_len, any ? (int64_t)num_groups * 4 : 0)};
+  const void* extra_ptrs[] = {kv_start, kv_len, group_cu, prefix_start, prefix_len};
+  st = check_attn(dims, num_seqs, cu_seqlens, total_tokens, q, q_stride, k, k_stride, v, v_stride, kv_rows, scale, out,
+                  lse, workspace, at.bytes, extra, extra_ptrs, 5, &p);
+  if (st != GDN_OK) return st;
+  const cudaStream_t s_ = static_cast<cudaStream_t>(stream);
+  p.kv_start = kv_start;
+  p.kv_len = kv_len;
+  if (any) {  // the prefixes, for their groups' tokens as one sequence each
+    gdn::AttnArgs g = p;
+    float* o = reinterpret_cast<float*>(static_cast<char*>(workspace) + at.o);
+    float* l = reinterpret_cast<float*>(static_cast<char*>(workspace) + at.lse);
+    g.cu_seqlens = group_cu;
+    g.N = num_groups;
+    g.kv_start = prefix_start;
+    g.kv_len = prefix_len;
+    g.causal = 0;
+    g.core = o;
+    g.lse = l;
+    const cudaError_t e = gdn::launch_attn(g, s, workspace, dims->io_dtype, dims->head_dim, s_);
+    if (e != cudaSuccess) return cuda_status(e);
+    p.prior_o = o;
+    p.prior_lse = l;
+    p.prior_cu = group_cu;
+    p.prior_n = num_groups;
+  }
+  return cuda_status(gdn::launch_attn(p, s, workspace, dims->io_dtype, dims->head_dim, s_));
 }
 
 gdn_status gdn_add_rmsnorm(int64_t rows, int64_t cols, int32_t io_dtype, const void* x, int64_t x_stride,
@@ -875,7 +1181,7 @@ gdn_status gdn_device_error(int32_t* status, int32_t clear) {
                                                gdn::read_error_linear, gdn::read_error_decay_step,
                                                gdn::read_error_decay_scan, gdn::read_error_decay_tc,
                                                gdn::read_error_linear_fp8,
-                                               gdn::read_error_add_rmsnorm};
+                                               gdn::read_error_add_rmsnorm, gdn::read_error_rope};
   for (auto rd : readers) {
     int32_t v = 0;
     if (rd(&v, clear != 0) != cudaSuccess) return GDN_ERR_CUDA;

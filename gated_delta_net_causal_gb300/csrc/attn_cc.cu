@@ -1,0 +1,247 @@
+// Softmax attention on the fp32 units: rows x keys in tiles of 64 x 64, one
+// pass over the keys with the running maximum and sum of each row.
+//
+// A CTA of 256 threads is a grid of 16 x 16; a thread has 4 x 4 scores (rows
+// 4 ty + i, keys 4 tx + j), then the outputs of the same four rows at D / 16
+// columns. q and k lie transposed in shared memory, so that a step of the
+// contraction is two 16-byte reads for 16 products; the weights take k's
+// place, transposed as well.
+#include "attn_common.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kAR = 64;    // rows of an item
+constexpr int kAK = 64;    // keys of a tile
+constexpr int kAT = 256;   // threads
+constexpr int kAP = 68;    // pitch of the transposed tiles, in floats
+
+// shared memory, in floats: q, k (whose place the weights take), v
+template <int D>
+struct CcSmem {
+  static constexpr int kK = D * kAP, kV = kK + (D > kAK ? D : kAK) * kAP, kEnd = kV + kAK * D;
+};
+
+template <typename T, int VEC>
+__device__ __forceinline__ void load_vec(const T* p, float (&x)[VEC]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) x[i] = to_f32(e[i]);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kAT, 2) attn_cc_kernel(const AttnArgs p) {
+  constexpr int VEC = 16 / (int)sizeof(T), NP = D / 32;  // NP pairs of output columns a thread
+  extern __shared__ __align__(16) float sm[];
+  float* qt = sm;                  // [D][kAP]
+  float* kt = sm + CcSmem<D>::kK;  // [D][kAP], then the weights [kAK][kAP]
+  float* vs = sm + CcSmem<D>::kV;  // [kAK][D]
+  __shared__ int64_t sums[kAT];
+  __shared__ AttnPlan plan;
+  __shared__ AttnPiece piece;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  attn_plan<kAK, kAT>(p, sums, &plan);
+  if (tid < 2 && p.part_o != nullptr) p.part_at[2 * blockIdx.x + tid] = make_int4(kAttnWhole, 0, 0, 0);
+  AttnWalk<kAK> walk;
+  if (tid == 0) walk.start(p, plan);
+  const T* gq = static_cast<const T*>(p.q);
+  const T* gk = static_cast<const T*>(p.k);
+  const T* gv = static_cast<const T*>(p.v);
+  const float sc = p.scale * kAttnLog2e;
+
+  for (;;) {
+    __syncthreads();
+    if (tid == 0) piece = walk.next(p);
+    __syncthreads();
+    const AttnPiece w = piece;
+    if (w.tokens == 0) break;
+    const int rows = w.tokens * p.group;
+    // q, transposed: thread = row, chunks of 16 bytes
+    for (int u = tid; u < kAR * (D / VEC); u += kAT) {
+      const int r = u % kAR, c = u / kAR * VEC;
+      float x[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[e] = 0.f;
+      if (r < rows)
+        load_vec<T, VEC>(gq + (int64_t)(w.q0 + r / p.group) * p.q_stride + attn_head(p, w.kh, r % p.group) * D + c, x);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) qt[(c + e) * kAP + r] = x[e];
+    }
+    int sees[4];
+    float top[4], sum[4];
+    float2 o[4][NP];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * ty + i;
+      sees[i] = r < rows ? attn_sees(p, w, r / p.group) : 0;
+      top[i] = -INFINITY;
+      sum[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) o[i][j] = make_float2(0.f, 0.f);
+    }
+    const int least = attn_sees(p, w, 0), most = attn_sees(p, w, w.tokens - 1);
+    for (int t = w.t0; t < w.t1; ++t) {
+      const int first = t * kAK, n = most - first < kAK ? most - first : kAK;
+      __syncthreads();
+      for (int u = tid; u < kAK * (D / VEC); u += kAT) {
+        const int r = u % kAK, c = u / kAK * VEC;
+        float x[VEC], y[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[e] = y[e] = 0.f;
+        if (r < n) {
+          const int64_t row = (int64_t)w.k0 + first + r;
+          load_vec<T, VEC>(gk + row * p.k_stride + w.kh * D + c, x);
+          load_vec<T, VEC>(gv + row * p.v_stride + w.kh * D + c, y);
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) kt[(c + e) * kAP + r] = x[e];
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4)
+          *reinterpret_cast<float4*>(vs + r * D + c + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+      }
+      __syncthreads();
+      float s[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 8
+      for (int d = 0; d < D; ++d) {
+        const float4 a = *reinterpret_cast<const float4*>(qt + d * kAP + 4 * ty);
+        const float4 b = *reinterpret_cast<const float4*>(kt + d * kAP + 4 * tx);
+        const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[i][j] = fmaf(av[i], bv[j], s[i][j]);
+      }
+      const bool masked = first + kAK > least;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (masked)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (first + 4 * tx + j >= sees[i]) s[i][j] = -INFINITY;
+        float m = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        m = fmaxf(m, top[i]);
+        const float base = m == -INFINITY ? 0.f : m;  // nothing seen so far: every weight is 0
+        const float f = exp2f((top[i] - base) * sc);
+        float l = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = exp2f((s[i][j] - base) * sc);
+          l += s[i][j];
+        }
+        sum[i] = fmaf(sum[i], f, l);
+        top[i] = m;
+#pragma unroll
+        for (int j = 0; j < NP; ++j) o[i][j] = make_float2(o[i][j].x * f, o[i][j].y * f);
+      }
+      __syncthreads();  // k is no longer read
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<float4*>(kt + (4 * tx + j) * kAP + 4 * ty) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
+      __syncthreads();
+      if (!masked) {
+#pragma unroll 4
+        for (int k = 0; k < kAK; ++k) {
+          const float4 a = *reinterpret_cast<const float4*>(kt + k * kAP + 4 * ty);
+          const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int j = 0; j < NP; ++j) {
+            const float2 b = *reinterpret_cast<const float2*>(vs + k * D + 32 * j + 2 * tx);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i][j] = fma2(make_float2(av[i], av[i]), b, o[i][j]);
+          }
+        }
+      } else {
+        // a key that a row does not see adds nothing to it, not even 0 times what is not finite
+        for (int k = 0; k < n; ++k) {
+          const float4 a = *reinterpret_cast<const float4*>(kt + k * kAP + 4 * ty);
+          const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int j = 0; j < NP; ++j) {
+            const float2 b = *reinterpret_cast<const float2*>(vs + k * D + 32 * j + 2 * tx);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (first + k < sees[i]) o[i][j] = fma2(make_float2(av[i], av[i]), b, o[i][j]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float l = sum[i];
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      const int r = 4 * ty + i;
+      if (r >= rows) continue;
+      if (w.part != kAttnWhole) {
+        const int64_t at = (int64_t)attn_slot(blockIdx.x, w.part) * p.part_rows + r;
+#pragma unroll
+        for (int j = 0; j < NP; ++j) *reinterpret_cast<float2*>(p.part_o + at * D + 32 * j + 2 * tx) = o[i][j];
+        if (tx == 0) p.part_ml[at] = make_float2(top[i] * sc, l);
+        continue;
+      }
+      const int64_t token = w.q0 + r / p.group;
+      const int head = attn_head(p, w.kh, r % p.group);
+      const AttnPrior prior = attn_prior(p, token, head);
+      const AttnScale f = attn_scale(top[i] * sc, l, prior);
+      const int64_t at = (token * p.Hq + head) * D;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const int c = 32 * j + 2 * tx;
+        float2 y = make_float2(o[i][j].x * f.own, o[i][j].y * f.own);
+        if (prior.any) {
+          const float2 b = *reinterpret_cast<const float2*>(p.prior_o + at + c);
+          y = fma2(make_float2(f.prior, f.prior), b, y);
+        }
+        if (p.core != nullptr) {
+          *reinterpret_cast<float2*>(p.core + at + c) = y;
+        } else {
+          static_cast<T*>(p.out)[at + c] = from_f32<T>(y.x);
+          static_cast<T*>(p.out)[at + c + 1] = from_f32<T>(y.y);
+        }
+      }
+      if (tx == 0 && p.lse != nullptr) p.lse[token * p.Hq + head] = f.lse;
+    }
+    if (tid == 0 && w.part != kAttnWhole)
+      p.part_at[attn_slot(blockIdx.x, w.part)] = make_int4(w.part, w.q0, w.tokens, w.kh);
+  }
+}
+
+template <typename T, int D>
+cudaError_t run(const AttnArgs& p, int grid, cudaStream_t stream) {
+  constexpr int smem = CcSmem<D>::kEnd * 4;
+  const cudaError_t e = cudaFuncSetAttribute(attn_cc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  attn_cc_kernel<T, D><<<grid, kAT, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t run_dim(const AttnArgs& p, int32_t D, int grid, cudaStream_t stream) {
+  switch (D) {
+    case 32: return run<T, 32>(p, grid, stream);
+    case 64: return run<T, 64>(p, grid, stream);
+    case 96: return run<T, 96>(p, grid, stream);
+    default: return run<T, 128>(p, grid, stream);
+  }
+}
+
+}  // namespace
+
+int attn_cc_rows() { return kAR; }
+int attn_cc_ctas(int sms) { return 2 * sms; }
+
+cudaError_t launch_attn_cc(const AttnArgs& p, int32_t dtype, int32_t D, int grid, cudaStream_t stream) {
+  switch (dtype) {
+    case GDN_F16: return run_dim<__half>(p, D, grid, stream);
+    case GDN_BF16: return run_dim<__nv_bfloat16>(p, D, grid, stream);
+    default: return run_dim<float>(p, D, grid, stream);
+  }
+}
+
+}  // namespace gdn

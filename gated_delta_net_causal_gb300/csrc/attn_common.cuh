@@ -1,0 +1,249 @@
+// Shared device code of softmax attention over packed sequences:
+//   o_t = sum_s w_ts v_s,  w_t = softmax over the visible keys s of scale q_t . k_s
+// with the query heads of a key head (a "group") side by side.
+//
+// How the work is cut. A sequence's tokens are taken `item` at a time: an item
+// is those tokens' rows (token, query head of the group) for one key head, its
+// keys are read in tiles of KT. A tile of an item is a unit; units lie in one
+// order (sequence, key head, item, tile), and CTA c of G takes the c-th of G
+// equal stretches of them, whatever the lengths are. An item that lies across
+// a border is left in parts, each (largest score, sum, unnormalised output)
+// in fp32 in the workspace, and attn_join_kernel puts them together. So one
+// long cache is spread over all SMs, ragged prompts leave no SM behind, and
+// sums do not depend on which CTA ran first. The lengths are on the device:
+// every CTA adds up the units for itself, its threads a slice of the
+// sequences each.
+#pragma once
+
+#include "gdn_common.cuh"
+#include "gdn_internal.h"
+
+namespace gdn {
+
+constexpr float kAttnLog2e = 1.4426950408889634f;
+constexpr float kAttnLn2 = 0.69314718055994531f;
+
+struct AttnSeq {
+  int q0, qn;  // first token and number of them
+  int k0, kn;  // first key row and number of them
+};
+
+__device__ __forceinline__ int attn_clamp(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
+
+__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& p, int n) {
+  AttnSeq s;
+  s.q0 = attn_clamp(p.cu_seqlens[n], 0, p.T);
+  s.qn = attn_clamp(p.cu_seqlens[n + 1], s.q0, p.T) - s.q0;
+  if (p.kv_start != nullptr) {
+    s.k0 = attn_clamp(p.kv_start[n], 0, p.kv_rows);
+    s.kn = attn_clamp(p.kv_len[n], 0, p.kv_rows - s.k0);
+  } else {
+    s.k0 = s.q0;
+    s.kn = s.qn;
+  }
+  return s;
+}
+
+// Keys that the token at `at` of the sequence sees.
+__device__ __forceinline__ int attn_visible(const AttnArgs& p, const AttnSeq& s, int at) {
+  if (!p.causal) return s.kn;
+  const int64_t v = (int64_t)s.kn - s.qn + at + 1;
+  return v > 0 ? (int)v : 0;
+}
+
+// Units of the item whose first token is `at`: its tiles, or one where it
+// sees nothing (its outputs are written all the same).
+template <int KT>
+__device__ __forceinline__ int attn_units(const AttnArgs& p, const AttnSeq& s, int at) {
+  const int last = (s.qn - at < p.item ? s.qn : at + p.item) - 1;
+  const int v = attn_visible(p, s, last);
+  return v > KT ? v / KT + (v % KT != 0) : 1;
+}
+// Units of a sequence for one key head.
+template <int KT>
+__device__ __forceinline__ int64_t attn_seq_units(const AttnArgs& p, const AttnSeq& s) {
+  if (s.qn == 0) return 0;
+  if (!p.causal) return (int64_t)((s.qn - 1) / p.item + 1) * attn_units<KT>(p, s, 0);
+  int64_t u = 0;
+  for (int64_t at = 0; at < s.qn; at += p.item) u += attn_units<KT>(p, s, (int)at);
+  return u;
+}
+
+// A stretch of an item's tiles, for one CTA.
+struct AttnPiece {
+  int q0;     // first token of the item
+  int tokens; // 0: no piece, the CTA is done
+  int kh;
+  int k0;     // row of the first key
+  int see;    // keys that its first token sees (causal: one more for each token after it; may be negative)
+  int t0, t1; // tiles of this piece
+  int part;   // kAttnWhole, or whether the item's tiles end with it
+  int bad;    // set where a masked tile of v holds what is not finite
+};
+enum { kAttnWhole = 0, kAttnFirst = 1, kAttnMiddle = 2, kAttnLast = 3 };
+
+// keys that token i of the piece sees
+__device__ __forceinline__ int attn_sees(const AttnArgs& p, const AttnPiece& w, int i) {
+  return p.causal ? (w.see + i > 0 ? w.see + i : 0) : w.see;
+}
+
+struct AttnPlan {
+  int64_t begin, count;  // the CTA's first unit, counted from sequence n, and how many
+  int n;
+};
+
+// Every thread of the CTA; sums: one of shared memory for each of them.
+template <int KT, int THREADS>
+__device__ __forceinline__ void attn_plan(const AttnArgs& p, int64_t* sums, AttnPlan* plan) {
+  const int per = (p.N + THREADS - 1) / THREADS;
+  {
+    const int64_t a = (int64_t)threadIdx.x * per, b = a + per < p.N ? a + per : p.N;
+    int64_t u = 0;
+    for (int64_t n = a; n < b; ++n) u += attn_seq_units<KT>(p, attn_seq(p, (int)n));
+    sums[threadIdx.x] = u * p.Hk;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    constexpr int PER = THREADS / 32;
+    const int lane = threadIdx.x;
+    int64_t own = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) own += sums[lane * PER + i];
+    int64_t incl = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    const int64_t total = __shfl_sync(0xffffffffu, incl, 31);
+    // units < 2^31 key tiles x 2^16 sequences' items x heads: the products stay in 64 bits
+    const int64_t G = gridDim.x, c = blockIdx.x;
+    const int64_t each = total / G, more = total % G;
+    const int64_t u0 = each * c + (c < more ? c : more), count = each + (c < more ? 1 : 0);
+    if (lane == 0 && count == 0) *plan = AttnPlan{0, 0, p.N};
+    if (count > 0 && u0 >= incl - own && u0 < incl) {
+      int64_t at = u0 - (incl - own);
+      int i = lane * PER;
+      while (at >= sums[i]) at -= sums[i++];
+      *plan = AttnPlan{at, count, i * per};
+    }
+  }
+  __syncthreads();
+}
+
+// Hands out a CTA's pieces in order; one thread's.
+template <int KT>
+struct AttnWalk {
+  AttnSeq s;
+  int64_t left;
+  int n, kh, at, tile;
+  bool whole;  // no item is cut: those that begin in the stretch are taken to their ends
+
+  __device__ __forceinline__ void start(const AttnArgs& p, const AttnPlan& plan) {
+    left = plan.count;
+    whole = p.part_o == nullptr;
+    n = plan.n;
+    kh = at = tile = 0;
+    if (left <= 0) return;
+    int64_t u = plan.begin, head;
+    for (;;) {
+      s = attn_seq(p, n);
+      head = attn_seq_units<KT>(p, s);
+      if (u < head * p.Hk) break;
+      u -= head * p.Hk;
+      ++n;
+    }
+    kh = (int)(u / head);
+    u -= kh * head;
+    for (;; at += p.item) {
+      const int k = attn_units<KT>(p, s, at);
+      if (u < k) break;
+      u -= k;
+    }
+    tile = (int)u;
+    if (whole && tile > 0) {  // the CTA before takes it
+      left -= attn_units<KT>(p, s, at) - tile;
+      tile = 0;
+      step(p);
+    }
+  }
+  // to the next item
+  __device__ __forceinline__ void step(const AttnArgs& p) {
+    if (s.qn - at > p.item) {
+      at += p.item;
+      return;
+    }
+    at = 0;
+    if (++kh < p.Hk) return;
+    kh = 0;
+    if (left <= 0) return;  // (there may be no sequence behind the last)
+    do s = attn_seq(p, ++n);
+    while (s.qn == 0);
+  }
+  __device__ __forceinline__ AttnPiece next(const AttnArgs& p) {
+    AttnPiece w{};
+    if (left <= 0) return w;
+    const int units = attn_units<KT>(p, s, at);
+    const int take = whole || left >= units - tile ? units - tile : (int)left;
+    w.q0 = s.q0 + at;
+    w.tokens = s.qn - at < p.item ? s.qn - at : p.item;
+    w.kh = kh;
+    w.k0 = s.k0;
+    w.see = p.causal ? (int)((int64_t)s.kn - s.qn + at + 1) : s.kn;
+    const int seen = attn_sees(p, w, w.tokens - 1);
+    const int tiles = seen / KT + (seen % KT != 0);  // 0 where a unit stands for none
+    w.t0 = tile < tiles ? tile : tiles;
+    w.t1 = tile + take < tiles ? tile + take : tiles;
+    w.part = tile > 0 ? (tile + take == units ? kAttnLast : kAttnMiddle) : (take == units ? kAttnWhole : kAttnFirst);
+    left -= take;
+    tile += take;
+    if (tile == units) {
+      tile = 0;
+      step(p);
+    }
+    return w;
+  }
+};
+
+// A CTA's two places for parts: the one that its stretch begins with, and the
+// one that it ends with.
+__device__ __forceinline__ int attn_slot(int cta, int part) { return 2 * cta + (part == kAttnFirst ? 1 : 0); }
+
+// query head of member m of key head kh's group
+__device__ __forceinline__ int attn_head(const AttnArgs& p, int kh, int m) {
+  return p.map == GDN_MAP_TILED ? m * p.Hk + kh : kh * p.group + m;
+}
+
+// What a row has over other keys: whether there is anything, and its lse.
+struct AttnPrior {
+  bool any;
+  float lse;
+};
+__device__ __forceinline__ AttnPrior attn_prior(const AttnArgs& p, int64_t token, int head) {
+  if (p.prior_o == nullptr || token < p.prior_cu[0] || token >= p.prior_cu[p.prior_n]) return AttnPrior{false, 0.f};
+  return AttnPrior{true, p.prior_lse[token * p.Hq + head]};
+}
+
+// A row's outputs from the largest score (times scale and log2 e), the sum of
+// exponentials to it and the prior part: the factors of the unnormalised
+// outputs and of the prior ones, and the logarithm of the sum. A row that sees
+// nothing has a sum of 0; scores that are all NaN have no largest, but a sum
+// that is NaN.
+struct AttnScale {
+  float own, prior, lse;
+};
+__device__ __forceinline__ AttnScale attn_scale(float top, float sum, AttnPrior prior) {
+  float m = top, a = 0.f;
+  if (prior.any) {
+    a = prior.lse * kAttnLog2e;
+    m = fmaxf(top, a);
+  }
+  if (m == -INFINITY) m = 0.f;
+  const float w0 = exp2f(top - m), w1 = prior.any ? exp2f(a - m) : 0.f;
+  const float s = fmaf(sum, w0, w1);
+  if (s == 0.f) return AttnScale{0.f, 0.f, -INFINITY};
+  const float inv = 1.f / s;
+  return AttnScale{w0 * inv, w1 * inv, (m + log2f(s)) * kAttnLn2};
+}
+
+}  // namespace gdn

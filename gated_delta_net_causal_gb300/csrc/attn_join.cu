@@ -1,0 +1,150 @@
+// Puts the parts of softmax attention together, and chooses the kernels.
+//
+// attn_join_kernel: block (b, y) looks whether CTA b of the attention kernel
+// ended its stretch within an item; the parts of that item are then its last
+// one, those of the CTAs after it that had nothing else, and the first one of
+// the CTA that ended it. A warp takes a row: the largest score of the parts,
+// their factors, and the sum of the parts' outputs, always in CTA order.
+#include "attn_common.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kJWarps = 8;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kJWarps) attn_join_kernel(const AttnArgs p, int ctas) {
+  grid_dependency_wait();
+  const int b = blockIdx.x, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * kJWarps + (threadIdx.x >> 5);
+  const int4 at = p.part_at[2 * b + 1];
+  if (at.x != kAttnFirst || r >= at.z * p.group) return;
+  // the CTA that ends the item
+  int last = ctas;
+  for (int c = b + 1; c < ctas; c += 32) {
+    const bool end = c + lane < ctas && p.part_at[2 * (c + lane)].x == kAttnLast;
+    const unsigned any = __ballot_sync(0xffffffffu, end);
+    if (any != 0) {
+      last = c + __ffs(any) - 1;
+      break;
+    }
+  }
+  if (last == ctas) return;  // (an item that is begun is ended)
+  const int parts = last - b + 1;
+  const auto row_of = [&](int j) { return (int64_t)(j == 0 ? 2 * b + 1 : 2 * (b + j)) * p.part_rows + r; };
+  const int64_t token = at.y + r / p.group;
+  const int head = attn_head(p, at.w, r % p.group);
+  float top = -INFINITY;
+  for (int j = lane; j < parts; j += 32) top = fmaxf(top, p.part_ml[row_of(j)].x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float base = top == -INFINITY ? 0.f : top;
+  const bool holds = 4 * lane < D;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  for (int j0 = 0; j0 < parts; j0 += 32) {
+    float f = 0.f;
+    if (j0 + lane < parts) {
+      const float2 ml = p.part_ml[row_of(j0 + lane)];
+      f = exp2f(ml.x - base);
+      sum = fmaf(ml.y, f, sum);
+    }
+    const int n = parts - j0 < 32 ? parts - j0 : 32;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) {
+      const float w = __shfl_sync(0xffffffffu, f, j);
+      if (holds) {
+        const float4 x = *reinterpret_cast<const float4*>(p.part_o + row_of(j0 + j) * D + 4 * lane);
+        // (a part without keys has the factor 0 and zeros)
+        o.x = fmaf(w, x.x, o.x), o.y = fmaf(w, x.y, o.y), o.z = fmaf(w, x.z, o.z), o.w = fmaf(w, x.w, o.w);
+      }
+    }
+  }
+  sum = group_sum<32>(sum);
+  const AttnPrior prior = attn_prior(p, token, head);
+  const AttnScale f = attn_scale(top, sum, prior);
+  o = make_float4(o.x * f.own, o.y * f.own, o.z * f.own, o.w * f.own);
+  const int64_t to = (token * p.Hq + head) * D + 4 * lane;
+  if (holds) {
+    if (prior.any) {
+      const float4 x = *reinterpret_cast<const float4*>(p.prior_o + to);
+      o.x = fmaf(f.prior, x.x, o.x), o.y = fmaf(f.prior, x.y, o.y);
+      o.z = fmaf(f.prior, x.z, o.z), o.w = fmaf(f.prior, x.w, o.w);
+    }
+    if (p.core != nullptr) {
+      *reinterpret_cast<float4*>(p.core + to) = o;
+    } else {
+      T* y = static_cast<T*>(p.out) + to;
+      y[0] = from_f32<T>(o.x), y[1] = from_f32<T>(o.y), y[2] = from_f32<T>(o.z), y[3] = from_f32<T>(o.w);
+    }
+  }
+  if (lane == 0 && p.lse != nullptr) p.lse[token * p.Hq + head] = f.lse;
+}
+
+template <typename T, int D>
+cudaError_t join(const AttnArgs& p, int ctas, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)((p.part_rows + kJWarps - 1) / kJWarps));
+  cfg.blockDim = dim3(32 * kJWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];  // its launch overlaps the attention kernel's end
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D>, p, ctas);
+}
+template <typename T>
+cudaError_t join_dim(const AttnArgs& p, int32_t D, int ctas, cudaStream_t stream) {
+  switch (D) {
+    case 32: return join<T, 32>(p, ctas, stream);
+    case 64: return join<T, 64>(p, ctas, stream);
+    case 96: return join<T, 96>(p, ctas, stream);
+    default: return join<T, 128>(p, ctas, stream);
+  }
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 152;
+  return n;
+}
+
+int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+AttnSplit attn_split(int32_t dtype, int64_t T, int32_t group, int32_t D) {
+  AttnSplit s{};
+  s.ctas = attn_cc_ctas(sm_count());
+  s.item = attn_cc_rows() / group;
+  s.rows = (int32_t)(T < s.item ? T : s.item) * group;
+  const int64_t slots = 2ll * s.ctas;
+  s.ml_at = round256(slots * s.rows * D * 4);
+  s.at_at = s.ml_at + round256(slots * s.rows * 8);
+  s.bytes = s.at_at + round256(slots * 16);
+  return s;
+}
+
+cudaError_t launch_attn(AttnArgs p, const AttnSplit& s, void* workspace, int32_t dtype, int32_t D,
+                        cudaStream_t stream) {
+  p.item = s.item;
+  p.part_rows = s.rows;
+  char* ws = static_cast<char*>(workspace);
+  if (ws != nullptr) {
+    p.part_o = reinterpret_cast<float*>(ws);
+    p.part_ml = reinterpret_cast<float2*>(ws + s.ml_at);
+    p.part_at = reinterpret_cast<int4*>(ws + s.at_at);
+  }
+  const cudaError_t e = launch_attn_cc(p, dtype, D, s.ctas, stream);
+  if (e != cudaSuccess || ws == nullptr) return e;
+  switch (dtype) {
+    case GDN_F16: return join_dim<__half>(p, D, s.ctas, stream);
+    case GDN_BF16: return join_dim<__nv_bfloat16>(p, D, s.ctas, stream);
+    default: return join_dim<float>(p, D, s.ctas, stream);
+  }
+}
+
+}  // namespace gdn

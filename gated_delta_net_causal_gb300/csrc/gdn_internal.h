@@ -164,6 +164,68 @@ struct LinearFp8Args {
   int64_t y_stride;
 };
 
+// Rotary positions (rope.cu): rows of q, k and v are tokens, strides in elements.
+struct RopeArgs {
+  const int32_t* positions;
+  const int32_t* cache_rows;  // or null: the outputs' rows are the tokens
+  int32_t num_rows;           // of k_out and v_out
+  int64_t T;
+  const void* q;              // or null
+  int64_t q_stride;
+  void* q_out;
+  int64_t q_out_stride;
+  const void* k;              // or null
+  int64_t k_stride;
+  void* k_out;
+  int64_t k_out_stride;
+  const void* v;              // or null
+  int64_t v_stride;
+  void* v_out;
+  int64_t v_out_stride;
+  int32_t Hq, Hk, D;
+  int32_t inverse;
+  gdn_rope_table table;
+};
+
+// Softmax attention (attn_common.cuh): rows of q are tokens, rows of k and v
+// tokens too or a cache's, strides in elements.
+struct AttnArgs {
+  const void* q;
+  int64_t q_stride;
+  const void* k;
+  int64_t k_stride;
+  const void* v;
+  int64_t v_stride;
+  const int32_t* cu_seqlens;
+  int32_t N, T;             // T <= 2^31 - 1025
+  const int32_t* kv_start;  // null: the keys are the sequence's own rows
+  const int32_t* kv_len;
+  int32_t kv_rows;          // <= 2^31 - 1025
+  int32_t causal;           // 0: every token sees all of its sequence's keys
+  int32_t Hq, Hk, group, map;
+  float scale;
+  void* out;                // [T][Hq][D] io dtype
+  float* core;              // or, instead, fp32
+  float* lse;               // [T][Hq], or null
+  // outputs over other keys, joined with these (null: none), of the tokens
+  // from prior_cu[0] to prior_cu[prior_n]
+  const float* prior_o;     // [T][Hq][D]
+  const float* prior_lse;   // [T][Hq]
+  const int32_t* prior_cu;
+  int32_t prior_n;
+  // set by launch_attn
+  int32_t item;             // tokens of an item
+  int32_t part_rows;        // rows of a part
+  float* part_o;            // [2 CTAs][part_rows][D], null: no item is cut
+  float2* part_ml;          // [2 CTAs][part_rows]
+  int4* part_at;            // [2 CTAs] what the part is: AttnPiece's part, q0, tokens, kh
+};
+// How launch_attn cuts the work, and its workspace
+struct AttnSplit {
+  int32_t ctas, item, rows;
+  int64_t ml_at, at_at, bytes;
+};
+
 // Each launcher dispatches on (io dtype, head_dim) and returns the launch
 // status (cudaSuccess when everything was enqueued).
 cudaError_t launch_decode(const DecodeArgs& p, int32_t dtype, int32_t D, int32_t batch,
@@ -217,6 +279,16 @@ cudaError_t read_error_add_rmsnorm(int32_t* status, bool clear);
 cudaError_t read_error_decay_step(int32_t* status, bool clear);
 cudaError_t read_error_decay_scan(int32_t* status, bool clear);
 cudaError_t read_error_linear_fp8(int32_t* status, bool clear);
+cudaError_t launch_rope(const RopeArgs& p, int32_t dtype, cudaStream_t stream);
+cudaError_t read_error_rope(int32_t* status, bool clear);
+// attn_join.cu
+AttnSplit attn_split(int32_t dtype, int64_t T, int32_t group, int32_t D);
+cudaError_t launch_attn(AttnArgs p, const AttnSplit& s, void* workspace, int32_t dtype, int32_t D,
+                        cudaStream_t stream);
+// attn_cc.cu: rows of an item, CTAs
+int attn_cc_rows();
+int attn_cc_ctas(int sms);
+cudaError_t launch_attn_cc(const AttnArgs& p, int32_t dtype, int32_t D, int grid, cudaStream_t stream);
 // diag.cu: one warp's bounded wait on an mbarrier nothing arrives on
 cudaError_t launch_wait_timeout(uint64_t limit_ns, int32_t* gave_up, cudaStream_t stream);
 

@@ -94,7 +94,8 @@ const char* gdn_status_string(int32_t status);
 /* ABI version: major * 10000 + minor * 100 + patch. 0.3.0 added
  * gdn_decode_multi and gdn_decode_step_slots; 0.4.0 gdn_linear,
  * gdn_decode_layer and gdn_host_pointer; 0.5.0 gdn_decay_step,
- * gdn_decay_prefill, gdn_add_rmsnorm and gdn_linear_fp8. */
+ * gdn_decay_prefill, gdn_add_rmsnorm and gdn_linear_fp8; 0.6.0 gdn_rope,
+ * gdn_attn_prefill and gdn_attn_shared. */
 int32_t gdn_version(void);
 
 /* Channels of the packed pre-conv activation: C = 2*Hk*D + Hv*D, laid out
@@ -507,6 +508,170 @@ gdn_status gdn_decay_prefill(const gdn_dims* dims, int32_t num_seqs, const int32
 /* Bytes of workspace gdn_decay_prefill uses for these sizes (0: none). */
 gdn_status gdn_decay_prefill_workspace_size(const gdn_dims* dims, int32_t num_seqs,
                                             int64_t total_tokens, int64_t* bytes);
+
+/* Rotary layouts: the pairs of the first R = rotary_dim elements of a head are
+ * (i, i + R/2) or (2 i, 2 i + 1), i < R/2. */
+typedef enum gdn_rope_layout { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_layout;
+
+/* Frequencies f_i (radians a position) of the pairs, from
+ * b_i = base^(-2 i / R):
+ *   PLAIN   b_i
+ *   LINEAR  b_i / factor
+ *   BANDS   b_i (w + (1 - w) / factor), w = clamp((n_i - low) / (high - low), 0, 1)
+ *           with n_i = original_length b_i / (2 pi) turns over the original
+ *           length: what turns more often than high stays, what turns less
+ *           often than low is stretched
+ *   RAMP    the same with w = 1 - clamp((i - first) / (last - first), 0, 1),
+ *           first = max(floor(at(high)), 0), last = min(ceil(at(low)), R - 1),
+ *           last - first at least 0.001, at(n) = R ln(original_length /
+ *           (2 pi n)) / (2 ln base), the index whose pair makes n turns
+ */
+typedef enum gdn_rope_scaling {
+  GDN_ROPE_PLAIN = 0,
+  GDN_ROPE_LINEAR = 1,
+  GDN_ROPE_BANDS = 2,
+  GDN_ROPE_RAMP = 3
+} gdn_rope_scaling;
+
+/* A model's rotary positions, made once by gdn_rope_frequencies (host
+ * memory). step[i] is f_i as a fraction of a turn, 2^64 one turn. */
+typedef struct gdn_rope_table {
+  int32_t rotary_dim; /* R: even, 2..128 */
+  int32_t layout;     /* gdn_rope_layout */
+  float amplitude;    /* factor of the rotated elements */
+  int32_t reserved;   /* 0 */
+  uint64_t step[64];
+} gdn_rope_table;
+
+/*
+ * Fills *table. base > 1; factor > 0 (LINEAR, BANDS, RAMP);
+ * original_length > 0 and 0 < low < high (BANDS, RAMP); all of them and
+ * amplitude finite, else GDN_ERR_INVALID_ARG. What a scaling does not use is
+ * ignored.
+ */
+gdn_status gdn_rope_frequencies(int32_t rotary_dim, int32_t layout, double base, int32_t scaling,
+                                double factor, double original_length, double low, double high,
+                                double amplitude, gdn_rope_table* table);
+
+/* gdn_rope flags */
+enum {
+  GDN_ROPE_INVERSE = 1 /* rotates back (the sines negated, the amplitude as it
+                          is): the transposed map, so the gradient of the
+                          forward call */
+};
+
+/*
+ * Rotary positions of the queries and keys of a softmax attention layer, with
+ * its keys and values written to the rows of a cache where one is given. For
+ * pair i of a head's first R elements, at position p:
+ *     t = p f_i,  y1 = a (x1 cos t - x2 sin t),  y2 = a (x2 cos t + x1 sin t)
+ * and the other D - R elements are copied. p f_i is taken modulo a turn in
+ * integers, exactly, so far positions are as right as near ones. Computed in
+ * fp32, rounded once.
+ *
+ * dims         n_v_heads query heads (Hq), n_k_heads key and value heads (Hk),
+ *              head_dim, io_dtype; the rest is not used.
+ * tokens       0 <= T <= 2^31 - 65.
+ * positions    device int32 [T], any value.
+ * q, q_out     [T] rows of Hq D (strides in elements, at least the row, a
+ *              multiple of 16 bytes; slices of wider rows may be given), or
+ *              both NULL.
+ * k, k_out     [T] rows of Hk D, or both NULL. q or k is needed.
+ * v, v_out     rows of Hk D copied as they are, only with cache_rows; or both
+ *              NULL.
+ * cache_rows   device int32 [T] or NULL. Row of k_out and v_out that token t
+ *              goes to, of num_rows (0 <= num_rows <= 2^31 - 1); a negative
+ *              entry marks a padded token, whose key and value go nowhere; an
+ *              entry >= num_rows is treated the same and records
+ *              GDN_ERR_EXTENT in the device error word. Two tokens with the
+ *              same row are a caller error (either's elements end up there, no
+ *              fault). NULL: row t, num_rows is not used.
+ * q_out may be q and, without cache_rows, k_out may be k, with the same
+ * stride; no output may overlap anything else.
+ */
+gdn_status gdn_rope(const gdn_dims* dims, const gdn_rope_table* table, int64_t tokens,
+                    const int32_t* positions, const void* q, int64_t q_stride, void* q_out,
+                    int64_t q_out_stride, const void* k, int64_t k_stride, void* k_out,
+                    int64_t k_out_stride, const void* v, int64_t v_stride, void* v_out,
+                    int64_t v_out_stride, const int32_t* cache_rows, int64_t num_rows,
+                    int32_t flags, void* stream);
+
+/*
+ * Causal softmax attention with grouped heads over a packed batch of
+ * variable-length sequences: the layers that a hybrid model places between
+ * linear ones. Query head h reads key head kh (dims->map as for the V and K
+ * heads). Token i of the n new tokens of a sequence with m keys sees its keys
+ * s <= m - n + i:
+ *     w_s = softmax over the visible s of scale q . k_s     o = sum_s w_s v_s
+ *     lse = log sum_s exp(scale q . k_s)
+ * A token that sees no key has the output 0 and lse -inf.
+ *
+ * dims         n_v_heads query heads (Hq), n_k_heads key and value heads (Hk),
+ *              Hq / Hk <= 64, head_dim, map, io_dtype; the rest is not used.
+ * cu_seqlens   device int32 [N+1] as for gdn_conv_update: the new tokens; a
+ *              sequence may have none. Rows behind the last sequence are
+ *              neither read into results nor written.
+ * total_tokens 0 <= T <= 2^31 - 1025; num_seqs 0 <= N <= 65535.
+ * q            [T] rows of Hq D, q_stride apart (elements; at least the row, a
+ *              multiple of 16 bytes).
+ * k, v         [kv_rows] rows of Hk D, k_stride and v_stride apart;
+ *              0 <= kv_rows <= 2^31 - 1025.
+ * kv_start, kv_len  device int32 [N]: sequence n's keys are rows kv_start[n]
+ *              to kv_start[n] + kv_len[n] of k and v (a cache that already
+ *              holds those of the new tokens; sequences may share rows).
+ *              Values are clamped to the rows that there are. Both NULL: a
+ *              sequence's keys are its tokens' own rows, kv_rows must be T.
+ * scale        finite, > 0.
+ * out          [T][Hq][D] io dtype;  lse [T][Hq] fp32 or NULL.
+ * workspace    device scratch of at least gdn_attn_prefill_workspace_size
+ *              bytes, 256-byte aligned, not overlapping any other argument;
+ *              contents irrelevant. NULL: no sequence's keys are split over
+ *              several CTAs (slow for few tokens and long caches). Two calls
+ *              that may run at the same time, replayed graphs among them, need
+ *              one each.
+ *
+ * f16 and bf16 run on the tensor cores, with fp32 scores, sums and outputs
+ * and the weights rounded to io dtype (their sum is taken before that); f32
+ * on the fp32 units. What is not finite in a key or value reaches only tokens
+ * that see it.
+ */
+gdn_status gdn_attn_prefill(const gdn_dims* dims, int32_t num_seqs, const int32_t* cu_seqlens,
+                            int64_t total_tokens, const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, const void* v, int64_t v_stride, int64_t kv_rows,
+                            const int32_t* kv_start, const int32_t* kv_len, float scale,
+                            void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                            void* stream);
+
+/* Bytes of workspace gdn_attn_prefill uses for these sizes. */
+gdn_status gdn_attn_prefill_workspace_size(const gdn_dims* dims, int32_t num_seqs,
+                                           int64_t total_tokens, int64_t* bytes);
+
+/*
+ * gdn_attn_prefill for a batch in which groups of neighbouring tokens share a
+ * prefix: every token sees all keys of its group's prefix and, causally, its
+ * sequence's own. The prefix is read once for all query rows of its group.
+ *
+ * num_groups   0 <= N_g <= 65535.
+ * group_cu     device int32 [N_g + 1], non-decreasing: group j is the tokens
+ *              group_cu[j] to group_cu[j + 1] (values are clamped as
+ *              cu_seqlens'); tokens outside of all groups have no prefix.
+ * prefix_start, prefix_len  device int32 [N_g]: its prefix is these rows of k
+ *              and v.
+ * kv_start, kv_len  are needed. workspace as for gdn_attn_prefill, but
+ *              needed, of gdn_attn_shared_workspace_size bytes.
+ */
+gdn_status gdn_attn_shared(const gdn_dims* dims, int32_t num_seqs, const int32_t* cu_seqlens,
+                           int64_t total_tokens, const void* q, int64_t q_stride, const void* k,
+                           int64_t k_stride, const void* v, int64_t v_stride, int64_t kv_rows,
+                           const int32_t* kv_start, const int32_t* kv_len, int32_t num_groups,
+                           const int32_t* group_cu, const int32_t* prefix_start,
+                           const int32_t* prefix_len, float scale, void* out, float* lse,
+                           void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace gdn_attn_shared needs for these sizes. */
+gdn_status gdn_attn_shared_workspace_size(const gdn_dims* dims, int32_t num_seqs,
+                                          int64_t total_tokens, int32_t num_groups,
+                                          int64_t* bytes);
 
 /*
  * Residual addition, RMSNorm and 8-bit quantisation of rows, in one pass:
