@@ -1181,7 +1181,8 @@ gdn_status gdn_device_error(int32_t* status, int32_t clear) {
                                                gdn::read_error_linear, gdn::read_error_decay_step,
                                                gdn::read_error_decay_scan, gdn::read_error_decay_tc,
                                                gdn::read_error_linear_fp8,
-                                               gdn::read_error_add_rmsnorm, gdn::read_error_rope};
+                                               gdn::read_error_add_rmsnorm, gdn::read_error_rope,
+                                               gdn::read_error_attn_tc};
   for (auto rd : readers) {
     int32_t v = 0;
     if (rd(&v, clear != 0) != cudaSuccess) return GDN_ERR_CUDA;

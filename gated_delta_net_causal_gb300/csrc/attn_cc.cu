@@ -1,4 +1,4 @@
-// Softmax attention on the fp32 units: rows x keys in tiles of 64 x 64, one
+// Softmax attention on the fp32 units (f32): rows x keys in tiles of 64 x 64, one
 // pass over the keys with the running maximum and sum of each row.
 //
 // A CTA of 256 threads is a grid of 16 x 16; a thread has 4 x 4 scores (rows
@@ -22,17 +22,15 @@ struct CcSmem {
   static constexpr int kK = D * kAP, kV = kK + (D > kAK ? D : kAK) * kAP, kEnd = kV + kAK * D;
 };
 
-template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, float (&x)[VEC]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const T* e = reinterpret_cast<const T*>(&u);
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) x[i] = to_f32(e[i]);
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+// four elements of a row, into a column of a transposed tile
+__device__ __forceinline__ void put(float* t, float4 x) {
+  t[0] = x.x, t[kAP] = x.y, t[2 * kAP] = x.z, t[3 * kAP] = x.w;
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kAT, 2) attn_cc_kernel(const AttnArgs p) {
-  constexpr int VEC = 16 / (int)sizeof(T), NP = D / 32;  // NP pairs of output columns a thread
+  constexpr int NP = D / 32;  // pairs of output columns a thread
   extern __shared__ __align__(16) float sm[];
   float* qt = sm;                  // [D][kAP]
   float* kt = sm + CcSmem<D>::kK;  // [D][kAP], then the weights [kAK][kAP]
@@ -45,9 +43,9 @@ __global__ void __launch_bounds__(kAT, 2) attn_cc_kernel(const AttnArgs p) {
   if (tid < 2 && p.part_o != nullptr) p.part_at[2 * blockIdx.x + tid] = make_int4(kAttnWhole, 0, 0, 0);
   AttnWalk<kAK> walk;
   if (tid == 0) walk.start(p, plan);
-  const T* gq = static_cast<const T*>(p.q);
-  const T* gk = static_cast<const T*>(p.k);
-  const T* gv = static_cast<const T*>(p.v);
+  const float* gq = static_cast<const float*>(p.q);
+  const float* gk = static_cast<const float*>(p.k);
+  const float* gv = static_cast<const float*>(p.v);
   const float sc = p.scale * kAttnLog2e;
 
   for (;;) {
@@ -58,15 +56,12 @@ __global__ void __launch_bounds__(kAT, 2) attn_cc_kernel(const AttnArgs p) {
     if (w.tokens == 0) break;
     const int rows = w.tokens * p.group;
     // q, transposed: thread = row, chunks of 16 bytes
-    for (int u = tid; u < kAR * (D / VEC); u += kAT) {
-      const int r = u % kAR, c = u / kAR * VEC;
-      float x[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) x[e] = 0.f;
+    for (int u = tid; u < kAR * (D / 4); u += kAT) {
+      const int r = u % kAR, c = u / kAR * 4;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows)
-        load_vec<T, VEC>(gq + (int64_t)(w.q0 + r / p.group) * p.q_stride + attn_head(p, w.kh, r % p.group) * D + c, x);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) qt[(c + e) * kAP + r] = x[e];
+        x = load4(gq + (int64_t)(w.q0 + r / p.group) * p.q_stride + attn_head(p, w.kh, r % p.group) * D + c);
+      put(qt + c * kAP + r, x);
     }
     int sees[4];
     float top[4], sum[4];
@@ -84,21 +79,16 @@ __global__ void __launch_bounds__(kAT, 2) attn_cc_kernel(const AttnArgs p) {
     for (int t = w.t0; t < w.t1; ++t) {
       const int first = t * kAK, n = most - first < kAK ? most - first : kAK;
       __syncthreads();
-      for (int u = tid; u < kAK * (D / VEC); u += kAT) {
-        const int r = u % kAK, c = u / kAK * VEC;
-        float x[VEC], y[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) x[e] = y[e] = 0.f;
+      for (int u = tid; u < kAK * (D / 4); u += kAT) {
+        const int r = u % kAK, c = u / kAK * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
         if (r < n) {
           const int64_t row = (int64_t)w.k0 + first + r;
-          load_vec<T, VEC>(gk + row * p.k_stride + w.kh * D + c, x);
-          load_vec<T, VEC>(gv + row * p.v_stride + w.kh * D + c, y);
+          x = load4(gk + row * p.k_stride + w.kh * D + c);
+          y = load4(gv + row * p.v_stride + w.kh * D + c);
         }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) kt[(c + e) * kAP + r] = x[e];
-#pragma unroll
-        for (int e = 0; e < VEC; e += 4)
-          *reinterpret_cast<float4*>(vs + r * D + c + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+        put(kt + c * kAP + r, x);
+        *reinterpret_cast<float4*>(vs + r * D + c) = y;
       }
       __syncthreads();
       float s[4][4];
@@ -199,12 +189,7 @@ __global__ void __launch_bounds__(kAT, 2) attn_cc_kernel(const AttnArgs p) {
           const float2 b = *reinterpret_cast<const float2*>(p.prior_o + at + c);
           y = fma2(make_float2(f.prior, f.prior), b, y);
         }
-        if (p.core != nullptr) {
-          *reinterpret_cast<float2*>(p.core + at + c) = y;
-        } else {
-          static_cast<T*>(p.out)[at + c] = from_f32<T>(y.x);
-          static_cast<T*>(p.out)[at + c + 1] = from_f32<T>(y.y);
-        }
+        *reinterpret_cast<float2*>((p.core != nullptr ? p.core : static_cast<float*>(p.out)) + at + c) = y;
       }
       if (tx == 0 && p.lse != nullptr) p.lse[token * p.Hq + head] = f.lse;
     }
@@ -213,34 +198,25 @@ __global__ void __launch_bounds__(kAT, 2) attn_cc_kernel(const AttnArgs p) {
   }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t run(const AttnArgs& p, int grid, cudaStream_t stream) {
   constexpr int smem = CcSmem<D>::kEnd * 4;
-  const cudaError_t e = cudaFuncSetAttribute(attn_cc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = cudaFuncSetAttribute(attn_cc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  attn_cc_kernel<T, D><<<grid, kAT, smem, stream>>>(p);
+  attn_cc_kernel<D><<<grid, kAT, smem, stream>>>(p);
   return cudaGetLastError();
 }
-template <typename T>
-cudaError_t run_dim(const AttnArgs& p, int32_t D, int grid, cudaStream_t stream) {
-  switch (D) {
-    case 32: return run<T, 32>(p, grid, stream);
-    case 64: return run<T, 64>(p, grid, stream);
-    case 96: return run<T, 96>(p, grid, stream);
-    default: return run<T, 128>(p, grid, stream);
-  }
-}
-
 }  // namespace
 
 int attn_cc_rows() { return kAR; }
 int attn_cc_ctas(int sms) { return 2 * sms; }
 
-cudaError_t launch_attn_cc(const AttnArgs& p, int32_t dtype, int32_t D, int grid, cudaStream_t stream) {
-  switch (dtype) {
-    case GDN_F16: return run_dim<__half>(p, D, grid, stream);
-    case GDN_BF16: return run_dim<__nv_bfloat16>(p, D, grid, stream);
-    default: return run_dim<float>(p, D, grid, stream);
+cudaError_t launch_attn_cc(const AttnArgs& p, int32_t D, int grid, cudaStream_t stream) {
+  switch (D) {
+    case 32: return run<32>(p, grid, stream);
+    case 64: return run<64>(p, grid, stream);
+    case 96: return run<96>(p, grid, stream);
+    default: return run<128>(p, grid, stream);
   }
 }
 

@@ -118,8 +118,13 @@ int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
 
 AttnSplit attn_split(int32_t dtype, int64_t T, int32_t group, int32_t D) {
   AttnSplit s{};
-  s.ctas = attn_cc_ctas(sm_count());
-  s.item = attn_cc_rows() / group;
+  if (dtype == GDN_F32) {
+    s.ctas = attn_cc_ctas(sm_count());
+    s.item = attn_cc_rows() / group;
+  } else {
+    s.ctas = sm_count();
+    s.item = 2 * (attn_tc_rows() / group);
+  }
   s.rows = (int32_t)(T < s.item ? T : s.item) * group;
   const int64_t slots = 2ll * s.ctas;
   s.ml_at = round256(slots * s.rows * D * 4);
@@ -138,7 +143,8 @@ cudaError_t launch_attn(AttnArgs p, const AttnSplit& s, void* workspace, int32_t
     p.part_ml = reinterpret_cast<float2*>(ws + s.ml_at);
     p.part_at = reinterpret_cast<int4*>(ws + s.at_at);
   }
-  const cudaError_t e = launch_attn_cc(p, dtype, D, s.ctas, stream);
+  const cudaError_t e = dtype == GDN_F32 ? launch_attn_cc(p, D, s.ctas, stream)
+                                         : launch_attn_tc(p, dtype, D, s.ctas, stream);
   if (e != cudaSuccess || ws == nullptr) return e;
   switch (dtype) {
     case GDN_F16: return join_dim<__half>(p, D, s.ctas, stream);

@@ -1,0 +1,637 @@
+// Softmax attention on the 5th-generation tensor cores (f16, bf16).
+//
+// An item is two tiles of 128 rows (token, query head of the group), A and B,
+// that share the keys' tiles of 128: two chains of
+//   S = Q K^T        both from shared memory, fp32 into TMEM
+//   P = exp2(S scale log2 e - M)     a thread per row, into S's place, 16 bits
+//   O += P V         P from TMEM, V read transposed, fp32 in TMEM
+// so that one tile's softmax runs under the other's products. A row lies in a
+// lane of TMEM, so its maximum and sum are one thread's and need no exchange.
+// M follows the row's maximum only where that has grown by more than 8 (in
+// log2) since: then the row's O and sum are rescaled, which is rare; else the
+// weights are up to 2^8, as exact as below 1. The sum is of the weights before
+// their rounding to 16 bits.
+//
+// Warps 0 to 3 are A's rows, 4 to 7 B's; one warp issues the products, one
+// loads (Q once an item, K and V through a ring of tiles), one hands out the
+// pieces of work (attn_common.cuh), one looks through masked tiles of V: a
+// masked weight is 0, but 0 times what is not finite would reach rows that do
+// not see it. So rows of V that nobody sees become 0, and in rows that only
+// some see what is not finite is replaced by 0 and added, at the end, to the
+// rows that do see it.
+//
+// A wait that gives up raises the CTA's abort flag; every role then leaves its
+// loop at once.
+#include <cuda.h>
+
+#include "attn_common.cuh"
+#include "tc_common.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kBR = 128;          // rows of a tile
+constexpr int kBK = 128;          // keys of a tile
+constexpr int kBThreads = 384;
+constexpr int kBMma = 8, kBLoad = 9, kBPlan = 10, kBCheck = 11;  // warps
+constexpr int kBRing = 4;         // pieces handed out ahead
+constexpr int kBTakers = 11;      // warps that take each piece
+constexpr float kBGrow = 8.f;     // log2 by which a weight may exceed 1
+
+template <int D>
+struct TcGeom {
+  static constexpr int kBoxes = (D + 63) / 64;
+  static constexpr uint32_t kTile = kBoxes * kBK * 128;  // bytes
+  static constexpr int kStages = kBoxes == 2 ? 5 : 8;
+  static constexpr uint32_t kSmem = (2 + kStages) * kTile;
+};
+
+// TMEM columns: S (P in its first half) and O of both tiles
+constexpr uint32_t kColS = 0, kColO = 256, kCols = 512;
+
+struct BShared {
+  uint64_t kv_full[8], kv_empty[8], v_ok[8];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_full[2];
+  uint64_t piece_full[kBRing], piece_empty[kBRing];
+  AttnPiece piece[kBRing];
+  AttnPlan plan;
+  int abort;
+  uint32_t tmem;
+};
+
+// the tile [k][mn] of 16-bit elements with k as the contraction (MN-major,
+// 128-byte swizzle), boxes of 64 mn columns kTile / kBoxes apart; 16 of k
+// advance it by 2048 bytes
+__device__ __forceinline__ uint64_t sdesc_v(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr & 0x3FFFF) >> 4);
+  d |= (uint64_t)((kBK * 128) >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+constexpr uint32_t kTransB = 1u << 16;
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <typename T>
+struct Half;
+template <>
+struct Half<__nv_bfloat16> {
+  static constexpr uint32_t kFormat = tc::kBF16;
+  static constexpr uint32_t kExponent = 0x7f807f80u, kCarry = 0x00800080u;
+  // log2 that the weights are scaled by
+  static constexpr float kLift = 0.f;
+  __device__ __forceinline__ static uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+};
+template <>
+struct Half<__half> {
+  static constexpr uint32_t kFormat = tc::kF16;
+  static constexpr uint32_t kExponent = 0x7c007c00u, kCarry = 0x04000400u;
+  // fp16's smallest normal weight would be 2^-14: 2^7 of its range above 2^8
+  // is moved below
+  static constexpr float kLift = 7.f;
+  __device__ __forceinline__ static uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+};
+
+// Tiles of keys that half h (A or B) of the piece has, from t0 on.
+__device__ __forceinline__ int half_tiles(const AttnArgs& p, const AttnPiece& w, int h) {
+  const int tokens = p.item / 2, first = h * tokens;
+  if (first >= w.tokens) return 0;
+  const int last = (first + tokens < w.tokens ? first + tokens : w.tokens) - 1;
+  const int seen = attn_sees(p, w, last);
+  int end = seen / kBK + (seen % kBK != 0);
+  end = end < w.t1 ? end : w.t1;
+  return end > w.t0 ? end - w.t0 : 0;
+}
+// Whether some row of the item does not see all of the tile.
+__device__ __forceinline__ bool masked_tile(int least, int t) { return (int64_t)(t + 1) * kBK > least; }
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kBThreads, 1)
+    attn_tc_kernel(const AttnArgs p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v) {
+  using G = TcGeom<D>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned char* ring = sm + 2 * G::kTile;
+  __shared__ BShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (warp == kBMma) {
+    tc::tmem_alloc(&sh.tmem, kCols);
+    tc::tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < G::kStages; ++i) {
+      mbar_init(&sh.kv_full[i], 1);
+      mbar_init(&sh.kv_empty[i], 1);
+      mbar_init(&sh.v_ok[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_ready[i][0], 4);
+      mbar_init(&sh.p_ready[i][1], 4);
+      mbar_init(&sh.o_full[i], 1);
+    }
+    for (int i = 0; i < kBRing; ++i) {
+      mbar_init(&sh.piece_full[i], 1);
+      mbar_init(&sh.piece_empty[i], kBTakers);
+    }
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (tid < 2 && p.part_o != nullptr) p.part_at[2 * blockIdx.x + tid] = make_int4(kAttnWhole, 0, 0, 0);
+  attn_plan<kBK, kBThreads>(p, reinterpret_cast<int64_t*>(ring), &sh.plan);  // (the ring is not in use yet)
+  fence_proxy_async_smem();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tb = sh.tmem;
+  volatile int* abort_flag = &sh.abort;
+  const auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, abort_flag); };
+  // piece i of the CTA, for a whole warp; false: there is none
+  const auto take = [&](int i, AttnPiece* w) {
+    const bool ok = wait(&sh.piece_full[i % kBRing], (i / kBRing) & 1);
+    *w = sh.piece[i % kBRing];
+    return __all_sync(0xffffffffu, ok) && w->tokens != 0;
+  };
+  const auto give = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.piece_empty[i % kBRing]);
+  };
+
+  // The softmax holds a row of scores in registers. Of the 168 a thread that
+  // the block has, 384 x 168 = 64512, two groups of 128 threads take 208 and
+  // one keeps 80: 63488.
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == kBPlan) {
+      // -------------------------------------------------------------- pieces
+      if (lane == 0) {
+        AttnWalk<kBK> walk;
+        walk.start(p, sh.plan);
+        for (int i = 0;; ++i) {
+          if (i >= kBRing && !wait(&sh.piece_empty[i % kBRing], (i / kBRing - 1) & 1)) break;
+          const AttnPiece w = walk.next(p);
+          sh.piece[i % kBRing] = w;
+          mbar_arrive(&sh.piece_full[i % kBRing]);
+          if (w.tokens == 0) break;
+        }
+      }
+    } else if (warp == kBLoad) {
+      // --------------------------------------------------------------- loads
+      uint32_t n_kv = 0, n_q[2] = {0, 0};
+      const uint32_t q_bytes = (uint32_t)(G::kBoxes * 128 * (p.item / 2) * p.group);
+      bool ok = true;
+      for (int i = 0;; ++i) {
+        AttnPiece w;
+        if (!take(i, &w)) break;
+        if (lane == 0 && ok) {
+          const auto load_kv = [&](const CUtensorMap* map, int t) {
+            const uint32_t st = n_kv % G::kStages, round = n_kv / G::kStages;
+            ok = ok && (round == 0 || wait(&sh.kv_empty[st], (round - 1) & 1));
+            if (!ok) return;
+            ++n_kv;
+            mbar_arrive_expect_tx(&sh.kv_full[st], G::kTile);
+            for (int b = 0; b < G::kBoxes; ++b)
+              tma_load_3d(ring + st * G::kTile + b * kBK * 128, map, 64 * b, w.kh, w.k0 + t * kBK, &sh.kv_full[st]);
+          };
+          for (int h = 0; h < 2; ++h) {
+            if (half_tiles(p, w, h) == 0) continue;
+            ok = ok && (n_q[h] == 0 || wait(&sh.q_empty[h], (n_q[h] - 1) & 1));
+            if (!ok) break;
+            ++n_q[h];
+            mbar_arrive_expect_tx(&sh.q_full[h], q_bytes);
+            for (int b = 0; b < G::kBoxes; ++b)
+              tma_load_4d(sm + h * G::kTile + b * kBR * 128, &tm_q, 64 * b, 0, w.kh, w.q0 + h * (p.item / 2),
+                          &sh.q_full[h]);
+            if (h == 0) load_kv(&tm_k, w.t0);  // before B's rows
+          }
+          for (int t = w.t0; ok && t < w.t1; ++t) {
+            if (t > w.t0 || half_tiles(p, w, 0) == 0) load_kv(&tm_k, t);
+            load_kv(&tm_v, t);
+          }
+        }
+        give(i);
+      }
+      if (lane == 0) {
+        // nothing may be in flight when the CTA ends: neither a copy nor the
+        // arrival that gives a tile back
+        for (uint32_t u = n_kv > G::kStages ? n_kv - G::kStages : 0; u < n_kv; ++u) {
+          mbar_wait(&sh.kv_full[u % G::kStages], (u / G::kStages) & 1);
+          wait(&sh.kv_empty[u % G::kStages], (u / G::kStages) & 1);
+        }
+        for (int h = 0; h < 2; ++h)
+          if (n_q[h] > 0) {
+            mbar_wait(&sh.q_full[h], (n_q[h] - 1) & 1);
+            wait(&sh.q_empty[h], (n_q[h] - 1) & 1);
+          }
+      }
+    } else if (warp == kBMma) {
+      // ------------------------------------------------------------ products
+      const uint32_t id_s = tc::idesc(Half<T>::kFormat, kBR, kBK), id_o = tc::idesc(Half<T>::kFormat, kBR, D) | kTransB;
+      uint32_t n_kv = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0}, ok_bits = 0;
+      bool ok = true;
+      for (int i = 0;; ++i) {
+        AttnPiece w;
+        if (!take(i, &w)) break;
+        if (lane == 0 && ok) {
+          const int least = attn_sees(p, w, 0), n[2] = {half_tiles(p, w, 0), half_tiles(p, w, 1)};
+          const int tiles = w.t1 - w.t0;
+          const auto scores = [&](int h, uint32_t st, bool last) {
+            const uint64_t dq = tc::sdesc_sw128(smem_u32(sm + h * G::kTile));
+            const uint64_t dk = tc::sdesc_sw128(smem_u32(ring + st * G::kTile));
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+              tc::mma_f16(tb + kColS + 128 * h, tc::sdesc_at(dq, kBR, s), tc::sdesc_at(dk, kBK, s), id_s, s > 0);
+            tc::mma_commit(&sh.s_full[h]);
+            if (last) tc::mma_commit(&sh.q_empty[h]);
+          };
+          // the stage of the next tile of the ring, once it is there
+          const auto next_tile = [&]() {
+            const uint32_t st = n_kv % G::kStages;
+            ok = ok && wait(&sh.kv_full[st], (n_kv / G::kStages) & 1);
+            ++n_kv;
+            return st;
+          };
+          if (tiles > 0) {
+            uint32_t st = next_tile();
+            for (int h = 0; ok && h < 2; ++h)
+              if (n[h] > 0) {
+                ok = ok && wait(&sh.q_full[h], n_q[h] & 1);
+                ++n_q[h];
+                if (ok) scores(h, st, n[h] == 1);
+              }
+            if (ok) tc::mma_commit(&sh.kv_empty[st]);
+            for (int j = 0; ok && j < tiles; ++j) {
+              const uint32_t sv = next_tile();
+              if (masked_tile(least, w.t0 + j)) {
+                ok = ok && wait(&sh.v_ok[sv], (ok_bits >> sv) & 1);
+                ok_bits ^= 1u << sv;
+              }
+              uint32_t sk = 0;
+              bool have_k = false;
+              for (int h = 0; ok && h < 2; ++h) {
+                if (j >= n[h]) continue;
+                const uint64_t dv = sdesc_v(smem_u32(ring + sv * G::kTile));
+                for (int half = 0; ok && half < 2; ++half) {
+                  ok = wait(&sh.p_ready[h][half], n_p[h] & 1);
+                  tc::fence_after_sync();
+                  if (ok)
+#pragma unroll
+                    for (int s = 4 * half; s < 4 * half + 4; ++s)
+                      tc::mma_f16_ts(tb + kColO + 128 * h, tb + kColS + 128 * h + 8 * s, dv + (uint64_t)(s * 2048 >> 4),
+                                     id_o, j > 0 || s > 0);
+                }
+                ++n_p[h];
+                if (!ok) break;
+                if (j + 1 < n[h]) {
+                  if (!have_k) {
+                    sk = next_tile();
+                    have_k = true;
+                  }
+                  if (ok) scores(h, sk, j + 2 == n[h]);
+                } else {
+                  tc::mma_commit(&sh.o_full[h]);
+                }
+              }
+              if (ok) tc::mma_commit(&sh.kv_empty[sv]);
+              if (ok && have_k) tc::mma_commit(&sh.kv_empty[sk]);
+            }
+          }
+        }
+        give(i);
+      }
+    } else if (warp == kBCheck) {
+      // ------------------------------------------------- masked tiles of v
+      uint32_t n_kv = 0;
+      for (int i = 0;; ++i) {
+        AttnPiece w;
+        if (!take(i, &w)) break;
+        const int least = attn_sees(p, w, 0), most = attn_sees(p, w, w.tokens - 1);
+        for (int t = w.t0; t < w.t1; ++t) {
+          // (the order in which they are loaded: every phase is waited for)
+          wait(&sh.kv_full[n_kv % G::kStages], (n_kv / G::kStages) & 1);
+          ++n_kv;
+          const uint32_t st = n_kv % G::kStages;
+          wait(&sh.kv_full[st], (n_kv / G::kStages) & 1);
+          ++n_kv;
+          if (__any_sync(0xffffffffu, *abort_flag)) break;
+          if (!masked_tile(least, t)) continue;
+          unsigned char* v = ring + st * G::kTile;
+          const int base = t * kBK, from = least > base ? least - base : 0;  // rows from which some row sees no more
+          bool hit = false;
+          for (int u = from * (8 * G::kBoxes) + lane; u < kBK * 8 * G::kBoxes; u += 32) {
+            const int row = u / (8 * G::kBoxes), c16 = u % (8 * G::kBoxes);
+            const int off = (c16 >> 3) * kBK * 128 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4);
+            uint4* at = reinterpret_cast<uint4*>(v + off);
+            if (row >= most - base) {
+              *at = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint4 x = *at;
+            uint32_t* e = &x.x;
+            bool here = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t m = ((e[j] & Half<T>::kExponent) + Half<T>::kCarry) & 0x80008000u;
+              if (m != 0) {
+                here = true;
+                if (m & 0x8000u) e[j] &= 0xffff0000u;
+                if (m & 0x80000000u) e[j] &= 0x0000ffffu;
+              }
+            }
+            if (here) *at = x;
+            hit |= here;
+          }
+          if (hit) sh.piece[i % kBRing].bad = 1;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.v_ok[st]);
+        }
+        give(i);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ------------------------------------------------------------- softmax
+    const int h = warp >> 2, qd = warp & 3, row = 32 * qd + lane;
+    const uint32_t ts = tb + ((uint32_t)(32 * qd) << 16) + kColS + 128 * h;
+    const uint32_t to = tb + ((uint32_t)(32 * qd) << 16) + kColO + 128 * h;
+    const float sc = p.scale * kAttnLog2e;
+    uint32_t n_s = 0, n_o = 0;
+    bool alive = true;
+    for (int i = 0;; ++i) {
+      AttnPiece w;
+      if (!take(i, &w)) break;
+      const int half = p.item / 2, at = h * half + row / p.group;  // token of the item
+      const bool valid = row < half * p.group && at < w.tokens;
+      const int sees = valid ? attn_sees(p, w, at) : 0;
+      const int n = half_tiles(p, w, h);
+      const bool some = __any_sync(0xffffffffu, valid);
+      const int least = (int)__reduce_min_sync(0xffffffffu, valid ? (unsigned)sees : 0x7fffffffu);
+      float M = -INFINITY;  // largest score so far, times scale log2 e (or a little less)
+      float2 sum = make_float2(0.f, 0.f);
+      for (int j = 0; j < n; ++j) {
+        alive = __all_sync(0xffffffffu, wait(&sh.s_full[h], n_s & 1));
+        if (!alive) break;
+        ++n_s;
+        tc::fence_after_sync();
+        if (!some) {  // no row of this warp counts
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sh.p_ready[h][0]);
+            mbar_arrive(&sh.p_ready[h][1]);
+          }
+          continue;
+        }
+        float s[kBK];
+#pragma unroll
+        for (int c = 0; c < kBK; c += 32) tmem_ld32(ts + c, s + c);
+        tc::tmem_wait_ld();
+        const int t = w.t0 + j;
+        if (masked_tile(least, t)) {
+          const int lim = sees - t * kBK;
+#pragma unroll
+          for (int c = 0; c < kBK; ++c)
+            if (c >= lim) s[c] = -INFINITY;
+        }
+        float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < kBK; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top[e] = fmaxf(fmaxf(top[e], s[c + e]), c + 4 + e < kBK ? s[c + 4 + e] : top[e]);
+        const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
+        if (j == 0) {
+          M = high;
+        } else {
+          const bool grow = high - M > kBGrow;
+          if (__any_sync(0xffffffffu, grow)) {
+            // (the products before these scores, and with them O, are complete)
+            const float f = grow ? exp2_fast(M - high) : 1.f;
+            if (grow) M = high;
+            sum = make_float2(sum.x * f, sum.y * f);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              float o[16];
+              tc::tmem_ld16(to + c, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= f;
+              tc::tmem_st16(to + c, o);
+            }
+          }
+        }
+        const float base = M == -INFINITY ? 0.f : Half<T>::kLift - M;
+        const float2 sc2 = make_float2(sc, sc), base2 = make_float2(base, base), one = make_float2(1.f, 1.f);
+#pragma unroll
+        for (int c = 0; c < kBK; c += 32) {
+          uint32_t r[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float2 x = fma2(make_float2(s[c + 2 * e], s[c + 2 * e + 1]), sc2, base2);
+            x.x = exp2_fast(x.x);
+            x.y = exp2_fast(x.y);
+            sum = fma2(x, one, sum);
+            r[e] = Half<T>::pack(x.x, x.y);
+          }
+          tc::tmem_st16u(ts + c / 2, r);
+          if (c == 32 || c == 96) {
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_ready[h][c / 64]);
+          }
+        }
+      }
+      // ---- the outputs
+      if (n > 0) {
+        alive = alive && __all_sync(0xffffffffu, wait(&sh.o_full[h], n_o & 1));
+        if (!alive) break;
+        ++n_o;
+        tc::fence_after_sync();
+      }
+      if (some) {
+        const float l = sum.x + sum.y, top = M - (M == -INFINITY ? 0.f : Half<T>::kLift);
+        const bool bad = *(volatile int*)&sh.piece[i % kBRing].bad != 0;
+        const int item_least = attn_sees(p, w, 0);
+        int64_t to_row = 0;
+        AttnScale f{1.f, 0.f, 0.f};
+        AttnPrior prior{false, 0.f};
+        if (valid) {
+          const int64_t token = w.q0 + at;
+          const int head = attn_head(p, w.kh, row % p.group);
+          if (w.part != kAttnWhole) {
+            const int64_t slot = attn_slot(blockIdx.x, w.part);
+            const int64_t slot_row = slot * p.part_rows + at * p.group + row % p.group;
+            p.part_ml[slot_row] = make_float2(top, l);
+            to_row = slot_row * D;
+          } else {
+            prior = attn_prior(p, token, head);
+            f = attn_scale(top, l, prior);
+            to_row = (token * p.Hq + head) * D;
+            if (p.lse != nullptr) p.lse[token * p.Hq + head] = f.lse;
+          }
+        }
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
+          if (n > 0) {
+            tc::tmem_ld16(to + c, o);
+            tc::tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = 0.f;
+          }
+          if (!valid) continue;
+          if (bad) {
+            const T* v = static_cast<const T*>(p.v) + (int64_t)w.kh * D + c;
+            const int first = max(item_least, w.t0 * kBK), last = (int)min((int64_t)sees, (int64_t)w.t1 * kBK);
+            for (int k = first; k < last; ++k)
+              for (int e = 0; e < 16; ++e) {
+                const float x = to_f32(v[(int64_t)(w.k0 + k) * p.v_stride + e]);
+                if (!isfinite(x)) {
+#pragma unroll
+                  for (int g = 0; g < 16; ++g)
+                    if (g == e) o[g] += x;
+                }
+              }
+          }
+          if (w.part != kAttnWhole || p.core != nullptr) {
+            float* y = (w.part != kAttnWhole ? p.part_o : p.core) + to_row + c;
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<float4*>(y + e) =
+                  make_float4(o[e] * f.own, o[e + 1] * f.own, o[e + 2] * f.own, o[e + 3] * f.own);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] *= f.own;
+            if (prior.any)
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(p.prior_o + to_row + c + e);
+                o[e] = fmaf(f.prior, x.x, o[e]), o[e + 1] = fmaf(f.prior, x.y, o[e + 1]);
+                o[e + 2] = fmaf(f.prior, x.z, o[e + 2]), o[e + 3] = fmaf(f.prior, x.w, o[e + 3]);
+              }
+            T* y = static_cast<T*>(p.out) + to_row + c;
+#pragma unroll
+            for (int e = 0; e < 16; e += 8)
+              *reinterpret_cast<uint4*>(y + e) =
+                  make_uint4(Half<T>::pack(o[e], o[e + 1]), Half<T>::pack(o[e + 2], o[e + 3]),
+                             Half<T>::pack(o[e + 4], o[e + 5]), Half<T>::pack(o[e + 6], o[e + 7]));
+          }
+        }
+        if (tid == 0 && w.part != kAttnWhole)
+          p.part_at[attn_slot(blockIdx.x, w.part)] = make_int4(w.part, w.q0, w.tokens, w.kh);
+      }
+      give(i);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kBMma) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tb, kCols);
+  }
+}
+
+bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank, const cuuint64_t* dims,
+              const cuuint64_t* strides, const cuuint32_t* box) {
+  const tc::EncodeTiledFn fn = tc::encode_fn();
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return fn != nullptr && fn(m, dt, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, one,
+                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D>
+cudaError_t run(const AttnArgs& p, CUtensorMapDataType dt, int grid, cudaStream_t stream) {
+  CUtensorMap mq, mk, mv;
+  const cuuint64_t g = (cuuint64_t)p.group, Hk = (cuuint64_t)p.Hk, head = D * 2;
+  // q as [token][key head][member of its group][D], whichever of the two lie
+  // side by side
+  const bool tiled = p.map == GDN_MAP_TILED;
+  const cuuint64_t qd[4] = {D, g, Hk, (cuuint64_t)p.T};
+  const cuuint64_t qs[3] = {tiled ? Hk * head : head, tiled ? head : g * head, (cuuint64_t)p.q_stride * 2};
+  const cuuint32_t qb[4] = {64, (cuuint32_t)g, 1, (cuuint32_t)(p.item / 2)};
+  const cuuint64_t kd[3] = {D, Hk, (cuuint64_t)(p.kv_rows > 0 ? p.kv_rows : 1)};
+  const cuuint64_t ks[2] = {head, (cuuint64_t)p.k_stride * 2}, vs[2] = {head, (cuuint64_t)p.v_stride * 2};
+  const cuuint32_t kb[3] = {64, 1, kBK};
+  // (a cache of no rows is never read)
+  if (!make_map(&mq, p.q, dt, 4, qd, qs, qb) || !make_map(&mk, p.kv_rows > 0 ? p.k : p.q, dt, 3, kd, ks, kb) ||
+      !make_map(&mv, p.kv_rows > 0 ? p.v : p.q, dt, 3, kd, vs, kb))
+    return cudaErrorInvalidValue;
+  constexpr int smem = (int)TcGeom<D>::kSmem + 1024;
+  const cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  attn_tc_kernel<T, D><<<grid, kBThreads, smem, stream>>>(p, mq, mk, mv);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t run_dim(const AttnArgs& p, CUtensorMapDataType dt, int32_t D, int grid, cudaStream_t stream) {
+  switch (D) {
+    case 32: return run<T, 32>(p, dt, grid, stream);
+    case 64: return run<T, 64>(p, dt, grid, stream);
+    case 96: return run<T, 96>(p, dt, grid, stream);
+    default: return run<T, 128>(p, dt, grid, stream);
+  }
+}
+
+}  // namespace
+
+int attn_tc_rows() { return kBR; }
+
+cudaError_t launch_attn_tc(const AttnArgs& p, int32_t dtype, int32_t D, int grid, cudaStream_t stream) {
+  if (dtype == GDN_F16) return run_dim<__half>(p, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, D, grid, stream);
+  return run_dim<__nv_bfloat16>(p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, D, grid, stream);
+}
+
+}  // namespace gdn
+
+GDN_DEFINE_ERROR_READER(attn_tc)

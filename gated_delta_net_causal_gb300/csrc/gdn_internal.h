@@ -288,7 +288,11 @@ cudaError_t launch_attn(AttnArgs p, const AttnSplit& s, void* workspace, int32_t
 // attn_cc.cu: rows of an item, CTAs
 int attn_cc_rows();
 int attn_cc_ctas(int sms);
-cudaError_t launch_attn_cc(const AttnArgs& p, int32_t dtype, int32_t D, int grid, cudaStream_t stream);
+cudaError_t launch_attn_cc(const AttnArgs& p, int32_t D, int grid, cudaStream_t stream);
+// attn_tc.cu: rows of a tile (an item has two)
+int attn_tc_rows();
+cudaError_t launch_attn_tc(const AttnArgs& p, int32_t dtype, int32_t D, int grid, cudaStream_t stream);
+cudaError_t read_error_attn_tc(int32_t* status, bool clear);
 // diag.cu: one warp's bounded wait on an mbarrier nothing arrives on
 cudaError_t launch_wait_timeout(uint64_t limit_ns, int32_t* gave_up, cudaStream_t stream);
 
