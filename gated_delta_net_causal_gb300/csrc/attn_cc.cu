@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kAT, 2) attn_cc_kernel(const AttnArgs p) {
   attn_plan<kAK, kAT>(p, sums, &plan);
   if (tid < 2 && p.part_o != nullptr) p.part_at[2 * blockIdx.x + tid] = make_int4(kAttnWhole, 0, 0, 0);
   AttnWalk<kAK> walk;
-  if (tid == 0) walk.start(p, plan);
+  if (tid < 32) walk.start(p, plan, tid);
   const float* gq = static_cast<const float*>(p.q);
   const float* gk = static_cast<const float*>(p.k);
   const float* gv = static_cast<const float*>(p.v);
@@ -50,7 +50,10 @@ __global__ void __launch_bounds__(kAT, 2) attn_cc_kernel(const AttnArgs p) {
 
   for (;;) {
     __syncthreads();
-    if (tid == 0) piece = walk.next(p);
+    if (tid < 32) {
+      const AttnPiece w = walk.next(p);
+      if (tid == 0) piece = w;
+    }
     __syncthreads();
     const AttnPiece w = piece;
     if (w.tokens == 0) break;

@@ -4,15 +4,16 @@
 //
 // How the work is cut. A sequence's tokens are taken `item` at a time: an item
 // is those tokens' rows (token, query head of the group) for one key head, its
-// keys are read in tiles of KT. A tile of an item is a unit; units lie in one
-// order (sequence, key head, item, tile), and CTA c of G takes the c-th of G
-// equal stretches of them, whatever the lengths are. An item that lies across
+// keys are read in tiles of KT. A tile of an item is a unit, and kAttnStart
+// more stand for an item's start and end; units lie in one order (sequence,
+// key head, item, tile), and CTA c of G takes the c-th of G equal stretches of
+// them, whatever the lengths are. An item that lies across
 // a border is left in parts, each (largest score, sum, unnormalised output)
 // in fp32 in the workspace, and attn_join_kernel puts them together. So one
 // long cache is spread over all SMs, ragged prompts leave no SM behind, and
 // sums do not depend on which CTA ran first. The lengths are on the device:
 // every CTA adds up the units for itself, its threads a slice of the
-// sequences each.
+// sequences each, the items of a sequence in closed form.
 #pragma once
 
 #include "gdn_common.cuh"
@@ -51,22 +52,61 @@ __device__ __forceinline__ int attn_visible(const AttnArgs& p, const AttnSeq& s,
   return v > 0 ? (int)v : 0;
 }
 
-// Units of the item whose first token is `at`: its tiles, or one where it
-// sees nothing (its outputs are written all the same).
+// What an item costs besides its tiles, in tiles: those of the first tokens of
+// a prompt have few.
+constexpr int kAttnStart = 1;
+
+// Tiles of the item whose first token is `at`, or one where it sees nothing
+// (its outputs are written all the same).
 template <int KT>
-__device__ __forceinline__ int attn_units(const AttnArgs& p, const AttnSeq& s, int at) {
+__device__ __forceinline__ int attn_tiles(const AttnArgs& p, const AttnSeq& s, int at) {
   const int last = (s.qn - at < p.item ? s.qn : at + p.item) - 1;
   const int v = attn_visible(p, s, last);
   return v > KT ? v / KT + (v % KT != 0) : 1;
+}
+
+// sum of floor((a i + b) / m) over 0 <= i < n, for a, b >= 0: whole multiples
+// of m in a and b add arithmetic series, and what is left counts the points of
+// a lattice under a line, the same with the axes exchanged.
+__device__ __forceinline__ int64_t attn_floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t sum = 0;
+  for (;;) {
+    if (a >= m) {
+      sum += (a / m) * (n * (n - 1) / 2);
+      a %= m;
+    }
+    if (b >= m) {
+      sum += (b / m) * n;
+      b %= m;
+    }
+    const int64_t top = a * n + b;
+    if (top < m) return sum;
+    n = top / m;
+    b = top % m;
+    const int64_t t = m;
+    m = a;
+    a = t;
+  }
+}
+// Units of a sequence's first n items, for one key head; all but the last item
+// of a sequence are full.
+template <int KT>
+__device__ __forceinline__ int64_t attn_units_before(const AttnArgs& p, const AttnSeq& s, int64_t n) {
+  if (!p.causal) return n * (attn_tiles<KT>(p, s, 0) + kAttnStart);
+  const int64_t off = (int64_t)s.kn - s.qn;  // item i's last token sees off + (i + 1) item keys
+  // the first `one` items have one tile (they see KT keys at most)
+  int64_t one = off + p.item > KT ? 0 : (KT - off) / p.item;
+  if (one > n) one = n;
+  // ceil((off + (one + 1 + i) item) / KT) for the others
+  const int64_t first = off + (one + 1) * p.item + KT - 1;
+  return one + (n > one ? attn_floor_sum(n - one, KT, p.item, first) : 0) + n * kAttnStart;
 }
 // Units of a sequence for one key head.
 template <int KT>
 __device__ __forceinline__ int64_t attn_seq_units(const AttnArgs& p, const AttnSeq& s) {
   if (s.qn == 0) return 0;
-  if (!p.causal) return (int64_t)((s.qn - 1) / p.item + 1) * attn_units<KT>(p, s, 0);
-  int64_t u = 0;
-  for (int64_t at = 0; at < s.qn; at += p.item) u += attn_units<KT>(p, s, (int)at);
-  return u;
+  const int items = (s.qn - 1) / p.item + 1;
+  return attn_units_before<KT>(p, s, items - 1) + attn_tiles<KT>(p, s, (items - 1) * p.item) + kAttnStart;
 }
 
 // A stretch of an item's tiles, for one CTA.
@@ -131,7 +171,7 @@ __device__ __forceinline__ void attn_plan(const AttnArgs& p, int64_t* sums, Attn
   __syncthreads();
 }
 
-// Hands out a CTA's pieces in order; one thread's.
+// Hands out a CTA's pieces in order. A warp's: all lanes have the same.
 template <int KT>
 struct AttnWalk {
   AttnSeq s;
@@ -139,30 +179,50 @@ struct AttnWalk {
   int n, kh, at, tile;
   bool whole;  // no item is cut: those that begin in the stretch are taken to their ends
 
-  __device__ __forceinline__ void start(const AttnArgs& p, const AttnPlan& plan) {
+  __device__ __forceinline__ void start(const AttnArgs& p, const AttnPlan& plan, int lane) {
     left = plan.count;
     whole = p.part_o == nullptr;
     n = plan.n;
     kh = at = tile = 0;
     if (left <= 0) return;
-    int64_t u = plan.begin, head;
-    for (;;) {
-      s = attn_seq(p, n);
-      head = attn_seq_units<KT>(p, s);
-      if (u < head * p.Hk) break;
-      u -= head * p.Hk;
-      ++n;
+    // the sequence: the lanes have 32 of them
+    int64_t u = plan.begin;
+    for (;; n += 32) {
+      const int64_t own = n + lane < p.N ? attn_seq_units<KT>(p, attn_seq(p, n + lane)) * p.Hk : 0;
+      int64_t incl = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, incl > u);
+      if (past != 0) {
+        const int l = __ffs(past) - 1;
+        n += l;
+        u -= __shfl_sync(0xffffffffu, incl - own, l);
+        break;
+      }
+      u -= __shfl_sync(0xffffffffu, incl, 31);
     }
+    s = attn_seq(p, n);
+    const int64_t head = attn_seq_units<KT>(p, s);
     kh = (int)(u / head);
     u -= kh * head;
-    for (;; at += p.item) {
-      const int k = attn_units<KT>(p, s, at);
-      if (u < k) break;
-      u -= k;
+    // the item: the last one with no more than u units before it, among 32 evenly spaced ones at a time
+    int64_t lo = 0, count = (s.qn - 1) / p.item + 1;
+    while (count > 1) {
+      const int64_t step = (count + 31) / 32, i = lo + lane * step;
+      const bool in = lane * step < count && attn_units_before<KT>(p, s, i) <= u;
+      const int l = 31 - __clz(__ballot_sync(0xffffffffu, in));  // (lane 0's is)
+      lo += l * step;
+      count = count - l * step < step ? count - l * step : step;
     }
+    u -= attn_units_before<KT>(p, s, lo);
+    at = (int)(lo * p.item);
     tile = (int)u;
-    if (whole && tile > 0) {  // the CTA before takes it
-      left -= attn_units<KT>(p, s, at) - tile;
+    const int tiles = attn_tiles<KT>(p, s, at);
+    if (tile >= tiles || (whole && tile > 0)) {  // the CTA before takes it to its end
+      left -= tiles + kAttnStart - tile;
       tile = 0;
       step(p);
     }
@@ -183,24 +243,22 @@ struct AttnWalk {
   __device__ __forceinline__ AttnPiece next(const AttnArgs& p) {
     AttnPiece w{};
     if (left <= 0) return w;
-    const int units = attn_units<KT>(p, s, at);
-    const int take = whole || left >= units - tile ? units - tile : (int)left;
+    const int tiles = attn_tiles<KT>(p, s, at), rest = tiles + kAttnStart - tile;
+    const int take = whole || left >= rest ? rest : (int)left;
+    const bool ends = tile + take >= tiles;
     w.q0 = s.q0 + at;
     w.tokens = s.qn - at < p.item ? s.qn - at : p.item;
     w.kh = kh;
     w.k0 = s.k0;
     w.see = p.causal ? (int)((int64_t)s.kn - s.qn + at + 1) : s.kn;
     const int seen = attn_sees(p, w, w.tokens - 1);
-    const int tiles = seen / KT + (seen % KT != 0);  // 0 where a unit stands for none
-    w.t0 = tile < tiles ? tile : tiles;
-    w.t1 = tile + take < tiles ? tile + take : tiles;
-    w.part = tile > 0 ? (tile + take == units ? kAttnLast : kAttnMiddle) : (take == units ? kAttnWhole : kAttnFirst);
+    const int keys = seen / KT + (seen % KT != 0);  // 0 where a tile stands for none
+    w.t0 = tile < keys ? tile : keys;
+    w.t1 = tile + take < keys ? tile + take : keys;
+    w.part = tile > 0 ? (ends ? kAttnLast : kAttnMiddle) : (ends ? kAttnWhole : kAttnFirst);
     left -= take;
-    tile += take;
-    if (tile == units) {
-      tile = 0;
-      step(p);
-    }
+    tile = 0;
+    step(p);  // (where the item goes on, so does another CTA)
     return w;
   }
 };

@@ -42,8 +42,9 @@ template <int D>
 struct TcGeom {
   static constexpr int kBoxes = (D + 63) / 64;
   static constexpr uint32_t kTile = kBoxes * kBK * 128;  // bytes
-  static constexpr int kStages = kBoxes == 2 ? 5 : 8;
-  static constexpr uint32_t kSmem = (2 + kStages) * kTile;
+  static constexpr int kStages = kBoxes == 2 ? 4 : 8;
+  static constexpr uint32_t kOut = (2 + kStages) * kTile;  // 4 KB for each warp of rows
+  static constexpr uint32_t kSmem = kOut + 8 * 4096;
 };
 
 // TMEM columns: S (P in its first half) and O of both tiles
@@ -100,6 +101,49 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int x, i
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Consecutive k-steps issued by one elected lane of a converged warp, their
+// descriptors counted up here: one election and one pair of descriptors for
+// all of them. Four steps of both operands K-major (32 bytes each)...
+template <int STEPS>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, bool accumulate) {
+  static_assert(STEPS == 2 || STEPS == 4, "within a 128-byte atom");
+  if constexpr (STEPS == 4)
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(id), "r"((uint32_t)accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\t.reg .b64 a1, b1;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "add.s64 a1, %1, 2;\n\tadd.s64 b1, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(id), "r"((uint32_t)accumulate)
+        : "memory");
+}
+// ... and four of A from TMEM (8 columns each), B MN-major (2048 bytes).
+__device__ __forceinline__ void mma_ts4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+      "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(id), "r"((uint32_t)accumulate)
       : "memory");
 }
 
@@ -213,16 +257,16 @@ __global__ void __launch_bounds__(kBThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == kBPlan) {
       // -------------------------------------------------------------- pieces
-      if (lane == 0) {
-        AttnWalk<kBK> walk;
-        walk.start(p, sh.plan);
-        for (int i = 0;; ++i) {
-          if (i >= kBRing && !wait(&sh.piece_empty[i % kBRing], (i / kBRing - 1) & 1)) break;
-          const AttnPiece w = walk.next(p);
+      AttnWalk<kBK> walk;
+      walk.start(p, sh.plan, lane);
+      for (int i = 0;; ++i) {
+        const AttnPiece w = walk.next(p);
+        if (i >= kBRing && !__all_sync(0xffffffffu, wait(&sh.piece_empty[i % kBRing], (i / kBRing - 1) & 1))) break;
+        if (lane == 0) {
           sh.piece[i % kBRing] = w;
           mbar_arrive(&sh.piece_full[i % kBRing]);
-          if (w.tokens == 0) break;
         }
+        if (w.tokens == 0) break;
       }
     } else if (warp == kBLoad) {
       // --------------------------------------------------------------- loads
@@ -275,75 +319,77 @@ __global__ void __launch_bounds__(kBThreads, 1)
       }
     } else if (warp == kBMma) {
       // ------------------------------------------------------------ products
+      // (the whole warp goes through this, and one lane issues: addresses stay
+      // in uniform registers, where one lane's branch took twice as long)
       const uint32_t id_s = tc::idesc(Half<T>::kFormat, kBR, kBK), id_o = tc::idesc(Half<T>::kFormat, kBR, D) | kTransB;
+      const uint64_t dq = tc::sdesc_sw128(smem_u32(sm)), dk = tc::sdesc_sw128(smem_u32(ring));
+      const uint64_t dv = sdesc_v(smem_u32(ring));
+      const auto all = [&](bool x) { return __all_sync(0xffffffffu, x); };
       uint32_t n_kv = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0}, ok_bits = 0;
       bool ok = true;
-      for (int i = 0;; ++i) {
+      for (int i = 0; ok; ++i) {
         AttnPiece w;
         if (!take(i, &w)) break;
-        if (lane == 0 && ok) {
-          const int least = attn_sees(p, w, 0), n[2] = {half_tiles(p, w, 0), half_tiles(p, w, 1)};
-          const int tiles = w.t1 - w.t0;
-          const auto scores = [&](int h, uint32_t st, bool last) {
-            const uint64_t dq = tc::sdesc_sw128(smem_u32(sm + h * G::kTile));
-            const uint64_t dk = tc::sdesc_sw128(smem_u32(ring + st * G::kTile));
+        const int least = attn_sees(p, w, 0), n[2] = {half_tiles(p, w, 0), half_tiles(p, w, 1)};
+        const int tiles = w.t1 - w.t0;
+        const auto scores = [&](int h, uint32_t st, bool last) {
+          const uint64_t a = dq + (h * G::kTile >> 4), b = dk + (st * G::kTile >> 4);
+          constexpr uint32_t next = kBK * 128 >> 4;  // the second 64 columns
+          mma_ss<D == 32 ? 2 : 4>(tb + kColS + 128 * h, a, b, id_s, false);
+          if (D > 64) mma_ss<D == 96 ? 2 : 4>(tb + kColS + 128 * h, a + next, b + next, id_s, true);
+          tc::mma_commit_elect(&sh.s_full[h]);
+          if (last) tc::mma_commit_elect(&sh.q_empty[h]);
+        };
+        // the stage of the next tile of the ring, once it is there
+        const auto next_tile = [&]() {
+          const uint32_t st = n_kv % G::kStages;
+          ok = all(wait(&sh.kv_full[st], (n_kv / G::kStages) & 1));
+          ++n_kv;
+          return st;
+        };
+        if (tiles > 0) {
+          const uint32_t st = next_tile();
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-              tc::mma_f16(tb + kColS + 128 * h, tc::sdesc_at(dq, kBR, s), tc::sdesc_at(dk, kBK, s), id_s, s > 0);
-            tc::mma_commit(&sh.s_full[h]);
-            if (last) tc::mma_commit(&sh.q_empty[h]);
-          };
-          // the stage of the next tile of the ring, once it is there
-          const auto next_tile = [&]() {
-            const uint32_t st = n_kv % G::kStages;
-            ok = ok && wait(&sh.kv_full[st], (n_kv / G::kStages) & 1);
-            ++n_kv;
-            return st;
-          };
-          if (tiles > 0) {
-            uint32_t st = next_tile();
-            for (int h = 0; ok && h < 2; ++h)
-              if (n[h] > 0) {
-                ok = ok && wait(&sh.q_full[h], n_q[h] & 1);
-                ++n_q[h];
-                if (ok) scores(h, st, n[h] == 1);
-              }
-            if (ok) tc::mma_commit(&sh.kv_empty[st]);
-            for (int j = 0; ok && j < tiles; ++j) {
-              const uint32_t sv = next_tile();
-              if (masked_tile(least, w.t0 + j)) {
-                ok = ok && wait(&sh.v_ok[sv], (ok_bits >> sv) & 1);
-                ok_bits ^= 1u << sv;
-              }
-              uint32_t sk = 0;
-              bool have_k = false;
-              for (int h = 0; ok && h < 2; ++h) {
-                if (j >= n[h]) continue;
-                const uint64_t dv = sdesc_v(smem_u32(ring + sv * G::kTile));
-                for (int half = 0; ok && half < 2; ++half) {
-                  ok = wait(&sh.p_ready[h][half], n_p[h] & 1);
-                  tc::fence_after_sync();
-                  if (ok)
-#pragma unroll
-                    for (int s = 4 * half; s < 4 * half + 4; ++s)
-                      tc::mma_f16_ts(tb + kColO + 128 * h, tb + kColS + 128 * h + 8 * s, dv + (uint64_t)(s * 2048 >> 4),
-                                     id_o, j > 0 || s > 0);
-                }
-                ++n_p[h];
-                if (!ok) break;
-                if (j + 1 < n[h]) {
-                  if (!have_k) {
-                    sk = next_tile();
-                    have_k = true;
-                  }
-                  if (ok) scores(h, sk, j + 2 == n[h]);
-                } else {
-                  tc::mma_commit(&sh.o_full[h]);
-                }
-              }
-              if (ok) tc::mma_commit(&sh.kv_empty[sv]);
-              if (ok && have_k) tc::mma_commit(&sh.kv_empty[sk]);
+          for (int h = 0; h < 2; ++h)
+            if (ok && n[h] > 0) {
+              ok = all(wait(&sh.q_full[h], n_q[h] & 1));
+              ++n_q[h];
+              if (ok) scores(h, st, n[h] == 1);
             }
+          if (ok) tc::mma_commit_elect(&sh.kv_empty[st]);
+          for (int j = 0; ok && j < tiles; ++j) {
+            const uint32_t sv = next_tile();
+            if (ok && masked_tile(least, w.t0 + j)) {
+              ok = all(wait(&sh.v_ok[sv], (ok_bits >> sv) & 1));
+              ok_bits ^= 1u << sv;
+            }
+            uint32_t sk = 0;
+            bool have_k = false;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (!ok || j >= n[h]) continue;
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                ok = ok && all(wait(&sh.p_ready[h][half], n_p[h] & 1));
+                tc::fence_after_sync();
+                if (ok)
+                  mma_ts4(tb + kColO + 128 * h, tb + kColS + 128 * h + 32 * half,
+                          dv + ((sv * G::kTile + half * 8192) >> 4), id_o, j > 0 || half > 0);
+              }
+              ++n_p[h];
+              if (!ok) continue;
+              if (j + 1 < n[h]) {
+                if (!have_k) {
+                  sk = next_tile();
+                  have_k = true;
+                }
+                if (ok) scores(h, sk, j + 2 == n[h]);
+              } else {
+                tc::mma_commit_elect(&sh.o_full[h]);
+              }
+            }
+            if (ok) tc::mma_commit_elect(&sh.kv_empty[sv]);
+            if (ok && have_k) tc::mma_commit_elect(&sh.kv_empty[sk]);
           }
         }
         give(i);
@@ -367,30 +413,31 @@ __global__ void __launch_bounds__(kBThreads, 1)
           unsigned char* v = ring + st * G::kTile;
           const int base = t * kBK, from = least > base ? least - base : 0;  // rows from which some row sees no more
           bool hit = false;
-          for (int u = from * (8 * G::kBoxes) + lane; u < kBK * 8 * G::kBoxes; u += 32) {
-            const int row = u / (8 * G::kBoxes), c16 = u % (8 * G::kBoxes);
-            const int off = (c16 >> 3) * kBK * 128 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4);
-            uint4* at = reinterpret_cast<uint4*>(v + off);
-            if (row >= most - base) {
-              *at = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint4 x = *at;
-            uint32_t* e = &x.x;
-            bool here = false;
+        const auto place = [&](int u) {  // 16-byte chunk u, row after row
+          const int row = u / (8 * G::kBoxes), c16 = u % (8 * G::kBoxes);
+          return reinterpret_cast<uint4*>(v + (c16 >> 3) * kBK * 128 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4));
+        };
+        const int until = most - base < kBK ? (most - base) * (8 * G::kBoxes) : kBK * 8 * G::kBoxes;
+#pragma unroll 8
+        for (int u = from * (8 * G::kBoxes) + lane; u < until; u += 32) {
+          uint4 x = *place(u);
+          uint32_t* e = &x.x;
+          uint32_t any = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t m = ((e[j] & Half<T>::kExponent) + Half<T>::kCarry) & 0x80008000u;
-              if (m != 0) {
-                here = true;
-                if (m & 0x8000u) e[j] &= 0xffff0000u;
-                if (m & 0x80000000u) e[j] &= 0x0000ffffu;
-              }
-            }
-            if (here) *at = x;
-            hit |= here;
+          for (int j = 0; j < 4; ++j) any |= (e[j] & Half<T>::kExponent) + Half<T>::kCarry;
+          if ((any & 0x80008000u) == 0) continue;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t m = (e[j] & Half<T>::kExponent) + Half<T>::kCarry;
+            if (m & 0x8000u) e[j] &= 0xffff0000u;
+            if (m & 0x80000000u) e[j] &= 0x0000ffffu;
           }
-          if (hit) sh.piece[i % kBRing].bad = 1;
+          *place(u) = x;
+          hit = true;
+        }
+#pragma unroll 8
+        for (int u = until + lane; u < kBK * 8 * G::kBoxes; u += 32) *place(u) = make_uint4(0, 0, 0, 0);
+        if (hit) sh.piece[i % kBRing].bad = 1;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.v_ok[st]);
@@ -519,52 +566,73 @@ __global__ void __launch_bounds__(kBThreads, 1)
             if (p.lse != nullptr) p.lse[token * p.Hq + head] = f.lse;
           }
         }
+        // 32 columns at a time through shared memory, so that a row's are
+        // stored side by side (from the lanes' rows a store of 16 bytes each
+        // touches 32 lines, 8000 cycles an item)
+        const bool wide = w.part != kAttnWhole || p.core != nullptr;  // fp32
+        unsigned char* stage = sm + G::kOut + warp * 4096;
+        const unsigned live = __ballot_sync(0xffffffffu, valid);
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          float o[16];
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
           if (n > 0) {
-            tc::tmem_ld16(to + c, o);
+            tmem_ld32(to + c, o);
             tc::tmem_wait_ld();
           } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = 0.f;
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
           }
-          if (!valid) continue;
-          if (bad) {
+          if (valid && bad) {
             const T* v = static_cast<const T*>(p.v) + (int64_t)w.kh * D + c;
             const int first = max(item_least, w.t0 * kBK), last = (int)min((int64_t)sees, (int64_t)w.t1 * kBK);
             for (int k = first; k < last; ++k)
-              for (int e = 0; e < 16; ++e) {
-                const float x = to_f32(v[(int64_t)(w.k0 + k) * p.v_stride + e]);
-                if (!isfinite(x)) {
 #pragma unroll
-                  for (int g = 0; g < 16; ++g)
-                    if (g == e) o[g] += x;
-                }
+              for (int e = 0; e < 32; ++e) {
+                const float x = to_f32(v[(int64_t)(w.k0 + k) * p.v_stride + e]);
+                if (!isfinite(x)) o[e] += x;
               }
           }
-          if (w.part != kAttnWhole || p.core != nullptr) {
-            float* y = (w.part != kAttnWhole ? p.part_o : p.core) + to_row + c;
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<float4*>(y + e) =
-                  make_float4(o[e] * f.own, o[e + 1] * f.own, o[e + 2] * f.own, o[e + 3] * f.own);
+          for (int e = 0; e < 32; ++e) o[e] *= f.own;
+          if (prior.any)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(p.prior_o + to_row + c + e);
+              o[e] = fmaf(f.prior, x.x, o[e]), o[e + 1] = fmaf(f.prior, x.y, o[e + 1]);
+              o[e + 2] = fmaf(f.prior, x.z, o[e + 2]), o[e + 3] = fmaf(f.prior, x.w, o[e + 3]);
+            }
+          __syncwarp();
+          if (wide) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                  make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            __syncwarp();
+            float* y = w.part != kAttnWhole ? p.part_o : p.core;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = 4 * i + (lane >> 3), e = lane & 7;
+              const int64_t at_row = __shfl_sync(0xffffffffu, to_row, r);
+              if (live >> r & 1)
+                *reinterpret_cast<float4*>(y + at_row + c + 4 * e) =
+                    *reinterpret_cast<const float4*>(stage + r * 128 + ((e ^ (r & 7)) << 4));
+            }
           } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] *= f.own;
-            if (prior.any)
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ (lane >> 1 & 3)) << 4)) =
+                  make_uint4(Half<T>::pack(o[8 * e], o[8 * e + 1]), Half<T>::pack(o[8 * e + 2], o[8 * e + 3]),
+                             Half<T>::pack(o[8 * e + 4], o[8 * e + 5]), Half<T>::pack(o[8 * e + 6], o[8 * e + 7]));
+            __syncwarp();
+            T* y = static_cast<T*>(p.out);
 #pragma unroll
-              for (int e = 0; e < 16; e += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(p.prior_o + to_row + c + e);
-                o[e] = fmaf(f.prior, x.x, o[e]), o[e + 1] = fmaf(f.prior, x.y, o[e + 1]);
-                o[e + 2] = fmaf(f.prior, x.z, o[e + 2]), o[e + 3] = fmaf(f.prior, x.w, o[e + 3]);
-              }
-            T* y = static_cast<T*>(p.out) + to_row + c;
-#pragma unroll
-            for (int e = 0; e < 16; e += 8)
-              *reinterpret_cast<uint4*>(y + e) =
-                  make_uint4(Half<T>::pack(o[e], o[e + 1]), Half<T>::pack(o[e + 2], o[e + 3]),
-                             Half<T>::pack(o[e + 4], o[e + 5]), Half<T>::pack(o[e + 6], o[e + 7]));
+            for (int i = 0; i < 4; ++i) {
+              const int r = 8 * i + (lane >> 2), e = lane & 3;
+              const int64_t at_row = __shfl_sync(0xffffffffu, to_row, r);
+              if (live >> r & 1)
+                *reinterpret_cast<uint4*>(y + at_row + c + 8 * e) =
+                    *reinterpret_cast<const uint4*>(stage + r * 64 + ((e ^ (r >> 1 & 3)) << 4));
+            }
           }
         }
         if (tid == 0 && w.part != kAttnWhole)
