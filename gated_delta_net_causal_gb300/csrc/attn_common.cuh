@@ -65,28 +65,47 @@ __device__ __forceinline__ int attn_tiles(const AttnArgs& p, const AttnSeq& s, i
   return v > KT ? v / KT + (v % KT != 0) : 1;
 }
 
-// sum of floor((a i + b) / m) over 0 <= i < n, for a, b >= 0: whole multiples
-// of m in a and b add arithmetic series, and what is left counts the points of
-// a lattice under a line, the same with the axes exchanged.
-__device__ __forceinline__ int64_t attn_floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+// a / b and its remainder, in 32 bits where they fit (a 64-bit division takes
+// several hundred cycles)
+__device__ __forceinline__ int64_t attn_divide(int64_t a, int64_t b, int64_t* rest) {
+  int64_t q;
+  if (((a | b) >> 32) == 0) q = (unsigned)a / (unsigned)b;
+  else q = a / b;
+  *rest = a - q * b;
+  return q;
+}
+
+// sum of floor((a i + b) / m) over 0 <= i < n, for a, b < m: what reaches m
+// counts the points of a lattice under a line, the same with the axes
+// exchanged, and whole multiples of m in a and b add arithmetic series.
+// a n + b has to fit U.
+template <typename U>
+__device__ __forceinline__ int64_t attn_lattice(U n, U m, U a, U b) {
   int64_t sum = 0;
   for (;;) {
-    if (a >= m) {
-      sum += (a / m) * (n * (n - 1) / 2);
-      a %= m;
-    }
-    if (b >= m) {
-      sum += (b / m) * n;
-      b %= m;
-    }
-    const int64_t top = a * n + b;
+    const U top = a * n + b;
     if (top < m) return sum;
     n = top / m;
     b = top % m;
-    const int64_t t = m;
+    const U t = m;
     m = a;
     a = t;
+    if (a >= m) {
+      sum += (int64_t)(a / m) * ((int64_t)n * (n - 1) / 2);
+      a %= m;
+    }
+    if (b >= m) {
+      sum += (int64_t)(b / m) * n;
+      b %= m;
+    }
   }
+}
+// sum of floor((item i + b) / KT) over 0 <= i < n, b >= 0
+template <int KT>
+__device__ __forceinline__ int64_t attn_floor_sum(int64_t n, int item, int64_t b) {
+  const int64_t sum = (item / KT) * (n * (n - 1) / 2) + (b / KT) * n;
+  const unsigned a = (unsigned)item % KT, r = (unsigned)(b % KT);
+  return sum + (n < (1 << 22) ? attn_lattice<unsigned>((unsigned)n, KT, a, r) : attn_lattice<int64_t>(n, KT, a, r));
 }
 // Units of a sequence's first n items, for one key head; all but the last item
 // of a sequence are full.
@@ -95,11 +114,11 @@ __device__ __forceinline__ int64_t attn_units_before(const AttnArgs& p, const At
   if (!p.causal) return n * (attn_tiles<KT>(p, s, 0) + kAttnStart);
   const int64_t off = (int64_t)s.kn - s.qn;  // item i's last token sees off + (i + 1) item keys
   // the first `one` items have one tile (they see KT keys at most)
-  int64_t one = off + p.item > KT ? 0 : (KT - off) / p.item;
+  int64_t one = off + p.item > KT ? 0 : (unsigned)(KT - off) / (unsigned)p.item;
   if (one > n) one = n;
   // ceil((off + (one + 1 + i) item) / KT) for the others
   const int64_t first = off + (one + 1) * p.item + KT - 1;
-  return one + (n > one ? attn_floor_sum(n - one, KT, p.item, first) : 0) + n * kAttnStart;
+  return one + (n > one ? attn_floor_sum<KT>(n - one, p.item, first) : 0) + n * kAttnStart;
 }
 // Units of a sequence for one key head.
 template <int KT>
@@ -158,7 +177,8 @@ __device__ __forceinline__ void attn_plan(const AttnArgs& p, int64_t* sums, Attn
     const int64_t total = __shfl_sync(0xffffffffu, incl, 31);
     // units < 2^31 key tiles x 2^16 sequences' items x heads: the products stay in 64 bits
     const int64_t G = gridDim.x, c = blockIdx.x;
-    const int64_t each = total / G, more = total % G;
+    int64_t more;
+    const int64_t each = attn_divide(total, G, &more);
     const int64_t u0 = each * c + (c < more ? c : more), count = each + (c < more ? 1 : 0);
     if (lane == 0 && count == 0) *plan = AttnPlan{0, 0, p.N};
     if (count > 0 && u0 >= incl - own && u0 < incl) {
@@ -206,8 +226,7 @@ struct AttnWalk {
     }
     s = attn_seq(p, n);
     const int64_t head = attn_seq_units<KT>(p, s);
-    kh = (int)(u / head);
-    u -= kh * head;
+    kh = (int)attn_divide(u, head, &u);
     // the item: the last one with no more than u units before it, among 32 evenly spaced ones at a time
     int64_t lo = 0, count = (s.qn - 1) / p.item + 1;
     while (count > 1) {

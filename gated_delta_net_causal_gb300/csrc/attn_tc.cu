@@ -1,16 +1,23 @@
 // Softmax attention on the 5th-generation tensor cores (f16, bf16).
 //
 // An item is two tiles of 128 rows (token, query head of the group), A and B,
-// that share the keys' tiles of 128: two chains of
+// that share the keys' tiles of 128. For both, tile after tile:
 //   S = Q K^T        both from shared memory, fp32 into TMEM
-//   P = exp2(S scale log2 e - M)     a thread per row, into S's place, 16 bits
+//   P = exp2(S scale log2 e - M)     a thread per row, 16 bits, into TMEM
 //   O += P V         P from TMEM, V read transposed, fp32 in TMEM
-// so that one tile's softmax runs under the other's products. A row lies in a
-// lane of TMEM, so its maximum and sum are one thread's and need no exchange.
-// M follows the row's maximum only where that has grown by more than 8 (in
-// log2) since: then the row's O and sum are rescaled, which is rare; else the
-// weights are up to 2^8, as exact as below 1. The sum is of the weights before
-// their rounding to 16 bits.
+// A row lies in a lane of TMEM, so its maximum and sum are one thread's and
+// need no exchange. M follows the row's maximum only where that has grown by
+// more than 8 (in log2) since: then the row's O and sum are rescaled, which is
+// rare; else the weights are up to 2^8, as exact as below 1. The sum is of the
+// weights before their rounding to 16 bits.
+//
+// TMEM's 512 columns hold O of both tiles (256), P of both (128) and one S.
+// The tiles take turns in it: a row's thread reads all of its scores into
+// registers at once, so S is free again long before the softmax is done, and
+// the scores of the other tile, then the tile's own next ones, are made under
+// it. With two S, each with its P in its place, the next scores of a tile had
+// to wait for its O += P V: a chain of softmax and both products, 3400 cycles
+// for both tiles, where the products alone take 2048.
 //
 // Warps 0 to 3 are A's rows, 4 to 7 B's; one warp issues the products, one
 // loads (Q once an item, K and V through a ring of tiles), one hands out the
@@ -19,6 +26,13 @@
 // not see it. So rows of V that nobody sees become 0, and in rows that only
 // some see what is not finite is replaced by 0 and added, at the end, to the
 // rows that do see it.
+//
+// Order of a piece's products over its tiles of keys k: O of B for k - 2,
+// scores of A for k, O of A for k - 1, scores of B for k. So a tile's O comes as
+// soon as its weights are there and is done before the next ones want their
+// place, and what follows are the scores that the other tile wants next. (The
+// scores first: 225 instead of 194 us for a prompt of 4096 tokens.) The ring's
+// order is that of the first use: K of k, V of k - 1.
 //
 // A wait that gives up raises the CTA's abort flag; every role then leaves its
 // loop at once.
@@ -47,12 +61,12 @@ struct TcGeom {
   static constexpr uint32_t kSmem = kOut + 8 * 4096;
 };
 
-// TMEM columns: S (P in its first half) and O of both tiles
-constexpr uint32_t kColS = 0, kColO = 256, kCols = 512;
+// TMEM columns: S, P of both tiles (64 each), O of both (128 each)
+constexpr uint32_t kColS = 0, kColP = 128, kColO = 256, kCols = 512;
 
 struct BShared {
   uint64_t kv_full[8], kv_empty[8], v_ok[8];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_full[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], s_free, p_ready[2], o_done[2];
   uint64_t piece_full[kBRing], piece_empty[kBRing];
   AttnPiece piece[kBRing];
   AttnPlan plan;
@@ -153,6 +167,33 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// A bounded wait that sleeps in the barrier: a warp that asks again and again
+// takes shared memory's cycles from the products' operands. Gives up as
+// mbar_wait_bounded does.
+constexpr uint32_t kNap = 100000;  // ns that one question may take
+__device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(kNap)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  const uint64_t t0 = global_ns();
+  while (!*abort_flag) {
+    if (try_wait_long(bar, parity)) return true;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      record_device_error(GDN_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+  }
+  return false;
+}
+
 template <typename T>
 struct Half;
 template <>
@@ -203,7 +244,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
   unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   unsigned char* ring = sm + 2 * G::kTile;
   __shared__ BShared sh;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
   if (warp == kBMma) {
     tc::tmem_alloc(&sh.tmem, kCols);
@@ -219,10 +260,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_ready[i][0], 4);
-      mbar_init(&sh.p_ready[i][1], 4);
-      mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.p_ready[i], 4);
+      mbar_init(&sh.o_done[i], 1);
     }
+    mbar_init(&sh.s_free, 4);
     for (int i = 0; i < kBRing; ++i) {
       mbar_init(&sh.piece_full[i], 1);
       mbar_init(&sh.piece_empty[i], kBTakers);
@@ -236,9 +277,11 @@ __global__ void __launch_bounds__(kBThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tb = sh.tmem;
+  const uint32_t tb = __shfl_sync(0xffffffffu, sh.tmem, 0);
   volatile int* abort_flag = &sh.abort;
-  const auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, abort_flag); };
+  const auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return try_wait_long(bar, parity) || wait_slow(bar, parity, abort_flag);
+  };
   // piece i of the CTA, for a whole warp; false: there is none
   const auto take = [&](int i, AttnPiece* w) {
     const bool ok = wait(&sh.piece_full[i % kBRing], (i / kBRing) & 1);
@@ -273,34 +316,36 @@ __global__ void __launch_bounds__(kBThreads, 1)
       uint32_t n_kv = 0, n_q[2] = {0, 0};
       const uint32_t q_bytes = (uint32_t)(G::kBoxes * 128 * (p.item / 2) * p.group);
       bool ok = true;
+      const auto load_kv = [&](const CUtensorMap* map, int kh, int row) {
+        const uint32_t st = n_kv % G::kStages, round = n_kv / G::kStages;
+        ok = ok && (round == 0 || wait(&sh.kv_empty[st], (round - 1) & 1));
+        if (!ok) return;
+        ++n_kv;
+        mbar_arrive_expect_tx(&sh.kv_full[st], G::kTile);
+        for (int b = 0; b < G::kBoxes; ++b)
+          tma_load_3d(ring + st * G::kTile + b * kBK * 128, map, 64 * b, kh, row, &sh.kv_full[st]);
+      };
       for (int i = 0;; ++i) {
         AttnPiece w;
         if (!take(i, &w)) break;
         if (lane == 0 && ok) {
-          const auto load_kv = [&](const CUtensorMap* map, int t) {
-            const uint32_t st = n_kv % G::kStages, round = n_kv / G::kStages;
-            ok = ok && (round == 0 || wait(&sh.kv_empty[st], (round - 1) & 1));
-            if (!ok) return;
-            ++n_kv;
-            mbar_arrive_expect_tx(&sh.kv_full[st], G::kTile);
-            for (int b = 0; b < G::kBoxes; ++b)
-              tma_load_3d(ring + st * G::kTile + b * kBK * 128, map, 64 * b, w.kh, w.k0 + t * kBK, &sh.kv_full[st]);
-          };
-          for (int h = 0; h < 2; ++h) {
-            if (half_tiles(p, w, h) == 0) continue;
+          const auto load_q = [&](int h) {
+            if (half_tiles(p, w, h) == 0) return;
             ok = ok && (n_q[h] == 0 || wait(&sh.q_empty[h], (n_q[h] - 1) & 1));
-            if (!ok) break;
+            if (!ok) return;
             ++n_q[h];
             mbar_arrive_expect_tx(&sh.q_full[h], q_bytes);
             for (int b = 0; b < G::kBoxes; ++b)
               tma_load_4d(sm + h * G::kTile + b * kBR * 128, &tm_q, 64 * b, 0, w.kh, w.q0 + h * (p.item / 2),
                           &sh.q_full[h]);
-            if (h == 0) load_kv(&tm_k, w.t0);  // before B's rows
-          }
+          };
           for (int t = w.t0; ok && t < w.t1; ++t) {
-            if (t > w.t0 || half_tiles(p, w, 0) == 0) load_kv(&tm_k, t);
-            load_kv(&tm_v, t);
+            if (t == w.t0) load_q(0);
+            load_kv(&tm_k, w.kh, w.k0 + t * kBK);
+            if (t == w.t0) load_q(1);
+            else load_kv(&tm_v, w.kh, w.k0 + (t - 1) * kBK);
           }
+          if (ok && w.t0 < w.t1) load_kv(&tm_v, w.kh, w.k0 + (w.t1 - 1) * kBK);
         }
         give(i);
       }
@@ -325,94 +370,90 @@ __global__ void __launch_bounds__(kBThreads, 1)
       const uint64_t dq = tc::sdesc_sw128(smem_u32(sm)), dk = tc::sdesc_sw128(smem_u32(ring));
       const uint64_t dv = sdesc_v(smem_u32(ring));
       const auto all = [&](bool x) { return __all_sync(0xffffffffu, x); };
-      uint32_t n_kv = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0}, ok_bits = 0;
+      uint32_t n_kv = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_s = 0, ok_bits = 0;
       bool ok = true;
+      // the stage of the ring's next tile, once it is there
+      const auto next_tile = [&]() {
+        const uint32_t st = n_kv % G::kStages;
+        ok = all(wait(&sh.kv_full[st], (n_kv / G::kStages) & 1));
+        ++n_kv;
+        return st;
+      };
+      const auto scores = [&](int h, uint32_t st, bool first, bool last) {
+        if (first) {
+          ok = ok && all(wait(&sh.q_full[h], n_q[h] & 1));
+          ++n_q[h];
+        }
+        ok = ok && (n_s == 0 || all(wait(&sh.s_free, (n_s - 1) & 1)));
+        ++n_s;
+        if (!ok) return;
+        tc::fence_after_sync();
+        const uint64_t a = dq + (h * G::kTile >> 4), b = dk + (st * G::kTile >> 4);
+        constexpr uint32_t next = kBK * 128 >> 4;  // the second 64 columns
+        mma_ss<D == 32 ? 2 : 4>(tb + kColS, a, b, id_s, false);
+        if (D > 64) mma_ss<D == 96 ? 2 : 4>(tb + kColS, a + next, b + next, id_s, true);
+        tc::mma_commit_elect(&sh.s_full[h]);
+        if (last) tc::mma_commit_elect(&sh.q_empty[h]);
+      };
+      const auto outputs = [&](int h, uint32_t st, bool accumulate) {
+        ok = ok && all(wait(&sh.p_ready[h], n_p[h] & 1));
+        ++n_p[h];
+        if (!ok) return;
+        tc::fence_after_sync();
+        const uint64_t b = dv + (st * G::kTile >> 4);
+        mma_ts4(tb + kColO + 128 * h, tb + kColP + 64 * h, b, id_o, accumulate);
+        mma_ts4(tb + kColO + 128 * h, tb + kColP + 64 * h + 32, b + (8192 >> 4), id_o, true);
+        tc::mma_commit_elect(&sh.o_done[h]);
+      };
       for (int i = 0; ok; ++i) {
         AttnPiece w;
         if (!take(i, &w)) break;
-        const int least = attn_sees(p, w, 0), n[2] = {half_tiles(p, w, 0), half_tiles(p, w, 1)};
-        const int tiles = w.t1 - w.t0;
-        const auto scores = [&](int h, uint32_t st, bool last) {
-          const uint64_t a = dq + (h * G::kTile >> 4), b = dk + (st * G::kTile >> 4);
-          constexpr uint32_t next = kBK * 128 >> 4;  // the second 64 columns
-          mma_ss<D == 32 ? 2 : 4>(tb + kColS + 128 * h, a, b, id_s, false);
-          if (D > 64) mma_ss<D == 96 ? 2 : 4>(tb + kColS + 128 * h, a + next, b + next, id_s, true);
-          tc::mma_commit_elect(&sh.s_full[h]);
-          if (last) tc::mma_commit_elect(&sh.q_empty[h]);
-        };
-        // the stage of the next tile of the ring, once it is there
-        const auto next_tile = [&]() {
-          const uint32_t st = n_kv % G::kStages;
-          ok = all(wait(&sh.kv_full[st], (n_kv / G::kStages) & 1));
-          ++n_kv;
-          return st;
-        };
-        if (tiles > 0) {
-          const uint32_t st = next_tile();
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (ok && n[h] > 0) {
-              ok = all(wait(&sh.q_full[h], n_q[h] & 1));
-              ++n_q[h];
-              if (ok) scores(h, st, n[h] == 1);
-            }
-          if (ok) tc::mma_commit_elect(&sh.kv_empty[st]);
-          for (int j = 0; ok && j < tiles; ++j) {
-            const uint32_t sv = next_tile();
-            if (ok && masked_tile(least, w.t0 + j)) {
+        // from one lane, so that the compiler knows them to be the same in all
+        const int least = __shfl_sync(0xffffffffu, attn_sees(p, w, 0), 0), t0 = __shfl_sync(0xffffffffu, w.t0, 0);
+        const int na = __shfl_sync(0xffffffffu, half_tiles(p, w, 0), 0);
+        const int nb = __shfl_sync(0xffffffffu, half_tiles(p, w, 1), 0);
+        const int tiles = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
+        uint32_t sv = 0;  // the stage of V of the tile before
+        for (int j = 0; ok && j <= tiles; ++j) {
+          uint32_t sk = 0;
+          if (j < tiles) sk = next_tile();
+          if (j > 1) {
+            if (j - 2 < nb) outputs(1, sv, j > 2);
+            if (ok) tc::mma_commit_elect(&sh.kv_empty[sv]);
+          }
+          if (j < na) scores(0, sk, j == 0, j + 1 == na);
+          if (ok && j > 0) {
+            sv = next_tile();
+            if (ok && masked_tile(least, t0 + j - 1)) {
               ok = all(wait(&sh.v_ok[sv], (ok_bits >> sv) & 1));
               ok_bits ^= 1u << sv;
             }
-            uint32_t sk = 0;
-            bool have_k = false;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (!ok || j >= n[h]) continue;
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                ok = ok && all(wait(&sh.p_ready[h][half], n_p[h] & 1));
-                tc::fence_after_sync();
-                if (ok)
-                  mma_ts4(tb + kColO + 128 * h, tb + kColS + 128 * h + 32 * half,
-                          dv + ((sv * G::kTile + half * 8192) >> 4), id_o, j > 0 || half > 0);
-              }
-              ++n_p[h];
-              if (!ok) continue;
-              if (j + 1 < n[h]) {
-                if (!have_k) {
-                  sk = next_tile();
-                  have_k = true;
-                }
-                if (ok) scores(h, sk, j + 2 == n[h]);
-              } else {
-                tc::mma_commit_elect(&sh.o_full[h]);
-              }
-            }
-            if (ok) tc::mma_commit_elect(&sh.kv_empty[sv]);
-            if (ok && have_k) tc::mma_commit_elect(&sh.kv_empty[sk]);
+            if (j - 1 < na) outputs(0, sv, j > 1);
           }
+          if (j < nb) scores(1, sk, j == 0, j + 1 == nb);
+          if (ok && j < tiles) tc::mma_commit_elect(&sh.kv_empty[sk]);
+        }
+        if (ok && tiles > 0) {
+          if (tiles == nb) outputs(1, sv, tiles > 1);
+          if (ok) tc::mma_commit_elect(&sh.kv_empty[sv]);
         }
         give(i);
       }
     } else if (warp == kBCheck) {
       // ------------------------------------------------- masked tiles of v
       uint32_t n_kv = 0;
-      for (int i = 0;; ++i) {
-        AttnPiece w;
-        if (!take(i, &w)) break;
-        const int least = attn_sees(p, w, 0), most = attn_sees(p, w, w.tokens - 1);
-        for (int t = w.t0; t < w.t1; ++t) {
-          // (the order in which they are loaded: every phase is waited for)
-          wait(&sh.kv_full[n_kv % G::kStages], (n_kv / G::kStages) & 1);
-          ++n_kv;
-          const uint32_t st = n_kv % G::kStages;
-          wait(&sh.kv_full[st], (n_kv / G::kStages) & 1);
-          ++n_kv;
-          if (__any_sync(0xffffffffu, *abort_flag)) break;
-          if (!masked_tile(least, t)) continue;
-          unsigned char* v = ring + st * G::kTile;
-          const int base = t * kBK, from = least > base ? least - base : 0;  // rows from which some row sees no more
-          bool hit = false;
+      const auto next_tile = [&]() {  // (every phase is waited for, in the ring's order)
+        const uint32_t st = n_kv % G::kStages;
+        wait(&sh.kv_full[st], (n_kv / G::kStages) & 1);
+        ++n_kv;
+        return st;
+      };
+      const auto look = [&](int i, int least, int most, int t) {  // through V of tile t of piece i
+        const uint32_t st = next_tile();
+        if (!masked_tile(least, t) || __any_sync(0xffffffffu, *abort_flag)) return;
+        unsigned char* v = ring + st * G::kTile;
+        const int base = t * kBK, from = least > base ? least - base : 0;  // rows from which some row sees no more
+        bool hit = false;
         const auto place = [&](int u) {  // 16-byte chunk u, row after row
           const int row = u / (8 * G::kBoxes), c16 = u % (8 * G::kBoxes);
           return reinterpret_cast<uint4*>(v + (c16 >> 3) * kBK * 128 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4));
@@ -438,10 +479,19 @@ __global__ void __launch_bounds__(kBThreads, 1)
 #pragma unroll 8
         for (int u = until + lane; u < kBK * 8 * G::kBoxes; u += 32) *place(u) = make_uint4(0, 0, 0, 0);
         if (hit) sh.piece[i % kBRing].bad = 1;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.v_ok[st]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.v_ok[st]);
+      };
+      for (int i = 0;; ++i) {
+        AttnPiece w;
+        if (!take(i, &w)) break;
+        const int least = attn_sees(p, w, 0), most = attn_sees(p, w, w.tokens - 1);
+        for (int t = w.t0; t < w.t1; ++t) {
+          next_tile();  // K
+          if (t > w.t0) look(i, least, most, t - 1);
         }
+        if (w.t0 < w.t1) look(i, least, most, w.t1 - 1);
         give(i);
       }
     }
@@ -449,16 +499,24 @@ __global__ void __launch_bounds__(kBThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------------- softmax
     const int h = warp >> 2, qd = warp & 3, row = 32 * qd + lane;
-    const uint32_t ts = tb + ((uint32_t)(32 * qd) << 16) + kColS + 128 * h;
+    const uint32_t ts = tb + ((uint32_t)(32 * qd) << 16) + kColS, tp = ts + kColP + 64 * h;
     const uint32_t to = tb + ((uint32_t)(32 * qd) << 16) + kColO + 128 * h;
     const float sc = p.scale * kAttnLog2e;
-    uint32_t n_s = 0, n_o = 0;
+    const int half = p.item / 2, row_token = h * half + row / p.group, member = row % p.group;
+    const bool row_used = row < half * p.group;
+    uint32_t n_s = 0;  // tiles so far
     bool alive = true;
+    // whether O has taken the weights of tile n of this half (from 1 on)
+    const auto o_done = [&](uint32_t n) {
+      if (n > 0) alive = __all_sync(0xffffffffu, wait(&sh.o_done[h], (n - 1) & 1));
+      tc::fence_after_sync();
+      return alive;
+    };
     for (int i = 0;; ++i) {
       AttnPiece w;
       if (!take(i, &w)) break;
-      const int half = p.item / 2, at = h * half + row / p.group;  // token of the item
-      const bool valid = row < half * p.group && at < w.tokens;
+      const int at = row_token;  // of the item
+      const bool valid = row_used && at < w.tokens;
       const int sees = valid ? attn_sees(p, w, at) : 0;
       const int n = half_tiles(p, w, h);
       const bool some = __any_sync(0xffffffffu, valid);
@@ -472,16 +530,19 @@ __global__ void __launch_bounds__(kBThreads, 1)
         tc::fence_after_sync();
         if (!some) {  // no row of this warp counts
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&sh.p_ready[h][0]);
-            mbar_arrive(&sh.p_ready[h][1]);
-          }
+          if (lane == 0) mbar_arrive(&sh.s_free);
+          // (the other warps' weights of the tile before are counted)
+          if (!o_done(n_s - 1)) break;
+          if (lane == 0) mbar_arrive(&sh.p_ready[h]);
           continue;
         }
         float s[kBK];
 #pragma unroll
         for (int c = 0; c < kBK; c += 32) tmem_ld32(ts + c, s + c);
         tc::tmem_wait_ld();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.s_free);
         const int t = w.t0 + j;
         if (masked_tile(least, t)) {
           const int lim = sees - t * kBK;
@@ -500,7 +561,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
         } else {
           const bool grow = high - M > kBGrow;
           if (__any_sync(0xffffffffu, grow)) {
-            // (the products before these scores, and with them O, are complete)
+            if (!o_done(n_s - 1)) break;
             const float f = grow ? exp2_fast(M - high) : 1.f;
             if (grow) M = high;
             sum = make_float2(sum.x * f, sum.y * f);
@@ -515,6 +576,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
             }
           }
         }
+        // O has taken the weights of the tile before, whose place these take
+        if (!o_done(n_s - 1)) break;
         const float base = M == -INFINITY ? 0.f : Half<T>::kLift - M;
         const float2 sc2 = make_float2(sc, sc), base2 = make_float2(base, base), one = make_float2(1.f, 1.f);
 #pragma unroll
@@ -528,23 +591,17 @@ __global__ void __launch_bounds__(kBThreads, 1)
             sum = fma2(x, one, sum);
             r[e] = Half<T>::pack(x.x, x.y);
           }
-          tc::tmem_st16u(ts + c / 2, r);
-          if (c == 32 || c == 96) {
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_ready[h][c / 64]);
-          }
+          tc::tmem_st16u(tp + c / 2, r);
         }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_ready[h]);
       }
+      if (!alive) break;
       // ---- the outputs
-      if (n > 0) {
-        alive = alive && __all_sync(0xffffffffu, wait(&sh.o_full[h], n_o & 1));
-        if (!alive) break;
-        ++n_o;
-        tc::fence_after_sync();
-      }
       if (some) {
+        if (n > 0 && !o_done(n_s)) break;
         const float l = sum.x + sum.y, top = M - (M == -INFINITY ? 0.f : Half<T>::kLift);
         const bool bad = *(volatile int*)&sh.piece[i % kBRing].bad != 0;
         const int item_least = attn_sees(p, w, 0);
@@ -553,10 +610,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
         AttnPrior prior{false, 0.f};
         if (valid) {
           const int64_t token = w.q0 + at;
-          const int head = attn_head(p, w.kh, row % p.group);
+          const int head = attn_head(p, w.kh, member);
           if (w.part != kAttnWhole) {
             const int64_t slot = attn_slot(blockIdx.x, w.part);
-            const int64_t slot_row = slot * p.part_rows + at * p.group + row % p.group;
+            const int64_t slot_row = slot * p.part_rows + at * p.group + member;
             p.part_ml[slot_row] = make_float2(top, l);
             to_row = slot_row * D;
           } else {
