@@ -751,10 +751,9 @@ gdn_status check_attn(const gdn_dims* dims, int32_t num_seqs, const int32_t* cu_
       return GDN_ERR_EXTENT;
     if (st * es % 16 != 0) return GDN_ERR_ALIGN;
   }
-  // the units of the work (tiles of keys, of items, of heads) are counted in
-  // 64 bits: at most a tile of 64 keys for each token and key head
-  int64_t units = 0;
-  if (!mul_ok((total_tokens + num_seqs) * Hk, kv_rows / 64 + 2, &units)) return GDN_ERR_EXTENT;
+  // the work (keys, of at most so many items and heads) is counted in 64 bits
+  int64_t cost = 0;
+  if (!mul_ok((total_tokens + num_seqs) * Hk, kv_rows + 1024, &cost)) return GDN_ERR_EXTENT;
   const void* ptrs[] = {cu_seqlens, q, k, v, out, lse, workspace};
   for (const void* ptr : ptrs)
     if (!aligned16(ptr)) return GDN_ERR_ALIGN;

@@ -4,16 +4,18 @@
 //
 // How the work is cut. A sequence's tokens are taken `item` at a time: an item
 // is those tokens' rows (token, query head of the group) for one key head, its
-// keys are read in tiles of KT. A tile of an item is a unit, and kAttnStart
-// more stand for an item's start and end; units lie in one order (sequence,
-// key head, item, tile), and CTA c of G takes the c-th of G equal stretches of
-// them, whatever the lengths are. An item that lies across
-// a border is left in parts, each (largest score, sum, unnormalised output)
-// in fp32 in the workspace, and attn_join_kernel puts them together. So one
-// long cache is spread over all SMs, ragged prompts leave no SM behind, and
+// keys are read in tiles of KT. An item costs the keys that its last token
+// sees, and kAttnStart tiles for its start and end; costs lie in one order
+// (sequence, key head, item, key), and CTA c of G takes the c-th of G equal
+// stretches of them, whatever the lengths are, cut to tiles. An item that lies
+// across a border is left in parts, each (largest score, sum, unnormalised
+// output) in fp32 in the workspace, and attn_join_kernel puts them together. So
+// one long cache is spread over all SMs, ragged prompts leave no SM behind, and
 // sums do not depend on which CTA ran first. The lengths are on the device:
-// every CTA adds up the units for itself, its threads a slice of the
-// sequences each, the items of a sequence in closed form.
+// every CTA adds up the costs for itself, its threads a slice of the sequences
+// each. What a CTA runs once comes from a cold instruction cache, so this is
+// kept short: costs are sums of arithmetic series (exact numbers of tiles would
+// be sums of floors: 17,000 cycles instead of 5,000).
 #pragma once
 
 #include "gdn_common.cuh"
@@ -52,17 +54,37 @@ __device__ __forceinline__ int attn_visible(const AttnArgs& p, const AttnSeq& s,
   return v > 0 ? (int)v : 0;
 }
 
-// What an item costs besides its tiles, in tiles: those of the first tokens of
-// a prompt have few.
-constexpr int kAttnStart = 1;
+// What an item costs besides its keys, in tiles.
+constexpr int kAttnStart = 2;
 
-// Tiles of the item whose first token is `at`, or one where it sees nothing
-// (its outputs are written all the same).
+// Keys that the last token of the item from `at` on sees.
+__device__ __forceinline__ int attn_last_sees(const AttnArgs& p, const AttnSeq& s, int at) {
+  return attn_visible(p, s, (s.qn - at < p.item ? s.qn : at + p.item) - 1);
+}
+
+// Cost of a sequence's first n items, for one key head; all but the last item
+// of a sequence are full.
 template <int KT>
-__device__ __forceinline__ int attn_tiles(const AttnArgs& p, const AttnSeq& s, int at) {
-  const int last = (s.qn - at < p.item ? s.qn : at + p.item) - 1;
-  const int v = attn_visible(p, s, last);
-  return v > KT ? v / KT + (v % KT != 0) : 1;
+__device__ __forceinline__ int64_t attn_cost_before(const AttnArgs& p, const AttnSeq& s, int n) {
+  const int64_t start = (int64_t)n * (kAttnStart * KT);
+  if (!p.causal) return start + (int64_t)n * s.kn;
+  const int64_t off = (int64_t)s.kn - s.qn;  // item i's last token sees off + (i + 1) item keys
+  int none = 0;                              // items that see nothing
+  if (off < 0) {
+    none = (int)((unsigned)-off / (unsigned)p.item);
+    if (none > n) none = n;
+  }
+  const int64_t m = n - none;
+  return start + m * off + p.item * (m * none + m * (m + 1) / 2);
+}
+__device__ __forceinline__ int attn_items(const AttnArgs& p, const AttnSeq& s) {
+  return (int)((unsigned)(s.qn - 1) / (unsigned)p.item) + 1;
+}
+// Cost of a sequence for one key head.
+template <int KT>
+__device__ __forceinline__ int64_t attn_seq_cost(const AttnArgs& p, const AttnSeq& s) {
+  if (s.qn == 0) return 0;
+  return attn_cost_before<KT>(p, s, attn_items(p, s) - 1) + s.kn + kAttnStart * KT;
 }
 
 // a / b and its remainder, in 32 bits where they fit (a 64-bit division takes
@@ -73,59 +95,6 @@ __device__ __forceinline__ int64_t attn_divide(int64_t a, int64_t b, int64_t* re
   else q = a / b;
   *rest = a - q * b;
   return q;
-}
-
-// sum of floor((a i + b) / m) over 0 <= i < n, for a, b < m: what reaches m
-// counts the points of a lattice under a line, the same with the axes
-// exchanged, and whole multiples of m in a and b add arithmetic series.
-// a n + b has to fit U.
-template <typename U>
-__device__ __forceinline__ int64_t attn_lattice(U n, U m, U a, U b) {
-  int64_t sum = 0;
-  for (;;) {
-    const U top = a * n + b;
-    if (top < m) return sum;
-    n = top / m;
-    b = top % m;
-    const U t = m;
-    m = a;
-    a = t;
-    if (a >= m) {
-      sum += (int64_t)(a / m) * ((int64_t)n * (n - 1) / 2);
-      a %= m;
-    }
-    if (b >= m) {
-      sum += (int64_t)(b / m) * n;
-      b %= m;
-    }
-  }
-}
-// sum of floor((item i + b) / KT) over 0 <= i < n, b >= 0
-template <int KT>
-__device__ __forceinline__ int64_t attn_floor_sum(int64_t n, int item, int64_t b) {
-  const int64_t sum = (item / KT) * (n * (n - 1) / 2) + (b / KT) * n;
-  const unsigned a = (unsigned)item % KT, r = (unsigned)(b % KT);
-  return sum + (n < (1 << 22) ? attn_lattice<unsigned>((unsigned)n, KT, a, r) : attn_lattice<int64_t>(n, KT, a, r));
-}
-// Units of a sequence's first n items, for one key head; all but the last item
-// of a sequence are full.
-template <int KT>
-__device__ __forceinline__ int64_t attn_units_before(const AttnArgs& p, const AttnSeq& s, int64_t n) {
-  if (!p.causal) return n * (attn_tiles<KT>(p, s, 0) + kAttnStart);
-  const int64_t off = (int64_t)s.kn - s.qn;  // item i's last token sees off + (i + 1) item keys
-  // the first `one` items have one tile (they see KT keys at most)
-  int64_t one = off + p.item > KT ? 0 : (unsigned)(KT - off) / (unsigned)p.item;
-  if (one > n) one = n;
-  // ceil((off + (one + 1 + i) item) / KT) for the others
-  const int64_t first = off + (one + 1) * p.item + KT - 1;
-  return one + (n > one ? attn_floor_sum<KT>(n - one, p.item, first) : 0) + n * kAttnStart;
-}
-// Units of a sequence for one key head.
-template <int KT>
-__device__ __forceinline__ int64_t attn_seq_units(const AttnArgs& p, const AttnSeq& s) {
-  if (s.qn == 0) return 0;
-  const int items = (s.qn - 1) / p.item + 1;
-  return attn_units_before<KT>(p, s, items - 1) + attn_tiles<KT>(p, s, (items - 1) * p.item) + kAttnStart;
 }
 
 // A stretch of an item's tiles, for one CTA.
@@ -147,7 +116,7 @@ __device__ __forceinline__ int attn_sees(const AttnArgs& p, const AttnPiece& w, 
 }
 
 struct AttnPlan {
-  int64_t begin, count;  // the CTA's first unit, counted from sequence n, and how many
+  int64_t begin, count;  // where the CTA's stretch begins, counted from sequence n, and its cost
   int n;
 };
 
@@ -158,7 +127,7 @@ __device__ __forceinline__ void attn_plan(const AttnArgs& p, int64_t* sums, Attn
   {
     const int64_t a = (int64_t)threadIdx.x * per, b = a + per < p.N ? a + per : p.N;
     int64_t u = 0;
-    for (int64_t n = a; n < b; ++n) u += attn_seq_units<KT>(p, attn_seq(p, (int)n));
+    for (int64_t n = a; n < b; ++n) u += attn_seq_cost<KT>(p, attn_seq(p, (int)n));
     sums[threadIdx.x] = u * p.Hk;
   }
   __syncthreads();
@@ -175,11 +144,12 @@ __device__ __forceinline__ void attn_plan(const AttnArgs& p, int64_t* sums, Attn
       if (lane >= d) incl += o;
     }
     const int64_t total = __shfl_sync(0xffffffffu, incl, 31);
-    // units < 2^31 key tiles x 2^16 sequences' items x heads: the products stay in 64 bits
-    const int64_t G = gridDim.x, c = blockIdx.x;
+    // no stretch is shorter than a tile, so that the parts of an item are neighbouring CTAs'
+    const int64_t c = blockIdx.x, most = total / KT;
+    const int64_t G = most < 1 ? 1 : most < gridDim.x ? most : gridDim.x;
     int64_t more;
     const int64_t each = attn_divide(total, G, &more);
-    const int64_t u0 = each * c + (c < more ? c : more), count = each + (c < more ? 1 : 0);
+    const int64_t u0 = each * c + (c < more ? c : more), count = c < G ? each + (c < more ? 1 : 0) : 0;
     if (lane == 0 && count == 0) *plan = AttnPlan{0, 0, p.N};
     if (count > 0 && u0 >= incl - own && u0 < incl) {
       int64_t at = u0 - (incl - own);
@@ -195,54 +165,55 @@ __device__ __forceinline__ void attn_plan(const AttnArgs& p, int64_t* sums, Attn
 template <int KT>
 struct AttnWalk {
   AttnSeq s;
-  int64_t left;
-  int n, kh, at, tile;
+  int64_t left, pos;  // cost left of the stretch; where in the item it goes on
+  int n, kh, at;
   bool whole;  // no item is cut: those that begin in the stretch are taken to their ends
 
   __device__ __forceinline__ void start(const AttnArgs& p, const AttnPlan& plan, int lane) {
     left = plan.count;
     whole = p.part_o == nullptr;
     n = plan.n;
-    kh = at = tile = 0;
+    kh = at = 0;
+    pos = 0;
     if (left <= 0) return;
     // the sequence: the lanes have 32 of them
-    int64_t u = plan.begin;
-    for (;; n += 32) {
-      const int64_t own = n + lane < p.N ? attn_seq_units<KT>(p, attn_seq(p, n + lane)) * p.Hk : 0;
-      int64_t incl = own;
-#pragma unroll
+    int64_t u = plan.begin, own, incl;
+    unsigned past;
+    for (;;) {
+      own = n + lane < p.N ? attn_seq_cost<KT>(p, attn_seq(p, n + lane)) * p.Hk : 0;
+      incl = own;
+#pragma unroll 1
       for (int d = 1; d < 32; d <<= 1) {
         const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
         if (lane >= d) incl += o;
       }
-      const unsigned past = __ballot_sync(0xffffffffu, incl > u);
-      if (past != 0) {
-        const int l = __ffs(past) - 1;
-        n += l;
-        u -= __shfl_sync(0xffffffffu, incl - own, l);
-        break;
-      }
+      past = __ballot_sync(0xffffffffu, incl > u);
+      if (past != 0) break;
       u -= __shfl_sync(0xffffffffu, incl, 31);
+      n += 32;
     }
+    const int l = __ffs(past) - 1;
+    n += l;
+    u -= __shfl_sync(0xffffffffu, incl - own, l);
     s = attn_seq(p, n);
-    const int64_t head = attn_seq_units<KT>(p, s);
-    kh = (int)attn_divide(u, head, &u);
-    // the item: the last one with no more than u units before it, among 32 evenly spaced ones at a time
-    int64_t lo = 0, count = (s.qn - 1) / p.item + 1;
+    kh = (int)attn_divide(u, attn_seq_cost<KT>(p, s), &u);
+    // the item: the last one with no more than u before it, among 32 evenly spaced ones at a time
+    int lo = 0, count = attn_items(p, s);
+#pragma unroll 1
     while (count > 1) {
-      const int64_t step = (count + 31) / 32, i = lo + lane * step;
-      const bool in = lane * step < count && attn_units_before<KT>(p, s, i) <= u;
-      const int l = 31 - __clz(__ballot_sync(0xffffffffu, in));  // (lane 0's is)
-      lo += l * step;
-      count = count - l * step < step ? count - l * step : step;
+      const int step = (count + 31) / 32;
+      const bool in = lane * step < count && attn_cost_before<KT>(p, s, lo + lane * step) <= u;
+      const int k = 31 - __clz(__ballot_sync(0xffffffffu, in));  // (lane 0's is)
+      lo += k * step;
+      count = count - k * step < step ? count - k * step : step;
     }
-    u -= attn_units_before<KT>(p, s, lo);
-    at = (int)(lo * p.item);
-    tile = (int)u;
-    const int tiles = attn_tiles<KT>(p, s, at);
-    if (tile >= tiles || (whole && tile > 0)) {  // the CTA before takes it to its end
-      left -= tiles + kAttnStart - tile;
-      tile = 0;
+    pos = u - attn_cost_before<KT>(p, s, lo);
+    at = lo * p.item;
+    // the CTA before takes it to its end?
+    const int seen = attn_last_sees(p, s, at);
+    if (whole ? pos > 0 : pos / KT >= (seen > KT ? (seen + KT - 1) / KT : 1)) {
+      left -= seen + kAttnStart * KT - pos;
+      pos = 0;
       step(p);
     }
   }
@@ -262,22 +233,23 @@ struct AttnWalk {
   __device__ __forceinline__ AttnPiece next(const AttnArgs& p) {
     AttnPiece w{};
     if (left <= 0) return w;
-    const int tiles = attn_tiles<KT>(p, s, at), rest = tiles + kAttnStart - tile;
-    const int take = whole || left >= rest ? rest : (int)left;
-    const bool ends = tile + take >= tiles;
+    const int seen = attn_last_sees(p, s, at), keys = (seen + KT - 1) / KT, tiles = keys > 0 ? keys : 1;
+    const int64_t rest = seen + kAttnStart * KT - pos;
+    const int from = (int)(pos / KT);
+    int to = tiles;
+    if (!whole && left < rest && (pos + left) / KT < tiles) to = (int)((pos + left) / KT);
+    left -= rest;
+    if (to == from) return w;  // less than a tile, which the CTA after takes
     w.q0 = s.q0 + at;
     w.tokens = s.qn - at < p.item ? s.qn - at : p.item;
     w.kh = kh;
     w.k0 = s.k0;
     w.see = p.causal ? (int)((int64_t)s.kn - s.qn + at + 1) : s.kn;
-    const int seen = attn_sees(p, w, w.tokens - 1);
-    const int keys = seen / KT + (seen % KT != 0);  // 0 where a tile stands for none
-    w.t0 = tile < keys ? tile : keys;
-    w.t1 = tile + take < keys ? tile + take : keys;
-    w.part = tile > 0 ? (ends ? kAttnLast : kAttnMiddle) : (ends ? kAttnWhole : kAttnFirst);
-    left -= take;
-    tile = 0;
-    step(p);  // (where the item goes on, so does another CTA)
+    w.t0 = from < keys ? from : keys;
+    w.t1 = to < keys ? to : keys;  // (no tile where one stands for none)
+    w.part = from > 0 ? (to == tiles ? kAttnLast : kAttnMiddle) : (to == tiles ? kAttnWhole : kAttnFirst);
+    pos = 0;
+    step(p);  // (where the item goes on, so does another CTA: nothing is left here)
     return w;
   }
 };

@@ -19,20 +19,19 @@
 // to wait for its O += P V: a chain of softmax and both products, 3400 cycles
 // for both tiles, where the products alone take 2048.
 //
-// Warps 0 to 3 are A's rows, 4 to 7 B's; one warp issues the products, one
-// loads (Q once an item, K and V through a ring of tiles), one hands out the
-// pieces of work (attn_common.cuh), one looks through masked tiles of V: a
+// Warps 0 to 3 are A's rows, 4 to 7 B's; two issue the products, one hands out
+// the pieces of work (attn_common.cuh) and loads (Q once an item, K and V
+// through a ring of tiles), one looks through masked tiles of V: a
 // masked weight is 0, but 0 times what is not finite would reach rows that do
 // not see it. So rows of V that nobody sees become 0, and in rows that only
 // some see what is not finite is replaced by 0 and added, at the end, to the
 // rows that do see it.
 //
-// Order of a piece's products over its tiles of keys k: O of B for k - 2,
-// scores of A for k, O of A for k - 1, scores of B for k. So a tile's O comes as
-// soon as its weights are there and is done before the next ones want their
-// place, and what follows are the scores that the other tile wants next. (The
-// scores first: 225 instead of 194 us for a prompt of 4096 tokens.) The ring's
-// order is that of the first use: K of k, V of k - 1.
+// One warp issues the scores, another O += P V: the tensor cores take a few
+// products ahead from each, and an issuing warp is held until they do, so that
+// with one warp for both whatever the other kind waited for was looked at late
+// (a gap of 600 cycles in each 1800). The order between the two is what S and P
+// make it.
 //
 // A wait that gives up raises the CTA's abort flag; every role then leaves its
 // loop at once.
@@ -47,25 +46,29 @@ namespace {
 constexpr int kBR = 128;          // rows of a tile
 constexpr int kBK = 128;          // keys of a tile
 constexpr int kBThreads = 384;
-constexpr int kBMma = 8, kBLoad = 9, kBPlan = 10, kBCheck = 11;  // warps
+constexpr int kBScores = 8, kBLoad = 9, kBOut = 10, kBCheck = 11;  // warps
 constexpr int kBRing = 4;         // pieces handed out ahead
-constexpr int kBTakers = 11;      // warps that take each piece
+constexpr int kBTakers = 11;      // warps that take each piece: all but the one that loads
 constexpr float kBGrow = 8.f;     // log2 by which a weight may exceed 1
 
 template <int D>
 struct TcGeom {
   static constexpr int kBoxes = (D + 63) / 64;
   static constexpr uint32_t kTile = kBoxes * kBK * 128;  // bytes
-  static constexpr int kStages = kBoxes == 2 ? 4 : 8;
-  static constexpr uint32_t kOut = (2 + kStages) * kTile;  // 4 KB for each warp of rows
-  static constexpr uint32_t kSmem = kOut + 8 * 4096;
+  static constexpr int kStages = kBoxes == 2 ? 2 : 4;  // of each ring
+  static constexpr uint32_t kK = 2 * kTile, kV = kK + kStages * kTile;
+  static constexpr uint32_t kOut = kV + kStages * kTile;  // 2 KB for each warp of rows
+  static constexpr uint32_t kSmem = kOut + 8 * 2048;
 };
 
 // TMEM columns: S, P of both tiles (64 each), O of both (128 each)
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 256, kCols = 512;
 
 struct BShared {
-  uint64_t kv_full[8], kv_empty[8], v_ok[8];
+  // the rings of K, which the scores' warp empties, and of V, which the
+  // outputs' warp and the one that looks through it do: whoever waits for a
+  // tile also has to give it back, so no phase of a barrier goes by unseen
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], v_ok[4];
   uint64_t q_full[2], q_empty[2], s_full[2], s_free, p_ready[2], o_done[2];
   uint64_t piece_full[kBRing], piece_empty[kBRing];
   AttnPiece piece[kBRing];
@@ -242,18 +245,19 @@ __global__ void __launch_bounds__(kBThreads, 1)
   using G = TcGeom<D>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  unsigned char* ring = sm + 2 * G::kTile;
   __shared__ BShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
-  if (warp == kBMma) {
+  if (warp == kBScores) {
     tc::tmem_alloc(&sh.tmem, kCols);
     tc::tmem_relinquish();
   }
   if (tid == 0) {
     for (int i = 0; i < G::kStages; ++i) {
-      mbar_init(&sh.kv_full[i], 1);
-      mbar_init(&sh.kv_empty[i], 1);
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.v_full[i], 1);
+      mbar_init(&sh.v_empty[i], 2);
       mbar_init(&sh.v_ok[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
     fence_mbar_init();
   }
   if (tid < 2 && p.part_o != nullptr) p.part_at[2 * blockIdx.x + tid] = make_int4(kAttnWhole, 0, 0, 0);
-  attn_plan<kBK, kBThreads>(p, reinterpret_cast<int64_t*>(ring), &sh.plan);  // (the ring is not in use yet)
+  attn_plan<kBK, kBThreads>(p, reinterpret_cast<int64_t*>(sm), &sh.plan);  // (nothing is loaded yet)
   fence_proxy_async_smem();
   tc::fence_before_sync();
   __syncthreads();
@@ -298,8 +302,23 @@ __global__ void __launch_bounds__(kBThreads, 1)
   // one keeps 80: 63488.
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == kBPlan) {
-      // -------------------------------------------------------------- pieces
+    if (warp == kBLoad) {
+      // ----------------------------------------------------- pieces and loads
+      uint32_t n_k = 0, n_v = 0, n_q[2] = {0, 0};
+      const uint32_t q_bytes = (uint32_t)(G::kBoxes * 128 * (p.item / 2) * p.group);
+      bool ok = true;
+      const auto load = [&](const CUtensorMap* map, unsigned char* ring, uint64_t* full, uint64_t* empty, uint32_t& n,
+                            int kh, int row) {
+        const uint32_t st = n % G::kStages, round = n / G::kStages;
+        ok = ok && (round == 0 || wait(&empty[st], (round - 1) & 1));
+        if (!ok) return;
+        ++n;
+        mbar_arrive_expect_tx(&full[st], G::kTile);
+        for (int b = 0; b < G::kBoxes; ++b)
+          tma_load_3d(ring + st * G::kTile + b * kBK * 128, map, 64 * b, kh, row, &full[st]);
+      };
+      const auto load_k = [&](int kh, int row) { load(&tm_k, sm + G::kK, sh.k_full, sh.k_empty, n_k, kh, row); };
+      const auto load_v = [&](int kh, int row) { load(&tm_v, sm + G::kV, sh.v_full, sh.v_empty, n_v, kh, row); };
       AttnWalk<kBK> walk;
       walk.start(p, sh.plan, lane);
       for (int i = 0;; ++i) {
@@ -310,24 +329,6 @@ __global__ void __launch_bounds__(kBThreads, 1)
           mbar_arrive(&sh.piece_full[i % kBRing]);
         }
         if (w.tokens == 0) break;
-      }
-    } else if (warp == kBLoad) {
-      // --------------------------------------------------------------- loads
-      uint32_t n_kv = 0, n_q[2] = {0, 0};
-      const uint32_t q_bytes = (uint32_t)(G::kBoxes * 128 * (p.item / 2) * p.group);
-      bool ok = true;
-      const auto load_kv = [&](const CUtensorMap* map, int kh, int row) {
-        const uint32_t st = n_kv % G::kStages, round = n_kv / G::kStages;
-        ok = ok && (round == 0 || wait(&sh.kv_empty[st], (round - 1) & 1));
-        if (!ok) return;
-        ++n_kv;
-        mbar_arrive_expect_tx(&sh.kv_full[st], G::kTile);
-        for (int b = 0; b < G::kBoxes; ++b)
-          tma_load_3d(ring + st * G::kTile + b * kBK * 128, map, 64 * b, kh, row, &sh.kv_full[st]);
-      };
-      for (int i = 0;; ++i) {
-        AttnPiece w;
-        if (!take(i, &w)) break;
         if (lane == 0 && ok) {
           const auto load_q = [&](int h) {
             if (half_tiles(p, w, h) == 0) return;
@@ -341,157 +342,162 @@ __global__ void __launch_bounds__(kBThreads, 1)
           };
           for (int t = w.t0; ok && t < w.t1; ++t) {
             if (t == w.t0) load_q(0);
-            load_kv(&tm_k, w.kh, w.k0 + t * kBK);
+            load_k(w.kh, w.k0 + t * kBK);
             if (t == w.t0) load_q(1);
-            else load_kv(&tm_v, w.kh, w.k0 + (t - 1) * kBK);
+            else load_v(w.kh, w.k0 + (t - 1) * kBK);
           }
-          if (ok && w.t0 < w.t1) load_kv(&tm_v, w.kh, w.k0 + (w.t1 - 1) * kBK);
+          if (ok && w.t0 < w.t1) load_v(w.kh, w.k0 + (w.t1 - 1) * kBK);
         }
-        give(i);
+        __syncwarp();
       }
       if (lane == 0) {
         // nothing may be in flight when the CTA ends: neither a copy nor the
         // arrival that gives a tile back
-        for (uint32_t u = n_kv > G::kStages ? n_kv - G::kStages : 0; u < n_kv; ++u) {
-          mbar_wait(&sh.kv_full[u % G::kStages], (u / G::kStages) & 1);
-          wait(&sh.kv_empty[u % G::kStages], (u / G::kStages) & 1);
-        }
+        const auto over = [&](uint64_t* full, uint64_t* empty, uint32_t n) {
+          for (uint32_t u = n > G::kStages ? n - G::kStages : 0; u < n; ++u) {
+            mbar_wait(&full[u % G::kStages], (u / G::kStages) & 1);
+            wait(&empty[u % G::kStages], (u / G::kStages) & 1);
+          }
+        };
+        over(sh.k_full, sh.k_empty, n_k);
+        over(sh.v_full, sh.v_empty, n_v);
         for (int h = 0; h < 2; ++h)
           if (n_q[h] > 0) {
             mbar_wait(&sh.q_full[h], (n_q[h] - 1) & 1);
             wait(&sh.q_empty[h], (n_q[h] - 1) & 1);
           }
       }
-    } else if (warp == kBMma) {
+    } else if (warp == kBScores || warp == kBOut) {
       // ------------------------------------------------------------ products
-      // (the whole warp goes through this, and one lane issues: addresses stay
-      // in uniform registers, where one lane's branch took twice as long)
-      const uint32_t id_s = tc::idesc(Half<T>::kFormat, kBR, kBK), id_o = tc::idesc(Half<T>::kFormat, kBR, D) | kTransB;
-      const uint64_t dq = tc::sdesc_sw128(smem_u32(sm)), dk = tc::sdesc_sw128(smem_u32(ring));
-      const uint64_t dv = sdesc_v(smem_u32(ring));
+      // (a whole warp goes through this, and one lane issues: addresses stay
+      // in uniform registers, where one lane's branch took twice as long. For
+      // the same end what is read from shared memory is taken from one lane,
+      // so that the compiler knows it to be the same in all.)
       const auto all = [&](bool x) { return __all_sync(0xffffffffu, x); };
-      uint32_t n_kv = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_s = 0, ok_bits = 0;
+      const auto same = [&](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+      uint32_t n_kv = 0, n[2] = {0, 0};
       bool ok = true;
       // the stage of the ring's next tile, once it is there
-      const auto next_tile = [&]() {
+      const auto next_tile = [&](uint64_t* full) {
         const uint32_t st = n_kv % G::kStages;
-        ok = all(wait(&sh.kv_full[st], (n_kv / G::kStages) & 1));
+        ok = all(wait(&full[st], (n_kv / G::kStages) & 1)) && ok;
         ++n_kv;
         return st;
       };
-      const auto scores = [&](int h, uint32_t st, bool first, bool last) {
-        if (first) {
-          ok = ok && all(wait(&sh.q_full[h], n_q[h] & 1));
-          ++n_q[h];
-        }
-        ok = ok && (n_s == 0 || all(wait(&sh.s_free, (n_s - 1) & 1)));
-        ++n_s;
-        if (!ok) return;
-        tc::fence_after_sync();
-        const uint64_t a = dq + (h * G::kTile >> 4), b = dk + (st * G::kTile >> 4);
-        constexpr uint32_t next = kBK * 128 >> 4;  // the second 64 columns
-        mma_ss<D == 32 ? 2 : 4>(tb + kColS, a, b, id_s, false);
-        if (D > 64) mma_ss<D == 96 ? 2 : 4>(tb + kColS, a + next, b + next, id_s, true);
-        tc::mma_commit_elect(&sh.s_full[h]);
-        if (last) tc::mma_commit_elect(&sh.q_empty[h]);
-      };
-      const auto outputs = [&](int h, uint32_t st, bool accumulate) {
-        ok = ok && all(wait(&sh.p_ready[h], n_p[h] & 1));
-        ++n_p[h];
-        if (!ok) return;
-        tc::fence_after_sync();
-        const uint64_t b = dv + (st * G::kTile >> 4);
-        mma_ts4(tb + kColO + 128 * h, tb + kColP + 64 * h, b, id_o, accumulate);
-        mma_ts4(tb + kColO + 128 * h, tb + kColP + 64 * h + 32, b + (8192 >> 4), id_o, true);
-        tc::mma_commit_elect(&sh.o_done[h]);
-      };
-      for (int i = 0; ok; ++i) {
-        AttnPiece w;
-        if (!take(i, &w)) break;
-        // from one lane, so that the compiler knows them to be the same in all
-        const int least = __shfl_sync(0xffffffffu, attn_sees(p, w, 0), 0), t0 = __shfl_sync(0xffffffffu, w.t0, 0);
-        const int na = __shfl_sync(0xffffffffu, half_tiles(p, w, 0), 0);
-        const int nb = __shfl_sync(0xffffffffu, half_tiles(p, w, 1), 0);
-        const int tiles = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
-        uint32_t sv = 0;  // the stage of V of the tile before
-        for (int j = 0; ok && j <= tiles; ++j) {
-          uint32_t sk = 0;
-          if (j < tiles) sk = next_tile();
-          if (j > 1) {
-            if (j - 2 < nb) outputs(1, sv, j > 2);
-            if (ok) tc::mma_commit_elect(&sh.kv_empty[sv]);
-          }
-          if (j < na) scores(0, sk, j == 0, j + 1 == na);
-          if (ok && j > 0) {
-            sv = next_tile();
-            if (ok && masked_tile(least, t0 + j - 1)) {
-              ok = all(wait(&sh.v_ok[sv], (ok_bits >> sv) & 1));
-              ok_bits ^= 1u << sv;
+      if (warp == kBScores) {
+        const uint32_t id = tc::idesc(Half<T>::kFormat, kBR, kBK);
+        const uint64_t dq = tc::sdesc_sw128(smem_u32(sm)), dk = tc::sdesc_sw128(smem_u32(sm + G::kK));
+        uint32_t n_s = 0;
+        for (int i = 0; ok; ++i) {
+          AttnPiece w;
+          if (!take(i, &w)) break;
+          const int tiles = same(w.t1 - w.t0), na = same(half_tiles(p, w, 0)), nb = same(half_tiles(p, w, 1));
+          for (int j = 0; ok && j < tiles; ++j) {
+            const uint32_t st = next_tile(sh.k_full);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (j >= (h ? nb : na)) continue;
+              if (j == 0) {
+                ok = ok && all(wait(&sh.q_full[h], n[h] & 1));
+                ++n[h];
+              }
+              ok = ok && (n_s == 0 || all(wait(&sh.s_free, (n_s - 1) & 1)));
+              ++n_s;
+              if (!ok) continue;
+              tc::fence_after_sync();
+              const uint64_t a = dq + (h * G::kTile >> 4), b = dk + (st * G::kTile >> 4);
+              constexpr uint32_t next = kBK * 128 >> 4;  // the second 64 columns
+              mma_ss<D == 32 ? 2 : 4>(tb + kColS, a, b, id, false);
+              if (D > 64) mma_ss<D == 96 ? 2 : 4>(tb + kColS, a + next, b + next, id, true);
+              tc::mma_commit_elect(&sh.s_full[h]);
+              if (j + 1 == (h ? nb : na)) tc::mma_commit_elect(&sh.q_empty[h]);
             }
-            if (j - 1 < na) outputs(0, sv, j > 1);
+            if (ok) tc::mma_commit_elect(&sh.k_empty[st]);
           }
-          if (j < nb) scores(1, sk, j == 0, j + 1 == nb);
-          if (ok && j < tiles) tc::mma_commit_elect(&sh.kv_empty[sk]);
+          give(i);
         }
-        if (ok && tiles > 0) {
-          if (tiles == nb) outputs(1, sv, tiles > 1);
-          if (ok) tc::mma_commit_elect(&sh.kv_empty[sv]);
+      } else {
+        const uint32_t id = tc::idesc(Half<T>::kFormat, kBR, D) | kTransB;
+        const uint64_t dv = sdesc_v(smem_u32(sm + G::kV));
+        uint32_t ok_bits = 0;
+        for (int i = 0; ok; ++i) {
+          AttnPiece w;
+          if (!take(i, &w)) break;
+          const int tiles = same(w.t1 - w.t0), na = same(half_tiles(p, w, 0)), nb = same(half_tiles(p, w, 1));
+          const int least = same(attn_sees(p, w, 0)), t0 = same(w.t0);
+          for (int j = 0; ok && j < tiles; ++j) {
+            const uint32_t st = next_tile(sh.v_full);
+            if (ok && masked_tile(least, t0 + j)) {
+              ok = all(wait(&sh.v_ok[st], (ok_bits >> st) & 1));
+              ok_bits ^= 1u << st;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (j >= (h ? nb : na)) continue;
+              ok = ok && all(wait(&sh.p_ready[h], n[h] & 1));
+              ++n[h];
+              if (!ok) continue;
+              tc::fence_after_sync();
+              const uint64_t b = dv + (st * G::kTile >> 4);
+              mma_ts4(tb + kColO + 128 * h, tb + kColP + 64 * h, b, id, j > 0);
+              mma_ts4(tb + kColO + 128 * h, tb + kColP + 64 * h + 32, b + (8192 >> 4), id, true);
+              tc::mma_commit_elect(&sh.o_done[h]);
+            }
+            if (ok) tc::mma_commit_elect(&sh.v_empty[st]);
+          }
+          give(i);
         }
-        give(i);
       }
     } else if (warp == kBCheck) {
       // ------------------------------------------------- masked tiles of v
-      uint32_t n_kv = 0;
-      const auto next_tile = [&]() {  // (every phase is waited for, in the ring's order)
-        const uint32_t st = n_kv % G::kStages;
-        wait(&sh.kv_full[st], (n_kv / G::kStages) & 1);
-        ++n_kv;
-        return st;
-      };
-      const auto look = [&](int i, int least, int most, int t) {  // through V of tile t of piece i
-        const uint32_t st = next_tile();
-        if (!masked_tile(least, t) || __any_sync(0xffffffffu, *abort_flag)) return;
-        unsigned char* v = ring + st * G::kTile;
-        const int base = t * kBK, from = least > base ? least - base : 0;  // rows from which some row sees no more
-        bool hit = false;
-        const auto place = [&](int u) {  // 16-byte chunk u, row after row
-          const int row = u / (8 * G::kBoxes), c16 = u % (8 * G::kBoxes);
-          return reinterpret_cast<uint4*>(v + (c16 >> 3) * kBK * 128 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4));
-        };
-        const int until = most - base < kBK ? (most - base) * (8 * G::kBoxes) : kBK * 8 * G::kBoxes;
-#pragma unroll 8
-        for (int u = from * (8 * G::kBoxes) + lane; u < until; u += 32) {
-          uint4 x = *place(u);
-          uint32_t* e = &x.x;
-          uint32_t any = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) any |= (e[j] & Half<T>::kExponent) + Half<T>::kCarry;
-          if ((any & 0x80008000u) == 0) continue;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t m = (e[j] & Half<T>::kExponent) + Half<T>::kCarry;
-            if (m & 0x8000u) e[j] &= 0xffff0000u;
-            if (m & 0x80000000u) e[j] &= 0x0000ffffu;
-          }
-          *place(u) = x;
-          hit = true;
-        }
-#pragma unroll 8
-        for (int u = until + lane; u < kBK * 8 * G::kBoxes; u += 32) *place(u) = make_uint4(0, 0, 0, 0);
-        if (hit) sh.piece[i % kBRing].bad = 1;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.v_ok[st]);
-      };
+      uint32_t n_v = 0;
       for (int i = 0;; ++i) {
         AttnPiece w;
         if (!take(i, &w)) break;
         const int least = attn_sees(p, w, 0), most = attn_sees(p, w, w.tokens - 1);
         for (int t = w.t0; t < w.t1; ++t) {
-          next_tile();  // K
-          if (t > w.t0) look(i, least, most, t - 1);
+          const uint32_t st = n_v % G::kStages;
+          if (!__all_sync(0xffffffffu, wait(&sh.v_full[st], (n_v / G::kStages) & 1))) break;
+          ++n_v;
+          if (!masked_tile(least, t)) {
+            if (lane == 0) mbar_arrive(&sh.v_empty[st]);
+            continue;
+          }
+          unsigned char* v = sm + G::kV + st * G::kTile;
+          const int base = t * kBK, from = least > base ? least - base : 0;  // rows from which some row sees no more
+          bool hit = false;
+          const auto place = [&](int u) {  // 16-byte chunk u, row after row
+            const int row = u / (8 * G::kBoxes), c16 = u % (8 * G::kBoxes);
+            return reinterpret_cast<uint4*>(v + (c16 >> 3) * kBK * 128 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4));
+          };
+          const int until = most - base < kBK ? (most - base) * (8 * G::kBoxes) : kBK * 8 * G::kBoxes;
+#pragma unroll 8
+          for (int u = from * (8 * G::kBoxes) + lane; u < until; u += 32) {
+            uint4 x = *place(u);
+            uint32_t* e = &x.x;
+            uint32_t any = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) any |= (e[j] & Half<T>::kExponent) + Half<T>::kCarry;
+            if ((any & 0x80008000u) == 0) continue;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t m = (e[j] & Half<T>::kExponent) + Half<T>::kCarry;
+              if (m & 0x8000u) e[j] &= 0xffff0000u;
+              if (m & 0x80000000u) e[j] &= 0x0000ffffu;
+            }
+            *place(u) = x;
+            hit = true;
+          }
+#pragma unroll 8
+          for (int u = until + lane; u < kBK * 8 * G::kBoxes; u += 32) *place(u) = make_uint4(0, 0, 0, 0);
+          if (hit) sh.piece[i % kBRing].bad = 1;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sh.v_ok[st]);
+            mbar_arrive(&sh.v_empty[st]);
+          }
         }
-        if (w.t0 < w.t1) look(i, least, most, w.t1 - 1);
         give(i);
       }
     }
@@ -576,23 +582,21 @@ __global__ void __launch_bounds__(kBThreads, 1)
             }
           }
         }
-        // O has taken the weights of the tile before, whose place these take
-        if (!o_done(n_s - 1)) break;
         const float base = M == -INFINITY ? 0.f : Half<T>::kLift - M;
         const float2 sc2 = make_float2(sc, sc), base2 = make_float2(base, base), one = make_float2(1.f, 1.f);
+        uint32_t r[kBK / 2];
 #pragma unroll
-        for (int c = 0; c < kBK; c += 32) {
-          uint32_t r[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float2 x = fma2(make_float2(s[c + 2 * e], s[c + 2 * e + 1]), sc2, base2);
-            x.x = exp2_fast(x.x);
-            x.y = exp2_fast(x.y);
-            sum = fma2(x, one, sum);
-            r[e] = Half<T>::pack(x.x, x.y);
-          }
-          tc::tmem_st16u(tp + c / 2, r);
+        for (int c = 0; c < kBK / 2; ++c) {
+          float2 x = fma2(make_float2(s[2 * c], s[2 * c + 1]), sc2, base2);
+          x.x = exp2_fast(x.x);
+          x.y = exp2_fast(x.y);
+          sum = fma2(x, one, sum);
+          r[c] = Half<T>::pack(x.x, x.y);
         }
+        // O has taken the weights of the tile before, whose place these take
+        if (!o_done(n_s - 1)) break;
+#pragma unroll
+        for (int c = 0; c < kBK / 2; c += 16) tc::tmem_st16u(tp + c, *reinterpret_cast<uint32_t(*)[16]>(r + c));
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
@@ -603,8 +607,28 @@ __global__ void __launch_bounds__(kBThreads, 1)
       if (some) {
         if (n > 0 && !o_done(n_s)) break;
         const float l = sum.x + sum.y, top = M - (M == -INFINITY ? 0.f : Half<T>::kLift);
-        const bool bad = *(volatile int*)&sh.piece[i % kBRing].bad != 0;
-        const int item_least = attn_sees(p, w, 0);
+        if (n > 0 && *(volatile int*)&sh.piece[i % kBRing].bad != 0) {
+          // what the look through V took out of rows that this one sees
+          const int item_least = attn_sees(p, w, 0);
+          const int first = max(item_least, w.t0 * kBK), last = (int)min((int64_t)sees, (int64_t)w.t1 * kBK);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            tc::tmem_ld16(to + c, o);
+            tc::tmem_wait_ld();
+            const T* v = static_cast<const T*>(p.v) + (int64_t)w.kh * D + c;
+#pragma unroll 1
+            for (int k = first; valid && k < last; ++k)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float x = to_f32(v[(int64_t)(w.k0 + k) * p.v_stride + e]);
+                if (!isfinite(x)) o[e] += x;
+              }
+            __syncwarp();
+            tc::tmem_st16(to + c, o);
+          }
+          tc::tmem_wait_st();
+        }
         int64_t to_row = 0;
         AttnScale f{1.f, 0.f, 0.f};
         AttnPrior prior{false, 0.f};
@@ -623,72 +647,58 @@ __global__ void __launch_bounds__(kBThreads, 1)
             if (p.lse != nullptr) p.lse[token * p.Hq + head] = f.lse;
           }
         }
-        // 32 columns at a time through shared memory, so that a row's are
-        // stored side by side (from the lanes' rows a store of 16 bytes each
-        // touches 32 lines, 8000 cycles an item)
+        // 64 bytes of each row at a time through shared memory, so that they
+        // are stored side by side (from the lanes' rows a store of 16 bytes
+        // each touches 32 lines)
         const bool wide = w.part != kAttnWhole || p.core != nullptr;  // fp32
-        unsigned char* stage = sm + G::kOut + warp * 4096;
+        unsigned char* stage = sm + G::kOut + warp * 2048;
+        float* yw = w.part != kAttnWhole ? p.part_o : p.core;
+        T* yn = static_cast<T*>(p.out);
         const unsigned live = __ballot_sync(0xffffffffu, valid);
+        int64_t at_row[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) at_row[k] = __shfl_sync(0xffffffffu, to_row, 8 * k + (lane >> 2));
+        const int cols = wide ? 16 : 32;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < D; c += cols) {
           float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
           if (n > 0) {
-            tmem_ld32(to + c, o);
+            tc::tmem_ld16(to + c, *reinterpret_cast<float(*)[16]>(o));
+            if (!wide) tc::tmem_ld16(to + c + 16, *reinterpret_cast<float(*)[16]>(o + 16));
             tc::tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.f;
-          }
-          if (valid && bad) {
-            const T* v = static_cast<const T*>(p.v) + (int64_t)w.kh * D + c;
-            const int first = max(item_least, w.t0 * kBK), last = (int)min((int64_t)sees, (int64_t)w.t1 * kBK);
-            for (int k = first; k < last; ++k)
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float x = to_f32(v[(int64_t)(w.k0 + k) * p.v_stride + e]);
-                if (!isfinite(x)) o[e] += x;
-              }
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] *= f.own;
           if (prior.any)
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(p.prior_o + to_row + c + e);
-              o[e] = fmaf(f.prior, x.x, o[e]), o[e + 1] = fmaf(f.prior, x.y, o[e + 1]);
-              o[e + 2] = fmaf(f.prior, x.z, o[e + 2]), o[e + 3] = fmaf(f.prior, x.w, o[e + 3]);
-            }
+            for (int e = 0; e < 32; e += 4)
+              if (e < cols) {
+                const float4 x = *reinterpret_cast<const float4*>(p.prior_o + to_row + c + e);
+                o[e] = fmaf(f.prior, x.x, o[e]), o[e + 1] = fmaf(f.prior, x.y, o[e + 1]);
+                o[e + 2] = fmaf(f.prior, x.z, o[e + 2]), o[e + 3] = fmaf(f.prior, x.w, o[e + 3]);
+              }
           __syncwarp();
-          if (wide) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
-                  make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            __syncwarp();
-            float* y = w.part != kAttnWhole ? p.part_o : p.core;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = 4 * i + (lane >> 3), e = lane & 7;
-              const int64_t at_row = __shfl_sync(0xffffffffu, to_row, r);
-              if (live >> r & 1)
-                *reinterpret_cast<float4*>(y + at_row + c + 4 * e) =
-                    *reinterpret_cast<const float4*>(stage + r * 128 + ((e ^ (r & 7)) << 4));
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ (lane >> 1 & 3)) << 4)) =
-                  make_uint4(Half<T>::pack(o[8 * e], o[8 * e + 1]), Half<T>::pack(o[8 * e + 2], o[8 * e + 3]),
+          for (int e = 0; e < 4; ++e) {
+            uint4 x;
+            if (wide)
+              x = make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]), __float_as_uint(o[4 * e + 2]),
+                             __float_as_uint(o[4 * e + 3]));
+            else
+              x = make_uint4(Half<T>::pack(o[8 * e], o[8 * e + 1]), Half<T>::pack(o[8 * e + 2], o[8 * e + 3]),
                              Half<T>::pack(o[8 * e + 4], o[8 * e + 5]), Half<T>::pack(o[8 * e + 6], o[8 * e + 7]));
-            __syncwarp();
-            T* y = static_cast<T*>(p.out);
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ (lane >> 1 & 3)) << 4)) = x;
+          }
+          __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = 8 * i + (lane >> 2), e = lane & 3;
-              const int64_t at_row = __shfl_sync(0xffffffffu, to_row, r);
-              if (live >> r & 1)
-                *reinterpret_cast<uint4*>(y + at_row + c + 8 * e) =
-                    *reinterpret_cast<const uint4*>(stage + r * 64 + ((e ^ (r >> 1 & 3)) << 4));
+          for (int k = 0; k < 4; ++k) {
+            const int r = 8 * k + (lane >> 2), e = lane & 3;
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 64 + ((e ^ (r >> 1 & 3)) << 4));
+            if (live >> r & 1) {
+              if (wide) *reinterpret_cast<uint4*>(yw + at_row[k] + c + 4 * e) = x;
+              else *reinterpret_cast<uint4*>(yn + at_row[k] + c + 8 * e) = x;
             }
           }
         }
@@ -700,7 +710,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == kBMma) {
+  if (warp == kBScores) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tb, kCols);
   }
