@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kAT, 2) attn_cc_kernel(const AttnArgs p) {
       const int64_t token = w.q0 + r / p.group;
       const int head = attn_head(p, w.kh, r % p.group);
       const AttnPrior prior = attn_prior(p, token, head);
-      const AttnScale f = attn_scale(top[i] * sc, l, prior);
+      const AttnScale f = attn_scale(top[i] * sc, l, prior, p.lse != nullptr);
       const int64_t at = (token * p.Hq + head) * D;
 #pragma unroll
       for (int j = 0; j < NP; ++j) {

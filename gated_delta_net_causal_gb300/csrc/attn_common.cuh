@@ -87,13 +87,22 @@ __device__ __forceinline__ int64_t attn_seq_cost(const AttnArgs& p, const AttnSe
   return attn_cost_before<KT>(p, s, attn_items(p, s) - 1) + s.kn + kAttnStart * KT;
 }
 
-// a / b and its remainder, in 32 bits where they fit (a 64-bit division takes
-// several hundred cycles)
+// a / b and its remainder for a >= 0, b > 0: in 32 bits where they fit, else bit by bit (the instructions of a 64-bit
+// division are many, and these rarely run)
 __device__ __forceinline__ int64_t attn_divide(int64_t a, int64_t b, int64_t* rest) {
-  int64_t q;
-  if (((a | b) >> 32) == 0) q = (unsigned)a / (unsigned)b;
-  else q = a / b;
-  *rest = a - q * b;
+  if (((a | b) >> 32) == 0) {
+    const unsigned q = (unsigned)a / (unsigned)b;
+    *rest = (unsigned)a - q * (unsigned)b;
+    return q;
+  }
+  int64_t q = 0, r = 0;
+#pragma unroll 1
+  for (int i = 62; i >= 0; --i) {
+    r = 2 * r + (a >> i & 1);
+    q *= 2;
+    if (r >= b) r -= b, ++q;
+  }
+  *rest = r;
   return q;
 }
 
@@ -127,6 +136,7 @@ __device__ __forceinline__ void attn_plan(const AttnArgs& p, int64_t* sums, Attn
   {
     const int64_t a = (int64_t)threadIdx.x * per, b = a + per < p.N ? a + per : p.N;
     int64_t u = 0;
+#pragma unroll 1
     for (int64_t n = a; n < b; ++n) u += attn_seq_cost<KT>(p, attn_seq(p, (int)n));
     sums[threadIdx.x] = u * p.Hk;
   }
@@ -135,10 +145,10 @@ __device__ __forceinline__ void attn_plan(const AttnArgs& p, int64_t* sums, Attn
     constexpr int PER = THREADS / 32;
     const int lane = threadIdx.x;
     int64_t own = 0;
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < PER; ++i) own += sums[lane * PER + i];
     int64_t incl = own;
-#pragma unroll
+#pragma unroll 1
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += o;
@@ -179,9 +189,12 @@ struct AttnWalk {
     // the sequence: the lanes have 32 of them
     int64_t u = plan.begin, own, incl;
     unsigned past;
+    AttnSeq mine{0, 0, 0, 0};
     for (;;) {
-      own = n + lane < p.N ? attn_seq_cost<KT>(p, attn_seq(p, n + lane)) * p.Hk : 0;
-      incl = own;
+      if (n + lane < p.N) mine = attn_seq(p, n + lane);
+      else mine.qn = 0;
+      own = attn_seq_cost<KT>(p, mine);
+      incl = own * p.Hk;
 #pragma unroll 1
       for (int d = 1; d < 32; d <<= 1) {
         const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
@@ -194,24 +207,26 @@ struct AttnWalk {
     }
     const int l = __ffs(past) - 1;
     n += l;
-    u -= __shfl_sync(0xffffffffu, incl - own, l);
-    s = attn_seq(p, n);
-    kh = (int)attn_divide(u, attn_seq_cost<KT>(p, s), &u);
+    u -= __shfl_sync(0xffffffffu, incl - own * p.Hk, l);
+    s = AttnSeq{__shfl_sync(0xffffffffu, mine.q0, l), __shfl_sync(0xffffffffu, mine.qn, l),
+                __shfl_sync(0xffffffffu, mine.k0, l), __shfl_sync(0xffffffffu, mine.kn, l)};
+    kh = (int)attn_divide(u, __shfl_sync(0xffffffffu, own, l), &u);
     // the item: the last one with no more than u before it, among 32 evenly spaced ones at a time
     int lo = 0, count = attn_items(p, s);
+    pos = u;
 #pragma unroll 1
     while (count > 1) {
-      const int step = (count + 31) / 32;
-      const bool in = lane * step < count && attn_cost_before<KT>(p, s, lo + lane * step) <= u;
-      const int k = 31 - __clz(__ballot_sync(0xffffffffu, in));  // (lane 0's is)
+      const int step = (int)((unsigned)(count + 31) / 32);
+      const int64_t rest = u - attn_cost_before<KT>(p, s, lo + lane * step);
+      const int k = 31 - __clz(__ballot_sync(0xffffffffu, lane * step < count && rest >= 0));  // (lane 0's is)
+      pos = __shfl_sync(0xffffffffu, rest, k);
       lo += k * step;
       count = count - k * step < step ? count - k * step : step;
     }
-    pos = u - attn_cost_before<KT>(p, s, lo);
     at = lo * p.item;
     // the CTA before takes it to its end?
     const int seen = attn_last_sees(p, s, at);
-    if (whole ? pos > 0 : pos / KT >= (seen > KT ? (seen + KT - 1) / KT : 1)) {
+    if (whole ? pos > 0 : (int)(pos / KT) >= (seen > KT ? (seen + KT - 1) / KT : 1)) {
       left -= seen + kAttnStart * KT - pos;
       pos = 0;
       step(p);
@@ -281,18 +296,19 @@ __device__ __forceinline__ AttnPrior attn_prior(const AttnArgs& p, int64_t token
 struct AttnScale {
   float own, prior, lse;
 };
-__device__ __forceinline__ AttnScale attn_scale(float top, float sum, AttnPrior prior) {
-  float m = top, a = 0.f;
+__device__ __forceinline__ AttnScale attn_scale(float top, float sum, AttnPrior prior, bool lse) {
+  float m = top, w0 = 1.f, w1 = 0.f, s = sum;
   if (prior.any) {
-    a = prior.lse * kAttnLog2e;
+    const float a = prior.lse * kAttnLog2e;
     m = fmaxf(top, a);
+    if (m == -INFINITY) m = 0.f;
+    w0 = exp2f(top - m);
+    w1 = exp2f(a - m);
+    s = fmaf(sum, w0, w1);
   }
-  if (m == -INFINITY) m = 0.f;
-  const float w0 = exp2f(top - m), w1 = prior.any ? exp2f(a - m) : 0.f;
-  const float s = fmaf(sum, w0, w1);
   if (s == 0.f) return AttnScale{0.f, 0.f, -INFINITY};
-  const float inv = 1.f / s;
-  return AttnScale{w0 * inv, w1 * inv, (m + log2f(s)) * kAttnLn2};
+  const float inv = __frcp_rn(s);
+  return AttnScale{w0 * inv, w1 * inv, lse ? (m + log2f(s)) * kAttnLn2 : 0.f};
 }
 
 }  // namespace gdn

@@ -17,25 +17,26 @@ __global__ void __launch_bounds__(32 * kJWarps) attn_join_kernel(const AttnArgs 
   grid_dependency_wait();
   const int b = blockIdx.x, lane = threadIdx.x & 31;
   const int r = blockIdx.y * kJWarps + (threadIdx.x >> 5);
+  // part j of the item: what CTA b ended with, then what CTA b + j began with;
+  // lane j looks at it (and at its row) before it is known to be one, so that
+  // the loads wait for memory together
+  const auto slot_of = [&](int j) { return (int64_t)(j == 0 ? 2 * b + 1 : 2 * (b + j)); };
   const int4 at = p.part_at[2 * b + 1];
+  const bool in = b + lane < ctas;
+  const int4 mine = in ? p.part_at[slot_of(lane)] : make_int4(0, 0, 0, 0);
+  float2 ml = in && r < p.part_rows ? p.part_ml[slot_of(lane) * p.part_rows + r] : make_float2(0.f, 0.f);
   if (at.x != kAttnFirst || r >= at.z * p.group) return;
-  // the CTA that ends the item
-  int last = ctas;
-  for (int c = b + 1; c < ctas; c += 32) {
-    const bool end = c + lane < ctas && p.part_at[2 * (c + lane)].x == kAttnLast;
-    const unsigned any = __ballot_sync(0xffffffffu, end);
-    if (any != 0) {
-      last = c + __ffs(any) - 1;
-      break;
-    }
+  unsigned end = __ballot_sync(0xffffffffu, mine.x == kAttnLast && lane > 0);
+  int parts = end != 0 ? __ffs(end) : 0;
+  for (int j0 = 32; parts == 0; j0 += 32) {  // more than 32 parts
+    if (b + j0 >= ctas) return;              // (an item that is begun is ended)
+    end = __ballot_sync(0xffffffffu, b + j0 + lane < ctas && p.part_at[slot_of(j0 + lane)].x == kAttnLast);
+    if (end != 0) parts = j0 + __ffs(end);
   }
-  if (last == ctas) return;  // (an item that is begun is ended)
-  const int parts = last - b + 1;
-  const auto row_of = [&](int j) { return (int64_t)(j == 0 ? 2 * b + 1 : 2 * (b + j)) * p.part_rows + r; };
   const int64_t token = at.y + r / p.group;
   const int head = attn_head(p, at.w, r % p.group);
-  float top = -INFINITY;
-  for (int j = lane; j < parts; j += 32) top = fmaxf(top, p.part_ml[row_of(j)].x);
+  float top = lane < parts ? ml.x : -INFINITY;
+  for (int j = lane + 32; j < parts; j += 32) top = fmaxf(top, p.part_ml[slot_of(j) * p.part_rows + r].x);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   const float base = top == -INFINITY ? 0.f : top;
@@ -43,26 +44,32 @@ __global__ void __launch_bounds__(32 * kJWarps) attn_join_kernel(const AttnArgs 
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
   for (int j0 = 0; j0 < parts; j0 += 32) {
+    if (j0 > 0 && j0 + lane < parts) ml = p.part_ml[slot_of(j0 + lane) * p.part_rows + r];
     float f = 0.f;
     if (j0 + lane < parts) {
-      const float2 ml = p.part_ml[row_of(j0 + lane)];
       f = exp2f(ml.x - base);
       sum = fmaf(ml.y, f, sum);
     }
     const int n = parts - j0 < 32 ? parts - j0 : 32;
-#pragma unroll 8
-    for (int j = 0; j < n; ++j) {
-      const float w = __shfl_sync(0xffffffffu, f, j);
-      if (holds) {
-        const float4 x = *reinterpret_cast<const float4*>(p.part_o + row_of(j0 + j) * D + 4 * lane);
+#pragma unroll 1
+    for (int j1 = 0; j1 < n; j1 += 8) {
+      float4 x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        x[j] = holds && j1 + j < n ? *reinterpret_cast<const float4*>(
+                                         p.part_o + (slot_of(j0 + j1 + j) * p.part_rows + r) * D + 4 * lane)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
         // (a part without keys has the factor 0 and zeros)
-        o.x = fmaf(w, x.x, o.x), o.y = fmaf(w, x.y, o.y), o.z = fmaf(w, x.z, o.z), o.w = fmaf(w, x.w, o.w);
+        const float w = __shfl_sync(0xffffffffu, f, (j1 + j) & 31);
+        o.x = fmaf(w, x[j].x, o.x), o.y = fmaf(w, x[j].y, o.y), o.z = fmaf(w, x[j].z, o.z), o.w = fmaf(w, x[j].w, o.w);
       }
     }
   }
   sum = group_sum<32>(sum);
   const AttnPrior prior = attn_prior(p, token, head);
-  const AttnScale f = attn_scale(top, sum, prior);
+  const AttnScale f = attn_scale(top, sum, prior, p.lse != nullptr);
   o = make_float4(o.x * f.own, o.y * f.own, o.z * f.own, o.w * f.own);
   const int64_t to = (token * p.Hq + head) * D + 4 * lane;
   if (holds) {

@@ -57,8 +57,8 @@ struct TcGeom {
   static constexpr uint32_t kTile = kBoxes * kBK * 128;  // bytes
   static constexpr int kStages = kBoxes == 2 ? 2 : 4;  // of each ring
   static constexpr uint32_t kK = 2 * kTile, kV = kK + kStages * kTile;
-  static constexpr uint32_t kOut = kV + kStages * kTile;  // 2 KB for each warp of rows
-  static constexpr uint32_t kSmem = kOut + 8 * 2048;
+  static constexpr uint32_t kOut = kV + kStages * kTile;  // 4 KB for each warp of rows
+  static constexpr uint32_t kSmem = kOut + 8 * 4096;
 };
 
 // TMEM columns: S, P of both tiles (64 each), O of both (128 each)
@@ -106,6 +106,9 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ void prefetch_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
@@ -170,31 +173,34 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// A bounded wait that sleeps in the barrier: a warp that asks again and again
-// takes shared memory's cycles from the products' operands. Gives up as
-// mbar_wait_bounded does.
-constexpr uint32_t kNap = 100000;  // ns that one question may take
-__device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
+// A bounded wait that sleeps in the barrier; false when *abort_flag is set or
+// after kWaitLimitNs, and then it sets the flag. (In a few instructions: there
+// are many of these, and what a CTA runs must fit the instruction cache.)
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int* abort_flag) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 t0, t1;\n\t.reg .b32 f;\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "@p bra DONE;\n\t"
+      "mov.u64 t0, %%globaltimer;\n"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "@p bra DONE;\n\t"
+      "ld.volatile.shared.b32 f, [%4];\n\t"
+      "setp.ne.b32 q, f, 0;\n\t"
+      "@q bra DONE;\n\t"
+      "mov.u64 t1, %%globaltimer;\n\t"
+      "sub.u64 t1, t1, t0;\n\t"
+      "setp.lt.u64 q, t1, %5;\n\t"
+      "@q bra AGAIN;\n\t"
+      "mov.b32 f, 1;\n\t"
+      "st.volatile.shared.b32 [%4], f;\n"
+      "DONE:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(kNap)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u), "r"(smem_u32(abort_flag)), "l"(kWaitLimitNs)
       : "memory");
   return ok != 0;
-}
-__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  const uint64_t t0 = global_ns();
-  while (!*abort_flag) {
-    if (try_wait_long(bar, parity)) return true;
-    if (global_ns() - t0 > kWaitLimitNs) {
-      record_device_error(GDN_ERR_TIMEOUT);
-      *abort_flag = 1;
-    }
-  }
-  return false;
 }
 
 template <typename T>
@@ -252,6 +258,11 @@ __global__ void __launch_bounds__(kBThreads, 1)
     tc::tmem_alloc(&sh.tmem, kCols);
     tc::tmem_relinquish();
   }
+  if (tid == 32) {
+    prefetch_map(&tm_q);
+    prefetch_map(&tm_k);
+    prefetch_map(&tm_v);
+  }
   if (tid == 0) {
     for (int i = 0; i < G::kStages; ++i) {
       mbar_init(&sh.k_full[i], 1);
@@ -282,10 +293,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tb = __shfl_sync(0xffffffffu, sh.tmem, 0);
-  volatile int* abort_flag = &sh.abort;
-  const auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return try_wait_long(bar, parity) || wait_slow(bar, parity, abort_flag);
-  };
+  const auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_for(bar, parity, &sh.abort); };
   // piece i of the CTA, for a whole warp; false: there is none
   const auto take = [&](int i, AttnPiece* w) {
     const bool ok = wait(&sh.piece_full[i % kBRing], (i / kBRing) & 1);
@@ -471,24 +479,33 @@ __global__ void __launch_bounds__(kBThreads, 1)
             return reinterpret_cast<uint4*>(v + (c16 >> 3) * kBK * 128 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4));
           };
           const int until = most - base < kBK ? (most - base) * (8 * G::kBoxes) : kBK * 8 * G::kBoxes;
-#pragma unroll 8
-          for (int u = from * (8 * G::kBoxes) + lane; u < until; u += 32) {
-            uint4 x = *place(u);
-            uint32_t* e = &x.x;
+          // eight accesses in flight: nearly always there is nothing to store
+#pragma unroll 1
+          for (int u0 = from * (8 * G::kBoxes) + lane; u0 < until; u0 += 8 * 32) {
+            uint4 x[8];
             uint32_t any = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) any |= (e[j] & Half<T>::kExponent) + Half<T>::kCarry;
-            if ((any & 0x80008000u) == 0) continue;
+            for (int k = 0; k < 8; ++k) x[k] = u0 + 32 * k < until ? *place(u0 + 32 * k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t m = (e[j] & Half<T>::kExponent) + Half<T>::kCarry;
-              if (m & 0x8000u) e[j] &= 0xffff0000u;
-              if (m & 0x80000000u) e[j] &= 0x0000ffffu;
-            }
-            *place(u) = x;
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) any |= ((&x[k].x)[j] & Half<T>::kExponent) + Half<T>::kCarry;
+            if ((any & 0x80008000u) == 0) continue;
             hit = true;
+#pragma unroll 1
+            for (int u = u0; u < until && u < u0 + 8 * 32; u += 32) {
+              uint4 y = *place(u);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t& e = (&y.x)[j];
+                const uint32_t m = (e & Half<T>::kExponent) + Half<T>::kCarry;
+                if (m & 0x8000u) e &= 0xffff0000u;
+                if (m & 0x80000000u) e &= 0x0000ffffu;
+              }
+              *place(u) = y;
+            }
           }
-#pragma unroll 8
+#pragma unroll 4
           for (int u = until + lane; u < kBK * 8 * G::kBoxes; u += 32) *place(u) = make_uint4(0, 0, 0, 0);
           if (hit) sh.piece[i % kBRing].bad = 1;
           fence_proxy_async_smem();
@@ -642,66 +659,71 @@ __global__ void __launch_bounds__(kBThreads, 1)
             to_row = slot_row * D;
           } else {
             prior = attn_prior(p, token, head);
-            f = attn_scale(top, l, prior);
+            f = attn_scale(top, l, prior, p.lse != nullptr);
             to_row = (token * p.Hq + head) * D;
             if (p.lse != nullptr) p.lse[token * p.Hq + head] = f.lse;
           }
         }
-        // 64 bytes of each row at a time through shared memory, so that they
-        // are stored side by side (from the lanes' rows a store of 16 bytes
+        // up to 128 bytes of each row at a time through shared memory, so that
+        // they are stored side by side (from the lanes' rows a store of 16 bytes
         // each touches 32 lines)
         const bool wide = w.part != kAttnWhole || p.core != nullptr;  // fp32
-        unsigned char* stage = sm + G::kOut + warp * 2048;
-        float* yw = w.part != kAttnWhole ? p.part_o : p.core;
-        T* yn = static_cast<T*>(p.out);
+        unsigned char* stage = sm + G::kOut + warp * 4096;
         const unsigned live = __ballot_sync(0xffffffffu, valid);
-        int64_t at_row[4];
+        const auto store = [&](auto* y, auto as) {
+          using E = decltype(as);
+          constexpr int kCols = sizeof(E) == 4 ? 32 : (D % 64 == 0 ? 64 : 32), kBytes = kCols * (int)sizeof(E);
+          constexpr int kLanes = kBytes / 16, kRows = 32 / kLanes;  // lanes a row, rows an access
+          int64_t at_row[32 / kRows];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) at_row[k] = __shfl_sync(0xffffffffu, to_row, 8 * k + (lane >> 2));
-        const int cols = wide ? 16 : 32;
+          for (int k = 0; k < 32 / kRows; ++k) at_row[k] = __shfl_sync(0xffffffffu, to_row, kRows * k + lane / kLanes);
+          // 16-byte chunk e of row r: eight lanes of a row or of eight rows use all banks
+          const auto chunk = [&](int r, int e) {
+            const int x = kLanes == 8 ? r & 7 : r >> 1 & 3;
+            return reinterpret_cast<uint4*>(stage + r * kBytes + ((e ^ x) << 4));
+          };
 #pragma unroll 1
-        for (int c = 0; c < D; c += cols) {
-          float o[32];
+          for (int c = 0; c < D; c += kCols) {
+            float o[kCols];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
-          if (n > 0) {
-            tc::tmem_ld16(to + c, *reinterpret_cast<float(*)[16]>(o));
-            if (!wide) tc::tmem_ld16(to + c + 16, *reinterpret_cast<float(*)[16]>(o + 16));
-            tc::tmem_wait_ld();
-          }
+            for (int e = 0; e < kCols; ++e) o[e] = 0.f;
+            if (n > 0) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= f.own;
-          if (prior.any)
+              for (int e = 0; e < kCols; e += 32) tmem_ld32(to + c + e, o + e);
+              tc::tmem_wait_ld();
+            }
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              if (e < cols) {
+            for (int e = 0; e < kCols; ++e) o[e] *= f.own;
+            if (prior.any)
+#pragma unroll
+              for (int e = 0; e < kCols; e += 4) {
                 const float4 x = *reinterpret_cast<const float4*>(p.prior_o + to_row + c + e);
                 o[e] = fmaf(f.prior, x.x, o[e]), o[e + 1] = fmaf(f.prior, x.y, o[e + 1]);
                 o[e + 2] = fmaf(f.prior, x.z, o[e + 2]), o[e + 3] = fmaf(f.prior, x.w, o[e + 3]);
               }
-          __syncwarp();
+            __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint4 x;
-            if (wide)
-              x = make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]), __float_as_uint(o[4 * e + 2]),
-                             __float_as_uint(o[4 * e + 3]));
-            else
-              x = make_uint4(Half<T>::pack(o[8 * e], o[8 * e + 1]), Half<T>::pack(o[8 * e + 2], o[8 * e + 3]),
-                             Half<T>::pack(o[8 * e + 4], o[8 * e + 5]), Half<T>::pack(o[8 * e + 6], o[8 * e + 7]));
-            *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ (lane >> 1 & 3)) << 4)) = x;
-          }
-          __syncwarp();
+            for (int e = 0; e < kLanes; ++e) {
+              const float* y4 = o + 4 * e;
+              const float* y8 = o + 8 * e;
+              if constexpr (sizeof(E) == 4)
+                *chunk(lane, e) = make_uint4(__float_as_uint(y4[0]), __float_as_uint(y4[1]), __float_as_uint(y4[2]),
+                                             __float_as_uint(y4[3]));
+              else
+                *chunk(lane, e) = make_uint4(Half<T>::pack(y8[0], y8[1]), Half<T>::pack(y8[2], y8[3]),
+                                             Half<T>::pack(y8[4], y8[5]), Half<T>::pack(y8[6], y8[7]));
+            }
+            __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = 8 * k + (lane >> 2), e = lane & 3;
-            const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 64 + ((e ^ (r >> 1 & 3)) << 4));
-            if (live >> r & 1) {
-              if (wide) *reinterpret_cast<uint4*>(yw + at_row[k] + c + 4 * e) = x;
-              else *reinterpret_cast<uint4*>(yn + at_row[k] + c + 8 * e) = x;
+            for (int k = 0; k < 32 / kRows; ++k) {
+              const int r = kRows * k + lane / kLanes, e = lane % kLanes;
+              const uint4 x = *chunk(r, e);
+              if (live >> r & 1) *reinterpret_cast<uint4*>(y + at_row[k] + c + e * (16 / (int)sizeof(E))) = x;
             }
           }
-        }
+        };
+        if (wide) store(w.part != kAttnWhole ? p.part_o : p.core, 0.f);
+        else store(static_cast<T*>(p.out), T());
         if (tid == 0 && w.part != kAttnWhole)
           p.part_at[attn_slot(blockIdx.x, w.part)] = make_int4(w.part, w.q0, w.tokens, w.kh);
       }
@@ -710,6 +732,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
+  if (tid == 0 && sh.abort) record_device_error(GDN_ERR_TIMEOUT);
   if (warp == kBScores) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tb, kCols);
