@@ -30,8 +30,9 @@
 // One warp issues the scores, another O += P V: the tensor cores take a few
 // products ahead from each, and an issuing warp is held until they do, so that
 // with one warp for both whatever the other kind waited for was looked at late
-// (a gap of 600 cycles in each 1800). The order between the two is what S and P
-// make it.
+// (a gap of 600 cycles in each 1800). A tile's next scores go first, then its
+// O: its rows wait for the scores, and for O only when their next weights are
+// done (the other way round a tile of both halves took 2900 cycles).
 //
 // A wait that gives up raises the CTA's abort flag; every role then leaves its
 // loop at once.
@@ -69,6 +70,7 @@ struct BShared {
   // outputs' warp and the one that looks through it do: whoever waits for a
   // tile also has to give it back, so no phase of a barrier goes by unseen
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], v_ok[4];
+  // p_ready: the four warps' weights, and the scores of the tile after
   uint64_t q_full[2], q_empty[2], s_full[2], s_free, p_ready[2], o_done[2];
   uint64_t piece_full[kBRing], piece_empty[kBRing];
   AttnPiece piece[kBRing];
@@ -208,7 +210,6 @@ struct Half;
 template <>
 struct Half<__nv_bfloat16> {
   static constexpr uint32_t kFormat = tc::kBF16;
-  static constexpr uint32_t kExponent = 0x7f807f80u, kCarry = 0x00800080u;
   // log2 that the weights are scaled by
   static constexpr float kLift = 0.f;
   __device__ __forceinline__ static uint32_t pack(float lo, float hi) {
@@ -216,17 +217,27 @@ struct Half<__nv_bfloat16> {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
   }
+  // 0 x + c: NaN where x is not finite, c elsewhere (c a zero of either sign, or NaN)
+  __device__ __forceinline__ static uint32_t zero_times(uint32_t x, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(c));
+    return r;
+  }
 };
 template <>
 struct Half<__half> {
   static constexpr uint32_t kFormat = tc::kF16;
-  static constexpr uint32_t kExponent = 0x7c007c00u, kCarry = 0x04000400u;
   // fp16's smallest normal weight would be 2^-14: 2^7 of its range above 2^8
   // is moved below
   static constexpr float kLift = 7.f;
   __device__ __forceinline__ static uint32_t pack(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+  __device__ __forceinline__ static uint32_t zero_times(uint32_t x, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(c));
     return r;
   }
 };
@@ -275,7 +286,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_ready[i], 4);
+      mbar_init(&sh.p_ready[i], 5);
       mbar_init(&sh.o_done[i], 1);
     }
     mbar_init(&sh.s_free, 4);
@@ -418,6 +429,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
               mma_ss<D == 32 ? 2 : 4>(tb + kColS, a, b, id, false);
               if (D > 64) mma_ss<D == 96 ? 2 : 4>(tb + kColS, a + next, b + next, id, true);
               tc::mma_commit_elect(&sh.s_full[h]);
+              if (j > 0 && lane == 0) mbar_arrive(&sh.p_ready[h]);  // O of the tile before may come now
               if (j + 1 == (h ? nb : na)) tc::mma_commit_elect(&sh.q_empty[h]);
             }
             if (ok) tc::mma_commit_elect(&sh.k_empty[st]);
@@ -474,39 +486,42 @@ __global__ void __launch_bounds__(kBThreads, 1)
           unsigned char* v = sm + G::kV + st * G::kTile;
           const int base = t * kBK, from = least > base ? least - base : 0;  // rows from which some row sees no more
           bool hit = false;
-          const auto place = [&](int u) {  // 16-byte chunk u, row after row
-            const int row = u / (8 * G::kBoxes), c16 = u % (8 * G::kBoxes);
-            return reinterpret_cast<uint4*>(v + (c16 >> 3) * kBK * 128 + row * 128 + (((c16 & 7) ^ (row & 7)) << 4));
+          constexpr int kC = 8 * G::kBoxes, kR = 32 / kC;  // 16-byte chunks of a row, rows an access
+          const int c16 = lane % kC, some = lane / kC;
+          unsigned char* col = v + (c16 >> 3) * kBK * 128;
+          const auto place = [&](int row) {
+            return reinterpret_cast<uint4*>(col + row * 128 + (((c16 & 7) ^ (row & 7)) << 4));
           };
-          const int until = most - base < kBK ? (most - base) * (8 * G::kBoxes) : kBK * 8 * G::kBoxes;
-          // eight accesses in flight: nearly always there is nothing to store
+          const int until = most - base < kBK ? most - base : kBK;
+          // Eight accesses in flight. 0 times anything finite adds nothing; nearly
+          // always there is nothing to store.
 #pragma unroll 1
-          for (int u0 = from * (8 * G::kBoxes) + lane; u0 < until; u0 += 8 * 32) {
+          for (int r0 = from + some; r0 < until; r0 += 8 * kR) {
             uint4 x[8];
             uint32_t any = 0;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = u0 + 32 * k < until ? *place(u0 + 32 * k) : make_uint4(0, 0, 0, 0);
+            for (int k = 0; k < 8; ++k) x[k] = r0 + kR * k < until ? *place(r0 + kR * k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) any |= ((&x[k].x)[j] & Half<T>::kExponent) + Half<T>::kCarry;
-            if ((any & 0x80008000u) == 0) continue;
+              for (int j = 0; j < 4; ++j) any = Half<T>::zero_times((&x[k].x)[j], any);
+            if ((any & 0x7fff7fffu) == 0) continue;
             hit = true;
 #pragma unroll 1
-            for (int u = u0; u < until && u < u0 + 8 * 32; u += 32) {
-              uint4 y = *place(u);
+            for (int r = r0; r < until && r < r0 + 8 * kR; r += kR) {
+              uint4 y = *place(r);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 uint32_t& e = (&y.x)[j];
-                const uint32_t m = (e & Half<T>::kExponent) + Half<T>::kCarry;
-                if (m & 0x8000u) e &= 0xffff0000u;
-                if (m & 0x80000000u) e &= 0x0000ffffu;
+                const uint32_t m = Half<T>::zero_times(e, 0);
+                if (m & 0x7fffu) e &= 0xffff0000u;
+                if (m & 0x7fff0000u) e &= 0x0000ffffu;
               }
-              *place(u) = y;
+              *place(r) = y;
             }
           }
 #pragma unroll 4
-          for (int u = until + lane; u < kBK * 8 * G::kBoxes; u += 32) *place(u) = make_uint4(0, 0, 0, 0);
+          for (int r = until + some; r < kBK; r += kR) *place(r) = make_uint4(0, 0, 0, 0);
           if (hit) sh.piece[i % kBRing].bad = 1;
           fence_proxy_async_smem();
           __syncwarp();
@@ -529,6 +544,12 @@ __global__ void __launch_bounds__(kBThreads, 1)
     const bool row_used = row < half * p.group;
     uint32_t n_s = 0;  // tiles so far
     bool alive = true;
+    // this warp's weights are there; where the tile has no scores to come, so are those
+    const auto ready = [&](bool last) {
+      if (lane != 0) return;
+      mbar_arrive(&sh.p_ready[h]);
+      if (last && qd == 0) mbar_arrive(&sh.p_ready[h]);
+    };
     // whether O has taken the weights of tile n of this half (from 1 on)
     const auto o_done = [&](uint32_t n) {
       if (n > 0) alive = __all_sync(0xffffffffu, wait(&sh.o_done[h], (n - 1) & 1));
@@ -556,7 +577,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
           if (lane == 0) mbar_arrive(&sh.s_free);
           // (the other warps' weights of the tile before are counted)
           if (!o_done(n_s - 1)) break;
-          if (lane == 0) mbar_arrive(&sh.p_ready[h]);
+          ready(j + 1 == n);
           continue;
         }
         float s[kBK];
@@ -617,7 +638,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_ready[h]);
+        ready(j + 1 == n);
       }
       if (!alive) break;
       // ---- the outputs
