@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
             if (p.lse != nullptr) p.lse[token * p.Hq + head] = f.lse;
           }
         }
-        // up to 128 bytes of each row at a time through shared memory, so that
+        // 64 or 128 bytes of each row at a time through shared memory, so that
         // they are stored side by side (from the lanes' rows a store of 16 bytes
         // each touches 32 lines)
         const bool wide = w.part != kAttnWhole || p.core != nullptr;  // fp32
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
         const unsigned live = __ballot_sync(0xffffffffu, valid);
         const auto store = [&](auto* y, auto as) {
           using E = decltype(as);
-          constexpr int kCols = sizeof(E) == 4 ? 32 : (D % 64 == 0 ? 64 : 32), kBytes = kCols * (int)sizeof(E);
+          constexpr int kCols = 32, kBytes = kCols * (int)sizeof(E);
           constexpr int kLanes = kBytes / 16, kRows = 32 / kLanes;  // lanes a row, rows an access
           int64_t at_row[32 / kRows];
 #pragma unroll
@@ -706,15 +706,18 @@ __global__ void __launch_bounds__(kBThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < D; c += kCols) {
             float o[kCols];
-#pragma unroll
-            for (int e = 0; e < kCols; ++e) o[e] = 0.f;
             if (n > 0) {
-#pragma unroll
-              for (int e = 0; e < kCols; e += 32) tmem_ld32(to + c + e, o + e);
+              tmem_ld32(to + c, o);
               tc::tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int e = 0; e < kCols; ++e) o[e] = 0.f;
             }
 #pragma unroll
-            for (int e = 0; e < kCols; ++e) o[e] *= f.own;
+            for (int e = 0; e < kCols; e += 2) {
+              const float2 y = fma2(make_float2(o[e], o[e + 1]), make_float2(f.own, f.own), make_float2(-0.f, -0.f));
+              o[e] = y.x, o[e + 1] = y.y;
+            }
             if (prior.any)
 #pragma unroll
               for (int e = 0; e < kCols; e += 4) {
