@@ -717,17 +717,20 @@ gdn::AttnSplit attn_split_of(const gdn_dims* dims, int64_t total_tokens) {
   return gdn::attn_split(dims->io_dtype, total_tokens, dims->n_v_heads / dims->n_k_heads, dims->head_dim);
 }
 
-// gdn_attn_shared's workspace: that of the splits, then the prefixes' outputs
-// and logarithms of sums.
-struct AttnPrior {
-  int64_t o, lse, bytes;
+// gdn_attn_shared's workspace: that of the splits, then outputs and logarithms
+// of sums over the sequences' own keys, and over the prefixes.
+struct AttnParts {
+  int64_t out[2], lse[2], bytes;
 };
-AttnPrior attn_prior_at(const gdn_dims* dims, int64_t total_tokens) {
-  AttnPrior a{};
-  a.o = attn_split_of(dims, total_tokens).bytes;
+AttnParts attn_parts_at(const gdn_dims* dims, int64_t total_tokens) {
+  AttnParts a{};
   const int64_t rows = total_tokens * dims->n_v_heads;  // < 2^31 2^16
-  a.lse = a.o + (rows * dims->head_dim * 4 + 255) / 256 * 256;
-  a.bytes = a.lse + (rows * 4 + 255) / 256 * 256;
+  a.bytes = attn_split_of(dims, total_tokens).bytes;
+  for (int i = 0; i < 2; ++i) {
+    a.out[i] = a.bytes;
+    a.lse[i] = a.out[i] + (rows * dims->head_dim * 4 + 255) / 256 * 256;
+    a.bytes = a.lse[i] + (rows * 4 + 255) / 256 * 256;
+  }
   return a;
 }
 
@@ -753,7 +756,7 @@ gdn_status check_attn(const gdn_dims* dims, int32_t num_seqs, const int32_t* cu_
   }
   // the work (keys, of at most so many items and heads) is counted in 64 bits
   int64_t cost = 0;
-  if (!mul_ok((total_tokens + num_seqs) * Hk, kv_rows + 1024, &cost)) return GDN_ERR_EXTENT;
+  if (!mul_ok((2 * total_tokens + 2 * kMaxGridY) * Hk, kv_rows + 1024, &cost)) return GDN_ERR_EXTENT;
   const void* ptrs[] = {cu_seqlens, q, k, v, out, lse, workspace};
   for (const void* ptr : ptrs)
     if (!aligned16(ptr)) return GDN_ERR_ALIGN;
@@ -785,7 +788,6 @@ gdn_status check_attn(const gdn_dims* dims, int32_t num_seqs, const int32_t* cu_
   p->N = num_seqs;
   p->T = (int32_t)total_tokens;
   p->kv_rows = (int32_t)kv_rows;
-  p->causal = 1;
   p->Hq = (int32_t)Hq;
   p->Hk = (int32_t)Hk;
   p->group = (int32_t)(Hq / Hk);
@@ -998,7 +1000,7 @@ gdn_status gdn_attn_shared_workspace_size(const gdn_dims* dims, int32_t num_seqs
   gdn_status st = check_attn_sizes(dims, num_seqs, total_tokens);
   if (st == GDN_OK) st = check_attn_sizes(dims, num_groups, 0);
   if (st != GDN_OK || total_tokens == 0) return st;
-  *bytes = attn_prior_at(dims, total_tokens).bytes;
+  *bytes = attn_parts_at(dims, total_tokens).bytes;
   return GDN_OK;
 }
 
@@ -1040,7 +1042,7 @@ gdn_status gdn_attn_shared(const gdn_dims* dims, int32_t num_seqs, const int32_t
   if (!kv_start || !kv_len) return GDN_ERR_INVALID_ARG;
   if (num_groups > 0 && (!group_cu || !prefix_start || !prefix_len)) return GDN_ERR_INVALID_ARG;
   const gdn::AttnSplit s = attn_split_of(dims, total_tokens);
-  const AttnPrior at = attn_prior_at(dims, total_tokens);
+  const AttnParts at = attn_parts_at(dims, total_tokens);
   if (workspace == nullptr || workspace_bytes < at.bytes) return GDN_ERR_INVALID_ARG;
   gdn::AttnArgs p{};
   const bool any = num_groups > 0;
@@ -1052,28 +1054,19 @@ gdn_status gdn_attn_shared(const gdn_dims* dims, int32_t num_seqs, const int32_t
   st = check_attn(dims, num_seqs, cu_seqlens, total_tokens, q, q_stride, k, k_stride, v, v_stride, kv_rows, scale, out,
                   lse, workspace, at.bytes, extra, extra_ptrs, 5, &p);
   if (st != GDN_OK) return st;
-  const cudaStream_t s_ = static_cast<cudaStream_t>(stream);
+  if (total_tokens * dims->n_v_heads > INT32_MAX) return GDN_ERR_EXTENT;  // a grid over the rows
   p.kv_start = kv_start;
   p.kv_len = kv_len;
-  if (any) {  // the prefixes, for their groups' tokens as one sequence each
-    gdn::AttnArgs g = p;
-    float* o = reinterpret_cast<float*>(static_cast<char*>(workspace) + at.o);
-    float* l = reinterpret_cast<float*>(static_cast<char*>(workspace) + at.lse);
-    g.cu_seqlens = group_cu;
-    g.N = num_groups;
-    g.kv_start = prefix_start;
-    g.kv_len = prefix_len;
-    g.causal = 0;
-    g.core = o;
-    g.lse = l;
-    const cudaError_t e = gdn::launch_attn(g, s, workspace, dims->io_dtype, dims->head_dim, s_);
-    if (e != cudaSuccess) return cuda_status(e);
-    p.prior_o = o;
-    p.prior_lse = l;
-    p.prior_cu = group_cu;
-    p.prior_n = num_groups;
+  p.group_cu = group_cu;
+  p.prefix_start = prefix_start;
+  p.prefix_len = prefix_len;
+  p.groups = num_groups;
+  for (int i = 0; i < 2; ++i) {
+    p.part_out[i] = reinterpret_cast<float*>(static_cast<char*>(workspace) + at.out[i]);
+    p.part_lse[i] = reinterpret_cast<float*>(static_cast<char*>(workspace) + at.lse[i]);
   }
-  return cuda_status(gdn::launch_attn(p, s, workspace, dims->io_dtype, dims->head_dim, s_));
+  return cuda_status(
+      gdn::launch_attn(p, s, workspace, dims->io_dtype, dims->head_dim, static_cast<cudaStream_t>(stream)));
 }
 
 gdn_status gdn_add_rmsnorm(int64_t rows, int64_t cols, int32_t io_dtype, const void* x, int64_t x_stride,

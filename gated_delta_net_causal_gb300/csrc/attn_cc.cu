@@ -72,13 +72,13 @@ __global__ void __launch_bounds__(kAT, 2) attn_cc_kernel(const AttnArgs p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 4 * ty + i;
-      sees[i] = r < rows ? attn_sees(p, w, r / p.group) : 0;
+      sees[i] = r < rows ? attn_sees(w, r / p.group) : 0;
       top[i] = -INFINITY;
       sum[i] = 0.f;
 #pragma unroll
       for (int j = 0; j < NP; ++j) o[i][j] = make_float2(0.f, 0.f);
     }
-    const int least = attn_sees(p, w, 0), most = attn_sees(p, w, w.tokens - 1);
+    const int least = attn_sees(w, 0), most = attn_sees(w, w.tokens - 1);
     for (int t = w.t0; t < w.t1; ++t) {
       const int first = t * kAK, n = most - first < kAK ? most - first : kAK;
       __syncthreads();
@@ -181,23 +181,18 @@ __global__ void __launch_bounds__(kAT, 2) attn_cc_kernel(const AttnArgs p) {
       }
       const int64_t token = w.q0 + r / p.group;
       const int head = attn_head(p, w.kh, r % p.group);
-      const AttnPrior prior = attn_prior(p, token, head);
-      const AttnScale f = attn_scale(top[i] * sc, l, prior, p.lse != nullptr);
-      const int64_t at = (token * p.Hq + head) * D;
+      float* lse = attn_lse(p, w.causal);
+      float* to = attn_part_out(p, w.causal);
+      if (to == nullptr) to = static_cast<float*>(p.out);
+      const AttnScale f = attn_scale(top[i] * sc, l, lse != nullptr);
+      to += (token * p.Hq + head) * D;
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const int c = 32 * j + 2 * tx;
-        float2 y = make_float2(o[i][j].x * f.own, o[i][j].y * f.own);
-        if (prior.any) {
-          const float2 b = *reinterpret_cast<const float2*>(p.prior_o + at + c);
-          y = fma2(make_float2(f.prior, f.prior), b, y);
-        }
-        *reinterpret_cast<float2*>((p.core != nullptr ? p.core : static_cast<float*>(p.out)) + at + c) = y;
-      }
-      if (tx == 0 && p.lse != nullptr) p.lse[token * p.Hq + head] = f.lse;
+      for (int j = 0; j < NP; ++j)
+        *reinterpret_cast<float2*>(to + 32 * j + 2 * tx) = make_float2(o[i][j].x * f.factor, o[i][j].y * f.factor);
+      if (tx == 0 && lse != nullptr) lse[token * p.Hq + head] = f.lse;
     }
     if (tid == 0 && w.part != kAttnWhole)
-      p.part_at[attn_slot(blockIdx.x, w.part)] = make_int4(w.part, w.q0, w.tokens, w.kh);
+      p.part_at[attn_slot(blockIdx.x, w.part)] = make_int4(w.part + 4 * w.causal, w.q0, w.tokens, w.kh);
   }
 }
 

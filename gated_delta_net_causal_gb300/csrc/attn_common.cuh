@@ -29,17 +29,25 @@ constexpr float kAttnLn2 = 0.69314718055994531f;
 struct AttnSeq {
   int q0, qn;  // first token and number of them
   int k0, kn;  // first key row and number of them
+  int causal;  // 0: a prefix, which its group's tokens see all of
 };
 
 __device__ __forceinline__ int attn_clamp(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
 
+// The sequences, then the groups with their prefixes.
+__device__ __forceinline__ int attn_lists(const AttnArgs& p) { return p.N + p.groups; }
 __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& p, int n) {
   AttnSeq s;
-  s.q0 = attn_clamp(p.cu_seqlens[n], 0, p.T);
-  s.qn = attn_clamp(p.cu_seqlens[n + 1], s.q0, p.T) - s.q0;
-  if (p.kv_start != nullptr) {
-    s.k0 = attn_clamp(p.kv_start[n], 0, p.kv_rows);
-    s.kn = attn_clamp(p.kv_len[n], 0, p.kv_rows - s.k0);
+  s.causal = n < p.N;
+  if (!s.causal) n -= p.N;
+  const int32_t* cu = s.causal ? p.cu_seqlens : p.group_cu;
+  const int32_t* start = s.causal ? p.kv_start : p.prefix_start;
+  const int32_t* len = s.causal ? p.kv_len : p.prefix_len;
+  s.q0 = attn_clamp(cu[n], 0, p.T);
+  s.qn = attn_clamp(cu[n + 1], s.q0, p.T) - s.q0;
+  if (start != nullptr) {
+    s.k0 = attn_clamp(start[n], 0, p.kv_rows);
+    s.kn = attn_clamp(len[n], 0, p.kv_rows - s.k0);
   } else {
     s.k0 = s.q0;
     s.kn = s.qn;
@@ -48,8 +56,8 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& p, int n) {
 }
 
 // Keys that the token at `at` of the sequence sees.
-__device__ __forceinline__ int attn_visible(const AttnArgs& p, const AttnSeq& s, int at) {
-  if (!p.causal) return s.kn;
+__device__ __forceinline__ int attn_visible(const AttnSeq& s, int at) {
+  if (!s.causal) return s.kn;
   const int64_t v = (int64_t)s.kn - s.qn + at + 1;
   return v > 0 ? (int)v : 0;
 }
@@ -60,7 +68,7 @@ constexpr int kAttnStart = 4;
 
 // Keys that the last token of the item from `at` on sees.
 __device__ __forceinline__ int attn_last_sees(const AttnArgs& p, const AttnSeq& s, int at) {
-  return attn_visible(p, s, (s.qn - at < p.item ? s.qn : at + p.item) - 1);
+  return attn_visible(s, (s.qn - at < p.item ? s.qn : at + p.item) - 1);
 }
 
 // Cost of a sequence's first n items, for one key head; all but the last item
@@ -68,7 +76,7 @@ __device__ __forceinline__ int attn_last_sees(const AttnArgs& p, const AttnSeq& 
 template <int KT>
 __device__ __forceinline__ int64_t attn_cost_before(const AttnArgs& p, const AttnSeq& s, int n) {
   const int64_t start = (int64_t)n * (kAttnStart * KT);
-  if (!p.causal) return start + (int64_t)n * s.kn;
+  if (!s.causal) return start + (int64_t)n * s.kn;
   const int64_t off = (int64_t)s.kn - s.qn;  // item i's last token sees off + (i + 1) item keys
   int none = 0;                              // items that see nothing
   if (off < 0) {
@@ -114,6 +122,7 @@ struct AttnPiece {
   int kh;
   int k0;     // row of the first key
   int see;    // keys that its first token sees (causal: one more for each token after it; may be negative)
+  int causal; // 0: over a prefix
   int t0, t1; // tiles of this piece
   int part;   // kAttnWhole, or whether the item's tiles end with it
   int bad;    // set where a masked tile of v holds what is not finite
@@ -121,8 +130,9 @@ struct AttnPiece {
 enum { kAttnWhole = 0, kAttnFirst = 1, kAttnMiddle = 2, kAttnLast = 3 };
 
 // keys that token i of the piece sees
-__device__ __forceinline__ int attn_sees(const AttnArgs& p, const AttnPiece& w, int i) {
-  return p.causal ? (w.see + i > 0 ? w.see + i : 0) : w.see;
+__device__ __forceinline__ int attn_sees(const AttnPiece& w, int i) {
+  const int v = w.causal ? w.see + i : w.see;
+  return v > 0 ? v : 0;
 }
 
 struct AttnPlan {
@@ -133,9 +143,9 @@ struct AttnPlan {
 // Every thread of the CTA; sums: one of shared memory for each of them.
 template <int KT, int THREADS>
 __device__ __forceinline__ void attn_plan(const AttnArgs& p, int64_t* sums, AttnPlan* plan) {
-  const int per = (p.N + THREADS - 1) / THREADS;
+  const int per = (attn_lists(p) + THREADS - 1) / THREADS;
   {
-    const int64_t a = (int64_t)threadIdx.x * per, b = a + per < p.N ? a + per : p.N;
+    const int64_t a = (int64_t)threadIdx.x * per, b = a + per < attn_lists(p) ? a + per : attn_lists(p);
     int64_t u = 0;
 #pragma unroll 1
     for (int64_t n = a; n < b; ++n) u += attn_seq_cost<KT>(p, attn_seq(p, (int)n));
@@ -161,7 +171,7 @@ __device__ __forceinline__ void attn_plan(const AttnArgs& p, int64_t* sums, Attn
     int64_t more;
     const int64_t each = attn_divide(total, G, &more);
     const int64_t u0 = each * c + (c < more ? c : more), count = c < G ? each + (c < more ? 1 : 0) : 0;
-    if (lane == 0 && count == 0) *plan = AttnPlan{0, 0, p.N};
+    if (lane == 0 && count == 0) *plan = AttnPlan{0, 0, 0};
     if (count > 0 && u0 >= incl - own && u0 < incl) {
       int64_t at = u0 - (incl - own);
       int i = lane * PER;
@@ -190,9 +200,9 @@ struct AttnWalk {
     // the sequence: the lanes have 32 of them
     int64_t u = plan.begin, own, incl;
     unsigned past;
-    AttnSeq mine{0, 0, 0, 0};
+    AttnSeq mine{0, 0, 0, 0, 0};
     for (;;) {
-      if (n + lane < p.N) mine = attn_seq(p, n + lane);
+      if (n + lane < attn_lists(p)) mine = attn_seq(p, n + lane);
       else mine.qn = 0;
       own = attn_seq_cost<KT>(p, mine);
       incl = own * p.Hk;
@@ -210,7 +220,8 @@ struct AttnWalk {
     n += l;
     u -= __shfl_sync(0xffffffffu, incl - own * p.Hk, l);
     s = AttnSeq{__shfl_sync(0xffffffffu, mine.q0, l), __shfl_sync(0xffffffffu, mine.qn, l),
-                __shfl_sync(0xffffffffu, mine.k0, l), __shfl_sync(0xffffffffu, mine.kn, l)};
+                __shfl_sync(0xffffffffu, mine.k0, l), __shfl_sync(0xffffffffu, mine.kn, l),
+                __shfl_sync(0xffffffffu, mine.causal, l)};
     kh = (int)attn_divide(u, __shfl_sync(0xffffffffu, own, l), &u);
     // the item: the last one with no more than u before it, among 32 evenly spaced ones at a time
     int lo = 0, count = attn_items(p, s);
@@ -260,7 +271,8 @@ struct AttnWalk {
     w.tokens = s.qn - at < p.item ? s.qn - at : p.item;
     w.kh = kh;
     w.k0 = s.k0;
-    w.see = p.causal ? (int)((int64_t)s.kn - s.qn + at + 1) : s.kn;
+    w.see = s.causal ? (int)((int64_t)s.kn - s.qn + at + 1) : s.kn;
+    w.causal = s.causal;
     w.t0 = from < keys ? from : keys;
     w.t1 = to < keys ? to : keys;  // (no tile where one stands for none)
     w.part = from > 0 ? (to == tiles ? kAttnLast : kAttnMiddle) : (to == tiles ? kAttnWhole : kAttnFirst);
@@ -279,37 +291,25 @@ __device__ __forceinline__ int attn_head(const AttnArgs& p, int kh, int m) {
   return p.map == GDN_MAP_TILED ? m * p.Hk + kh : kh * p.group + m;
 }
 
-// What a row has over other keys: whether there is anything, and its lse.
-struct AttnPrior {
-  bool any;
-  float lse;
-};
-__device__ __forceinline__ AttnPrior attn_prior(const AttnArgs& p, int64_t token, int head) {
-  if (p.prior_o == nullptr || token < p.prior_cu[0] || token >= p.prior_cu[p.prior_n]) return AttnPrior{false, 0.f};
-  return AttnPrior{true, p.prior_lse[token * p.Hq + head]};
+// Where a piece's outputs go: out, or with groups, in fp32, those over the
+// sequences' keys and over the prefixes apart.
+__device__ __forceinline__ float* attn_part_out(const AttnArgs& p, int causal) {
+  return p.groups > 0 ? p.part_out[causal ? 0 : 1] : nullptr;
+}
+__device__ __forceinline__ float* attn_lse(const AttnArgs& p, int causal) {
+  return p.groups > 0 ? p.part_lse[causal ? 0 : 1] : p.lse;
 }
 
-// A row's outputs from the largest score (times scale and log2 e), the sum of
-// exponentials to it and the prior part: the factors of the unnormalised
-// outputs and of the prior ones, and the logarithm of the sum. A row that sees
-// nothing has a sum of 0; scores that are all NaN have no largest, but a sum
-// that is NaN.
+// A row's factor of its unnormalised outputs and the logarithm of its sum, from
+// the largest score (times scale and log2 e) and the sum of exponentials to it.
+// A row that sees nothing has a sum of 0; scores that are all NaN have no
+// largest, but a sum that is NaN.
 struct AttnScale {
-  float own, prior, lse;
+  float factor, lse;
 };
-__device__ __forceinline__ AttnScale attn_scale(float top, float sum, AttnPrior prior, bool lse) {
-  float m = top, w0 = 1.f, w1 = 0.f, s = sum;
-  if (prior.any) {
-    const float a = prior.lse * kAttnLog2e;
-    m = fmaxf(top, a);
-    if (m == -INFINITY) m = 0.f;
-    w0 = exp2f(top - m);
-    w1 = exp2f(a - m);
-    s = fmaf(sum, w0, w1);
-  }
-  if (s == 0.f) return AttnScale{0.f, 0.f, -INFINITY};
-  const float inv = __frcp_rn(s);
-  return AttnScale{w0 * inv, w1 * inv, lse ? (m + log2f(s)) * kAttnLn2 : 0.f};
+__device__ __forceinline__ AttnScale attn_scale(float top, float sum, bool lse) {
+  if (sum == 0.f) return AttnScale{0.f, -INFINITY};
+  return AttnScale{__frcp_rn(sum), lse ? (top + log2f(sum)) * kAttnLn2 : 0.f};
 }
 
 }  // namespace gdn

@@ -12,6 +12,18 @@ namespace {
 
 constexpr int kJWarps = 8;
 
+// four elements of a row times f, in fp32 where there is a place for that
+template <typename T>
+__device__ __forceinline__ void put_row(void* out, float* wide, int64_t at, float f, float4 o) {
+  o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+  if (wide != nullptr) {
+    *reinterpret_cast<float4*>(wide + at) = o;
+  } else {
+    T* y = static_cast<T*>(out) + at;
+    y[0] = from_f32<T>(o.x), y[1] = from_f32<T>(o.y), y[2] = from_f32<T>(o.z), y[3] = from_f32<T>(o.w);
+  }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kJWarps) attn_join_kernel(const AttnArgs p, int ctas) {
   grid_dependency_wait();
@@ -25,12 +37,12 @@ __global__ void __launch_bounds__(32 * kJWarps) attn_join_kernel(const AttnArgs 
   const bool in = b + lane < ctas;
   const int4 mine = in ? p.part_at[slot_of(lane)] : make_int4(0, 0, 0, 0);
   float2 ml = in && r < p.part_rows ? p.part_ml[slot_of(lane) * p.part_rows + r] : make_float2(0.f, 0.f);
-  if (at.x != kAttnFirst || r >= at.z * p.group) return;
-  unsigned end = __ballot_sync(0xffffffffu, mine.x == kAttnLast && lane > 0);
+  if ((at.x & 3) != kAttnFirst || r >= at.z * p.group) return;
+  unsigned end = __ballot_sync(0xffffffffu, (mine.x & 3) == kAttnLast && lane > 0);
   int parts = end != 0 ? __ffs(end) : 0;
   for (int j0 = 32; parts == 0; j0 += 32) {  // more than 32 parts
     if (b + j0 >= ctas) return;              // (an item that is begun is ended)
-    end = __ballot_sync(0xffffffffu, b + j0 + lane < ctas && p.part_at[slot_of(j0 + lane)].x == kAttnLast);
+    end = __ballot_sync(0xffffffffu, b + j0 + lane < ctas && (p.part_at[slot_of(j0 + lane)].x & 3) == kAttnLast);
     if (end != 0) parts = j0 + __ffs(end);
   }
   const int64_t token = at.y + r / p.group;
@@ -68,38 +80,63 @@ __global__ void __launch_bounds__(32 * kJWarps) attn_join_kernel(const AttnArgs 
     }
   }
   sum = group_sum<32>(sum);
-  const AttnPrior prior = attn_prior(p, token, head);
-  const AttnScale f = attn_scale(top, sum, prior, p.lse != nullptr);
-  o = make_float4(o.x * f.own, o.y * f.own, o.z * f.own, o.w * f.own);
-  const int64_t to = (token * p.Hq + head) * D + 4 * lane;
-  if (holds) {
-    if (prior.any) {
-      const float4 x = *reinterpret_cast<const float4*>(p.prior_o + to);
-      o.x = fmaf(f.prior, x.x, o.x), o.y = fmaf(f.prior, x.y, o.y);
-      o.z = fmaf(f.prior, x.z, o.z), o.w = fmaf(f.prior, x.w, o.w);
-    }
-    if (p.core != nullptr) {
-      *reinterpret_cast<float4*>(p.core + to) = o;
-    } else {
-      T* y = static_cast<T*>(p.out) + to;
-      y[0] = from_f32<T>(o.x), y[1] = from_f32<T>(o.y), y[2] = from_f32<T>(o.z), y[3] = from_f32<T>(o.w);
-    }
-  }
-  if (lane == 0 && p.lse != nullptr) p.lse[token * p.Hq + head] = f.lse;
+  const int causal = at.x >> 2;
+  float* lse = attn_lse(p, causal);
+  float* part_out = attn_part_out(p, causal);
+  const AttnScale f = attn_scale(top, sum, lse != nullptr);
+  if (holds) put_row<T>(p.out, part_out, (token * p.Hq + head) * D + 4 * lane, f.factor, o);
+  if (lane == 0 && lse != nullptr) lse[token * p.Hq + head] = f.lse;
 }
 
+// With groups: a row's outputs over its own keys and over its group's prefix,
+// by their sums. A warp a row.
 template <typename T, int D>
-cudaError_t join(const AttnArgs& p, int ctas, cudaStream_t stream) {
+__global__ void __launch_bounds__(32 * kJWarps) attn_merge_kernel(const AttnArgs p) {
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * kJWarps + (threadIdx.x >> 5), token = row / p.Hq;
+  if (token >= p.T || token < p.cu_seqlens[0] || token >= p.cu_seqlens[p.N]) return;  // no sequence's
+  const bool any = token >= p.group_cu[0] && token < p.group_cu[p.groups];
+  const float a = p.part_lse[0][row], b = any ? p.part_lse[1][row] : -INFINITY;
+  const bool holds = 4 * lane < D;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4 x = holds ? *reinterpret_cast<const float4*>(p.part_out[0] + row * D + 4 * lane) : zero;
+  const float4 y = holds && any ? *reinterpret_cast<const float4*>(p.part_out[1] + row * D + 4 * lane) : zero;
+  float m = fmaxf(a, b);
+  if (m == -INFINITY) m = 0.f;  // nothing is seen
+  const float wa = expf(a - m), wb = expf(b - m), s = wa + wb;
+  const float inv = s == 0.f ? 0.f : 1.f / s, fa = wa * inv, fb = wb * inv;
+  if (holds)
+    put_row<T>(p.out, nullptr, row * D + 4 * lane, 1.f,
+               make_float4(fmaf(fa, x.x, fb * y.x), fmaf(fa, x.y, fb * y.y), fmaf(fa, x.z, fb * y.z),
+                           fmaf(fa, x.w, fb * y.w)));
+  if (lane == 0 && p.lse != nullptr) p.lse[row] = s == 0.f ? -INFINITY : m + logf(s);
+}
+
+// Their launches overlap the end of the kernel before (all of them wait for it).
+template <typename... A>
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)ctas, (unsigned)((p.part_rows + kJWarps - 1) / kJWarps));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(32 * kJWarps);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];  // its launch overlaps the attention kernel's end
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D>, p, ctas);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+template <typename T, int D>
+cudaError_t join(const AttnArgs& p, int ctas, cudaStream_t stream) {
+  if (p.part_o != nullptr) {
+    const dim3 grid((unsigned)ctas, (unsigned)((p.part_rows + kJWarps - 1) / kJWarps));
+    const cudaError_t e = launch_after(attn_join_kernel<T, D>, grid, stream, p, ctas);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.groups == 0) return cudaSuccess;
+  const int64_t rows = (int64_t)p.T * p.Hq;
+  return launch_after(attn_merge_kernel<T, D>, dim3((unsigned)((rows + kJWarps - 1) / kJWarps)), stream, p);
 }
 template <typename T>
 cudaError_t join_dim(const AttnArgs& p, int32_t D, int ctas, cudaStream_t stream) {

@@ -247,7 +247,7 @@ __device__ __forceinline__ int half_tiles(const AttnArgs& p, const AttnPiece& w,
   const int tokens = p.item / 2, first = h * tokens;
   if (first >= w.tokens) return 0;
   const int last = (first + tokens < w.tokens ? first + tokens : w.tokens) - 1;
-  const int seen = attn_sees(p, w, last);
+  const int seen = attn_sees(w, last);
   int end = seen / kBK + (seen % kBK != 0);
   end = end < w.t1 ? end : w.t1;
   return end > w.t0 ? end - w.t0 : 0;
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
           AttnPiece w;
           if (!take(i, &w)) break;
           const int tiles = same(w.t1 - w.t0), na = same(half_tiles(p, w, 0)), nb = same(half_tiles(p, w, 1));
-          const int least = same(attn_sees(p, w, 0)), t0 = same(w.t0);
+          const int least = same(attn_sees(w, 0)), t0 = same(w.t0);
           for (int j = 0; ok && j < tiles; ++j) {
             const uint32_t st = next_tile(sh.v_full);
             if (ok && masked_tile(least, t0 + j)) {
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       for (int i = 0;; ++i) {
         AttnPiece w;
         if (!take(i, &w)) break;
-        const int least = attn_sees(p, w, 0), most = attn_sees(p, w, w.tokens - 1);
+        const int least = attn_sees(w, 0), most = attn_sees(w, w.tokens - 1);
         for (int t = w.t0; t < w.t1; ++t) {
           const uint32_t st = n_v % G::kStages;
           if (!__all_sync(0xffffffffu, wait(&sh.v_full[st], (n_v / G::kStages) & 1))) break;
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       if (!take(i, &w)) break;
       const int at = row_token;  // of the item
       const bool valid = row_used && at < w.tokens;
-      const int sees = valid ? attn_sees(p, w, at) : 0;
+      const int sees = valid ? attn_sees(w, at) : 0;
       const int n = half_tiles(p, w, h);
       const bool some = __any_sync(0xffffffffu, valid);
       const int least = (int)__reduce_min_sync(0xffffffffu, valid ? (unsigned)sees : 0x7fffffffu);
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
         const float l = sum.x + sum.y, top = M - (M == -INFINITY ? 0.f : Half<T>::kLift);
         if (n > 0 && *(volatile int*)&sh.piece[i % kBRing].bad != 0) {
           // what the look through V took out of rows that this one sees
-          const int item_least = attn_sees(p, w, 0);
+          const int item_least = attn_sees(w, 0);
           const int first = max(item_least, w.t0 * kBK), last = (int)min((int64_t)sees, (int64_t)w.t1 * kBK);
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
@@ -668,8 +668,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
           tc::tmem_wait_st();
         }
         int64_t to_row = 0;
-        AttnScale f{1.f, 0.f, 0.f};
-        AttnPrior prior{false, 0.f};
+        AttnScale f{1.f, 0.f};
+        float* part_out = attn_part_out(p, w.causal);
         if (valid) {
           const int64_t token = w.q0 + at;
           const int head = attn_head(p, w.kh, member);
@@ -679,16 +679,16 @@ __global__ void __launch_bounds__(kBThreads, 1)
             p.part_ml[slot_row] = make_float2(top, l);
             to_row = slot_row * D;
           } else {
-            prior = attn_prior(p, token, head);
-            f = attn_scale(top, l, prior, p.lse != nullptr);
+            float* lse = attn_lse(p, w.causal);
+            f = attn_scale(top, l, lse != nullptr);
             to_row = (token * p.Hq + head) * D;
-            if (p.lse != nullptr) p.lse[token * p.Hq + head] = f.lse;
+            if (lse != nullptr) lse[token * p.Hq + head] = f.lse;
           }
         }
         // 64 or 128 bytes of each row at a time through shared memory, so that
         // they are stored side by side (from the lanes' rows a store of 16 bytes
         // each touches 32 lines)
-        const bool wide = w.part != kAttnWhole || p.core != nullptr;  // fp32
+        const bool wide = w.part != kAttnWhole || part_out != nullptr;  // fp32
         unsigned char* stage = sm + G::kOut + warp * 4096;
         const unsigned live = __ballot_sync(0xffffffffu, valid);
         const auto store = [&](auto* y, auto as) {
@@ -715,16 +715,9 @@ __global__ void __launch_bounds__(kBThreads, 1)
             }
 #pragma unroll
             for (int e = 0; e < kCols; e += 2) {
-              const float2 y = fma2(make_float2(o[e], o[e + 1]), make_float2(f.own, f.own), make_float2(-0.f, -0.f));
+              const float2 y = fma2(make_float2(o[e], o[e + 1]), make_float2(f.factor, f.factor), make_float2(-0.f, -0.f));
               o[e] = y.x, o[e + 1] = y.y;
             }
-            if (prior.any)
-#pragma unroll
-              for (int e = 0; e < kCols; e += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(p.prior_o + to_row + c + e);
-                o[e] = fmaf(f.prior, x.x, o[e]), o[e + 1] = fmaf(f.prior, x.y, o[e + 1]);
-                o[e + 2] = fmaf(f.prior, x.z, o[e + 2]), o[e + 3] = fmaf(f.prior, x.w, o[e + 3]);
-              }
             __syncwarp();
 #pragma unroll
             for (int e = 0; e < kLanes; ++e) {
@@ -746,10 +739,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
             }
           }
         };
-        if (wide) store(w.part != kAttnWhole ? p.part_o : p.core, 0.f);
+        if (wide) store(w.part != kAttnWhole ? p.part_o : part_out, 0.f);
         else store(static_cast<T*>(p.out), T());
         if (tid == 0 && w.part != kAttnWhole)
-          p.part_at[attn_slot(blockIdx.x, w.part)] = make_int4(w.part, w.q0, w.tokens, w.kh);
+          p.part_at[attn_slot(blockIdx.x, w.part)] = make_int4(w.part + 4 * w.causal, w.q0, w.tokens, w.kh);
       }
       give(i);
     }

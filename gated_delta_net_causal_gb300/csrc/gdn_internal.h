@@ -201,24 +201,25 @@ struct AttnArgs {
   const int32_t* kv_start;  // null: the keys are the sequence's own rows
   const int32_t* kv_len;
   int32_t kv_rows;          // <= 2^31 - 1025
-  int32_t causal;           // 0: every token sees all of its sequence's keys
+  // groups of tokens that see all of a prefix as well
+  const int32_t* group_cu;
+  const int32_t* prefix_start;
+  const int32_t* prefix_len;
+  int32_t groups;           // 0: none
   int32_t Hq, Hk, group, map;
   float scale;
   void* out;                // [T][Hq][D] io dtype
-  float* core;              // or, instead, fp32
   float* lse;               // [T][Hq], or null
-  // outputs over other keys, joined with these (null: none), of the tokens
-  // from prior_cu[0] to prior_cu[prior_n]
-  const float* prior_o;     // [T][Hq][D]
-  const float* prior_lse;   // [T][Hq]
-  const int32_t* prior_cu;
-  int32_t prior_n;
+  // with groups: outputs and lse over the sequences' own keys and over the
+  // prefixes, which are joined into out and lse
+  float* part_out[2];       // [T][Hq][D]
+  float* part_lse[2];       // [T][Hq]
   // set by launch_attn
   int32_t item;             // tokens of an item
   int32_t part_rows;        // rows of a part
   float* part_o;            // [2 CTAs][part_rows][D], null: no item is cut
   float2* part_ml;          // [2 CTAs][part_rows]
-  int4* part_at;            // [2 CTAs] what the part is: AttnPiece's part, q0, tokens, kh
+  int4* part_at;            // [2 CTAs] what the part is: AttnPiece's part and list (x 4), q0, tokens, kh
 };
 // How launch_attn cuts the work, and its workspace
 struct AttnSplit {
