@@ -12,6 +12,12 @@ pytestmark = pytest.mark.gpu
 INF, NAN = float("inf"), float("nan")
 
 
+@pytest.fixture(autouse=True)
+def no_wait_gave_up():
+    yield
+    assert gdn.gdn_device_error() == 0
+
+
 def ints(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
@@ -132,6 +138,43 @@ def test_shared_prefixes(dtype, hq, hk, D, each, keys, prefixes):
     c = Case(D + len(keys), [each] * len(keys), keys, hq, hk, D, dtype, tiled=D == 64, prefixes=prefixes, extra=1)
     c.run_shared()
     c.check(shared=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("lengths,keys,hq,hk,D", [
+    ([4133], None, 8, 2, 128), ([3001, 5, 2500], None, 8, 1, 64), ([2111, 700], [2111, 5000], 3, 1, 96),
+    ([300], [9000], 16, 2, 32), ([1, 1, 1], [20000, 3, 9001], 4, 1, 128)])
+def test_long_sequences(dtype, lengths, keys, hq, hk, D):
+    """Many tiles in one item and many items in one CTA, twice over; every 97th token and the ends against fp64, the others
+    against the second run."""
+    if dtype == "f32" and keys is None:
+        lengths = [n // 2 for n in lengths]
+    c = Case(21, lengths, keys, hq, hk, D, dtype)
+    c.run()
+    first = c.out.clone(), c.lse.clone()
+    c.fresh()
+    c.run()
+    assert torch.equal(first[0], c.out) and torch.equal(first[1], c.lse)
+    at = 0
+    for n, m, start in zip(c.lengths, c.keys, c.start):
+        some = sorted(set(range(0, n, 97)) | {n - 1, n // 2, max(n - 65, 0)})
+        rows = [at + i for i in some]
+        k, v = (ref.f64(x[start:start + m]).reshape(m, hk, D) for x in (c.k, c.v))
+        o, tol, l, ltol = ref.attention(ref.f64(c.q[rows]).reshape(-1, hq, D), k, v, ref.causal(n, m)[some], D ** -0.5,
+                                        dtype)
+        ref.check(ref.f64(c.out[rows]), o, tol, "out")
+        ref.check(ref.f64(c.lse[rows]), l, ltol, "lse")
+        at += n
+
+
+def test_sequences_that_share_their_keys():
+    """The same rows of the cache for several sequences, as forked ones have them."""
+    c = Case(22, [1, 1, 4], [500, 500, 500], 8, 2, 64)
+    c.start = [c.start[0], c.start[0] + 100, c.start[0]]
+    c.keys = [500, 300, 400]
+    c.kv = {"kv_start": ints(c.start), "kv_len": ints(c.keys)}
+    c.run()
+    c.check()
 
 
 def test_shared_without_groups_is_the_plain_call():
