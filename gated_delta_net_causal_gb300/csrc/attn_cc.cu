@@ -5,7 +5,9 @@
 // 4 ty + i, keys 4 tx + j), then the outputs of the same four rows at D / 16
 // columns. q and k lie transposed in shared memory, so that a step of the
 // contraction is two 16-byte reads for 16 products; the weights take k's
-// place, transposed as well.
+// place, transposed as well. Warps without a row (a single token has a few of
+// the 64) only load. 4096 tokens, 8 heads of 128: 0.90 ms, 38 TFLOP/s, half of
+// the fp32 units' rate; bound by shared memory and the phases between barriers.
 #include "attn_common.cuh"
 
 namespace gdn {
@@ -78,20 +80,23 @@ __global__ void __launch_bounds__(kAT, 2) attn_cc_kernel(const AttnArgs p) {
 #pragma unroll
       for (int j = 0; j < NP; ++j) o[i][j] = make_float2(0.f, 0.f);
     }
+    const bool busy = (ty & ~1) * 4 < rows;  // whether this warp has a row: a single token has a few of the 64
     const int least = attn_sees(w, 0), most = attn_sees(w, w.tokens - 1);
     for (int t = w.t0; t < w.t1; ++t) {
       const int first = t * kAK, n = most - first < kAK ? most - first : kAK;
       __syncthreads();
+      // k: eight lanes along a row, which meets few lines and few banks; v: a row's lanes side by side
       for (int u = tid; u < kAK * (D / 4); u += kAT) {
-        const int r = u % kAK, c = u / kAK * 4;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-        if (r < n) {
-          const int64_t row = (int64_t)w.k0 + first + r;
-          x = load4(gk + row * p.k_stride + w.kh * D + c);
-          y = load4(gv + row * p.v_stride + w.kh * D + c);
-        }
+        const int r = (u >> 3) % kAK, c = ((u >> 3) / kAK * 8 + (u & 7)) * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < n) x = load4(gk + ((int64_t)w.k0 + first + r) * p.k_stride + w.kh * D + c);
         put(kt + c * kAP + r, x);
-        *reinterpret_cast<float4*>(vs + r * D + c) = y;
+      }
+      for (int u = tid; u < kAK * (D / 4); u += kAT) {
+        const int r = u / (D / 4), c = u % (D / 4) * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < n) x = load4(gv + ((int64_t)w.k0 + first + r) * p.v_stride + w.kh * D + c);
+        *reinterpret_cast<float4*>(vs + r * D + c) = x;
       }
       __syncthreads();
       float s[4][4];
@@ -99,16 +104,20 @@ __global__ void __launch_bounds__(kAT, 2) attn_cc_kernel(const AttnArgs p) {
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+      if (busy) {
 #pragma unroll 8
-      for (int d = 0; d < D; ++d) {
-        const float4 a = *reinterpret_cast<const float4*>(qt + d * kAP + 4 * ty);
-        const float4 b = *reinterpret_cast<const float4*>(kt + d * kAP + 4 * tx);
-        const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+        for (int d = 0; d < D; ++d) {
+          const float4 a = *reinterpret_cast<const float4*>(qt + d * kAP + 4 * ty);
+          const float4 b = *reinterpret_cast<const float4*>(kt + d * kAP + 4 * tx);
+          const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[i][j] = fmaf(av[i], bv[j], s[i][j]);
+            for (int j = 0; j < 4; ++j) s[i][j] = fmaf(av[i], bv[j], s[i][j]);
+        }
       }
+      __syncthreads();  // k is no longer read
+      if (!busy) continue;
       const bool masked = first + kAK > least;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -133,11 +142,10 @@ __global__ void __launch_bounds__(kAT, 2) attn_cc_kernel(const AttnArgs p) {
 #pragma unroll
         for (int j = 0; j < NP; ++j) o[i][j] = make_float2(o[i][j].x * f, o[i][j].y * f);
       }
-      __syncthreads();  // k is no longer read
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         *reinterpret_cast<float4*>(kt + (4 * tx + j) * kAP + 4 * ty) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
-      __syncthreads();
+      __syncwarp();  // (a warp reads the weights of its own rows)
       if (!masked) {
 #pragma unroll 4
         for (int k = 0; k < kAK; ++k) {
