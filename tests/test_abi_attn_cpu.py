@@ -247,3 +247,43 @@ def test_binding_refusals(monkeypatch):
             gdn.gdn_attn_prefill(d, *args, **kw)
     with pytest.raises(ValueError):
         gdn.gdn_attn_shared(d, cu, q, k, k, i(1), i(1), i(2), i(2), i(2), out)
+
+
+def test_workspaces_belong_to_the_calls_stream(monkeypatch):
+    """What the binding allocates by itself is allocated on the stream that the call runs on."""
+    import contextlib
+
+    seen, current = [], ["current"]
+
+    @contextlib.contextmanager
+    def stream(s):
+        current.append(s)
+        yield
+        current.pop()
+
+    real = torch.empty
+
+    def empty(*a, **kw):
+        if kw.get("dtype") == torch.uint8:
+            seen.append(current[-1])
+        return real(*a, **kw)
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: 0
+
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: ("external", handle))
+    monkeypatch.setattr(gdn, "library", Library)
+    monkeypatch.setattr(gdn, "_current_device", lambda: -1)
+    monkeypatch.setattr(gdn, "_current_raw_stream", lambda dev: 0)
+    for name in ("gdn_attn_prefill_workspace_size", "gdn_attn_shared_workspace_size"):
+        monkeypatch.setattr(gdn, name, lambda *a: 4096)
+    bf, i = torch.bfloat16, lambda *x: torch.tensor(x, dtype=torch.int32)
+    d, z = gdn.dims(1, 2, 64, io_dtype=bf), lambda *s: torch.zeros(s, dtype=bf)
+    for s, want in ((None, "current"), (7, ("external", 7))):
+        gdn.gdn_attn_prefill(d, i(0, 3), z(3, 128), z(3, 64), z(3, 64), z(3, 2, 64), stream=s)
+        gdn.gdn_attn_shared(d, i(0, 3), z(3, 128), z(9, 64), z(9, 64), i(0), i(5), i(0, 3), i(5), i(2), z(3, 2, 64), stream=s)
+        assert seen == [want, want]
+        seen.clear()
