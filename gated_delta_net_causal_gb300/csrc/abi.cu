@@ -754,7 +754,6 @@ gdn_status check_attn(const gdn_dims* dims, int32_t num_seqs, const int32_t* cu_
       return GDN_ERR_EXTENT;
     if (st * es % 16 != 0) return GDN_ERR_ALIGN;
   }
-  if (dims->io_dtype != GDN_F32 && !gdn::linear_supported()) return GDN_ERR_UNSUPPORTED;  // no TMA encoder
   // the work (keys, of at most so many items and heads) is counted in 64 bits
   int64_t cost = 0;
   if (!mul_ok((2 * total_tokens + 2 * kMaxGridY) * Hk, kv_rows + 1024, &cost)) return GDN_ERR_EXTENT;
@@ -779,6 +778,7 @@ gdn_status check_attn(const gdn_dims* dims, int32_t num_seqs, const int32_t* cu_
     for (int j = 0; j < i; ++j)
       if (overlap(outputs[i], outputs[j])) return GDN_ERR_ALIAS;
   }
+  if (dims->io_dtype != GDN_F32 && !gdn::linear_supported()) return GDN_ERR_UNSUPPORTED;  // no TMA encoder
   p->q = q;
   p->q_stride = q_stride;
   p->k = k;
