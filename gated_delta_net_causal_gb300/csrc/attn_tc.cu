@@ -21,7 +21,7 @@
 //
 // Warps 0 to 3 are A's rows, 4 to 7 B's; two issue the products, one hands out
 // the pieces of work (attn_common.cuh) and loads (Q once an item, K and V
-// through a ring of tiles), one looks through masked tiles of V: a
+// through a ring of tiles each), one looks through masked tiles of V: a
 // masked weight is 0, but 0 times what is not finite would reach rows that do
 // not see it. So rows of V that nobody sees become 0, and in rows that only
 // some see what is not finite is replaced by 0 and added, at the end, to the
@@ -38,7 +38,7 @@
 // key heads of 128, 104 us, 1.32 PFLOP/s of the visible pairs, the tensor pipe
 // 62 % active; 32,768 tokens, 16 and 2 heads, 1.95 PFLOP/s. 64 single tokens on
 // caches of up to 8192 keys 170 us, 6.4 TB/s. What bounds it: on prompts the
-// tensor cores, and the start and end of an item (about 8000 cycles in which
+// tensor cores, and the start and end of an item (about 5000 cycles in which
 // they idle); at head_dim 64 and below the softmax's 1600 cycles a tile; on
 // caches memory.
 //
