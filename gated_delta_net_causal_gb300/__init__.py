@@ -802,13 +802,15 @@ def gdn_attn_prefill(d: GdnDims, cu_seqlens, q, k, v, out, lse=None, scale: Opti
     cp = _dense(cu_seqlens, "cu_seqlens", torch.int32, n + 1, dev)
     rows, *operands = _attn_operands(d, n, q, k, v, kv_start, kv_len, dev)
     outputs = _attn_outputs(d, rows, scale, out, lse, dev)
+    ws_ptr, ws_bytes = None, 0
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto', None or a CUDA tensor")
-        need = gdn_attn_prefill_workspace_size(d, n, rows)
-        workspace = _scratch(need, q.device, stream) if need > 0 else None
-    ws_ptr, ws_bytes = None, 0
-    if workspace is not None:
+        ws_bytes = gdn_attn_prefill_workspace_size(d, n, rows)
+        if ws_bytes > 0:
+            workspace = _scratch(ws_bytes, q.device, stream)
+            ws_ptr = workspace.data_ptr()
+    elif workspace is not None:
         ws_bytes = workspace.numel()
         ws_ptr = _dense(workspace, "workspace", torch.uint8, ws_bytes, dev)
     st = library().gdn_attn_prefill(ctypes.byref(d), n, cp, rows, *operands, *outputs, ws_ptr, ws_bytes,
@@ -831,12 +833,16 @@ def gdn_attn_shared(d: GdnDims, cu_seqlens, q, k, v, kv_start, kv_len, group_cu,
                 _dense(prefix_start, "prefix_start", i32, groups, dev),
                 _dense(prefix_len, "prefix_len", i32, groups, dev))
     outputs = _attn_outputs(d, rows, scale, out, lse, dev)
+    ws_ptr, ws_bytes = None, 0
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto' or a CUDA tensor")
-        workspace = _scratch(gdn_attn_shared_workspace_size(d, n, rows, groups), q.device, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel()
-    ws_ptr = None if workspace is None else _dense(workspace, "workspace", torch.uint8, ws_bytes, dev)
+        ws_bytes = gdn_attn_shared_workspace_size(d, n, rows, groups)
+        workspace = _scratch(ws_bytes, q.device, stream)
+        ws_ptr = workspace.data_ptr()
+    elif workspace is not None:
+        ws_bytes = workspace.numel()
+        ws_ptr = _dense(workspace, "workspace", torch.uint8, ws_bytes, dev)
     st = library().gdn_attn_shared(ctypes.byref(d), n, cp, rows, *operands, *prefixes, *outputs, ws_ptr, ws_bytes,
                                    _stream_on(stream, dev))
     if st:
