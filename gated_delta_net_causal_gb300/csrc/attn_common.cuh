@@ -62,8 +62,9 @@ __device__ __forceinline__ int attn_visible(const AttnSeq& s, int at) {
   return v > 0 ? (int)v : 0;
 }
 
-// What an item costs besides its keys, in tiles (a prompt of 4096 tokens and ragged prompts of 34,482 tokens: with 2 114 and 938 us,
-// with 3 110 and 899, with 4 107 and 884, with 6 109 and 903).
+// What an item costs besides its keys, in tiles. A prompt of 4096 tokens and
+// ragged prompts of 34,482: with 2 114 and 938 us, with 3 110 and 899, with 4
+// 107 and 884, with 6 109 and 903.
 constexpr int kAttnStart = 4;
 
 // Keys that the last token of the item from `at` on sees.
