@@ -21,7 +21,7 @@ OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libgdn.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",
+NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC,-ffp-contract=off",
                      "-I", INCLUDE, "-I", CSRC]
 
 

@@ -869,7 +869,6 @@ gdn_status gdn_decay_prefill(const gdn_dims* dims, int32_t num_seqs, const int32
 gdn_status gdn_rope_frequencies(int32_t rotary_dim, int32_t layout, double base, int32_t scaling, double factor,
                                 double original_length, double low, double high, double amplitude,
                                 gdn_rope_table* table) {
-  const double two_pi = 6.283185307179586476925286766559;
   if (table == nullptr || rotary_dim < 2 || rotary_dim > 128 || rotary_dim % 2 != 0) return GDN_ERR_INVALID_ARG;
   if (layout != GDN_ROPE_HALF && layout != GDN_ROPE_INTERLEAVED) return GDN_ERR_INVALID_ARG;
   if (scaling < GDN_ROPE_PLAIN || scaling > GDN_ROPE_RAMP) return GDN_ERR_INVALID_ARG;
@@ -879,31 +878,11 @@ gdn_status gdn_rope_frequencies(int32_t rotary_dim, int32_t layout, double base,
   if (ranged && (!(original_length > 0.0) || !isfinite(original_length) || !(low > 0.0) || !(high > low) ||
                  !isfinite(high)))
     return GDN_ERR_INVALID_ARG;
-  const double R = rotary_dim;
-  double first = 0.0, last = 0.0;
-  if (scaling == GDN_ROPE_RAMP) {
-    const auto at = [&](double turns) { return R * log(original_length / (two_pi * turns)) / (2.0 * log(base)); };
-    first = fmax(floor(at(high)), 0.0);
-    last = fmin(ceil(at(low)), R - 1.0);
-  }
   gdn_rope_table t{};
   t.rotary_dim = rotary_dim;
   t.layout = layout;
   t.amplitude = (float)amplitude;
-  for (int i = 0; i < rotary_dim / 2; ++i) {
-    const double b = pow(base, -2.0 * i / R);
-    double f = b;
-    if (scaling == GDN_ROPE_LINEAR) {
-      f = b / factor;
-    } else if (ranged) {
-      const double w = scaling == GDN_ROPE_BANDS ? (original_length * b / two_pi - low) / (high - low)
-                                                 : 1.0 - (i - first) / fmax(last - first, 0.001);
-      const double keep = w < 0.0 ? 0.0 : w > 1.0 ? 1.0 : w;
-      f = b * (keep + (1.0 - keep) / factor);
-    }
-    const double turns = f / two_pi;
-    t.step[i] = (uint64_t)ldexp(turns - floor(turns), 64);
-  }
+  gdn::rope_steps(rotary_dim, base, scaling, factor, original_length, low, high, t.step);
   *table = t;
   return GDN_OK;
 }

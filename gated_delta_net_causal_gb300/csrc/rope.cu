@@ -7,8 +7,8 @@
 // An angle is a fraction of a turn, held as a 64-bit integer (2^64 one turn):
 // position times the pair's step modulo 2^64 is that fraction exactly, however
 // far the position is, where a product in fp32 would have lost it (2^-24 of
-// 10^6 turns is a sixteenth of one). The step is rounded at 2^-64 of a turn,
-// the fraction at 2^-24 of itself, then sincospif.
+// 10^6 turns is a sixteenth of one). The step is the frequency rounded to 2^-64
+// of a turn (rope_steps.cu), the fraction at 2^-24 of itself, then sincospif.
 //
 // A CTA takes one token or a few and puts the sines and cosines of their pairs
 // into shared memory. A thread has the same elements of every so-many-th head

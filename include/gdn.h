@@ -534,7 +534,8 @@ typedef enum gdn_rope_scaling {
 } gdn_rope_scaling;
 
 /* A model's rotary positions, made once by gdn_rope_frequencies (host
- * memory). step[i] is f_i as a fraction of a turn, 2^64 one turn. */
+ * memory). step[i] is f_i as a fraction of a turn, 2^64 one turn, rounded to
+ * the nearest unit. */
 typedef struct gdn_rope_table {
   int32_t rotary_dim; /* R: even, 2..128 */
   int32_t layout;     /* gdn_rope_layout */
