@@ -882,7 +882,8 @@ gdn_status gdn_rope_frequencies(int32_t rotary_dim, int32_t layout, double base,
   t.rotary_dim = rotary_dim;
   t.layout = layout;
   t.amplitude = (float)amplitude;
-  gdn::rope_steps(rotary_dim, base, scaling, factor, original_length, low, high, t.step);
+  if (!gdn::rope_steps(rotary_dim, base, scaling, factor, original_length, low, high, t.step))
+    return GDN_ERR_INVALID_ARG;
   *table = t;
   return GDN_OK;
 }

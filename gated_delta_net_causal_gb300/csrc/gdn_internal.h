@@ -280,8 +280,8 @@ cudaError_t read_error_add_rmsnorm(int32_t* status, bool clear);
 cudaError_t read_error_decay_step(int32_t* status, bool clear);
 cudaError_t read_error_decay_scan(int32_t* status, bool clear);
 cudaError_t read_error_linear_fp8(int32_t* status, bool clear);
-// rope_steps.cu: the steps of gdn_rope_table
-void rope_steps(int32_t rotary_dim, double base, int32_t scaling, double factor, double original_length, double low,
+// rope_steps.cu: the steps of gdn_rope_table; false: a frequency is not finite
+bool rope_steps(int32_t rotary_dim, double base, int32_t scaling, double factor, double original_length, double low,
                 double high, uint64_t* step);
 cudaError_t launch_rope(const RopeArgs& p, int32_t dtype, cudaStream_t stream);
 cudaError_t read_error_rope(int32_t* status, bool clear);

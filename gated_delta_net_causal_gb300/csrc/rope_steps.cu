@@ -66,7 +66,7 @@ uint64_t units(Two x) {
 
 }  // namespace
 
-void rope_steps(int32_t rotary_dim, double base, int32_t scaling, double factor, double original_length, double low,
+bool rope_steps(int32_t rotary_dim, double base, int32_t scaling, double factor, double original_length, double low,
                 double high, uint64_t* step) {
   const double R = rotary_dim, m = rotary_dim / 2;
   const double two_pi = 6.283185307179586476925286766559;
@@ -106,11 +106,14 @@ void rope_steps(int32_t rotary_dim, double base, int32_t scaling, double factor,
       if (scaling == GDN_ROPE_RAMP) keep = add(kOne, negative(keep));
     }
     const Two rest = add(kOne, negative(keep));
+    if (!isfinite(rest.hi / factor) && scaling != GDN_ROPE_PLAIN) return false;
     if (rest.hi != 0.0) keep = add(keep, div(rest, Two{factor, 0.0}));
     const Two turns = mul(mul(b, keep), kTurn);
+    if (!isfinite(turns.hi) || !isfinite(turns.lo)) return false;
     step[i] = units(turns);
     b = mul(b, ratio);
   }
+  return true;
 }
 
 }  // namespace gdn

@@ -547,8 +547,9 @@ typedef struct gdn_rope_table {
 /*
  * Fills *table. base > 1; factor > 0 (LINEAR, BANDS, RAMP);
  * original_length > 0 and 0 < low < high (BANDS, RAMP); all of them and
- * amplitude finite, else GDN_ERR_INVALID_ARG. What a scaling does not use is
- * ignored.
+ * amplitude finite, and the frequencies too (a factor next to 0 makes some
+ * that are not), else GDN_ERR_INVALID_ARG and *table is left as it was. What a
+ * scaling does not use is ignored.
  */
 gdn_status gdn_rope_frequencies(int32_t rotary_dim, int32_t layout, double base, int32_t scaling,
                                 double factor, double original_length, double low, double high,
