@@ -45,6 +45,7 @@
 // A wait that gives up raises the CTA's abort flag; every role then leaves its
 // loop at once.
 #include <cuda.h>
+#include <stddef.h>
 
 #include "attn_common.cuh"
 #include "tc_common.cuh"
@@ -83,9 +84,10 @@ struct BShared {
   uint64_t piece_full[kBRing], piece_empty[kBRing];
   AttnPiece piece[kBRing];
   AttnPlan plan;
-  int abort;
+  int abort, loads;  // (side by side: wait_for_piece); tiles that were asked for
   uint32_t tmem;
 };
+static_assert(offsetof(BShared, loads) == offsetof(BShared, abort) + 4, "wait_for_piece");
 
 // the tile [k][mn] of 16-bit elements with k as the contraction (MN-major,
 // 128-byte swizzle), boxes of 64 mn columns kTile / kBoxes apart; 16 of k
@@ -213,6 +215,44 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int* ab
   return ok != 0;
 }
 
+// The same for a piece of work, which the loading warp hands out behind the
+// last tile of the one before: a half without rows waits for it as long as the
+// other half's tiles take, and a long cache's take more than any fixed time. So
+// the limit counts from the last tile that was asked for (an int behind
+// *abort_flag); there are finitely many, and the loading warp's own waits have
+// the plain limit, so this one ends too.
+__device__ __forceinline__ bool wait_for_piece(uint64_t* bar, uint32_t parity, int* abort_flag) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 t0, t1;\n\t.reg .b32 f, n0, n1;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "@p bra DONE;\n\t"
+      "mov.u64 t0, %%globaltimer;\n\t"
+      "ld.volatile.shared.b32 n0, [%4+4];\n"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "@p bra DONE;\n\t"
+      "ld.volatile.shared.b32 f, [%4];\n\t"
+      "setp.ne.b32 q, f, 0;\n\t"
+      "@q bra DONE;\n\t"
+      "mov.u64 t1, %%globaltimer;\n\t"
+      "ld.volatile.shared.b32 n1, [%4+4];\n\t"
+      "setp.ne.b32 q, n1, n0;\n\t"
+      "@q mov.u64 t0, t1;\n\t"
+      "mov.b32 n0, n1;\n\t"
+      "sub.u64 t1, t1, t0;\n\t"
+      "setp.lt.u64 q, t1, %5;\n\t"
+      "@q bra AGAIN;\n\t"
+      "mov.b32 f, 1;\n\t"
+      "st.volatile.shared.b32 [%4], f;\n"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u), "r"(smem_u32(abort_flag)), "l"(kWaitLimitNs)
+      : "memory");
+  return ok != 0;
+}
+
 template <typename T>
 struct Half;
 template <>
@@ -302,7 +342,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       mbar_init(&sh.piece_full[i], 1);
       mbar_init(&sh.piece_empty[i], kBTakers);
     }
-    sh.abort = 0;
+    sh.abort = sh.loads = 0;
     fence_mbar_init();
   }
   if (tid < 2 && p.part_o != nullptr) p.part_at[2 * blockIdx.x + tid] = make_int4(kAttnWhole, 0, 0, 0);
@@ -315,7 +355,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
   const auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_for(bar, parity, &sh.abort); };
   // piece i of the CTA, for a whole warp; false: there is none
   const auto take = [&](int i, AttnPiece* w) {
-    const bool ok = wait(&sh.piece_full[i % kBRing], (i / kBRing) & 1);
+    const bool ok = wait_for_piece(&sh.piece_full[i % kBRing], (i / kBRing) & 1, &sh.abort);
     *w = sh.piece[i % kBRing];
     return __all_sync(0xffffffffu, ok) && w->tokens != 0;
   };
@@ -340,6 +380,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
         ok = ok && (round == 0 || wait(&empty[st], (round - 1) & 1));
         if (!ok) return;
         ++n;
+        *(volatile int*)&sh.loads = (int)(n_k + n_v);
         mbar_arrive_expect_tx(&full[st], G::kTile);
         for (int b = 0; b < G::kBoxes; ++b)
           tma_load_3d(ring + st * G::kTile + b * kBK * 128, map, 64 * b, kh, row, &full[st]);
