@@ -60,6 +60,7 @@ constexpr int kBScores = 8, kBLoad = 9, kBOut = 10, kBCheck = 11;  // warps
 constexpr int kBRing = 4;         // pieces handed out ahead
 constexpr int kBTakers = 11;      // warps that take each piece: all but the one that loads
 constexpr float kBGrow = 8.f;     // log2 by which a weight may exceed 1
+constexpr float kBFar = 65536.f;  // scaled scores from which on the maximum is taken off before they are scaled
 
 template <int D>
 struct TcGeom {
@@ -588,7 +589,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
     const int h = warp >> 2, qd = warp & 3, row = 32 * qd + lane;
     const uint32_t ts = tb + ((uint32_t)(32 * qd) << 16) + kColS, tp = ts + kColP + 64 * h;
     const uint32_t to = tb + ((uint32_t)(32 * qd) << 16) + kColO + 128 * h;
-    const float sc = p.scale * kAttnLog2e;
+    const float sc = p.scale * kAttnLog2e, grows = fminf(kBGrow / sc, 3.4e38f);
     const int half = p.item / 2, row_token = h * half + row / p.group, member = row % p.group;
     const bool row_used = row < half * p.group;
     uint32_t n_s = 0;  // tiles so far
@@ -614,7 +615,15 @@ __global__ void __launch_bounds__(kBThreads, 1)
       const int n = half_tiles(p, w, h);
       const bool some = __any_sync(0xffffffffu, valid);
       const int least = (int)__reduce_min_sync(0xffffffffu, valid ? (unsigned)sees : 0x7fffffffu);
-      float M = -INFINITY;  // largest score so far, times scale log2 e (or a little less)
+      // M: the largest score so far (or a little less), not scaled. base: what
+      // makes a scaled score its weight's exponent, kLift less the scaled M.
+      // Rounded, it is off by 2^-24 of itself, for all of a row's weights alike,
+      // which the division by their sum undoes; but 2^30 would move them by 2^5,
+      // out of what 16 bits hold. So from kBFar on M is taken off the scores
+      // before they are scaled, which is exact next to it, and kLift is added.
+      float M = -INFINITY, base = 0.f, plus = 0.f;
+      bool far = false;  // such a row is among the warp's
+      const auto base_of = [&](float m) { return m == -INFINITY ? 0.f : fmaf(-m, sc, Half<T>::kLift); };
       float2 sum = make_float2(0.f, 0.f);
       for (int j = 0; j < n; ++j) {
         alive = __all_sync(0xffffffffu, wait(&sh.s_full[h], n_s & 1));
@@ -648,15 +657,19 @@ __global__ void __launch_bounds__(kBThreads, 1)
         for (int c = 4; c < kBK; c += 8)
 #pragma unroll
           for (int e = 0; e < 4; ++e) top[e] = fmaxf(fmaxf(top[e], s[c + e]), c + 4 + e < kBK ? s[c + 4 + e] : top[e]);
-        const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
-        if (j == 0) {
-          M = high;
-        } else {
-          const bool grow = high - M > kBGrow;
-          if (__any_sync(0xffffffffu, grow)) {
+        const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        // rare: a maximum that has grown (in a first tile, from nothing), or rows far off
+        const bool grow = high - M > grows;
+        if (__any_sync(0xffffffffu, grow) || far) {
+          float f = 1.f;
+          if (grow) {
+            const float next = base_of(high);
+            f = exp2_fast(fabsf(next) >= kBFar || M == -INFINITY ? (M - high) * sc : next - base);
+            M = high;
+            base = next;
+          }
+          if (j > 0 && __any_sync(0xffffffffu, grow)) {
             if (!o_done(n_s - 1)) break;
-            const float f = grow ? exp2_fast(M - high) : 1.f;
-            if (grow) M = high;
             sum = make_float2(sum.x * f, sum.y * f);
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
@@ -668,9 +681,16 @@ __global__ void __launch_bounds__(kBThreads, 1)
               tc::tmem_st16(to + c, o);
             }
           }
+          plus = base;
+          far = __any_sync(0xffffffffu, fabsf(base) >= kBFar);
+          if (far) {
+            float off = 0.f;
+            if (fabsf(base) >= kBFar) off = M, plus = Half<T>::kLift;
+#pragma unroll
+            for (int c = 0; c < kBK; ++c) s[c] -= off;
+          }
         }
-        const float base = M == -INFINITY ? 0.f : Half<T>::kLift - M;
-        const float2 sc2 = make_float2(sc, sc), base2 = make_float2(base, base), one = make_float2(1.f, 1.f);
+        const float2 sc2 = make_float2(sc, sc), base2 = make_float2(plus, plus), one = make_float2(1.f, 1.f);
         uint32_t r[kBK / 2];
 #pragma unroll
         for (int c = 0; c < kBK / 2; ++c) {
@@ -693,7 +713,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       // ---- the outputs
       if (some) {
         if (n > 0 && !o_done(n_s)) break;
-        const float l = sum.x + sum.y, top = M - (M == -INFINITY ? 0.f : Half<T>::kLift);
+        const float l = sum.x + sum.y, top = M == -INFINITY ? M : -base;
         if (n > 0 && *(volatile int*)&sh.piece[i % kBRing].bad != 0) {
           // what the look through V took out of rows that this one sees
           const int item_least = attn_sees(w, 0);

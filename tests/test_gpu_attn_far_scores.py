@@ -1,0 +1,77 @@
+"""Softmax attention where scores are large: queries and keys of small whole numbers and scales that are powers of two, so
+that scores are exact, and either tie or differ by so much that one of them takes all."""
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_net_causal_gb300 as gdn
+from tests import attn_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def ints(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def inputs(seed, tokens, rows, hq, hk, D, dtype):
+    gen = torch.Generator().manual_seed(seed)
+    io = ref.DT[dtype]
+    q = torch.randint(-4, 5, (tokens, hq * D), generator=gen).to(io).cuda()
+    k = torch.randint(-4, 5, (rows, hk * D), generator=gen).to(io).cuda()  # |q . k| <= 16 D: exact in fp32
+    v = torch.randn((rows, hk * D), generator=gen).to(io).cuda()
+    return q, k, v
+
+
+def check(c, q, k, v, out, lse, visible, scale):
+    """Each row's output is the mean of the values whose scores tie for the largest. Bound: the weights are equal, but may
+    be off a power of two, so that their rounding to 16 bits counts (their sum is taken before it); then the fp32 sums
+    and the division, (n + 4) 2^-23 of the values' mean magnitude for n of them, and the output's rounding. lse: 2^-24 of
+    itself for the scores' factor, their product, the sum of both logarithms, and the way back from log2, of up to 8 more
+    than itself (7 of which the f16 kernel lifts the weights by)."""
+    hq, hk, D, dtype = c
+    Q, K, V = (ref.f64(x).reshape(x.shape[0], -1, D) for x in (q, k, v))
+    o, l = ref.f64(out), ref.f64(lse)
+    for h in range(hq):
+        kh = h // (hq // hk)
+        s = np.where(visible, Q[:, h] @ K[:, kh].T, -np.inf)
+        top = s.max(1)
+        tie = s == top[:, None]
+        n = tie.sum(1)
+        want = (tie @ V[:, kh]) / n[:, None]
+        mag = (tie @ np.abs(V[:, kh])) / n[:, None]
+        err = ((n[:, None] + 4) * 2.0 ** -23 + (ref.UNIT[dtype] if dtype != "f32" else 0.0)) * mag
+        ref.check(o[:, h], want, err + ref.UNIT[dtype] * (np.abs(want) + err) + ref.SMALLEST[dtype], f"head {h}")
+        w = scale * top + np.log(n)
+        ref.check(l[:, h], w, 4 * 2.0 ** -24 * (np.abs(w) + 8), f"lse of head {h}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("hq,hk,D", [(4, 2, 64), (2, 1, 128), (6, 1, 32)])
+@pytest.mark.parametrize("power", [10, 15, 20, 24, 30, 60, 110])
+def test_prompts(dtype, hq, hk, D, power):
+    T = 333
+    q, k, v = inputs(power, T, T, hq, hk, D, dtype)
+    out, lse = torch.empty((T, hq, D), device="cuda", dtype=ref.DT[dtype]), torch.empty((T, hq), device="cuda")
+    gdn.gdn_attn_prefill(gdn.dims(hk, hq, D, io_dtype=ref.DT[dtype]), ints(0, T), q, k, v, out, lse=lse,
+                         scale=2.0 ** power)
+    check((hq, hk, D, dtype), q, k, v, out, lse, ref.causal(T, T), 2.0 ** power)
+    assert gdn.gdn_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("workspace", ["auto", None])
+@pytest.mark.parametrize("power", [12, 24, 40, 100])
+def test_long_caches(dtype, workspace, power):
+    """Parts of several CTAs, rising maxima, ties across parts, negative scores only."""
+    hq, hk, D, m = 4, 1, 64, 6000
+    q, k, v = inputs(power, 3, m, hq, hk, D, dtype)
+    q[2] = -q[2].abs() - 1  # the last token's scores
+    k[:, :] = k.abs() + 1   # are all negative
+    d = gdn.dims(hk, hq, D, io_dtype=ref.DT[dtype])
+    out, lse = torch.empty((3, hq, D), device="cuda", dtype=ref.DT[dtype]), torch.empty((3, hq), device="cuda")
+    gdn.gdn_attn_prefill(d, ints(0, 1, 3), q, k, v, out, lse=lse, scale=2.0 ** power, kv_start=ints(0, 0),
+                         kv_len=ints(m, m), workspace=workspace)
+    see = np.concatenate([ref.causal(1, m), ref.causal(2, m)])
+    check((hq, hk, D, dtype), q, k, v, out, lse, see, 2.0 ** power)
