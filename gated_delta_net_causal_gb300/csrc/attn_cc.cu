@@ -182,9 +182,16 @@ __global__ void __launch_bounds__(kAT, 2) attn_cc_kernel(const AttnArgs p) {
       if (r >= rows) continue;
       if (w.part != kAttnWhole) {
         const int64_t at = (int64_t)attn_slot(blockIdx.x, w.part) * p.part_rows + r;
+        // The parts of a row meet by their scaled maxima, each rounded by up to
+        // 2^-24 of itself. The weights here are to the one that is not: what
+        // lies between them goes into the part (far off it could be anything,
+        // and scores themselves are rounded by more).
+        const float scaled = top[i] * sc;
+        const float f = fabsf(scaled) < 65536.f ? exp2f(fmaf(top[i], sc, -scaled)) : 1.f;
 #pragma unroll
-        for (int j = 0; j < NP; ++j) *reinterpret_cast<float2*>(p.part_o + at * D + 32 * j + 2 * tx) = o[i][j];
-        if (tx == 0) p.part_ml[at] = make_float2(top[i] * sc, l);
+        for (int j = 0; j < NP; ++j)
+          *reinterpret_cast<float2*>(p.part_o + at * D + 32 * j + 2 * tx) = make_float2(o[i][j].x * f, o[i][j].y * f);
+        if (tx == 0) p.part_ml[at] = make_float2(scaled, l * f);
         continue;
       }
       const int64_t token = w.q0 + r / p.group;

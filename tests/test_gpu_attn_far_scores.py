@@ -75,3 +75,40 @@ def test_long_caches(dtype, workspace, power):
                          kv_len=ints(m, m), workspace=workspace)
     see = np.concatenate([ref.causal(1, m), ref.causal(2, m)])
     check((hq, hk, D, dtype), q, k, v, out, lse, see, 2.0 ** power)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("order", [1, -1])
+@pytest.mark.parametrize("steep", [0.25, 4.0, 64.0, 1024.0])
+def test_scores_that_move_by_hundreds(dtype, order, steep):
+    """Scores that rise or fall by up to a million over the keys in exact steps (a quarter and more of a key's): rising,
+    every token's last visible key leads; falling, the first one. Against fp64, with the bound of exact scores: the
+    exponents' differences are off by 2^-23 of themselves where they matter (up to 110; the rounding of the maximum is
+    the same for all of a row); a sum's terms shrink by exp(-1/4) at least from one key to the next, so that after the
+    67th they are below its roundings: 72 of 2^-23, less than 2^-16; weights and outputs as in attn_reference."""
+    n, D = 1000, 64
+    io = ref.DT[dtype]
+    q = torch.zeros((n, D), device="cuda", dtype=io)
+    k = torch.zeros((n, D), device="cuda", dtype=io)
+    v = torch.randn((n, D), generator=torch.Generator().manual_seed(3)).to(io).cuda()
+    i = torch.arange(n, device="cuda")
+    q[:, 0], q[:, 1] = 32.0, 1.0
+    k[:, 0], k[:, 1] = (i // 32).to(io), (i % 32).to(io)  # q . k = the key's index
+    out, lse = torch.empty((n, 1, D), device="cuda", dtype=io), torch.empty((n, 1), device="cuda")
+    scale = steep
+    if order < 0:
+        q = -q
+    gdn.gdn_attn_prefill(gdn.dims(1, 1, D, io_dtype=io), ints(0, n), q, k, v, out, lse=lse, scale=scale)
+    s = np.where(ref.causal(n, n), order * scale * np.arange(n)[None, :], -np.inf)
+    top = s.max(1, keepdims=True)
+    w = np.exp(s - top)
+    total = w.sum(1, keepdims=True)
+    V = ref.f64(v)
+    want, mag = (w / total) @ V, (w / total) @ np.abs(V)
+    off = 110 * 2.0 ** -23
+    rel = 2 * off + 2.0 ** -21 + 2.0 ** -16 + (ref.UNIT[dtype] if dtype != "f32" else 0.0)
+    err = mag * rel + 2 * ref.SMALLEST[dtype] * np.abs(V).sum(0)
+    ref.check(ref.f64(out[:, 0]), want, err + ref.UNIT[dtype] * (np.abs(want) + err) + ref.SMALLEST[dtype], "out")
+    want_lse = (top + np.log(total))[:, 0]
+    ref.check(ref.f64(lse[:, 0]), want_lse, off + 2.0 ** -16 + 4 * 2.0 ** -24 * (np.abs(want_lse) + 8),
+              "lse")
