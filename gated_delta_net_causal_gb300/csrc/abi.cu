@@ -743,7 +743,7 @@ gdn_status check_attn(const gdn_dims* dims, int32_t num_seqs, const int32_t* cu_
   const int64_t es = dtype_size(dims->io_dtype), Hq = dims->n_v_heads, Hk = dims->n_k_heads, D = dims->head_dim;
   if (num_seqs == 0 || !cu_seqlens || !q || !out || kv_rows < 0 || (kv_rows > 0 && (!k || !v)))
     return GDN_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !isfinite(scale)) return GDN_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !isfinite(scale * 1.4426950408889634f)) return GDN_ERR_INVALID_ARG;
   if (q_stride < Hq * D || k_stride < Hk * D || v_stride < Hk * D) return GDN_ERR_INVALID_ARG;
   if (kv_rows > INT32_MAX - 1024) return GDN_ERR_EXTENT;
   const int64_t strides[] = {q_stride, k_stride, v_stride};

@@ -623,7 +623,8 @@ gdn_status gdn_rope(const gdn_dims* dims, const gdn_rope_table* table, int64_t t
  *              holds those of the new tokens; sequences may share rows).
  *              Values are clamped to the rows that there are. Both NULL: a
  *              sequence's keys are its tokens' own rows, kv_rows must be T.
- * scale        finite, > 0.
+ * scale        > 0, and finite times log2 e too (below 2.35e38); scaled scores
+ *              past fp32's range count as infinite.
  * out          [T][Hq][D] io dtype;  lse [T][Hq] fp32 or NULL.
  * workspace    device scratch of at least gdn_attn_prefill_workspace_size
  *              bytes, 256-byte aligned, not overlapping any other argument;
