@@ -112,3 +112,25 @@ def test_scores_that_move_by_hundreds(dtype, order, steep):
     want_lse = (top + np.log(total))[:, 0]
     ref.check(ref.f64(lse[:, 0]), want_lse, off + 2.0 ** -16 + 4 * 2.0 ** -24 * (np.abs(want_lse) + 8),
               "lse")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("power", [12, 24, 40, 100])
+def test_shared_prefixes(dtype, power):
+    """Odd scores over the prefix, even ones over the sequences' own keys, so that no tie lies across the two."""
+    hq, hk, D, p, own = 4, 2, 64, 700, [5, 300, 40]
+    n, rows = len(own), 700 + sum(own)
+    q, k, v = inputs(power, n, rows, hq, hk, D, dtype)
+    q[:, ::D] = 1.0  # each head's first element
+    k *= 2
+    k[:p, ::D] = 1.0
+    start = [p, p + own[0], p + own[0] + own[1]]
+    d = gdn.dims(hk, hq, D, io_dtype=ref.DT[dtype])
+    out, lse = torch.empty((n, hq, D), device="cuda", dtype=ref.DT[dtype]), torch.empty((n, hq), device="cuda")
+    gdn.gdn_attn_shared(d, ints(0, 1, 2, 3), q, k, v, ints(*start), ints(*own), ints(0, 2), ints(0), ints(p), out, lse=lse,
+                        scale=2.0 ** power)
+    see = np.zeros((n, rows), bool)
+    for i in range(n):
+        see[i, start[i]:start[i] + own[i]] = True
+        see[i, :p] = i < 2  # the last sequence is outside of the group
+    check((hq, hk, D, dtype), q, k, v, out, lse, see, 2.0 ** power)
