@@ -6,8 +6,11 @@
 // columns. q and k lie transposed in shared memory, so that a step of the
 // contraction is two 16-byte reads for 16 products; the weights take k's
 // place, transposed as well. Warps without a row (a single token has a few of
-// the 64) only load. 4096 tokens, 8 heads of 128: 0.90 ms, 38 TFLOP/s, half of
-// the fp32 units' rate; bound by shared memory and the phases between barriers.
+// the 64) only load. 4096 tokens, 8 / 2 heads of 128: 0.90 ms, 38 TFLOP/s, half
+// of the fp32 units' rate; 32 tokens on up to 8192 keys, 32 / 8 heads, 479 us,
+// 2.3 TB/s; 64 tokens behind 8192 shared keys 433 us. Bound by shared memory and
+// by the phases between barriers: with one buffer, memory idles while a tile is
+// computed, and the units while it is loaded.
 #include "attn_common.cuh"
 
 namespace gdn {

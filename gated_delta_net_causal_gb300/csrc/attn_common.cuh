@@ -14,8 +14,9 @@
 // sums do not depend on which CTA ran first. The lengths are on the device:
 // every CTA adds up the costs for itself, its threads a slice of the sequences
 // each. What a CTA runs once comes from a cold instruction cache, so this is
-// kept short: costs are sums of arithmetic series (exact numbers of tiles would
-// be sums of floors: 17,000 cycles instead of 5,000).
+// kept short: costs are sums of arithmetic series, where exact numbers of tiles
+// would be sums of floors (3,200 to 4,000 cycles now, with the barriers and the
+// TMEM set up).
 #pragma once
 
 #include "gdn_common.cuh"
@@ -62,9 +63,19 @@ __device__ __forceinline__ int attn_visible(const AttnSeq& s, int at) {
   return v > 0 ? (int)v : 0;
 }
 
-// What an item costs besides its keys, in tiles. A prompt of 4096 tokens and
-// ragged prompts of 34,482: with 2 114 and 938 us, with 3 110 and 899, with 4
-// 107 and 884, with 6 109 and 903.
+// What an item costs besides its keys, in tiles. With 1, 2, 4, 6 and 8 (us):
+//   bf16, one prompt of 4096 tokens, 32 / 8 heads of 128  122 110 105 108 110
+//   bf16, ragged prompts of 34,482, 32 / 4 heads of 128   987 962 936 960 988
+//   bf16, one prompt of 4096 tokens, 32 / 8 heads of 64    99  90  88  91  93
+//   f16, chunks of 812 tokens on caches, heads of 64       94  86  80  90  90
+//   bf16, 64 tokens on up to 8192 keys of 128             172 173 174 175 174
+//   bf16, 64 tokens behind 8192 shared keys                60  55  61  69  77
+//   f16, 52 tokens behind shared keys, heads of 96         23  22  20  20  21
+//   f32, one prompt of 4096 tokens, 8 / 2 heads of 128    864 880 901 923 935
+//   f32, 32 tokens on up to 8192 keys of 128              464 470 479 494 507
+//   f32, 64 tokens behind 8192 shared keys                374 393 433 463 490
+// So 4, which 16-bit prompts want, for all: batches behind a prefix would take
+// 2, f32 (tiles of 64 keys, no start to speak of) 1.
 constexpr int kAttnStart = 4;
 
 // Keys that the last token of the item from `at` on sees.

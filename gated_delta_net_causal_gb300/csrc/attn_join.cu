@@ -6,7 +6,8 @@
 // the CTA that ended it. A warp takes a row: the largest score of the parts,
 // their factors, and the sum of the parts' outputs, always in CTA order. Bound
 // by memory's latency, a wave of CTAs after the other: about 8 us for the 40 MB
-// of parts of a prompt, 4 us for a single token's.
+// of parts of a prompt, 4 us for a single token's. (At head_dim 128 it has
+// 32 registers and 4 bytes spilled.)
 #include "attn_common.cuh"
 
 namespace gdn {

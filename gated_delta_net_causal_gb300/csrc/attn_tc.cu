@@ -16,8 +16,8 @@
 // registers at once, so S is free again long before the softmax is done, and
 // the scores of the other tile, then the tile's own next ones, are made under
 // it. With two S, each with its P in its place, the next scores of a tile had
-// to wait for its O += P V: a chain of softmax and both products, 3400 cycles
-// for both tiles, where the products alone take 2048 (2300 to 2500 now).
+// to wait for its O += P V: a chain of softmax and both products. Now both
+// tiles take 2550 cycles at head_dim 128, of which the products are 2048.
 //
 // Warps 0 to 3 are A's rows, 4 to 7 B's; two issue the products, one hands out
 // the pieces of work (attn_common.cuh) and loads (Q once an item, K and V
@@ -29,18 +29,28 @@
 //
 // One warp issues the scores, another O += P V: the tensor cores take a few
 // products ahead from each, and an issuing warp is held until they do, so that
-// with one warp for both whatever the other kind waited for was looked at late
-// (a gap of 600 cycles in each 1800). A tile's next scores go first, then its
-// O: its rows wait for the scores, and for O only when their next weights are
-// done (the other way round a tile of both halves took 2900 cycles).
+// with one warp for both whatever the other kind waited for was looked at late.
+// A tile's next scores go first, then its O: its rows wait for the scores, and
+// for O only when their next weights are done.
+//
+// Rounding. The weights go to 16 bits because the tensor cores multiply them by
+// V in the type of V; the error that adds is that of the output's own rounding
+// again (0.0021 of the outputs' norm in bf16, where the exact result rounded
+// has 0.0016). The tensor cores cut their fp32 sums off, up to 1.5 2^-24 of O
+// for each step of 16 keys, always towards zero: 2^-11 once a CTA takes 131,072
+// keys in a row, 0.006 at 2^20 (measured; f16, no workspace).
 //
 // Measured (as graph nodes): one prompt of 4096 tokens, 32 query heads and 8
-// key heads of 128, 104 us, 1.32 PFLOP/s of the visible pairs, the tensor pipe
+// key heads of 128, 105 us, 1.31 PFLOP/s of the visible pairs, the tensor pipe
 // 62 % active; 32,768 tokens, 16 and 2 heads, 1.95 PFLOP/s. 64 single tokens on
-// caches of up to 8192 keys 170 us, 6.4 TB/s. What bounds it: on prompts the
-// tensor cores, and the start and end of an item (about 5000 cycles in which
-// they idle); at head_dim 64 and below the softmax's 1600 cycles a tile; on
-// caches memory.
+// caches of up to 8192 keys 174 us, 6.3 TB/s. What bounds it: on prompts of
+// head_dim 128 the tensor cores, and the end of an item and the start of the
+// next (5,900 cycles from its last weights to the next scores); on caches of
+// head_dim 128 memory. At head_dim 64 and below nothing is full (tensor pipe 40
+// %, exponentials 40 %, issue 45 %): a tile is a chain from scores to weights
+// of about 1,750 cycles whatever head_dim is, and the two warps of rows that a
+// scheduler has do not hide it (2,070 cycles for both tiles, products 1,024).
+// Items of at most 128 rows (single tokens) have half A alone.
 //
 // A wait that gives up raises the CTA's abort flag; every role then leaves its
 // loop at once.

@@ -14,8 +14,13 @@
 // into shared memory. A thread has the same elements of every so-many-th head
 // of q, k and v of one token: 16 bytes (two times 16 where the pairs are
 // halves; single elements where a half ends within 16 bytes), and so keeps
-// their sines and cosines in registers. Bound by memory: 8192 tokens of 64 + 8
-// heads of 128 in bf16 56 us, 5.35 TB/s.
+// their sines and cosines in registers. 8192 tokens of 64 + 8 heads of 128:
+//   bf16, halves, the whole head      56 us, 5.35 TB/s: bound by memory
+//   bf16, halves, 64 of 128 turn      76 us, 4.0 TB/s
+//   bf16, neighbours, all or a part   75 us, 4.0 TB/s
+//   bf16, halves of 18                178 us, 1.7 TB/s: 2 bytes an access
+//   fp32, halves of 18                190 us, 3.2 TB/s: 4 bytes an access
+// (16-bit halves of 16 bytes spill 8 bytes under the bound of four CTAs an SM.)
 #include <type_traits>
 
 #include "gdn_common.cuh"

@@ -635,8 +635,14 @@ gdn_status gdn_rope(const gdn_dims* dims, const gdn_rope_table* table, int64_t t
  *
  * f16 and bf16 run on the tensor cores, with fp32 scores, sums and outputs
  * and the weights rounded to io dtype (their sum is taken before that); f32
- * on the fp32 units. What is not finite in a key or value reaches only tokens
- * that see it.
+ * on the fp32 units. The tensor cores cut sums off: an output may be short of
+ * 1.5 2^-24 of itself for every 16 keys that one CTA takes in a row (2^-11 at
+ * 131,072 keys; with a workspace a call's keys are spread over all CTAs). What
+ * is not finite in a key or value reaches only tokens that see it.
+ *
+ * A sequence's keys are one stretch of rows: a cache in pages behind a table
+ * is not read, whatever rows gdn_rope wrote them to. Heads of 256 are refused
+ * as by every call here (GDN_ERR_UNSUPPORTED). There is no backward pass.
  */
 gdn_status gdn_attn_prefill(const gdn_dims* dims, int32_t num_seqs, const int32_t* cu_seqlens,
                             int64_t total_tokens, const void* q, int64_t q_stride, const void* k,
@@ -652,7 +658,10 @@ gdn_status gdn_attn_prefill_workspace_size(const gdn_dims* dims, int32_t num_seq
 /*
  * gdn_attn_prefill for a batch in which groups of neighbouring tokens share a
  * prefix: every token sees all keys of its group's prefix and, causally, its
- * sequence's own. The prefix is read once for all query rows of its group.
+ * sequence's own. A prefix is read once for every 256 query rows (tokens times
+ * the query heads of a key head; 64 rows in f32) of its group. A token's two
+ * outputs are joined by their lse, whose rounding in fp32, 2^-24 of it, is what
+ * their weights may be off by.
  *
  * num_groups   0 <= N_g <= 65535.
  * group_cu     device int32 [N_g + 1], non-decreasing: group j is the tokens
