@@ -134,3 +134,19 @@ def test_shared_prefixes(dtype, power):
         see[i, start[i]:start[i] + own[i]] = True
         see[i, :p] = i < 2  # the last sequence is outside of the group
     check((hq, hk, D, dtype), q, k, v, out, lse, see, 2.0 ** power)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_rows_that_see_nothing_beside_far_ones(dtype):
+    """Tokens without a key have zeros and -inf, whatever their neighbours' scores are."""
+    hq, hk, D, power = 4, 2, 64, 30
+    q, k, v = inputs(1, 9, 40, hq, hk, D, dtype)
+    out, lse = torch.empty((9, hq, D), device="cuda", dtype=ref.DT[dtype]), torch.empty((9, hq), device="cuda")
+    gdn.gdn_attn_prefill(gdn.dims(hk, hq, D, io_dtype=ref.DT[dtype]), ints(0, 5, 9), q, k, v, out, lse=lse,
+                         scale=2.0 ** power, kv_start=ints(0, 2), kv_len=ints(2, 38))
+    assert (out[:3] == 0).all() and (lse[:3] == -float("inf")).all()
+    see = np.zeros((9, 40), bool)
+    see[3, :1] = see[4, :2] = True
+    see[5:, 2:] = ref.causal(4, 38)
+    rows = slice(3, 9)
+    check((hq, hk, D, dtype), q[rows], k, v, out[rows], lse[rows], see[rows], 2.0 ** power)

@@ -116,3 +116,38 @@ def test_keys_and_values_side_by_side_in_a_cache(dtype):
     K, V = (ref.f64(x[first:first + T]).reshape(T, hk, D) for x in (kc, vc))
     o, tol, _, _ = ref.attention(ref.f64(q).reshape(T, hq, D), K, V, ref.causal(T, T), D ** -0.5, dtype)
     ref.check(ref.f64(out), o, tol, "out")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("hq,hk,D,each", [(8, 2, 64, 8), (12, 4, 96, 5), (16, 1, 128, 7), (3, 3, 32, 40)])
+def test_groups_of_several_items(dtype, hq, hk, D, each):
+    """More query rows of a group than one item holds, groups that end within one, and sequences behind the last."""
+    keys = [each + 7 * i % 61 for i in range(23)]
+    c = Case(35, [each] * 23, keys, hq, hk, D, dtype, tiled=D == 96, prefixes=[(300, 11), (129, 2), (40, 9)], extra=2)
+    c.run_shared()
+    c.check(shared=True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_shared_calls_side_by_side(dtype):
+    """Two captured calls with a workspace each, replayed on two streams at once."""
+    cs = [Case(36 + i, [2] * 9, [40 * j + 2 for j in range(9)], 8, 2, 64, dtype, prefixes=[(1500, 5), (64, 4)])
+          for i in range(2)]
+    streams, graphs, keep = [torch.cuda.Stream() for _ in cs], [], []
+    for c, s in zip(cs, streams):
+        ws = torch.empty(gdn.gdn_attn_shared_workspace_size(c.d, 9, 18, 2), dtype=torch.uint8, device="cuda")
+        groups = (ints([0, 10, 18]), ints([p for p, _, _ in c.prefix]), ints([n for _, n, _ in c.prefix]))
+        keep.append((ws, groups))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            gdn.gdn_attn_shared(c.d, c.cu, c.q, c.k, c.v, c.kv["kv_start"], c.kv["kv_len"], *groups, c.out, lse=c.lse,
+                                workspace=ws)
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for c in cs:
+        c.check(shared=True)
